@@ -332,7 +332,7 @@ def _handles(s):
         s["rotary"] = mtl.Rotary(c["D"], c["r"], layout=c["layout"], scaling=c.get("scaling", "none"), factor=c.get("factor", 1.0), **more)
     if "k" in s:
         s["cache"] = mtl.BlockCache.over(s["k"], s["v"], s["k_scale"], s["v_scale"])
-        s["batch"] = s["cache"].batch(s["cu"], s["lens"], s["table"], max_new=max(s["new_host"]), max_len=max(s["lens_host"]))
+        s["batch"] = s["cache"].batch(s["cu"], s["lens"], s["table"], max_new=max(1, *s["new_host"]), max_len=max(s["lens_host"]))
     s["ready"] = True
 
 
