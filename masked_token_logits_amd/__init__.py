@@ -13,6 +13,7 @@ from __future__ import annotations
 
 from ._abi import (  # noqa: F401
     DLLM_BATCH_MAX,
+    DLLM_CACHE_BLOCK,
     DLLM_ERR_HIP,
     DLLM_ERR_INVALID_ARG,
     DLLM_ERR_UNSUPPORTED,
@@ -20,12 +21,21 @@ from ._abi import (  # noqa: F401
     DLLM_K_MAX_LIMIT,
     DLLM_NOALLOC_SCRATCH_BYTES,
     DLLM_OK,
+    DLLM_ROTARY_DIM_MAX,
     DLLM_SCORE_CONF,
     DLLM_SCORE_MARGIN,
     DLLM_SCORE_NEG_ENTROPY,
     EXPORTED,
     LIB_PATH,
     DllmError,
+    dllm_cache,
+    dllm_cache_attention,
+    dllm_cache_attention_workspace_bytes,
+    dllm_cache_batch,
+    dllm_cache_evict,
+    dllm_cache_evict_workspace_bytes,
+    dllm_cache_weigh,
+    dllm_cache_write,
     dllm_ffn_pack_gate_up,
     dllm_ffn_swiglu_chunked,
     dllm_ffn_workspace_bytes,
@@ -42,6 +52,9 @@ from ._abi import (  # noqa: F401
     dllm_probe_source_bytes,
     dllm_probe_wall_clock_khz,
     dllm_policy,
+    dllm_rotary,
+    dllm_rotary_frequencies,
+    dllm_rotary_plan,
     dllm_seq,
     dllm_status_string,
     load,
@@ -244,3 +257,6 @@ class MaskedReadout:
             self.close()
         except Exception:
             pass
+
+
+from .cache import BlockCache, CacheBatch, Rotary  # noqa: E402,F401

@@ -44,7 +44,27 @@ EXPORTED = (
     "dllm_probe_source_bytes",
     "dllm_probe_wall_clock_khz",
     "dllm_probe_gemm_mix",
+    "dllm_rotary_frequencies",
+    "dllm_rotary",
+    "dllm_cache_write",
+    "dllm_cache_attention_workspace_bytes",
+    "dllm_cache_attention",
+    "dllm_cache_weigh",
+    "dllm_cache_evict_workspace_bytes",
+    "dllm_cache_evict",
 )
+
+DLLM_ROTARY_HALF = 0
+DLLM_ROTARY_INTERLEAVED = 1
+ROTARY_LAYOUTS = {"half": DLLM_ROTARY_HALF, "interleaved": DLLM_ROTARY_INTERLEAVED}
+DLLM_ROTARY_PLAIN = 0
+DLLM_ROTARY_LINEAR = 1
+DLLM_ROTARY_BASE = 2
+DLLM_ROTARY_RAMP = 3
+ROTARY_SCALINGS = {"none": DLLM_ROTARY_PLAIN, "linear": DLLM_ROTARY_LINEAR, "base": DLLM_ROTARY_BASE,
+                   "ramp": DLLM_ROTARY_RAMP}
+DLLM_ROTARY_DIM_MAX = 512
+DLLM_CACHE_BLOCK = 32
 
 
 class dllm_step_out(C.Structure):
@@ -76,6 +96,39 @@ class dllm_policy(C.Structure):
         ("score", C.c_int32),
         ("use_threshold", C.c_int32),
         ("tau", C.c_float),
+    ]
+
+
+class dllm_rotary_plan(C.Structure):
+    _fields_ = [
+        ("turns", C.c_void_p),
+        ("magnitude", C.c_float),
+        ("rotary_dim", C.c_int32),
+        ("layout", C.c_int32),
+    ]
+
+
+class dllm_cache(C.Structure):
+    _fields_ = [
+        ("k", C.c_void_p),
+        ("v", C.c_void_p),
+        ("k_scale", C.c_void_p),
+        ("v_scale", C.c_void_p),
+        ("pages", C.c_int64),
+        ("kv_heads", C.c_int32),
+        ("head_dim", C.c_int32),
+    ]
+
+
+class dllm_cache_batch(C.Structure):
+    _fields_ = [
+        ("cu", C.c_void_p),
+        ("lens", C.c_void_p),
+        ("table", C.c_void_p),
+        ("S", C.c_int32),
+        ("table_blocks", C.c_int32),
+        ("max_new", C.c_int32),
+        ("max_len", C.c_int32),
     ]
 
 
@@ -143,6 +196,25 @@ def load(path: str = LIB_PATH):
     lib.dllm_ffn_swiglu_chunked.restype = C.c_int
     lib.dllm_ffn_swiglu_chunked.argtypes = [C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64,
                                             C.c_int64, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]
+    P, i32, i64, f32 = C.c_void_p, C.c_int32, C.c_int64, C.c_float
+    plan_p, cache_p, batch_p = C.POINTER(dllm_rotary_plan), C.POINTER(dllm_cache), C.POINTER(dllm_cache_batch)
+    lib.dllm_rotary_frequencies.restype = C.c_int
+    lib.dllm_rotary_frequencies.argtypes = [i32, C.c_double, i32, C.c_double, i64, C.c_double, C.c_double,
+                                            C.POINTER(C.c_double)]
+    lib.dllm_rotary.restype = C.c_int
+    lib.dllm_rotary.argtypes = [plan_p, P, i64, i32, i32, i64, i64, P, i32, P, i64, i64, P]
+    lib.dllm_cache_write.restype = C.c_int
+    lib.dllm_cache_write.argtypes = [cache_p, batch_p, i64, P, i64, i64, P, i64, i64, P, P, plan_p, P]
+    lib.dllm_cache_attention_workspace_bytes.restype = C.c_size_t
+    lib.dllm_cache_attention_workspace_bytes.argtypes = [cache_p, batch_p, i32]
+    lib.dllm_cache_attention.restype = C.c_int
+    lib.dllm_cache_attention.argtypes = [cache_p, batch_p, i64, P, i64, i64, i32, f32, i32, P, P, P, C.c_size_t, P]
+    lib.dllm_cache_weigh.restype = C.c_int
+    lib.dllm_cache_weigh.argtypes = [cache_p, batch_p, i64, P, i64, i64, i32, f32, i32, P, f32, P, P]
+    lib.dllm_cache_evict_workspace_bytes.restype = C.c_size_t
+    lib.dllm_cache_evict_workspace_bytes.argtypes = [cache_p, batch_p]
+    lib.dllm_cache_evict.restype = C.c_int
+    lib.dllm_cache_evict.argtypes = [cache_p, batch_p, P, P, i32, i32, i32, i32, P, i32, P, P, P, P, C.c_size_t, P]
     _lib = lib
     return lib
 
@@ -283,3 +355,55 @@ def dllm_masked_readout_set_slices(handle, slices: int) -> int:
 
 def dllm_masked_readout_set_gemm_events(handle, ev_before, ev_after) -> int:
     return load().dllm_masked_readout_set_gemm_events(handle, ev_before, ev_after)
+
+
+def _ref(struct):
+    return C.byref(struct) if struct is not None else None
+
+
+def dllm_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: int = DLLM_ROTARY_PLAIN,
+                            factor: float = 1.0, original_len: int = 0, fast: float = 32.0,
+                            slow: float = 1.0) -> tuple[int, list[float]]:
+    """Returns (status, turns per position of each pair)."""
+    turns = (C.c_double * max(int(rotary_dim) // 2, 1))()
+    st = load().dllm_rotary_frequencies(rotary_dim, base, scaling, factor, original_len, fast, slow, turns)
+    return st, list(turns)
+
+
+def dllm_rotary(plan, x, T: int, H: int, D: int, x_token: int, x_head: int, positions, transpose: int, y,
+                y_token: int, y_head: int, stream=None) -> int:
+    return load().dllm_rotary(_ref(plan), _ptr(x), T, H, D, x_token, x_head, _ptr(positions), transpose, _ptr(y),
+                              y_token, y_head, _stream(stream))
+
+
+def dllm_cache_write(cache, batch, T: int, k, k_token: int, k_head: int, v, v_token: int, v_head: int, start,
+                     positions=None, plan=None, stream=None) -> int:
+    return load().dllm_cache_write(_ref(cache), _ref(batch), T, _ptr(k), k_token, k_head, _ptr(v), v_token, v_head,
+                                   _ptr(start), _ptr(positions), _ref(plan), _stream(stream))
+
+
+def dllm_cache_attention_workspace_bytes(cache, batch, q_heads: int) -> int:
+    return int(load().dllm_cache_attention_workspace_bytes(_ref(cache), _ref(batch), q_heads))
+
+
+def dllm_cache_attention(cache, batch, T: int, q, q_token: int, q_head: int, q_heads: int, scale: float, causal: int,
+                         out, lse, workspace, workspace_bytes: int, stream=None) -> int:
+    return load().dllm_cache_attention(_ref(cache), _ref(batch), T, _ptr(q), q_token, q_head, q_heads, scale, causal,
+                                       _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def dllm_cache_weigh(cache, batch, T: int, q, q_token: int, q_head: int, q_heads: int, scale: float, causal: int, lse,
+                     decay: float, weights, stream=None) -> int:
+    return load().dllm_cache_weigh(_ref(cache), _ref(batch), T, _ptr(q), q_token, q_head, q_heads, scale, causal,
+                                   _ptr(lse), decay, _ptr(weights), _stream(stream))
+
+
+def dllm_cache_evict_workspace_bytes(cache, batch) -> int:
+    return int(load().dllm_cache_evict_workspace_bytes(_ref(cache), _ref(batch)))
+
+
+def dllm_cache_evict(cache, batch, weights, keep, max_keep: int, sink: int, recent: int, pool: int, table_out,
+                     out_blocks: int, lens_out, kept, weights_out, workspace, workspace_bytes: int, stream=None) -> int:
+    return load().dllm_cache_evict(_ref(cache), _ref(batch), _ptr(weights), _ptr(keep), max_keep, sink, recent, pool,
+                                   _ptr(table_out), out_blocks, _ptr(lens_out), _ptr(kept), _ptr(weights_out),
+                                   _ptr(workspace), workspace_bytes, _stream(stream))

@@ -19,3 +19,4 @@ from .readout import (  # noqa: F401
     StepResult,
 )
 from .ffn import silu, ffn_rows, ffn_chunked  # noqa: F401,E402
+from . import cache  # noqa: F401,E402

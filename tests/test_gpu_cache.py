@@ -1,0 +1,456 @@
+"""GPU parity of the 8-bit block cache (write, attention, accumulated weights,
+eviction) against the fp64 oracle.
+
+Tolerances, from the arithmetic:
+- write: scales and value bytes are decided by exact comparisons and one
+  rounding, so they are equal.  A rotated key is an fp32 number within 2^-20
+  of its pair's length of the exact one, so its byte is equal unless a
+  rounding boundary is that near.
+- attention: a probability is rounded to fp16 for its product with v, a
+  relative error of at most 2^-11; those roundings are independent, so a
+  dimension's sum is held to six times their root of squares.  Scores are
+  fp32 sums of D exact products: with A = scale max_j sum_i |q_i k_ji|, a
+  score is within dS = (D + 8) 2^-24 A, which moves every probability by that
+  relatively.  The output's rounding adds 2^-8 of the value.
+    |d out| <= 6 2^-11 Q + (2 dS + 2^-20) B + 2^-8 |out|
+    |d lse| <= dS + 2^-21 (|lse| + A + 1)
+- weights: exp of such a score, summed in fp32 over n terms:
+    |d w| <= (dS + 2^-21 (|lse| + A + 1) + n 2^-24) (w - decay w0) + 2^-22 |w|
+- eviction moves bytes and weights: equal."""
+import numpy as np
+import pytest
+
+import workloads as WL
+from _cache_cases import bf16, cache, cu_of, dev_bf16, dev_i32, host, on_gpu, tables
+from oracle import cache as oc
+
+pytestmark = pytest.mark.gpu
+
+
+def _batch(bc, cu, lens, table, **kw):
+    return bc.batch(dev_i32(cu), dev_i32(lens), dev_i32(table), **kw)
+
+
+# ---- write ----------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("D,heads,lens,new,r,layout", [
+    (64, 2, [1], [1], 64, "half"),                         # one token in an empty cache
+    (128, 3, [33, 70, 5], [1, 1, 1], 128, "half"),         # one token each, blocks partly full
+    (128, 1, [64, 95, 200], [32, 33, 170], 64, "interleaved"),
+    (256, 2, [77, 32], [77, 32], 256, "half"),             # a prompt from the start
+    (64, 2, [40, 0, 31], [7, 0, 31], 10, "half"),          # a sequence without new tokens, few rotated dims
+    (128, 2, [50, 64], [20, 32], 0, "half"),               # no rotation
+])
+def test_write_parity(D, heads, lens, new, r, layout):
+    import torch
+
+    import masked_token_logits_amd as mtl
+    rng = np.random.default_rng(D + heads + sum(lens))
+    print(f"[case] write D={D} heads={heads} lens={lens} new={new} r={r} {layout}", flush=True)
+    table, pages = tables(rng, lens, extra=1)
+    old = [a - b for a, b in zip(lens, new)]
+    c = cache(rng, pages, heads, D, old, table)
+    cu, T = cu_of(new), sum(new)
+    k, kf = bf16(rng, (T, heads, D), 2.0)
+    v, vf = bf16(rng, (T, heads, D), 0.3)
+    pos = rng.integers(0, 131072, T)
+    bc = on_gpu(c)
+    rot = mtl.Rotary(D, r, layout=layout) if r else None
+    bc.write(_batch(bc, cu, lens, table), dev_bf16(k), dev_bf16(v), dev_i32(old),
+             positions=dev_i32(pos) if r else None, rotary=rot)
+    torch.cuda.synchronize()
+    want, loose = oc.write(c, cu, lens, table, old, kf, vf, pos, oc.rotary_theta(r) if r else None, layout)
+    got = host(bc)
+    np.testing.assert_array_equal(got["k_scale"], want["k_scale"])
+    np.testing.assert_array_equal(got["v_scale"], want["v_scale"])
+    np.testing.assert_array_equal(got["v"], want["v"])
+    off = got["k"] != want["k"]
+    assert not np.any(off & ~loose), np.argwhere(off & ~loose)[:5].tolist()
+    assert off.sum() <= max(2, 1e-3 * off.size)
+
+
+def test_write_overwrites_the_middle_of_a_block():
+    """A decoding block's keys are rewritten at every step: tokens around them
+    stay, requantised only if the scale grows, and writing the same again
+    changes nothing."""
+    import torch
+    rng = np.random.default_rng(20)
+    D, heads, lens, new, start = 64, 2, [90, 61], [32, 5], [40, 3]
+    table, pages = tables(rng, lens)
+    c = cache(rng, pages, heads, D, lens, table)
+    for std in (0.01, 50.0):      # below the old scale, far above it
+        k, kf = bf16(rng, (37, heads, D), std)
+        v, vf = bf16(rng, (37, heads, D), std)
+        bc = on_gpu(c)
+        b = _batch(bc, cu_of(new), lens, table)
+        for _ in range(2):
+            bc.write(b, dev_bf16(k), dev_bf16(v), dev_i32(start))
+            torch.cuda.synchronize()
+            want, _ = oc.write(c, cu_of(new), lens, table, start, kf, vf)
+            got = host(bc)
+            for name in want:
+                np.testing.assert_array_equal(got[name], want[name], err_msg=f"{name} std={std}")
+
+
+def test_write_extremes():
+    """Zeros, the largest and smallest bf16 values, NaN and infinity."""
+    import torch
+    rng = np.random.default_rng(21)
+    D, heads, lens = 64, 1, [32, 32, 32, 32]
+    table, pages = tables(rng, lens)
+    c = cache(rng, pages, heads, D)
+    x, _ = bf16(rng, (128, heads, D))
+    x[:32] = 0
+    x[32:64, :, ::2] = 0x7F7F            # largest
+    x[64:96] = x[64:96] & 0x807F         # subnormals
+    x[96, 0, 0], x[97, 0, 1], x[98, 0, 2] = 0x7FC0, 0x7F80, 0xFF80
+    xf = WL.bf16_to_f32(x).astype(np.float64)
+    bc = on_gpu(c)
+    bc.write(_batch(bc, cu_of(lens), lens, table), dev_bf16(x), dev_bf16(x), dev_i32([0] * 4))
+    torch.cuda.synchronize()
+    want, _ = oc.write(c, cu_of(lens), lens, table, [0] * 4, xf, xf)
+    got = host(bc)
+    for name in ("k_scale", "v_scale"):
+        np.testing.assert_array_equal(got[name], want[name])
+    for name in ("k", "v"):
+        nan_g, nan_w = (got[name] & 0x7F) == 0x7F, (want[name] & 0x7F) == 0x7F
+        np.testing.assert_array_equal(nan_g, nan_w)
+        np.testing.assert_array_equal(got[name][~nan_w], want[name][~nan_w])
+
+
+def test_write_leaves_the_rest_alone():
+    """Bad pages, negative starts, slots behind the table and tokens behind the
+    last sequence write nothing."""
+    import torch
+    rng = np.random.default_rng(22)
+    D, heads, lens, new, start = 64, 2, [40, 64, 60, 10], [40, 40, 8, 6], [0, 40, 60, -1]
+    table = np.array([[3, -1], [5, 999], [0, 1], [2, 4]], np.int32)   # second blocks of 0 and 1 are no pages
+    c = cache(rng, 7, heads, D)
+    T = sum(new) + 5
+    k, kf = bf16(rng, (T, heads, D))
+    v, vf = bf16(rng, (T, heads, D))
+    bc = on_gpu(c)
+    bc.write(_batch(bc, cu_of(new), lens, table), dev_bf16(k), dev_bf16(v), dev_i32(start))
+    torch.cuda.synchronize()
+    want, _ = oc.write(c, cu_of(new), lens, table, start, kf, vf)
+    got = host(bc)
+    for name in want:
+        np.testing.assert_array_equal(got[name], want[name], err_msg=name)
+    assert np.array_equal(got["k"][[2, 4, 6]], c["k"][[2, 4, 6]])
+
+
+def test_write_strided_inputs():
+    import torch
+
+    import masked_token_logits_amd as mtl
+    rng = np.random.default_rng(23)
+    D, heads, lens = 64, 2, [50, 3]
+    table, pages = tables(rng, lens)
+    c = cache(rng, pages, heads, D)
+    T = 53
+    fused, _ = bf16(rng, (T, 3 * heads * D + 1))
+    f = dev_bf16(fused)
+    k = f[:, 1:1 + heads * D].unflatten(1, (heads, D))                  # odd alignment
+    v = f[:, 2 * heads * D:3 * heads * D].unflatten(1, (heads, D)).transpose(0, 1).contiguous().transpose(0, 1)
+    pos = dev_i32(rng.integers(0, 5000, T))
+    rot = mtl.Rotary(D)
+    res = []
+    for kk, vv in ((k, v), (k.contiguous(), v.contiguous())):
+        bc = on_gpu(c)
+        bc.write(_batch(bc, cu_of(lens), lens, table), kk, vv, dev_i32([0, 0]), positions=pos, rotary=rot)
+        torch.cuda.synchronize()
+        res.append(host(bc))
+    for name in res[0]:
+        np.testing.assert_array_equal(res[0][name], res[1][name])
+    one = k[:, :1].expand(T, heads, D)                                  # one head for all
+    bc = on_gpu(c)
+    bc.write(_batch(bc, cu_of(lens), lens, table), one, one, dev_i32([0, 0]))
+    torch.cuda.synchronize()
+    g = host(bc)
+    np.testing.assert_array_equal(g["k"][table[0, :2], 0], g["k"][table[0, :2], 1])
+
+
+# ---- attention ------------------------------------------------------------------------------------------------
+
+def _dS(r, D):
+    return (D + 8) * 2.0 ** -24 * r["A"]
+
+
+def _check_attention(out, lse, r, D, where):
+    out = WL.bf16_to_f32(out.cpu().view(__import__("torch").int16).numpy().view(np.uint16)).astype(np.float64)
+    lse = lse.cpu().numpy().astype(np.float64)
+    real = ~np.isnan(r["lse"])
+    dS = _dS(r, D)
+    tol = 6 * 2.0 ** -11 * r["Q"] + (2 * dS[..., None] + 2.0 ** -20) * r["B"] + 2.0 ** -8 * np.abs(r["out"])
+    err = np.abs(out - r["out"])
+    bad = real[..., None] & ~(err <= tol)
+    assert not bad.any(), f"{where}: out {np.argwhere(bad)[:3].tolist()}, {np.nanmax(np.where(bad, err / tol, 0)):.3g} tolerances"
+    empty = real & np.isneginf(r["lse"])
+    assert np.all(np.isneginf(lse[empty])) and np.all(out[empty] == 0), where
+    seen = real & ~empty
+    err = np.abs(lse[seen] - r["lse"][seen])
+    tol = (dS + 2.0 ** -21 * (np.abs(r["lse"]) + r["A"] + 1))[seen]
+    assert np.all(err <= tol), f"{where}: lse off by {np.max(err / tol):.3g} tolerances"
+
+
+ATTEND = [
+    # D, kv heads, q heads, lens, new, causal
+    (64, 1, 1, [1], [1], 0),                           # one token
+    (128, 2, 2, [31, 32, 33], [1, 1, 1], 0),           # around a block's end
+    (128, 2, 8, [700, 1, 65], [1, 1, 1], 0),           # single tokens, shared heads
+    (128, 1, 7, [200, 64], [32, 32], 0),               # a decoding block, 224 rows
+    (64, 3, 3, [130, 77], [33, 5], 1),                 # causal, more than one tile of rows
+    (256, 2, 4, [97, 40], [20, 40], 1),
+    (256, 1, 1, [300], [3], 0),
+    (128, 1, 4, [100, 0, 50], [3, 4, 0], 0),           # an empty cache, a sequence without queries
+    (64, 1, 2, [5, 40], [9, 70], 1),                   # more queries than tokens: rows that see nothing
+    (128, 1, 28, [96], [40], 1),                       # 1120 rows
+    (64, 2, 2, [4000], [2], 0),                        # long
+]
+
+
+@pytest.mark.parametrize("D,heads,Hq,lens,new,causal", ATTEND)
+def test_attention_parity(D, heads, Hq, lens, new, causal):
+    import torch
+    rng = np.random.default_rng(D + Hq + sum(lens) + sum(new))
+    print(f"[case] attend D={D} heads={heads}/{Hq} lens={lens} new={new} causal={causal}", flush=True)
+    table, pages = tables(rng, lens, extra=1)
+    c = cache(rng, pages, heads, D, lens, table)     # NaN behind every sequence
+    cu, T = cu_of(new), sum(new) + 3                  # three tokens belong to no sequence
+    q, qf = bf16(rng, (T, Hq, D))
+    scale = 1.5 / np.sqrt(D)
+    bc = on_gpu(c)
+    out = torch.full((T, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, Hq), 7.0, device="cuda")
+    o, l = bc.attend(_batch(bc, cu, lens, table), dev_bf16(q), scale=scale, causal=bool(causal), out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert o is out and l is lse
+    assert torch.all(out[-3:] == 7) and torch.all(lse[-3:] == 7)      # left as they were
+    r = oc.attend(c, cu, lens, table, qf, float(np.float32(scale)), bool(causal))
+    _check_attention(out, lse, r, D, "attention")
+    # the tight bounds on the host's maxima change nothing
+    o2, l2 = bc.attend(_batch(bc, cu, lens, table, max_new=max(max(new), 1), max_len=max(max(lens), 1)), dev_bf16(q),
+                       scale=scale, causal=bool(causal), lse=True)
+    n = sum(new)
+    r2 = {k: v[:n] for k, v in r.items()}
+    _check_attention(o2[:n], l2[:n], r2, D, "tight bounds")
+
+
+@pytest.mark.parametrize("case", ["sharp", "equal", "outlier", "growing"])
+def test_attention_score_shapes(case):
+    """Scores of one winner, all alike, one far larger, and ever larger along
+    the cache (the running maximum is replaced again and again)."""
+    import torch
+    rng = np.random.default_rng(30)
+    D, heads, Hq, lens, new = 128, 1, 4, [515], [9]
+    table, pages = tables(rng, lens)
+    c = cache(rng, pages, heads, D, lens, table)
+    q, qf = bf16(rng, (9, Hq, D), {"sharp": 12.0, "equal": 0.0, "outlier": 1.0, "growing": 1.0}[case])
+    if case == "outlier":
+        q[..., 5], qf[..., 5] = 0x4500, 2048.0
+    if case == "growing":
+        q[:], qf[:] = 0x3F80, 1.0
+        for j in range(table.shape[1]):
+            c["k"][table[0, j], 0] = oc.e4m3_bytes(np.array([1.0 + j]))[0]
+            c["k"][table[0, j], 0, ::5] = oc.e4m3_bytes(np.array([2.0]))[0]
+            c["k_scale"][table[0, j], 0] = 124
+        for p in range(pages):
+            c["v"][p, 0][(c["v"][p, 0] & 0x7F) == 0x7F] = 0x7F
+    bc = on_gpu(c)
+    o, l = bc.attend(_batch(bc, cu_of(new), lens, table), dev_bf16(q), lse=True)
+    torch.cuda.synchronize()
+    r = oc.attend(c, cu_of(new), lens, table, qf, float(np.float32(D ** -0.5)), False)
+    _check_attention(o, l, r, D, case)
+
+
+def test_attention_value_scales_far_apart():
+    """Blocks whose values' scales differ by up to 2^20, ever larger and then
+    ever smaller along the cache: every block counts for what it is."""
+    import torch
+    rng = np.random.default_rng(33)
+    D, heads, Hq, lens, new = 64, 1, 2, [330, 330], [3, 3]
+    table, pages = tables(rng, lens)
+    c = cache(rng, pages, heads, D, lens, table)
+    c["v_scale"][table[0, :11], 0] = 110 + 2 * np.arange(11)
+    c["v_scale"][table[1, :11], 0] = 130 - 2 * np.arange(11)
+    q, qf = bf16(rng, (6, Hq, D))
+    bc = on_gpu(c)
+    o, l = bc.attend(_batch(bc, cu_of(new), lens, table), dev_bf16(q), lse=True)
+    torch.cuda.synchronize()
+    r = oc.attend(c, cu_of(new), lens, table, qf, float(np.float32(D ** -0.5)), False)
+    _check_attention(o, l, r, D, "scales")
+
+
+def test_attention_strides_bad_pages_and_bounds():
+    """q out of a fused projection; a table whose entries are partly no pages
+    (their tokens are absent); lengths beyond the bound are cut."""
+    import torch
+    rng = np.random.default_rng(31)
+    D, heads, Hq, lens, new = 64, 2, 4, [100, 64, 40], [5, 3, 2]
+    table, pages = tables(rng, lens)
+    table[0, 1], table[2, :] = -7, pages
+    c = cache(rng, pages, heads, D, lens, table)
+    x, xf = bf16(rng, (10, 3 * Hq, D))
+    q = dev_bf16(x)[:, Hq:2 * Hq]
+    bc = on_gpu(c)
+    b = _batch(bc, cu_of(new), lens, table)
+    o, l = bc.attend(b, q, lse=True)
+    torch.cuda.synchronize()
+    r = oc.attend(c, cu_of(new), lens, table, xf[:, Hq:2 * Hq], float(np.float32(D ** -0.5)), False)
+    _check_attention(o, l, r, D, "bad pages")
+    turned = q.transpose(0, 1).contiguous().transpose(0, 1)            # [H, T, D] in memory
+    assert torch.equal(bc.attend(b, turned), o)
+    wild = _batch(bc, cu_of(new), [2 ** 31 - 1, 64, -5], table, max_len=96)
+    o2, l2 = bc.attend(wild, q, lse=True)
+    torch.cuda.synchronize()
+    r = oc.attend(c, cu_of(new), [96, 64, 0], table, xf[:, Hq:2 * Hq], float(np.float32(D ** -0.5)), False)
+    _check_attention(o2, l2, r, D, "cut")
+
+
+def test_attention_nan_stays_where_it_is_seen():
+    """A NaN key or value token reaches the queries that see it and no other;
+    a NaN query only its own row."""
+    import torch
+    rng = np.random.default_rng(32)
+    D, heads, lens, new = 64, 1, [70], [40]
+    table, pages = tables(rng, lens)
+    q, _ = bf16(rng, (40, 1, D))
+    for name, token, causal in (("k", 69, True), ("v", 69, True), ("v", 45, True), ("k", 50, True), ("v", 3, False)):
+        c = cache(rng, pages, heads, D, lens, table)
+        c[name][table[0, token // 32], 0, oc.places(D, name == "k")[token % 32]] = 0x7F
+        bc = on_gpu(c)
+        o = bc.attend(_batch(bc, cu_of(new), lens, table), dev_bf16(q), causal=causal).float().cpu().numpy()
+        sees = np.arange(40) + 30 >= token if causal else np.ones(40, bool)
+        np.testing.assert_array_equal(np.isnan(o[:, 0]).all(1), sees, err_msg=f"{name} {token}")
+        np.testing.assert_array_equal(np.isnan(o[:, 0]).any(1), sees, err_msg=f"{name} {token}")
+    c = cache(rng, pages, heads, D, lens, table)
+    q[7, 0, 11] = 0x7FC0
+    bc = on_gpu(c)
+    o, l = bc.attend(_batch(bc, cu_of(new), lens, table), dev_bf16(q), lse=True)
+    bad = np.isnan(o.float().cpu().numpy()[:, 0]).all(1)
+    assert bad.sum() == 1 and bad[7] and np.array_equal(np.isnan(l.cpu().numpy()[:, 0]), bad)
+
+
+# ---- accumulated weights --------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("decay", [1.0, 0.5, 0.0])
+@pytest.mark.parametrize("D,heads,Hq,lens,new,causal", [
+    (128, 2, 8, [700, 1, 65], [1, 1, 1], 0),
+    (128, 1, 7, [200, 64], [32, 32], 0),
+    (64, 3, 3, [130, 77], [33, 5], 1),
+    (256, 2, 4, [97, 40], [20, 40], 1),
+    (64, 1, 2, [5, 40, 0, 9], [9, 70, 2, 0], 1),       # rows that see nothing, an empty cache, no queries
+])
+def test_weigh_parity(D, heads, Hq, lens, new, causal, decay):
+    import torch
+    rng = np.random.default_rng(D + Hq + sum(lens))
+    print(f"[case] weigh D={D} heads={heads}/{Hq} lens={lens} new={new} causal={causal} decay={decay}", flush=True)
+    table, pages = tables(rng, lens, extra=1)
+    if lens[0] == 700:
+        table[0, 3] = -1                               # a hole: its weights stay
+    c = cache(rng, pages, heads, D, lens, table)
+    cu, T = cu_of(new), sum(new) + 2
+    q, qf = bf16(rng, (T, Hq, D))
+    w0 = rng.random((len(lens), heads, table.shape[1] * 32)).astype(np.float32)
+    if decay == 0.0:
+        w0[:, :, ::3] = np.nan                         # not read
+    bc = on_gpu(c)
+    b = _batch(bc, cu, lens, table)
+    lse = torch.full((T, Hq), float("nan"), device="cuda")
+    bc.attend(b, dev_bf16(q), causal=bool(causal), lse=lse)
+    w = torch.from_numpy(w0.copy()).cuda()
+    bc.weigh(b, dev_bf16(q), lse, w, causal=bool(causal), decay=decay)
+    torch.cuda.synchronize()
+    lh = lse.cpu().numpy()
+    scale = float(np.float32(D ** -0.5))
+    want = oc.weigh(c, cu, lens, table, qf, lh, scale, bool(causal), w0, decay)
+    r = oc.attend(c, cu, lens, table, qf, scale, bool(causal))
+    rel = np.nanmax(np.where(np.isfinite(r["lse"]), _dS(r, D) + 2.0 ** -21 * (np.abs(r["lse"]) + r["A"] + 1), 0))
+    got = w.cpu().numpy().astype(np.float64)
+    for s, n in enumerate(lens):
+        np.testing.assert_array_equal(got[s, :, n:], w0[s, :, n:].astype(np.float64))
+        x, y = got[s, :, :n], want[s, :, :n]
+        add = y - (decay * w0[s, :, :n] if decay else 0)
+        tol = (rel + T * Hq * 2.0 ** -24) * np.abs(add) + 2.0 ** -22 * np.abs(y)
+        same = np.isnan(x) & np.isnan(y)                # the hole, where decay is 0
+        assert np.all(same | (np.abs(x - y) <= tol)), f"sequence {s}"
+
+
+# ---- eviction -------------------------------------------------------------------------------------------------
+
+def _evict(rng, lens, keep, sink, recent, pool, heads=2, D=64, w=None, max_keep=None, bad=False):
+    import torch
+    table, pages0 = tables(rng, lens, extra=1)
+    out_blocks = (max(max(keep), 1) + 31) // 32
+    pages = pages0 + len(lens) * out_blocks
+    table = np.where(table == pages0, -1, table)
+    table_out = (pages0 + rng.permutation(len(lens) * out_blocks).reshape(len(lens), out_blocks)).astype(np.int32)
+    if bad:
+        table[0, 0], table_out[-1, 0] = pages, -3
+    c = cache(rng, pages, heads, D, lens, table)
+    if w is None:
+        w = rng.random((len(lens), heads, table.shape[1] * 32)).astype(np.float32)
+        w[rng.random(w.shape) < 0.3] = 0
+    bc = on_gpu(c)
+    most = max_keep or out_blocks * 32
+    kept = torch.full((len(lens), heads, most), -5, dtype=torch.int32, device="cuda")
+    wout = torch.full((len(lens), heads, out_blocks * 32), -5.0, device="cuda")
+    lens_out = torch.full((len(lens),), -5, dtype=torch.int32, device="cuda")
+    bc.evict(_batch(bc, [0] * (len(lens) + 1), lens, table), torch.from_numpy(w).cuda(), dev_i32(keep),
+             dev_i32(table_out), sink=sink, recent=recent, pool=pool, lens_out=lens_out, kept=kept, weights_out=wout)
+    torch.cuda.synchronize()
+    cut = [min(k, most) for k in keep]
+    want, n, kk, ww = oc.evict(c, lens, table, w, cut, sink, recent, pool, table_out)
+    np.testing.assert_array_equal(lens_out.cpu().numpy(), n)
+    for s in range(len(lens)):
+        for h in range(heads):
+            got = kept[s, h].cpu().numpy()
+            np.testing.assert_array_equal(got[:n[s]], kk[s][h], err_msg=f"kept {s} {h}")
+            assert np.all(got[n[s]:] == -5)
+            gw = wout[s, h].cpu().numpy()
+            np.testing.assert_array_equal(gw[:n[s]], ww[s][h])
+            assert np.all(gw[n[s]:] == -5)
+    got = host(bc)
+    for name in want:
+        np.testing.assert_array_equal(got[name], want[name], err_msg=name)
+
+
+@pytest.mark.parametrize("lens,keep,sink,recent,pool", [
+    ([1], [1], 0, 0, 1),
+    ([100, 31, 64], [50, 31, 33], 0, 0, 1),
+    ([100, 31, 64], [50, 40, 0], 4, 8, 3),             # more than there are; none
+    ([300, 0, 33], [65, 5, 32], 2, 40, 7),             # an empty cache
+    ([200], [10], 20, 20, 3),                          # sink alone fills it
+    ([200], [30], 20, 20, 63),                         # sink and a part of recent
+    ([2000], [999], 4, 64, 5),
+])
+def test_evict_parity(lens, keep, sink, recent, pool):
+    print(f"[case] evict lens={lens} keep={keep} sink={sink} recent={recent} pool={pool}", flush=True)
+    _evict(np.random.default_rng(sum(lens) + sum(keep)), lens, keep, sink, recent, pool)
+
+
+@pytest.mark.parametrize("D,heads", [(128, 3), (256, 1)])
+def test_evict_head_sizes(D, heads):
+    _evict(np.random.default_rng(40), [130, 95], [70, 33], 1, 4, 3, heads=heads, D=D)
+
+
+@pytest.mark.parametrize("kind", ["equal", "zeros", "specials", "few values"])
+def test_evict_ties_and_special_weights(kind):
+    rng = np.random.default_rng(41)
+    w = np.zeros((2, 2, 160), np.float32)
+    if kind == "equal":
+        w[:] = 0.25
+    if kind == "zeros":
+        w[:, :, ::2] = -0.0
+    if kind == "specials":
+        w = rng.standard_normal(w.shape).astype(np.float32)
+        w[:, :, 3::11], w[:, :, 4::13], w[:, :, 5::17] = np.nan, np.inf, -np.inf
+    if kind == "few values":
+        w = rng.integers(0, 3, w.shape).astype(np.float32)
+    _evict(rng, [128, 77], [51, 40], 0, 0, 1, w=w)
+    _evict(rng, [128, 77], [51, 40], 3, 5, 3, w=w)
+
+
+def test_evict_bad_pages_and_cut_keep():
+    _evict(np.random.default_rng(42), [100, 90], [64, 60], 4, 0, 1, bad=True)
+    _evict(np.random.default_rng(43), [100, 90], [64, 60], 4, 0, 1, max_keep=37)
