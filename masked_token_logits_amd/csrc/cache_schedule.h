@@ -1,0 +1,176 @@
+// How attention over the cache is dealt out to workgroups.
+//
+// The work is a line of steps: sequences in order, in each its key/value
+// heads, in each its tiles of query rows, in each the steps along the cache
+// that the tile's rows can see.  A fixed number of workgroups takes equal
+// stretches of that line, so one long sequence among short ones, few rows
+// with a long cache, and many rows with a short one all fill the chip, and
+// the split follows the lengths on the device without the host knowing them.
+// A tile that a stretch's end cuts is written in parts, which a second kernel
+// joins in order: results do not depend on which workgroup ends first.
+#pragma once
+
+#include "cache_common.h"
+
+namespace dllm {
+
+struct AttendArgs {
+  dllm_cache c;
+  dllm_cache_batch b;
+  int64_t T;
+  const uint16_t* q;
+  int64_t q_token, q_head;
+  int q_heads, group;
+  float scale2;  // scale * log2 e
+  int causal;
+  uint16_t* out;
+  float* lse;
+  char* ws;
+  int parts;      // workgroups, a multiple of 8
+  int min_steps;  // the shortest stretch worth a workgroup
+};
+
+// Where a workgroup's stretch begins: tile rt of head h of sequence s, whose
+// first step is number `tile` on the line, at its step `begin`.  tile < 0: no
+// work.
+struct Stretch {
+  int64_t tile;
+  int s, h, rt, begin;
+};
+
+constexpr int kScheduleThreads = 256;
+
+// floor(x / y) for 0 <= x < 2^53, y > 0: a quotient that is not whole is further
+// below the next integer than fp64 rounds, and the division is a dozen
+// instructions where the 64-bit integer one is a hundred.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) { return (int64_t)((double)x / (double)y); }
+
+// Steps of KEYS tokens that row tile rt of BM rows (token * group + head of
+// the group) needs; at least one, which writes what rows without a visible
+// token get.
+template <int BM, int KEYS>
+__device__ __forceinline__ int tile_steps(const AttendArgs& a, const SeqView& q, int rt) {
+  int seen = q.len;
+  if (a.causal) {
+    const uint32_t last = (uint32_t)(min((rt + 1) * BM, q.rows * a.group) - 1) / (uint32_t)a.group;
+    seen = min(max(q.len - q.n + (int)last + 1, 0), q.len);
+  }
+  return max((seen + KEYS - 1) / KEYS, 1);
+}
+
+template <int BM>
+__device__ __forceinline__ int row_tiles(const AttendArgs& a, const SeqView& q) {
+  return (q.rows * a.group + BM - 1) / BM;
+}
+
+// Steps of one head of a sequence.
+template <int BM, int KEYS>
+__device__ __forceinline__ int64_t head_steps(const AttendArgs& a, const SeqView& q) {
+  const int tiles = row_tiles<BM>(a, q);
+  if (tiles == 0) return 0;
+  if (!a.causal) return (int64_t)tiles * tile_steps<BM, KEYS>(a, q, 0);
+  int64_t n = 0;
+  for (int i = 0; i < tiles; ++i) n += tile_steps<BM, KEYS>(a, q, i);
+  return n;
+}
+
+// Inclusive sum over the workgroup's 256 threads.
+__device__ __forceinline__ int64_t scan(int64_t x, int64_t* lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t y = __shfl_up(x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 63) lds[wave] = x;
+  __syncthreads();
+  for (int i = 0; i < wave; ++i) x += lds[i];
+  return x;
+}
+
+// This workgroup's number w on the line, its stretch and the number of its
+// steps, the same in every thread.  All 256 threads call it.  Workgroups go
+// to the chip's 8 XCDs in turn, and neighbours on the line, which read the
+// same keys, belong on one XCD's L2; where the line is too short for every
+// workgroup they stay in turn, for else the first XCD would get it all.
+template <int BM, int KEYS>
+__device__ Stretch find_stretch(const AttendArgs& a, int* number, int64_t* steps) {
+  __shared__ int64_t lds[kScheduleThreads / 64];
+  __shared__ int64_t found_at;
+  __shared__ int found_s;
+  const int tid = threadIdx.x;
+  int64_t total = 0, mine = 0, upto = 0;
+  if (a.b.S == 1) {
+    total = head_steps<BM, KEYS>(a, seq_view(a.b, a.T, 0)) * a.c.kv_heads;
+  } else {
+    for (int s0 = 0; s0 < a.b.S; s0 += kScheduleThreads) {
+      mine = s0 + tid < a.b.S ? head_steps<BM, KEYS>(a, seq_view(a.b, a.T, s0 + tid)) * a.c.kv_heads : 0;
+      upto = scan(mine, lds);
+      __syncthreads();
+      if (tid == kScheduleThreads - 1) lds[0] = upto;
+      __syncthreads();
+      total += lds[0];
+      __syncthreads();
+    }
+  }
+  const int64_t parts = min((int64_t)a.parts, max(quotient(total + a.min_steps - 1, a.min_steps), (int64_t)1));
+  const int w = parts == a.parts ? (int)(blockIdx.x % 8) * (a.parts / 8) + (int)blockIdx.x / 8 : (int)blockIdx.x;
+  *number = w;
+  Stretch r = {-1, 0, 0, 0, 0};
+  *steps = 0;
+  if (w >= parts || total == 0) return r;
+  const int64_t lo = quotient(total * w, parts), hi = quotient(total * (w + 1), parts);
+  *steps = hi - lo;
+  int64_t at = 0;  // the line up to sequence r.s
+  if (a.b.S > 1) {
+    for (int s0 = 0; s0 < a.b.S; s0 += kScheduleThreads) {
+      if (a.b.S > kScheduleThreads) {
+        mine = s0 + tid < a.b.S ? head_steps<BM, KEYS>(a, seq_view(a.b, a.T, s0 + tid)) * a.c.kv_heads : 0;
+        upto = scan(mine, lds);
+      }
+      __syncthreads();
+      if (tid == 0) found_s = -1;
+      if (tid == kScheduleThreads - 1) lds[0] = upto;
+      __syncthreads();
+      if (at + upto - mine <= lo && lo < at + upto) found_s = s0 + tid, found_at = at + upto - mine;
+      __syncthreads();
+      if (found_s >= 0) break;
+      at += lds[0];
+    }
+    r.s = found_s;
+    at = found_at;
+  }
+  const SeqView q = seq_view(a.b, a.T, r.s);
+  const int64_t per_head = head_steps<BM, KEYS>(a, q);
+  r.h = (int)quotient(lo - at, per_head);
+  at += r.h * per_head;
+  if (!a.causal) {
+    const int n = tile_steps<BM, KEYS>(a, q, 0);
+    r.rt = (int)quotient(lo - at, n);
+    at += (int64_t)r.rt * n;
+  } else {
+    for (;; ++r.rt) {
+      const int n = tile_steps<BM, KEYS>(a, q, r.rt);
+      if (lo < at + n) break;
+      at += n;
+    }
+  }
+  r.tile = at;
+  r.begin = (int)(lo - at);
+  return r;
+}
+
+// The next tile on the line (whose last one ended before the work did).
+template <int BM>
+__device__ __forceinline__ void next_tile(const AttendArgs& a, Stretch& r, int steps_of_this) {
+  r.tile += steps_of_this;
+  r.begin = 0;
+  if (++r.rt < row_tiles<BM>(a, seq_view(a.b, a.T, r.s))) return;
+  r.rt = 0;
+  if (++r.h < a.c.kv_heads) return;
+  r.h = 0;
+  do ++r.s;
+  while (r.s < a.b.S - 1 && seq_view(a.b, a.T, r.s).rows == 0);
+}
+
+}  // namespace dllm

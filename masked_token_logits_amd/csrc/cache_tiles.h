@@ -211,35 +211,33 @@ __device__ __forceinline__ void add_values(Accumulator<D>& a, const Frag* p, con
 // column's visible tokens of the block) the result is made NaN.  Rare, so the
 // product that finds those places is made only if there is such a byte.
 template <int D>
-__device__ __forceinline__ void add_values_masked(Accumulator<D>& a, const Frag* p, i32x4* raw, float v_scale,
+__device__ __forceinline__ void add_values_masked(Accumulator<D>& a, const Frag* p, const i32x4* raw, float v_scale,
                                                   int limit, int half) {
-  i32x4 nan[D / 32];
-  int some = 0;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = (((raw[i][j] & 0x7f7f7f7f) + 0x01010101) >> 7) & 0x01010101;  // 1 in each byte that is NaN
-      nan[i][j] = m * 0x38;                                                       // 1.0
-      raw[i][j] &= ~(m * 0xff);
-      some |= m;
-    }
-  add_values<D>(a, p, raw, v_scale);
-  if (!__any(some)) return;
-  Frag see[2];
-#pragma unroll
-  for (int i = 0; i < 16; i += 2)
-    see[i / 8].h2[(i % 8) / 2] = f16x2{(_Float16)(token_of(i, half) < limit ? 1.0f : 0.0f),
-                                       (_Float16)(token_of(i + 1, half) < limit ? 1.0f : 0.0f)};
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     Frag lo, hi;
-    widen_values(nan[i], 1.0f, lo, hi);
-    f32x16 hit = {};
-    hit = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo.h, see[0].h, hit, 0, 0, 0);
-    hit = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi.h, see[1].h, hit, 0, 0, 0);
+    i32x4 x = raw[i], nan;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) a.o[i][j] = hit[j] > 0.0f ? NAN : a.o[i][j];
+    for (int j = 0; j < 4; ++j) {
+      nan[j] = (((x[j] & 0x7f7f7f7f) + 0x01010101) >> 7) & 0x01010101;  // 1 in each byte that is NaN
+      x[j] &= ~(nan[j] * 0xff);
+    }
+    widen_values(x, v_scale, lo, hi);
+    a.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo.h, p[0].h, a.o[i], 0, 0, 0);
+    a.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi.h, p[1].h, a.o[i], 0, 0, 0);
+    if (__any(nan[0] | nan[1] | nan[2] | nan[3])) {
+      Frag see[2];
+#pragma unroll
+      for (int j = 0; j < 16; j += 2)
+        see[j / 8].h2[(j % 8) / 2] = f16x2{(_Float16)(token_of(j, half) < limit ? 1.0f : 0.0f),
+                                           (_Float16)(token_of(j + 1, half) < limit ? 1.0f : 0.0f)};
+      widen_values(nan * 0x38, 1.0f, lo, hi);  // 1.0
+      f32x16 hit = {};
+      hit = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo.h, see[0].h, hit, 0, 0, 0);
+      hit = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi.h, see[1].h, hit, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) a.o[i][j] = hit[j] > 0.0f ? NAN : a.o[i][j];
+    }
   }
 }
 
