@@ -2,6 +2,7 @@
 #include "cache_common.h"
 #include "cache_schedule.h"
 #include "cache_tiles.h"
+#include "persistent_sched.h"
 #include "rotary_angle.h"
 
 namespace dllm {
@@ -71,12 +72,6 @@ __device__ __forceinline__ void write_rows(const AttendArgs& a, const Row& r, in
     *reinterpret_cast<uint2*>(a.out + r.out * D + 32 * chunk + 8 * i + 4 * half) = make_uint2(lo, hi);
   }
   if (a.lse && chunk == 0 && half == 0) a.lse[r.out] = sum == 0.0f ? -INFINITY : (ref + __log2f(sum)) * kLn2;
-}
-
-// What a state counts for when it is joined to others with reference `ref`
-// and value scale `v_ref`.
-__device__ __forceinline__ float share_of(float own_ref, float ref) {
-  return own_ref == INFINITY ? 0.0f : __builtin_amdgcn_exp2f(own_ref - ref);
 }
 
 // ---- few rows: the waves of a workgroup share the keys ----------------------------------------------------------
@@ -187,7 +182,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void k_attend_few(Atten
         add_values<D>(acc, p, v, vs);
     }
     // join the waves: each takes some of the 32-dim chunks of all of them
-    const float sum = acc.sum + other_half(acc.sum);
+    const float sum = column_sum(acc.sum);
     if (half == 0) ref_lds[wave][col] = acc.ref, sum_lds[wave][col] = sum;
     if (lane == 0) v_lds[wave] = acc.v_ref;
 #pragma unroll
@@ -197,17 +192,16 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void k_attend_few(Atten
         *reinterpret_cast<float4*>(o_lds[wave][c][i][lane]) =
             make_float4(acc.o[c][4 * i], acc.o[c][4 * i + 1], acc.o[c][4 * i + 2], acc.o[c][4 * i + 3]);
     __syncthreads();
-    float ref = INFINITY, total = 0.0f, part[kWaves];
+    float ref = -INFINITY, total = 0.0f, part[kWaves];
     int v_ref = 0;
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) {
-      const float x = ref_lds[i][col];
-      ref = ref == INFINITY ? x : x == INFINITY ? ref : fmaxf(ref, x);
+      ref = fmaxf(ref, ref_lds[i][col]);
       v_ref = max(v_ref, v_lds[i]);
     }
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) {
-      const float x = share_of(ref_lds[i][col], ref);
+      const float x = part_of_ref(ref_lds[i][col], ref);
       total += x * sum_lds[i][col];
       part[i] = x * exact_power(v_lds[i] - v_ref);
     }
@@ -246,6 +240,416 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void k_attend_few(Atten
   }
 }
 
+// ---- many rows: the keys pass through LDS -----------------------------------------------------------------------
+
+#define LDS_AS __attribute__((address_space(3)))
+
+// What a block without a page reads: its scores are finite and then left out.
+__device__ __attribute__((aligned(16))) uint8_t no_page[kBlock * 256];
+
+constexpr int kManyParts = 256;  // one workgroup to a compute unit
+constexpr int kManyBlocks = 2;   // blocks of a step
+
+// Pages and scales of a run of blocks, 64 at a time, one to a lane, so that
+// in the loop they are a lane read instead of loads from two tables.
+struct Lookup {
+  int base;
+  int64_t at;  // byte offset of the block's keys, and of its values
+  int info;    // k byte | v byte << 8 | has a page << 16
+
+  // Makes block j's (and 63 more) known.
+  template <int D>
+  __device__ __forceinline__ void cover(const AttendArgs& a, int s, int h, int j, int last) {
+    if (__builtin_expect(j >= base && j < base + 64, 1)) return;
+    base = j;
+    const int b = j + (threadIdx.x & 63);
+    const int page = b < last ? page_of(a.b.table, a.b.table_blocks, a.c.pages, s, b) : -1;
+    const int64_t x = block_of(a.c, max(page, 0), h);
+    at = page < 0 ? -1 : x * (kBlock * D);
+    info = page < 0 ? 127 | 1 << 8 : a.c.k_scale[x] | a.c.v_scale[x] << 8 | 1 << 16;  // no page: moves no scale
+  }
+  __device__ __forceinline__ int info_of(int j) const { return __builtin_amdgcn_readlane(info, j - base); }
+  __device__ __forceinline__ int64_t at_of(int j) const {
+    const uint32_t lo = __builtin_amdgcn_readlane((int)at, j - base), hi = __builtin_amdgcn_readlane((int)(at >> 32), j - base);
+    return (int64_t)((uint64_t)hi << 32 | lo);
+  }
+};
+__device__ __forceinline__ int k_byte(int info) { return info & 0xff; }
+__device__ __forceinline__ int v_byte(int info) { return info >> 8 & 0xff; }
+__device__ __forceinline__ bool has_page(int info) { return info >> 16 != 0; }
+
+// One workgroup: its stretch of the line, BM = 128 RG rows at a time, 32 RG
+// to each of the 4 waves, one wave to a SIMD.  Blocks go from memory into a
+// ring in LDS as stored, kAhead steps ahead, once for all rows; each wave
+// widens them as it reads, once for its RG groups of 32 rows.  In the body of
+// the loop the products of three blocks are in flight, independent of each other:
+// the scores of block b + 1, the probabilities of block b and the output of
+// block b - 1, so that the matrix pipe and the VALU work at the same time.
+template <int D, int RG>
+__global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
+  constexpr int BM = kWaves * 32 * RG, KEYS = kBlock * kManyBlocks;
+  constexpr int CH = D / 32;              // 1 KiB chunks of a block's keys or values
+  constexpr int kStep = kManyBlocks * 2 * CH * 1024;  // bytes of a step: for each block its keys, then its values
+  constexpr int kRing = D == 256 ? 4 : 5;             // steps in LDS
+  constexpr int kAhead = kRing - 2;                   // steps that loads run ahead
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[kRing * kStep];
+  const int lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int w;
+  int64_t left;
+  Stretch at = find_stretch<BM, KEYS>(a, &w, &left);
+  if (threadIdx.x == 0) reinterpret_cast<Stretch*>(a.ws)[w] = at;
+  while (left > 0) {
+    const SeqView q = seq_view(a.b, a.T, at.s);
+    const int steps = tile_steps<BM, KEYS>(a, q, at.rt);
+    const int n = (int)min((int64_t)(steps - at.begin), left);
+    const int row0 = at.rt * BM + wave * 32 * RG;
+    Row r[RG];
+    int end[RG];
+    Frag qf[RG][D / 16];
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+      r[g] = row_of(a, q, at.h, row0 + g * 32 + col);
+      load_query<D>(qf[g], a.q + (q.q0 + r[g].tok) * a.q_token + (int64_t)r[g].head * a.q_head, half);
+      end[g] = a.causal ? min(max(q.len - q.n + r[g].tok + 1, 0), q.len) : q.len;
+      // queries are only ever matrix operands: in the accumulation registers
+      // they leave the others to the scores
+      each<0, D / 16>([&](auto i) {
+        i32x4 x = qf[g][decltype(i)::value].w;
+        asm volatile("" : "+a"(x));
+        qf[g][decltype(i)::value].w = x;
+      });
+    }
+    // blocks below `whole` are seen whole by every row of the workgroup's tile
+    const int least = a.causal ? min(max(q.len - q.n + (int)((uint32_t)(at.rt * BM) / (uint32_t)a.group) + 1, 0), q.len) : q.len;
+    const int first = at.begin * kManyBlocks;
+    const int last = min(first + n * kManyBlocks, (q.len + kBlock - 1) / kBlock);
+    const int clean = max(min(last, least / kBlock), first);
+
+    f32x16 o[RG][CH];
+    float ref[RG], sum[RG];
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+      ref[g] = -INFINITY, sum[g] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[g][c][i] = 0.0f;
+    }
+    int v_ref = 0;
+
+    Lookup ahead, here;
+    ahead.base = here.base = -1000;
+    // The wave's share of step t's loads: the keys or the values of one of its
+    // blocks, CH loads, for every step alike (behind the last block they read
+    // nothing of use), so that waits can count them.
+    int put = 0;  // where in the ring the next step goes
+    auto load_step = [&](int t) {
+      const int j0 = first + t * kManyBlocks;
+      ahead.cover<D>(a, at.s, at.h, j0, last);
+      const int64_t from = ahead.at_of(j0 + (wave >> 1));
+      const uint8_t* src = from < 0 ? no_page : (wave & 1 ? a.c.v : a.c.k) + from;
+      uint8_t* dst = ring + put + wave * CH * 1024;
+      each<0, CH>([&](auto c) {
+        constexpr int x = decltype(c)::value * 1024;  // the instruction's offset counts on both sides
+        __builtin_amdgcn_global_load_lds((const void*)(src + lane * 16 + (x & ~4095)), (LDS_AS void*)(dst + (x & ~4095)), 16,
+                                         x & 4095, 0);
+      });
+      put = put + kStep == kRing * kStep ? 0 : put + kStep;
+    };
+    constexpr int kSlot = 2 * CH * 1024;  // a block's keys and values
+    auto chunk_at = [&](int slot, int side, int c) {  // the lane's 16 bytes
+      return *reinterpret_cast<const i32x4*>(ring + slot + (side * CH + c) * 1024);
+    };
+    auto chunk = [&](int j, int side, int c) {
+      return chunk_at((j - first) % (kRing * kManyBlocks) * kSlot + lane * 16, side, c);
+    };
+    auto qk = [&](int j, int k_byte, f32x16* s) {
+      const float ks = scale_value(k_byte);
+#pragma unroll
+      for (int g = 0; g < RG; ++g) s[g] = f32x16{};
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        Frag lo, hi;
+        widen_keys(chunk(j, 0, c), ks, lo, hi);
+#pragma unroll
+        for (int g = 0; g < RG; ++g) s[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo.b, qf[g][2 * c].b, s[g], 0, 0, 0);
+#pragma unroll
+        for (int g = 0; g < RG; ++g) s[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi.b, qf[g][2 * c + 1].b, s[g], 0, 0, 0);
+      }
+    };
+    auto pv = [&](int j, float vs, const Frag (*p)[2]) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        Frag lo, hi;
+        widen_values(chunk(j, 1, c), vs, lo, hi);
+#pragma unroll
+        for (int g = 0; g < RG; ++g) o[g][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo.h, p[g][0].h, o[g][c], 0, 0, 0);
+#pragma unroll
+        for (int g = 0; g < RG; ++g) o[g][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi.h, p[g][1].h, o[g][c], 0, 0, 0);
+      }
+    };
+    // The same where rows see the block in part: values at or behind the length
+    // are cleared, and a NaN value reaches only the rows that see its token
+    // (add_values_masked in cache_tiles.h says how).
+    auto pv_masked = [&](int j, float vs, const Frag (*p)[2]) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        Frag lo, hi;
+        i32x4 x = clip_values(chunk(j, 1, c), half, q.len - j * kBlock), nan;
+        take_nan(x, nan);
+        widen_values(x, vs, lo, hi);
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+          o[g][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo.h, p[g][0].h, o[g][c], 0, 0, 0);
+          o[g][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi.h, p[g][1].h, o[g][c], 0, 0, 0);
+        }
+        if (__any(nan[0] | nan[1] | nan[2] | nan[3])) {
+#pragma unroll
+          for (int g = 0; g < RG; ++g) spread_nan(o[g][c], nan, end[g] - j * kBlock, half);
+        }
+      }
+    };
+    // (Constants and `each` here because loops in code marked as rare are not
+    // unrolled, and what they index would live in memory.)
+    auto rescale_all = [&](auto g, float alpha) {
+      each<0, CH>([&](auto c) { o[decltype(g)::value][decltype(c)::value] *= alpha; });
+    };
+    auto value_scale = [&](int vb) {
+      if (v_ref == 0) v_ref = vb;
+      if (__builtin_expect(vb > v_ref + kValueSlack, 0)) {
+        each<0, RG>([&](auto g) { rescale_all(g, exact_power(v_ref - vb)); });
+        v_ref = vb;
+      }
+      return __uint_as_float((uint32_t)max(vb - v_ref + 127, 1) << 23);
+    };
+
+    f32x16 s[RG];   // scores
+    Frag p[RG][2];  // probabilities
+    float top[RG];
+#pragma unroll
+    for (int g = 0; g < RG; ++g) p[g][0].w = p[g][1].w = i32x4{0, 0, 0, 0};
+    // Moves the references to cover s; O and the probabilities still to be used
+    // follow (those are rounded to fp16 once more by that, in the few blocks where it
+    // happens).
+    float neg[RG];  // -ref, or -inf where no token has been seen
+#pragma unroll
+    for (int g = 0; g < RG; ++g) neg[g] = -INFINITY;
+    auto cover_all = [&]() {
+      bool grow = false;
+#pragma unroll
+      for (int g = 0; g < RG; ++g) grow |= __builtin_fmaf(top[g], a.scale2, -kOffset) > ref[g] + kSlack;
+      if (__builtin_expect(__any(grow), 0)) {
+        each<0, RG>([&](auto G) {
+          constexpr int g = decltype(G)::value;
+          const float to = fmaxf(ref[g], __builtin_fmaf(column_max(top[g]), a.scale2, -kOffset));
+          const float alpha = part_of_ref(ref[g], to);
+          ref[g] = to;
+          neg[g] = negative(to);
+          sum[g] *= alpha;
+          rescale_all(G, alpha);
+          const _Float16 x = (_Float16)alpha;
+          p[g][0].h *= f16x8{x, x, x, x, x, x, x, x};
+          p[g][1].h *= f16x8{x, x, x, x, x, x, x, x};
+        });
+      }
+    };
+
+    // Before step t: step t + 1 has landed for every wave, every wave is done
+    // with step t - 2, and the loads of step t + kAhead begin in its place.
+    auto begin_step = [&](int t) {
+      stage_sync<(kAhead - 2) * CH>();
+      load_step(t + kAhead);
+    };
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) load_step(t);
+    int j = first, t = 0;
+    const int whole_steps = (clean - first) / kManyBlocks;
+    if (whole_steps > 0) {
+      begin_step(0);
+      here.cover<D>(a, at.s, at.h, first, last);
+      int i0 = here.info_of(first), i1 = here.info_of(first + 1), i_before = i0;
+      qk(first, k_byte(i0), s);
+#pragma unroll
+      for (int g = 0; g < RG; ++g) top[g] = largest(s[g]);
+      const int lane16 = lane * 16;
+      int cur = lane16, next = kStep + lane16, before = lane16;  // steps t, t + 1, t - 1 in the ring
+      i32x4 raw[2 * CH];  // chunks of the keys of j + 1, then of the values of j - 1
+      raw[0] = chunk_at(cur + kSlot, 0, 0);
+      raw[1] = chunk_at(cur + kSlot, 0, 1);
+      Frag f[2];  // widened chunk halves: the one in use and the next
+      {
+        Frag hi;
+        widen_keys(raw[0], scale_value(k_byte(i1)), f[0], hi);
+      }
+      // Scores of block j + 1 (keys at at_k), probabilities of j, output of j - 1
+      // (values at at_v; at first p is 0, and what is at at_v is block 1, which every
+      // row sees whole); at_k2: keys of j + 2.
+      auto body = [&](int at_k, int at_v, int at_k2, int info_s, int info_k, int info_k2, int info_v) {
+        if (__builtin_expect(!has_page(info_s), 0)) {
+          each<0, RG>([&](auto G) {
+            constexpr int g = decltype(G)::value;
+            top[g] = -INFINITY;
+            s[g] = s[g] * 0.0f - INFINITY;
+          });
+        }
+        const float vs = value_scale(v_byte(info_v));
+        cover_all();
+        const float ks = scale_value(k_byte(info_k)), ks2 = scale_value(k_byte(info_k2));
+        f32x16 s1[RG];
+        Frag p1[RG][2];
+        float x[16 * RG], add[RG];
+#pragma unroll
+        for (int g = 0; g < RG; ++g) add[g] = 0.0f;
+        // 4 CH RG beats of one matrix instruction each, and between them an even
+        // share of everything else: the next operand half widened, the next
+        // chunk but one read from LDS, the probabilities of block j in three
+        // stages a beat apart (argument, exponential, sum and rounding), and in
+        // the second half the maxima of the new scores.  The barriers keep the
+        // compiler from collecting like with like.
+        constexpr int kBeats = 4 * CH * RG, kE = 16 * RG;
+        each<0, kBeats + 2>([&](auto beat) {
+          constexpr int h = decltype(beat)::value, F = h / RG, g = h % RG;  // operand half, row group
+          if constexpr (h < kBeats) {
+            if constexpr (F < 2 * CH) {
+              const f32x16 zero = {};
+              s1[g] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[F & 1].b, qf[g][F].b, F == 0 ? zero : s1[g], 0, 0, 0);
+            } else {
+              constexpr int c = (F - 2 * CH) / 2;
+              o[g][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[F & 1].h, p[g][F & 1].h, o[g][c], 0, 0, 0);
+            }
+            // operand half F + 1: dwords 2 and 3 of its chunk if odd, else 0 and 1
+            constexpr int N = (F + 1) % (4 * CH);
+#pragma unroll
+            for (int i = g * 2 / RG; i < (g + 1) * 2 / RG; ++i) {
+              const int w = raw[N / 2][2 * (N & 1) + i];
+              if constexpr (N < 2 * CH) {
+                const float sc = N == 0 ? ks2 : ks;
+                f[N & 1].b2[2 * i] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, sc, false);
+                f[N & 1].b2[2 * i + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, sc, true);
+              } else {
+                f[N & 1].h2[2 * i] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, vs, false);
+                f[N & 1].h2[2 * i + 1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, vs, true);
+              }
+            }
+            if constexpr (g == 0 && (F + 3) % 2 == 0) {
+              constexpr int C = (F + 3) / 2;
+              if constexpr (C < CH)
+                raw[C] = chunk_at(at_k, 0, C);
+              else if constexpr (C < 2 * CH)
+                raw[C] = chunk_at(at_v, 1, C - CH);
+              else
+                raw[C - 2 * CH] = chunk_at(at_k2, 0, C - 2 * CH);
+            }
+            if constexpr (F >= 2 * CH + 1) {  // maxima of s1: 8 a row group, over the beats left
+              constexpr int kFirst = (2 * CH + 1) * RG, kLeft = kBeats - kFirst;
+              constexpr int m = h - kFirst;
+#pragma unroll
+              for (int i = m * 8 * RG / kLeft; i < (m + 1) * 8 * RG / kLeft; ++i) {
+                const int gg = i / 8, e = i % 8 * 2;
+                float most = __builtin_elementwise_maximum(s1[gg][e], s1[gg][e + 1]);
+                if (e != 0) most = __builtin_elementwise_maximum(top[gg], most);
+                asm volatile("" : "+v"(most));
+                top[gg] = most;
+              }
+            }
+          }
+#pragma unroll
+          for (int i = (h - 2) * kE / kBeats; i < (h - 1) * kE / kBeats; ++i)
+            if (i >= 0) {
+              float sum_to = add[i / 16] + x[i];
+              asm volatile("" : "+v"(sum_to));  // here, not where it is used
+              add[i / 16] = sum_to;
+              if (i & 1) {
+                int pair = __builtin_bit_cast(int, f16x2{(_Float16)x[i - 1], (_Float16)x[i]});
+                asm volatile("" : "+v"(pair));
+                p1[i / 16][i % 16 / 8].w[i % 8 / 2] = pair;
+              }
+            }
+#pragma unroll
+          for (int i = (h - 1) * kE / kBeats; i < h * kE / kBeats; ++i)
+            if (i >= 0 && h <= kBeats) x[i] = __builtin_amdgcn_exp2f(x[i]);
+          if (h < kBeats) {
+#pragma unroll
+            for (int i = h * kE / kBeats; i < (h + 1) * kE / kBeats; ++i)
+              x[i] = __builtin_fmaf(s[i / 16][i % 16], a.scale2, neg[i / 16]);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        });
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+          sum[g] += add[g];
+          s[g] = s1[g];
+          p[g][0] = p1[g][0], p[g][1] = p1[g][1];
+        }
+      };
+      int i2, i3;
+      for (;;) {
+        here.cover<D>(a, at.s, at.h, j + 2, last);  // behind `last`: no page, zeros
+        i2 = here.info_of(j + 2), i3 = here.info_of(j + 3);
+        body(cur + kSlot, before + kSlot, next, i0, i1, i2, i_before);
+        body(next, cur, next + kSlot, i1, i2, i3, i0);
+        i_before = i1, i0 = i2, i1 = i3;
+        before = cur, cur = next;
+        next = next + kStep >= kRing * kStep ? next + kStep - kRing * kStep : next + kStep;
+        j += kManyBlocks;
+        if (++t == whole_steps) break;
+        begin_step(t);
+      }
+      pv(j - 1, value_scale(v_byte(i_before)), p);
+    }
+    // blocks that some row sees in part, or not at all, one after the other
+    for (; j < last; ++j) {
+      if ((j - first) % kManyBlocks == 0) begin_step((j - first) / kManyBlocks);
+      here.cover<D>(a, at.s, at.h, j, last);
+      const int info = here.info_of(j);
+      qk(j, k_byte(info), s);
+#pragma unroll
+      for (int g = 0; g < RG; ++g) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s[g][i] = has_page(info) && token_of(i, half) < end[g] - j * kBlock ? s[g][i] : -INFINITY;
+        top[g] = largest(s[g]);
+      }
+      cover_all();
+#pragma unroll
+      for (int g = 0; g < RG; ++g) sum[g] += probabilities(s[g], a.scale2, neg[g], p[g]);
+      pv_masked(j, value_scale(v_byte(info)), p);
+    }
+    stage_sync<0>();  // loads that ran ahead have landed before the ring is used again
+    // rows or parts
+    const bool complete = n == steps;
+    PartRows<D>* out = part_of<D>(a, kWaves * RG, w, at.begin > 0 ? 0 : 1) + wave * RG;
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+      const float total = column_sum(sum[g]);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        if (complete) {
+          float x[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = o[g][c][i];
+          write_rows<D>(a, r[g], c, x, ref[g], total, v_ref);
+        } else if (r[g].real) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(out[g].o[c][i][lane]) =
+                make_float4(o[g][c][4 * i], o[g][c][4 * i + 1], o[g][c][4 * i + 2], o[g][c][4 * i + 3]);
+        }
+      }
+      if (!complete) {
+        if (half == 0) out[g].ref[col] = ref[g], out[g].sum[col] = total;
+        if (lane == 0) out[g].v_ref = v_ref;
+      }
+    }
+    left -= n;
+    if (left > 0) {
+      next_tile<BM>(a, at, steps);
+      __syncthreads();
+    }
+  }
+}
+
 // ---- joining a tile's parts -------------------------------------------------------------------------------------
 
 // One workgroup for each workgroup number w, 32-dim chunk and 32 rows of a tile: if w
@@ -278,14 +682,14 @@ __global__ __launch_bounds__(kJoinWaves * 64) void k_join(AttendArgs a) {
     if (m) break;
   }
   const int parts = more + 2;
-  float ref = INFINITY, sum = 0.0f, o[16];
+  float ref = -INFINITY, sum = 0.0f, o[16];
   int v_ref = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) o[i] = 0.0f;
   auto add = [&](float x_ref, float x_sum, int x_v, const float4* x) {
-    const float to = ref == INFINITY ? x_ref : x_ref == INFINITY ? ref : fmaxf(ref, x_ref);
+    const float to = fmaxf(ref, x_ref);
     const int v_to = max(v_ref, x_v);
-    const float mine = share_of(ref, to), theirs = share_of(x_ref, to);
+    const float mine = part_of_ref(ref, to), theirs = part_of_ref(x_ref, to);
     sum = sum * mine + x_sum * theirs;
     const float m = mine * exact_power(v_ref - v_to), t = theirs * exact_power(x_v - v_to);
 #pragma unroll
@@ -325,12 +729,27 @@ __global__ __launch_bounds__(kJoinWaves * 64) void k_join(AttendArgs a) {
   write_rows<D>(a, r, chunk, o, ref, sum, v_ref);
 }
 
+// Row tiles of more than this many rows take the kernel for many.
+constexpr int kFewRows = 32;
+
+constexpr int many_groups(int D) { return D == 256 ? 1 : 2; }
+
+int64_t rows_bound(const dllm_cache_batch& b, int64_t T, int group) { return (b.max_new < T ? b.max_new : T) * group; }
+
 template <int D>
 void launch(AttendArgs a, hipStream_t st) {
-  a.parts = kNarrowParts;
-  a.min_steps = kWaves;
-  hipLaunchKernelGGL(k_attend_few<D>, dim3(a.parts), dim3(kThreads), 0, st, a);
-  hipLaunchKernelGGL((k_join<D, 32>), dim3(a.parts, D / 32, 1), dim3(kJoinWaves * 64), 0, st, a);
+  constexpr int RG = many_groups(D), BM = kWaves * 32 * RG;
+  if (rows_bound(a.b, a.T, a.group) > kFewRows) {
+    a.parts = kManyParts;
+    a.min_steps = 2;
+    hipLaunchKernelGGL((k_attend_many<D, RG>), dim3(a.parts), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((k_join<D, BM>), dim3(a.parts, D / 32, BM / 32), dim3(kJoinWaves * 64), 0, st, a);
+  } else {
+    a.parts = kNarrowParts;
+    a.min_steps = kWaves;
+    hipLaunchKernelGGL(k_attend_few<D>, dim3(a.parts), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((k_join<D, 32>), dim3(a.parts, D / 32, 1), dim3(kJoinWaves * 64), 0, st, a);
+  }
 }
 
 }  // namespace
@@ -342,7 +761,9 @@ size_t dllm_cache_attention_workspace_bytes(const dllm_cache* cache, const dllm_
   using namespace dllm;
   if (!cache_ok(cache) || !cache_supported(cache) || !batch_ok(batch) || q_heads < 1 || q_heads % cache->kv_heads != 0)
     return 0;
-  return parts_bytes(cache->head_dim, kNarrowParts, 1);
+  const int D = cache->head_dim;
+  const size_t few = parts_bytes(D, kNarrowParts, 1), many = parts_bytes(D, kManyParts, kWaves * many_groups(D));
+  return batch->max_new * (int64_t)(q_heads / cache->kv_heads) > kFewRows ? (many > few ? many : few) : few;
 }
 
 dllm_status dllm_cache_attention(const dllm_cache* cache, const dllm_cache_batch* batch, int64_t T, const uint16_t* q,

@@ -56,7 +56,29 @@ union Frag {
   i32x4 w;
 };
 
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+// f(0), f(1), ... with constants, so that what they index is in registers from
+// the first pass of the compiler on.
+template <int I>
+struct Const {
+  static constexpr int value = I;
+};
+template <int I, int N, class F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (I < N) {
+    f(Const<I>{});
+    each<I + 1, N>(f);
+  }
+}
+
+// max and sum of the two lanes of a column, in both.
+__device__ __forceinline__ float column_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float column_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
 
 // 16 e4m3 bytes, times the scale, as two operands of 8 bf16.
 __device__ __forceinline__ void widen_keys(i32x4 raw, float scale, Frag& lo, Frag& hi) {
@@ -113,7 +135,7 @@ __device__ __forceinline__ int token_of(int i, int half) { return 8 * (i >> 2) +
 template <int D>
 struct Accumulator {
   f32x16 o[D / 32];
-  float ref;  // base-2 reference; +inf before the first visible token
+  float ref;  // base-2 reference; -inf before the first visible token
   float sum;
   int v_ref;  // scale byte that O is relative to; 0 before the first block
 };
@@ -124,7 +146,7 @@ __device__ __forceinline__ void clear(Accumulator<D>& a) {
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
     for (int j = 0; j < 16; ++j) a.o[i][j] = 0.0f;
-  a.ref = INFINITY;
+  a.ref = -INFINITY;
   a.sum = 0.0f;
   a.v_ref = 0;
 }
@@ -152,17 +174,23 @@ __device__ __forceinline__ float cover_values(Accumulator<D>& a, int v_byte) {
   return __uint_as_float((uint32_t)max(v_byte - a.v_ref + 127, 1) << 23);
 }
 
+// What a state with reference `own` counts for under reference `ref`.
+__device__ __forceinline__ float part_of_ref(float own, float ref) {
+  return own == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(own - ref);
+}
+
+// The negative of a reference, as the probabilities take it: a column that
+// has seen no token (ref = -inf) gets probabilities of 0.
+__device__ __forceinline__ float negative(float ref) { return ref == -INFINITY ? -INFINITY : -ref; }
+
 // Move the reference to cover scores up to `top` (this lane's largest), if
 // they have outgrown it.
 template <int D>
 __device__ __forceinline__ void cover(Accumulator<D>& a, float top, float scale2) {
-  top = fmaxf(top, other_half(top));
-  // a column without a visible token so far has top = -inf and keeps ref = +inf: its probabilities come out 0
-  const float want = top == -INFINITY ? INFINITY : __builtin_fmaf(top, scale2, -kOffset);
-  const bool grow = want != INFINITY && (a.ref == INFINITY || want > a.ref + kSlack);
-  if (__any(grow)) {
-    const float ref = want == INFINITY ? a.ref : a.ref == INFINITY ? want : fmaxf(a.ref, want);
-    const float alpha = a.ref == INFINITY ? 0.0f : __builtin_amdgcn_exp2f(a.ref - ref);
+  const float want = __builtin_fmaf(column_max(top), scale2, -kOffset);
+  if (__any(want > a.ref + kSlack)) {
+    const float ref = fmaxf(a.ref, want);
+    const float alpha = part_of_ref(a.ref, ref);
     a.ref = ref;
     a.sum *= alpha;
     rescale(a, alpha);
@@ -176,21 +204,24 @@ __device__ __forceinline__ float largest(const f32x16& s) {
   return top;
 }
 
-// Probabilities of one block's scores, summed in fp32 before they are rounded
-// to fp16 operands.
-template <int D>
-__device__ __forceinline__ void probabilities(Accumulator<D>& a, const f32x16& s, float scale2, Frag* p) {
-  const float neg = -a.ref;
-  float sum = 0.0f;
+// Probabilities of one block's scores against the reference -neg, rounded to
+// fp16 operands; returns their unrounded sum.
+__device__ __forceinline__ float probabilities(const f32x16& s, float scale2, float neg, Frag* p) {
+  float even = 0.0f, odd = 0.0f;
 #pragma unroll
   for (int i = 0; i < 16; i += 2) {
     const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale2, neg));
     const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i + 1], scale2, neg));
-    sum += x;
-    sum += y;
+    even += x;
+    odd += y;
     p[i / 8].h2[(i % 8) / 2] = f16x2{(_Float16)x, (_Float16)y};
   }
-  a.sum += sum;
+  return even + odd;
+}
+
+template <int D>
+__device__ __forceinline__ void probabilities(Accumulator<D>& a, const f32x16& s, float scale2, Frag* p) {
+  a.sum += probabilities(s, scale2, negative(a.ref), p);
 }
 
 // O^T += V^T P^T of one block.  raw: the lane's D / 32 loads of its values.
@@ -205,11 +236,35 @@ __device__ __forceinline__ void add_values(Accumulator<D>& a, const Frag* p, con
   }
 }
 
-// The same for a block that some of the tile's columns see only in part: a
+// NaN bytes of a chunk of values taken out of it: nan has a 1 in their place.
+__device__ __forceinline__ void take_nan(i32x4& x, i32x4& nan) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    nan[j] = (((x[j] & 0x7f7f7f7f) + 0x01010101) >> 7) & 0x01010101;
+    x[j] &= ~(nan[j] * 0xff);
+  }
+}
+
+// O^T of a chunk made NaN where a NaN value (take_nan) is visible to the
+// column: limit is its number of visible tokens of the block.
+__device__ __forceinline__ void spread_nan(f32x16& o, i32x4 nan, int limit, int half) {
+  Frag see[2], lo, hi;
+#pragma unroll
+  for (int j = 0; j < 16; j += 2)
+    see[j / 8].h2[(j % 8) / 2] = f16x2{(_Float16)(token_of(j, half) < limit ? 1.0f : 0.0f),
+                                       (_Float16)(token_of(j + 1, half) < limit ? 1.0f : 0.0f)};
+  widen_values(nan * 0x38, 1.0f, lo, hi);  // 1.0
+  f32x16 hit = {};
+  hit = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo.h, see[0].h, hit, 0, 0, 0);
+  hit = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi.h, see[1].h, hit, 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) o[j] = hit[j] > 0.0f ? NAN : o[j];
+}
+
+// add_values for a block that some of the tile's columns see only in part: a
 // NaN value must not reach, as 0 * NaN, a column that masks its token.  NaN
-// bytes are taken out of the product, and where one is visible (limit: the
-// column's visible tokens of the block) the result is made NaN.  Rare, so the
-// product that finds those places is made only if there is such a byte.
+// bytes are taken out of the product, and where one is visible the result is
+// made NaN; that second product is made only if there is such a byte.
 template <int D>
 __device__ __forceinline__ void add_values_masked(Accumulator<D>& a, const Frag* p, const i32x4* raw, float v_scale,
                                                   int limit, int half) {
@@ -217,27 +272,11 @@ __device__ __forceinline__ void add_values_masked(Accumulator<D>& a, const Frag*
   for (int i = 0; i < D / 32; ++i) {
     Frag lo, hi;
     i32x4 x = raw[i], nan;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      nan[j] = (((x[j] & 0x7f7f7f7f) + 0x01010101) >> 7) & 0x01010101;  // 1 in each byte that is NaN
-      x[j] &= ~(nan[j] * 0xff);
-    }
+    take_nan(x, nan);
     widen_values(x, v_scale, lo, hi);
     a.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo.h, p[0].h, a.o[i], 0, 0, 0);
     a.o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi.h, p[1].h, a.o[i], 0, 0, 0);
-    if (__any(nan[0] | nan[1] | nan[2] | nan[3])) {
-      Frag see[2];
-#pragma unroll
-      for (int j = 0; j < 16; j += 2)
-        see[j / 8].h2[(j % 8) / 2] = f16x2{(_Float16)(token_of(j, half) < limit ? 1.0f : 0.0f),
-                                           (_Float16)(token_of(j + 1, half) < limit ? 1.0f : 0.0f)};
-      widen_values(nan * 0x38, 1.0f, lo, hi);  // 1.0
-      f32x16 hit = {};
-      hit = __builtin_amdgcn_mfma_f32_32x32x16_f16(lo.h, see[0].h, hit, 0, 0, 0);
-      hit = __builtin_amdgcn_mfma_f32_32x32x16_f16(hi.h, see[1].h, hit, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) a.o[i][j] = hit[j] > 0.0f ? NAN : a.o[i][j];
-    }
+    if (__any(nan[0] | nan[1] | nan[2] | nan[3])) spread_nan(a.o[i], nan, limit, half);
   }
 }
 
