@@ -46,14 +46,14 @@ struct Row {
   bool real;
 };
 
-__device__ __forceinline__ Row row_of(const AttendArgs& a, const SeqView& q, int h, int row) {
-  const int rows = q.rows * a.group;
+__device__ __forceinline__ Row row_of(const AttendArgs& a, int64_t q0, int tokens, int h, int row) {
+  const int rows = tokens * a.group;
   Row r;
   r.real = row < rows;
   row = min(row, rows - 1);
   r.tok = (int)((uint32_t)row / (uint32_t)a.group);
   r.head = h * a.group + (row - r.tok * a.group);
-  r.out = (q.q0 + r.tok) * a.q_heads + r.head;
+  r.out = (q0 + r.tok) * a.q_heads + r.head;
   return r;
 }
 
@@ -99,6 +99,9 @@ struct Walk {
       const int64_t at = block_of(a.c, max(page, 0), h);
       k_byte = a.c.k_scale[at];
       v_byte = a.c.v_scale[at];
+      // wait for them here: behind the branch the wait would be for every load
+      // in flight, at every use
+      asm volatile("" : "+v"(page), "+v"(k_byte), "+v"(v_byte));
     }
     const int i = j - base;
     const int p = __builtin_amdgcn_readlane(page, i);
@@ -119,20 +122,21 @@ struct Walk {
 // are joined through LDS.
 template <int D>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void k_attend_few(AttendArgs a) {
-  __shared__ float o_lds[kWaves][D / 32][4][64][4];
+  __shared__ __attribute__((aligned(16))) float o_lds[kWaves][D / 32][4][64][4];
   __shared__ float ref_lds[kWaves][32], sum_lds[kWaves][32];
   __shared__ int v_lds[kWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, half = lane >> 5;
   int w;
   int64_t left;
-  Stretch at = find_stretch<32, kBlock>(a, &w, &left);
+  Stretch at = find_stretch<32, kBlock>(a, reinterpret_cast<int64_t*>(o_lds), &w, &left);
+  __syncthreads();
   if (threadIdx.x == 0) reinterpret_cast<Stretch*>(a.ws)[w] = at;
   while (left > 0) {
     const SeqView q = seq_view(a.b, a.T, at.s);
     const int steps = tile_steps<32, kBlock>(a, q, at.rt);
     const int n = (int)min((int64_t)(steps - at.begin), left);
     const int row0 = at.rt * 32;
-    const Row r = row_of(a, q, at.h, row0 + col);
+    const Row r = row_of(a, q.q0, q.rows, at.h, row0 + col);
     Frag qf[D / 16];
     load_query<D>(qf, a.q + (q.q0 + r.tok) * a.q_token + (int64_t)r.head * a.q_head, half);
     // this column sees tokens [0, end); blocks below `whole` are seen whole by every column
@@ -226,7 +230,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void k_attend_few(Atten
         }
       if (complete) {
         write_rows<D>(a, r, c, o, ref, total, v_ref);
-      } else if (r.real) {
+      } else if (r.real) {  // the rest is never used
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<float4*>(out->o[c][i][lane]) = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -260,13 +264,16 @@ struct Lookup {
   // Makes block j's (and 63 more) known.
   template <int D>
   __device__ __forceinline__ void cover(const AttendArgs& a, int s, int h, int j, int last) {
-    if (__builtin_expect(j >= base && j < base + 64, 1)) return;
-    base = j;
+    if (__builtin_expect((uint32_t)(j - base) < 64u, 1)) return;
+    base = __builtin_amdgcn_readfirstlane(j);
     const int b = j + (threadIdx.x & 63);
     const int page = b < last ? page_of(a.b.table, a.b.table_blocks, a.c.pages, s, b) : -1;
     const int64_t x = block_of(a.c, max(page, 0), h);
     at = page < 0 ? -1 : x * (kBlock * D);
     info = page < 0 ? 127 | 1 << 8 : a.c.k_scale[x] | a.c.v_scale[x] << 8 | 1 << 16;  // no page: moves no scale
+    // wait for them here: behind the branch the wait would be for every load
+    // in flight, at every use
+    asm volatile("" : "+v"(at), "+v"(info));
   }
   __device__ __forceinline__ int info_of(int j) const { return __builtin_amdgcn_readlane(info, j - base); }
   __device__ __forceinline__ int64_t at_of(int j) const {
@@ -297,7 +304,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int w;
   int64_t left;
-  Stretch at = find_stretch<BM, KEYS>(a, &w, &left);
+  Stretch at = find_stretch<BM, KEYS>(a, reinterpret_cast<int64_t*>(ring), &w, &left);
+  __syncthreads();
   if (threadIdx.x == 0) reinterpret_cast<Stretch*>(a.ws)[w] = at;
   while (left > 0) {
     const SeqView q = seq_view(a.b, a.T, at.s);
@@ -309,7 +317,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
     Frag qf[RG][D / 16];
 #pragma unroll
     for (int g = 0; g < RG; ++g) {
-      r[g] = row_of(a, q, at.h, row0 + g * 32 + col);
+      r[g] = row_of(a, q.q0, q.rows, at.h, row0 + g * 32 + col);
       load_query<D>(qf[g], a.q + (q.q0 + r[g].tok) * a.q_token + (int64_t)r[g].head * a.q_head, half);
       end[g] = a.causal ? min(max(q.len - q.n + r[g].tok + 1, 0), q.len) : q.len;
       // queries are only ever matrix operands: in the accumulation registers
@@ -344,11 +352,17 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
     // blocks, CH loads, for every step alike (behind the last block they read
     // nothing of use), so that waits can count them.
     int put = 0;  // where in the ring the next step goes
-    auto load_step = [&](int t) {
+    const uint8_t* mine = wave & 1 ? a.c.v : a.c.k;
+    const uint8_t* nothing = no_page;
+    asm volatile("" : "+s"(mine), "+s"(nothing));  // kept, not loaded again at every step
+    const uint8_t* src;
+    auto find_step = [&](int t) {
       const int j0 = first + t * kManyBlocks;
       ahead.cover<D>(a, at.s, at.h, j0, last);
       const int64_t from = ahead.at_of(j0 + (wave >> 1));
-      const uint8_t* src = from < 0 ? no_page : (wave & 1 ? a.c.v : a.c.k) + from;
+      src = from < 0 ? nothing : mine + from;
+    };
+    auto load_step = [&]() {
       uint8_t* dst = ring + put + wave * CH * 1024;
       each<0, CH>([&](auto c) {
         constexpr int x = decltype(c)::value * 1024;  // the instruction's offset counts on both sides
@@ -455,18 +469,22 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
       }
     };
 
-    // Before step t: step t + 1 has landed for every wave, every wave is done
-    // with step t - 2, and the loads of step t + kAhead begin in its place.
+    // In step t: step t + 1 has landed for every wave, every wave is done with
+    // step t - 2, and the loads of step t + kAhead begin in its place.
     auto begin_step = [&](int t) {
+      find_step(t + kAhead);
       stage_sync<(kAhead - 2) * CH>();
-      load_step(t + kAhead);
+      load_step();
     };
 #pragma unroll
-    for (int t = 0; t < kAhead; ++t) load_step(t);
+    for (int t = 0; t < kAhead; ++t) {
+      find_step(t);
+      load_step();
+    }
     int j = first, t = 0;
     const int whole_steps = (clean - first) / kManyBlocks;
     if (whole_steps > 0) {
-      begin_step(0);
+      stage_sync<(kAhead - 2) * CH>();
       here.cover<D>(a, at.s, at.h, first, last);
       int i0 = here.info_of(first), i1 = here.info_of(first + 1), i_before = i0;
       qk(first, k_byte(i0), s);
@@ -475,8 +493,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
       const int lane16 = lane * 16;
       int cur = lane16, next = kStep + lane16, before = lane16;  // steps t, t + 1, t - 1 in the ring
       i32x4 raw[2 * CH];  // chunks of the keys of j + 1, then of the values of j - 1
-      raw[0] = chunk_at(cur + kSlot, 0, 0);
-      raw[1] = chunk_at(cur + kSlot, 0, 1);
+      constexpr int kEarly = 3;  // chunks that reads from LDS run ahead
+      each<0, kEarly>([&](auto c) {
+        constexpr int C = decltype(c)::value;
+        raw[C] = C < CH ? chunk_at(cur + kSlot, 0, C) : chunk_at(before + kSlot, 1, C - CH);
+      });
       Frag f[2];  // widened chunk halves: the one in use and the next
       {
         Frag hi;
@@ -485,7 +506,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
       // Scores of block j + 1 (keys at at_k), probabilities of j, output of j - 1
       // (values at at_v; at first p is 0, and what is at at_v is block 1, which every
       // row sees whole); at_k2: keys of j + 2.
-      auto body = [&](int at_k, int at_v, int at_k2, int info_s, int info_k, int info_k2, int info_v) {
+      auto body = [&](auto first_of_step, int at_k, int at_v, int at_k2, int at_v2, int info_s, int info_k, int info_k2, int info_v) {
         if (__builtin_expect(!has_page(info_s), 0)) {
           each<0, RG>([&](auto G) {
             constexpr int g = decltype(G)::value;
@@ -518,6 +539,15 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
               constexpr int c = (F - 2 * CH) / 2;
               o[g][c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[F & 1].h, p[g][F & 1].h, o[g][c], 0, 0, 0);
             }
+            // In the first block of a step, while there is nothing yet to wait for:
+            // the step's barrier, and the loads that it lets begin.
+            if constexpr (decltype(first_of_step)::value && h == kBeats / 4) {
+              asm volatile("" ::: "memory");
+              __builtin_amdgcn_s_waitcnt(((kAhead - 2) * CH & 15) | (7 << 4) | (15 << 8));
+              __builtin_amdgcn_s_barrier();
+              asm volatile("" ::: "memory");
+            }
+            if constexpr (decltype(first_of_step)::value && h == kBeats / 4 + 1) load_step();
             // operand half F + 1: dwords 2 and 3 of its chunk if odd, else 0 and 1
             constexpr int N = (F + 1) % (4 * CH);
 #pragma unroll
@@ -532,14 +562,17 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
                 f[N & 1].h2[2 * i + 1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, vs, true);
               }
             }
-            if constexpr (g == 0 && (F + 3) % 2 == 0) {
-              constexpr int C = (F + 3) / 2;
+            __builtin_amdgcn_sched_barrier(0);  // widened early in the beat: the next instruction may need it
+            if constexpr (g == 0 && F % 2 == 1) {
+              constexpr int C = (F + 2 * kEarly - 1) / 2;
               if constexpr (C < CH)
                 raw[C] = chunk_at(at_k, 0, C);
               else if constexpr (C < 2 * CH)
                 raw[C] = chunk_at(at_v, 1, C - CH);
-              else
+              else if constexpr (C < 3 * CH)
                 raw[C - 2 * CH] = chunk_at(at_k2, 0, C - 2 * CH);
+              else
+                raw[C - 2 * CH] = chunk_at(at_v2, 1, C - 3 * CH);
             }
             if constexpr (F >= 2 * CH + 1) {  // maxima of s1: 8 a row group, over the beats left
               constexpr int kFirst = (2 * CH + 1) * RG, kLeft = kBeats - kFirst;
@@ -587,14 +620,14 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
       for (;;) {
         here.cover<D>(a, at.s, at.h, j + 2, last);  // behind `last`: no page, zeros
         i2 = here.info_of(j + 2), i3 = here.info_of(j + 3);
-        body(cur + kSlot, before + kSlot, next, i0, i1, i2, i_before);
-        body(next, cur, next + kSlot, i1, i2, i3, i0);
+        find_step(t + kAhead);
+        body(Const<1>{}, cur + kSlot, before + kSlot, next, cur, i0, i1, i2, i_before);
+        body(Const<0>{}, next, cur, next + kSlot, cur + kSlot, i1, i2, i3, i0);
         i_before = i1, i0 = i2, i1 = i3;
         before = cur, cur = next;
         next = next + kStep >= kRing * kStep ? next + kStep - kRing * kStep : next + kStep;
         j += kManyBlocks;
         if (++t == whole_steps) break;
-        begin_step(t);
       }
       pv(j - 1, value_scale(v_byte(i_before)), p);
     }
@@ -652,81 +685,94 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
 
 // ---- joining a tile's parts -------------------------------------------------------------------------------------
 
-// One workgroup for each workgroup number w, 32-dim chunk and 32 rows of a tile: if w
-// is the first to begin inside its tile, the tile is joined here from w - 1's
-// last part and the first parts of w, w + 1, ...  The 16 waves take the parts in
-// turn, and their shares are added in wave order.
-constexpr int kJoinWaves = 16;
+// One workgroup for each 8 stretches and 32-row, 32-dim piece of a tile: where
+// stretch w is the first to begin inside its tile, the piece is joined here from
+// w - 1's last part and the first parts of w, w + 1, ...  The waves take the parts
+// in turn, a few in flight at a time, and their shares are added in order.
+// (With a workgroup for every stretch, most of them only to find no work, this
+// kernel took 16 us where it now takes 6.)
+constexpr int kJoinStretches = 8;
+constexpr int kJoinThreads = 256, kJoinTurns = kJoinThreads / 64, kJoinFlight = 4;
+
+// o, sum of a column under reference ref and value scale v.
+struct Share {
+  float o[16];
+  float ref, sum;
+  int v;
+};
+
+__device__ __forceinline__ void add_share(Share& a, const float4* x, float ref, float sum, int v) {
+  const float to = fmaxf(a.ref, ref);
+  const int v_to = max(a.v, v);
+  const float mine = part_of_ref(a.ref, to), theirs = part_of_ref(ref, to);
+  a.sum = a.sum * mine + sum * theirs;
+  const float m = mine * exact_power(a.v - v_to), t = theirs * exact_power(v - v_to);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a.o[4 * i] = a.o[4 * i] * m + x[i].x * t;
+    a.o[4 * i + 1] = a.o[4 * i + 1] * m + x[i].y * t;
+    a.o[4 * i + 2] = a.o[4 * i + 2] * m + x[i].z * t;
+    a.o[4 * i + 3] = a.o[4 * i + 3] * m + x[i].w * t;
+  }
+  a.ref = to;
+  a.v = v_to;
+}
 
 template <int D, int BM>
-__global__ __launch_bounds__(kJoinWaves * 64) void k_join(AttendArgs a) {
-  __shared__ float o_lds[kJoinWaves][4][64][4];
-  __shared__ float ref_lds[kJoinWaves][32], sum_lds[kJoinWaves][32];
-  __shared__ int v_lds[kJoinWaves];
-  const int w = blockIdx.x, chunk = blockIdx.y, sub = blockIdx.z;
-  const Stretch* all = reinterpret_cast<const Stretch*>(a.ws);
-  const Stretch me = all[w];
-  if (me.tile < 0 || me.begin == 0) return;
-  if (w > 0 && all[w - 1].tile == me.tile && all[w - 1].begin > 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, half = lane >> 5;
-  const SeqView q = seq_view(a.b, a.T, me.s);
-  const int row0 = me.rt * BM + sub * 32;
-  if (row0 >= q.rows * a.group) return;
-  const Row r = row_of(a, q, me.h, row0 + col);
-  // parts: w - 1's slot 1, then slot 0 of w .. w + more
-  int more = 0;
-  for (int i0 = w + 1;; i0 += 64) {
-    const bool same = i0 + lane < a.parts && all[i0 + lane].tile == me.tile && all[i0 + lane].begin > 0;
-    const uint64_t m = ~__ballot(same);
-    more += m ? __ffsll((unsigned long long)m) - 1 : 64;
-    if (m) break;
-  }
-  const int parts = more + 2;
-  float ref = -INFINITY, sum = 0.0f, o[16];
-  int v_ref = 0;
+__global__ __launch_bounds__(kJoinThreads) void k_join(AttendArgs a) {
+  __shared__ float o_lds[kJoinTurns][4][64][4];
+  __shared__ float ref_lds[kJoinTurns][32], sum_lds[kJoinTurns][32];
+  __shared__ int v_lds[kJoinTurns];
+  const int sub = blockIdx.y, chunk = blockIdx.z;
+  const int lane = threadIdx.x & 63, turn = threadIdx.x >> 6, col = lane & 31, half = lane >> 5;
+  const Stretch* all = reinterpret_cast<const Stretch*>(a.ws) + blockIdx.x * kJoinStretches;
+  uint64_t todo = __ballot(lane < kJoinStretches && all[lane].parts > 0);
+  for (bool again = false; todo; todo &= todo - 1) {
+    const int w0 = __ffsll((unsigned long long)todo) - 1, w = blockIdx.x * kJoinStretches + w0;
+    const Stretch me = all[w0];
+    const int row0 = me.rt * BM + sub * 32, parts = me.parts;
+    if (row0 >= me.rows * a.group) continue;
+    if (again) __syncthreads();  // the shares of the one before are no longer read
+    again = true;
+    const Row r = row_of(a, me.q0, me.rows, me.h, row0 + col);
+    Share mine;
+    mine.ref = -INFINITY, mine.sum = 0.0f, mine.v = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = 0.0f;
-  auto add = [&](float x_ref, float x_sum, int x_v, const float4* x) {
-    const float to = fmaxf(ref, x_ref);
-    const int v_to = max(v_ref, x_v);
-    const float mine = part_of_ref(ref, to), theirs = part_of_ref(x_ref, to);
-    sum = sum * mine + x_sum * theirs;
-    const float m = mine * exact_power(v_ref - v_to), t = theirs * exact_power(x_v - v_to);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[4 * i] = o[4 * i] * m + x[i].x * t;
-      o[4 * i + 1] = o[4 * i + 1] * m + x[i].y * t;
-      o[4 * i + 2] = o[4 * i + 2] * m + x[i].z * t;
-      o[4 * i + 3] = o[4 * i + 3] * m + x[i].w * t;
+    for (int i = 0; i < 16; ++i) mine.o[i] = 0.0f;
+    for (int i0 = turn; i0 < parts; i0 += kJoinTurns * kJoinFlight) {
+      float4 x[kJoinFlight][4];
+      float ref[kJoinFlight], sum[kJoinFlight];
+      int v[kJoinFlight];
+      each<0, kJoinFlight>([&](auto F) {
+        constexpr int f = decltype(F)::value;
+        const int i = i0 + f * kJoinTurns;
+        if (i < parts) {
+          const PartRows<D>* p = part_of<D>(a, BM / 32, i == 0 ? w - 1 : w + i - 1, i == 0 ? 1 : 0) + sub;
+          each<0, 4>([&](auto c) { x[f][decltype(c)::value] = *reinterpret_cast<const float4*>(p->o[chunk][decltype(c)::value][lane]); });
+          ref[f] = p->ref[col], sum[f] = p->sum[col], v[f] = p->v_ref;
+        }
+      });
+      each<0, kJoinFlight>([&](auto F) {
+        constexpr int f = decltype(F)::value;
+        if (i0 + f * kJoinTurns < parts) add_share(mine, x[f], ref[f], sum[f], v[f]);
+      });
     }
-    ref = to;
-    v_ref = v_to;
-  };
-  for (int i = wave; i < parts; i += kJoinWaves) {
-    const PartRows<D>* p = part_of<D>(a, BM / 32, i == 0 ? w - 1 : w + i - 1, i == 0 ? 1 : 0) + sub;
-    float4 x[4];
-    if (r.real) {
+    if (half == 0) ref_lds[turn][col] = mine.ref, sum_lds[turn][col] = mine.sum;
+    if (lane == 0) v_lds[turn] = mine.v;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const float4*>(p->o[chunk][c][lane]);
-      add(p->ref[col], p->sum[col], p->v_ref, x);
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<float4*>(o_lds[turn][c][lane]) =
+          make_float4(mine.o[4 * c], mine.o[4 * c + 1], mine.o[4 * c + 2], mine.o[4 * c + 3]);
+    __syncthreads();
+    if (turn != 0) continue;
+    for (int i = 1; i < min(parts, kJoinTurns); ++i) {
+      float4 x[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const float4*>(o_lds[i][c][lane]);
+      add_share(mine, x, ref_lds[i][col], sum_lds[i][col], v_lds[i]);
     }
+    write_rows<D>(a, r, chunk, mine.o, mine.ref, mine.sum, mine.v);
   }
-  if (half == 0) ref_lds[wave][col] = ref, sum_lds[wave][col] = sum;
-  // v_ref may differ between the columns of a wave only where a column is not real
-  const int v_wave = __builtin_amdgcn_readfirstlane(v_ref);
-  if (lane == 0) v_lds[wave] = v_wave;
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<float4*>(o_lds[wave][c][lane]) = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-  __syncthreads();
-  if (wave != 0) return;
-  for (int i = 1; i < min(parts, kJoinWaves); ++i) {
-    float4 x[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const float4*>(o_lds[i][c][lane]);
-    add(ref_lds[i][col], sum_lds[i][col], v_lds[i], x);
-  }
-  write_rows<D>(a, r, chunk, o, ref, sum, v_ref);
 }
 
 // Row tiles of more than this many rows take the kernel for many.
@@ -743,12 +789,12 @@ void launch(AttendArgs a, hipStream_t st) {
     a.parts = kManyParts;
     a.min_steps = 2;
     hipLaunchKernelGGL((k_attend_many<D, RG>), dim3(a.parts), dim3(kThreads), 0, st, a);
-    hipLaunchKernelGGL((k_join<D, BM>), dim3(a.parts, D / 32, BM / 32), dim3(kJoinWaves * 64), 0, st, a);
+    hipLaunchKernelGGL((k_join<D, BM>), dim3(a.parts / kJoinStretches, BM / 32, D / 32), dim3(kJoinThreads), 0, st, a);
   } else {
     a.parts = kNarrowParts;
     a.min_steps = kWaves;
     hipLaunchKernelGGL(k_attend_few<D>, dim3(a.parts), dim3(kThreads), 0, st, a);
-    hipLaunchKernelGGL((k_join<D, 32>), dim3(a.parts, D / 32, 1), dim3(kJoinWaves * 64), 0, st, a);
+    hipLaunchKernelGGL((k_join<D, 32>), dim3(a.parts / kJoinStretches, 1, D / 32), dim3(kJoinThreads), 0, st, a);
   }
 }
 

@@ -32,10 +32,13 @@ struct AttendArgs {
 
 // Where a workgroup's stretch begins: tile rt of head h of sequence s, whose
 // first step is number `tile` on the line, at its step `begin`.  tile < 0: no
-// work.
+// work.  parts > 0: this is the first stretch to begin inside its tile, which
+// is in that many parts, the first of them the end of the stretch before.
+// Kept in the workspace for the kernel that joins the parts, with the
+// sequence's first token and rows, so that it has one load to wait for.
 struct Stretch {
-  int64_t tile;
-  int s, h, rt, begin;
+  int64_t tile, q0;
+  int s, h, rt, begin, rows, parts;
 };
 
 constexpr int kScheduleThreads = 256;
@@ -93,11 +96,13 @@ __device__ __forceinline__ int64_t scan(int64_t x, int64_t* lds) {
 // to the chip's 8 XCDs in turn, and neighbours on the line, which read the
 // same keys, belong on one XCD's L2; where the line is too short for every
 // workgroup they stay in turn, for else the first XCD would get it all.
+// lds: 64 bytes of the kernel's LDS (handed in, for a kernel with loads that
+// go straight to LDS must have one array of it: with more, the compiler waits for all
+// such loads before every read).
 template <int BM, int KEYS>
-__device__ Stretch find_stretch(const AttendArgs& a, int* number, int64_t* steps) {
-  __shared__ int64_t lds[kScheduleThreads / 64];
-  __shared__ int64_t found_at;
-  __shared__ int found_s;
+__device__ Stretch find_stretch(const AttendArgs& a, int64_t* lds, int* number, int64_t* steps) {
+  int64_t& found_at = lds[kScheduleThreads / 64];
+  int& found_s = *reinterpret_cast<int*>(lds + kScheduleThreads / 64 + 1);
   const int tid = threadIdx.x;
   int64_t total = 0, mine = 0, upto = 0;
   if (a.b.S == 1) {
@@ -116,7 +121,7 @@ __device__ Stretch find_stretch(const AttendArgs& a, int* number, int64_t* steps
   const int64_t parts = min((int64_t)a.parts, max(quotient(total + a.min_steps - 1, a.min_steps), (int64_t)1));
   const int w = parts == a.parts ? (int)(blockIdx.x % 8) * (a.parts / 8) + (int)blockIdx.x / 8 : (int)blockIdx.x;
   *number = w;
-  Stretch r = {-1, 0, 0, 0, 0};
+  Stretch r = {-1, 0, 0, 0, 0, 0, 0, 0};
   *steps = 0;
   if (w >= parts || total == 0) return r;
   const int64_t lo = quotient(total * w, parts), hi = quotient(total * (w + 1), parts);
@@ -141,22 +146,24 @@ __device__ Stretch find_stretch(const AttendArgs& a, int* number, int64_t* steps
     at = found_at;
   }
   const SeqView q = seq_view(a.b, a.T, r.s);
+  r.q0 = q.q0, r.rows = q.rows;
   const int64_t per_head = head_steps<BM, KEYS>(a, q);
   r.h = (int)quotient(lo - at, per_head);
   at += r.h * per_head;
+  int n = tile_steps<BM, KEYS>(a, q, 0);
   if (!a.causal) {
-    const int n = tile_steps<BM, KEYS>(a, q, 0);
     r.rt = (int)quotient(lo - at, n);
     at += (int64_t)r.rt * n;
   } else {
-    for (;; ++r.rt) {
-      const int n = tile_steps<BM, KEYS>(a, q, r.rt);
-      if (lo < at + n) break;
+    while (lo >= at + n) {
       at += n;
+      n = tile_steps<BM, KEYS>(a, q, ++r.rt);
     }
   }
   r.tile = at;
   r.begin = (int)(lo - at);
+  // stretches w .. that begin before the tile's end, and the one before w
+  if (r.begin > 0 && quotient(total * (w - 1), parts) <= at) r.parts = (int)quotient((at + n) * parts + total - 1, total) - w + 1;
   return r;
 }
 
