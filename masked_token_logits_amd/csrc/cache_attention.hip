@@ -493,20 +493,16 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
       const int lane16 = lane * 16;
       int cur = lane16, next = kStep + lane16, before = lane16;  // steps t, t + 1, t - 1 in the ring
       i32x4 raw[2 * CH];  // chunks of the keys of j + 1, then of the values of j - 1
-      constexpr int kEarly = 3;  // chunks that reads from LDS run ahead
-      each<0, kEarly>([&](auto c) {
-        constexpr int C = decltype(c)::value;
-        raw[C] = C < CH ? chunk_at(cur + kSlot, 0, C) : chunk_at(before + kSlot, 1, C - CH);
-      });
+      each<0, CH>([&](auto c) { raw[decltype(c)::value] = chunk_at(cur + kSlot, 0, decltype(c)::value); });
       Frag f[2];  // widened chunk halves: the one in use and the next
       {
         Frag hi;
         widen_keys(raw[0], scale_value(k_byte(i1)), f[0], hi);
       }
-      // Scores of block j + 1 (keys at at_k), probabilities of j, output of j - 1
+      // Scores of block j + 1 (keys in raw), probabilities of j, output of j - 1
       // (values at at_v; at first p is 0, and what is at at_v is block 1, which every
       // row sees whole); at_k2: keys of j + 2.
-      auto body = [&](auto first_of_step, int at_k, int at_v, int at_k2, int at_v2, int info_s, int info_k, int info_k2, int info_v) {
+      auto body = [&](auto first_of_step, int at_v, int at_k2, int info_s, int info_k, int info_k2, int info_v) {
         if (__builtin_expect(!has_page(info_s), 0)) {
           each<0, RG>([&](auto G) {
             constexpr int g = decltype(G)::value;
@@ -563,17 +559,16 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
               }
             }
             __builtin_amdgcn_sched_barrier(0);  // widened early in the beat: the next instruction may need it
-            if constexpr (g == 0 && F % 2 == 1) {
-              constexpr int C = (F + 2 * kEarly - 1) / 2;
-              if constexpr (C < CH)
-                raw[C] = chunk_at(at_k, 0, C);
-              else if constexpr (C < 2 * CH)
-                raw[C] = chunk_at(at_v, 1, C - CH);
-              else if constexpr (C < 3 * CH)
-                raw[C - 2 * CH] = chunk_at(at_k2, 0, C - 2 * CH);
+            // The values of j - 1 are read in the first half, the keys of j + 2 in the
+            // second, and each half ends with one wait for all of them.
+            if constexpr (h % (2 * RG) == 0) {
+              constexpr int c = h / (2 * RG);
+              if constexpr (c < CH)
+                raw[CH + c] = chunk_at(at_v, 1, c);
               else
-                raw[C - 2 * CH] = chunk_at(at_v2, 1, C - 3 * CH);
+                raw[c - CH] = chunk_at(at_k2, 0, c - CH);
             }
+            if constexpr (h + 1 == (2 * CH - 1) * RG || h + 1 == (4 * CH - 1) * RG) __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
             if constexpr (F >= 2 * CH + 1) {  // maxima of s1: 8 a row group, over the beats left
               constexpr int kFirst = (2 * CH + 1) * RG, kLeft = kBeats - kFirst;
               constexpr int m = h - kFirst;
@@ -621,8 +616,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
         here.cover<D>(a, at.s, at.h, j + 2, last);  // behind `last`: no page, zeros
         i2 = here.info_of(j + 2), i3 = here.info_of(j + 3);
         find_step(t + kAhead);
-        body(Const<1>{}, cur + kSlot, before + kSlot, next, cur, i0, i1, i2, i_before);
-        body(Const<0>{}, next, cur, next + kSlot, cur + kSlot, i1, i2, i3, i0);
+        body(Const<1>{}, before + kSlot, next, i0, i1, i2, i_before);
+        body(Const<0>{}, cur, next + kSlot, i1, i2, i3, i0);
         i_before = i1, i0 = i2, i1 = i3;
         before = cur, cur = next;
         next = next + kStep >= kRing * kStep ? next + kStep - kRing * kStep : next + kStep;
