@@ -2,12 +2,20 @@
 // (include/dllm_cache.h): selection of the kept tokens and their move.
 #include "cache_common.h"
 
+#include <utility>
+
 namespace dllm {
 namespace {
 
-constexpr int kSelectThreads = 1024;
+constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kEach = 8;                     // keys of a lane
+constexpr int kChunk = kThreads * kEach;     // keys of a workgroup
 constexpr int kMoveThreads = 256;
+constexpr int kReach = 31;                   // pool / 2 at most
+constexpr int kBins = 2048;                  // the first digit of a long selection: 11 bits
 
+// What selection works on.  Long sequences are cut into chunks of kChunk
+// tokens; a row is one sequence and head.
 struct SelectArgs {
   const int32_t* lens;
   int max_len;
@@ -20,7 +28,35 @@ struct SelectArgs {
   int32_t* kept;
   float* weights_out;
   int64_t out_slots;
+  // workspace of long selections
+  int chunks;
+  uint32_t* keys;        // [rows, chunks, kChunk]
+  uint32_t* candidates;  // [rows, chunks, kChunk] keys whose first digit is the threshold's
+  uint32_t* hist;        // [rows, chunks, kBins]
+  int32_t* above;        // [rows, chunks] keys of a larger first digit
+  int32_t* n_cand;       // [rows, chunks]
+  int32_t* place;        // [rows, chunks] kept tokens before the chunk's
+  int32_t* ties;         // [rows, chunks] tokens at the threshold before the chunk's
+  uint32_t* threshold;   // [rows, 2] key, how many equal to it are kept
 };
+
+// One row's counts: n kept, `first` and `last` of them unconditionally, m by
+// weight out of tokens [lo, hi).
+struct Row {
+  int len, n, first, last, m, lo, hi;
+};
+
+__device__ __forceinline__ Row row_of(const SelectArgs& a, int s) {
+  Row r;
+  r.len = min(max(a.lens[s], 0), a.max_len);
+  r.n = min(min(max(a.keep[s], 0), a.max_keep), r.len);
+  r.first = min(a.sink, r.n);
+  r.last = min(a.recent, r.n - r.first);
+  r.m = r.n - r.first - r.last;
+  r.lo = r.first;
+  r.hi = r.len - r.last;
+  return r;
+}
 
 // Order-preserving bits of a weight: a > b as floats iff key(a) > key(b);
 // -0 and 0 are equal, NaN is the lowest.
@@ -30,91 +66,326 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ uint32_t pooled_key(const float* __restrict__ w, int j, int len, int reach) {
-  uint32_t key = 0;
-  for (int i = max(j - reach, 0); i <= min(j + reach, len - 1); ++i) key = max(key, order_key(w[i]));
-  return key;
+// A lane's keys: token base + 64 i + lane of its wave's 64 kEach, so that a
+// wave's tokens are in order and a workgroup's waves too.
+__device__ __forceinline__ int token_at(int chunk, int i) {
+  return chunk * kChunk + (threadIdx.x >> 6) * 64 * kEach + i * 64 + (threadIdx.x & 63);
 }
 
-// One workgroup: the kept tokens of one sequence and head.  Four 8-bit radix
-// passes find the m-th largest pooled key and how many equal to it are taken;
-// a last pass writes the kept tokens in order.
-__global__ __launch_bounds__(kSelectThreads) void k_select(SelectArgs a) {
-  const int s = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int len = min(max(a.lens[s], 0), a.max_len);
-  const int n = min(min(max(a.keep[s], 0), a.max_keep), len);
-  const int first = min(a.sink, n), last = min(a.recent, n - first), m = n - first - last;
-  const int lo = first, hi = len - last;  // the tokens between
-  const float* w = a.weights + ((int64_t)s * a.kv_heads + h) * a.slots;
-  const int reach = a.pool / 2;
-  if (h == 0 && tid == 0) a.lens_out[s] = n;
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t prefix_s, want_s;
-  __shared__ int gt[kSelectThreads / 64], eq[kSelectThreads / 64];
-  uint32_t prefix = 0, mask = 0, want = (uint32_t)m;
-  if (m > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSelectThreads) hist[i] = 0;
-      __syncthreads();
-      for (int j = lo + tid; j < hi; j += kSelectThreads) {
-        const uint32_t key = pooled_key(w, j, len, reach);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1u);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        uint32_t left = want;
-        int d = 255;
-        for (; d > 0 && hist[d] < left; --d) left -= hist[d];
-        prefix_s = prefix | (uint32_t)d << shift;
-        want_s = left;
-      }
-      __syncthreads();
-      prefix = prefix_s;
-      want = want_s;
-      mask |= 255u << shift;
-    }
+// The pooled keys of a chunk, one load of each weight (and of its neighbours
+// at the chunk's ends); 0, below every key, outside [lo, hi).
+__device__ __forceinline__ void pooled_keys(const SelectArgs& a, const Row& r, const float* w, int chunk, uint32_t* lds,
+                                            uint32_t* key) {
+  const int reach = a.pool / 2, begin = chunk * kChunk - reach;
+  for (int i = threadIdx.x; i < kChunk + 2 * reach; i += kThreads) {
+    const int j = begin + i;
+    lds[i] = j >= 0 && j < r.len ? order_key(w[j]) : 0;
   }
-  // wave w takes a contiguous run of the tokens between, so that its places
-  // follow from the counts of the waves before it
-  const int waves = kSelectThreads / 64;
-  const int run = ((hi - lo + waves - 1) / waves + 63) / 64 * 64;
-  const int b0 = lo + wave * run, b1 = min(b0 + run, hi);
-  int n_gt = 0, n_eq = 0;
-  if (m > 0)
-    for (int j0 = b0; j0 < b1; j0 += 64) {
-      const int j = j0 + lane;
-      const uint32_t key = j < b1 ? pooled_key(w, j, len, reach) : 0;
-      n_gt += __popcll(__ballot(j < b1 && key > prefix));
-      n_eq += __popcll(__ballot(j < b1 && key == prefix));
-    }
-  if (lane == 0) gt[wave] = n_gt, eq[wave] = n_eq;
   __syncthreads();
-  int32_t* kept = a.kept + ((int64_t)s * a.kv_heads + h) * a.max_keep;
-  float* wo = a.weights_out ? a.weights_out + ((int64_t)s * a.kv_heads + h) * a.out_slots : nullptr;
-  auto put = [&](int place, int j) {
-    kept[place] = j;
-    if (wo) wo[place] = w[j];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int j = token_at(chunk, i), at = j - chunk * kChunk;
+    uint32_t k = 0;
+    if (j >= r.lo && j < r.hi)
+      for (int d = 0; d <= 2 * reach; ++d) k = max(k, lds[at + d]);
+    key[i] = k;
+  }
+}
+
+__device__ __forceinline__ int wave_count(bool x) { return __popcll(__ballot(x)); }
+
+// Sum over the workgroup of a value that is the same in a wave's lanes.
+// slots: kWaves ints that no wave still reads from the call before last.
+__device__ __forceinline__ int block_sum(int x, int* slots) {
+  if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = x;
+  __syncthreads();
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) sum += slots[i];
+  return sum;
+}
+
+// The want-th largest (want >= 1) of the keys that `count` counts: count(t) is
+// the number of keys >= t in the workgroup, the same in all its threads.  The
+// bits of lo ^ hi (lo <= every key <= hi) are found from the top.
+template <class Count>
+__device__ __forceinline__ uint32_t nth_largest(uint32_t lo, uint32_t hi, int want, Count count) {
+  if (lo == hi) return lo;
+  const int top = 31 - __clz(lo ^ hi);
+  uint32_t t = top == 31 ? 0 : lo >> (top + 1) << (top + 1);
+  for (int b = top; b >= 0; --b) {
+    const uint32_t trial = t | 1u << b;
+    if (count(trial) >= want) t = trial;
+  }
+  return t;
+}
+
+__device__ __forceinline__ void put(const SelectArgs& a, int64_t row, const float* w, int place, int j) {
+  a.kept[row * a.max_keep + place] = j;
+  if (a.weights_out) a.weights_out[row * a.out_slots + place] = w[j];
+}
+
+// The tokens kept unconditionally.
+__device__ __forceinline__ void put_ends(const SelectArgs& a, const Row& r, int64_t row, const float* w) {
+  for (int j = threadIdx.x; j < r.first; j += kThreads) put(a, row, w, j, j);
+  for (int j = threadIdx.x; j < r.last; j += kThreads) put(a, row, w, r.n - r.last + j, r.len - r.last + j);
+}
+
+// The chunk's kept tokens in order: those above the threshold, and of those at
+// it the first `want` of the row; `place` and `ties` are the counts before the chunk.
+__device__ __forceinline__ void put_chunk(const SelectArgs& a, int64_t row, const float* w, int chunk,
+                                          const uint32_t* key, uint32_t threshold, int want, int place, int ties,
+                                          int* slots) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint64_t below = (1ull << lane) - 1;
+  int n_gt = 0, n_eq = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    n_gt += wave_count(key[i] > threshold);
+    n_eq += wave_count(key[i] == threshold);
+  }
+  __syncthreads();
+  if (lane == 0) slots[wave] = n_gt, slots[kWaves + wave] = n_eq;
+  __syncthreads();
+  for (int i = 0; i < wave; ++i) {
+    place += slots[i] + min(slots[kWaves + i], max(want - ties, 0));
+    ties += slots[kWaves + i];
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const bool same = key[i] == threshold;
+    const uint64_t sames = __ballot(same);
+    const bool take = key[i] > threshold || (same && ties + __popcll(sames & below) < want);
+    const uint64_t takes = __ballot(take);
+    if (take) put(a, row, w, place + __popcll(takes & below), token_at(chunk, i));
+    place += __popcll(takes);
+    ties += __popcll(sames);
+  }
+}
+
+__device__ __forceinline__ uint32_t wave_extreme(uint32_t x, bool largest) {
+  for (int o = 32; o; o >>= 1) {
+    const uint32_t y = __shfl_xor(x, o);
+    x = largest ? max(x, y) : min(x, y);
+  }
+  return x;
+}
+
+// One workgroup: one row of at most kChunk tokens.  The keys stay in
+// registers; the threshold is found bit by bit with counts by ballot, which
+// unlike a histogram cost the same however the weights are spread.
+__global__ __launch_bounds__(kThreads) void k_select_one(SelectArgs a) {
+  __shared__ uint32_t lds[kChunk + 2 * kReach];
+  __shared__ int slots[4][kWaves];
+  const int s = blockIdx.y, h = blockIdx.x;
+  const Row r = row_of(a, s);
+  const int64_t row = (int64_t)s * a.kv_heads + h;
+  const float* w = a.weights + row * a.slots;
+  if (h == 0 && threadIdx.x == 0) a.lens_out[s] = r.n;
+  put_ends(a, r, row, w);
+  if (r.m == 0) return;
+  uint32_t key[kEach];
+  pooled_keys(a, r, w, 0, lds, key);
+  uint32_t lo = ~0u, hi = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (key[i] != 0) lo = min(lo, key[i]), hi = max(hi, key[i]);
+  lo = wave_extreme(lo, false), hi = wave_extreme(hi, true);
+  if ((threadIdx.x & 63) == 0) slots[0][threadIdx.x >> 6] = (int)lo, slots[1][threadIdx.x >> 6] = (int)hi;
+  __syncthreads();
+  for (int i = 0; i < kWaves; ++i) lo = min(lo, (uint32_t)slots[0][i]), hi = max(hi, (uint32_t)slots[1][i]);
+  int turn = 0;
+  auto count = [&](uint32_t t) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) n += wave_count(key[i] >= t);
+    turn ^= 1;
+    return block_sum(n, slots[2 + turn]);
   };
-  for (int j = tid; j < first; j += kSelectThreads) put(j, j);
-  for (int j = tid; j < last; j += kSelectThreads) put(n - last + j, len - last + j);
-  if (m > 0) {
-    int eq_before = 0, place = first;
-    for (int i = 0; i < wave; ++i) {
-      place += gt[i] + min(eq[i], max((int)want - eq_before, 0));
-      eq_before += eq[i];
+  const uint32_t t = nth_largest(lo, hi, r.m, count);
+  const int above = t == ~0u ? 0 : count(t + 1);
+  put_chunk(a, row, w, 0, key, t, r.m - above, r.first, 0, &slots[0][0]);
+}
+
+// ---- long rows, in four kernels -------------------------------------------------------------------------------
+
+// Keys of a chunk and the counts of their first 11 bits.
+__global__ __launch_bounds__(kThreads) void k_keys(SelectArgs a) {
+  __shared__ uint32_t lds[kChunk + 2 * kReach];
+  __shared__ uint32_t hist[kBins];
+  const int s = blockIdx.z, h = blockIdx.y, chunk = blockIdx.x;
+  const Row r = row_of(a, s);
+  const int64_t row = (int64_t)s * a.kv_heads + h, at = row * a.chunks + chunk;
+  const float* w = a.weights + row * a.slots;
+  if (chunk == 0) {
+    put_ends(a, r, row, w);
+    if (h == 0 && threadIdx.x == 0) a.lens_out[s] = r.n;
+  }
+  if (r.m == 0 || (int64_t)chunk * kChunk >= r.len) return;
+  for (int i = threadIdx.x; i < kBins; i += kThreads) hist[i] = 0;
+  uint32_t key[kEach];
+  pooled_keys(a, r, w, chunk, lds, key);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    a.keys[at * kChunk + token_at(0, i)] = key[i];
+    if (key[i] != 0) atomicAdd(&hist[key[i] >> 21], 1u);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kThreads) a.hist[at * kBins + i] = hist[i];
+}
+
+// The threshold's first digit, and the chunk's keys of that digit.
+__global__ __launch_bounds__(kThreads) void k_split(SelectArgs a) {
+  __shared__ int slots[kWaves], digit_s, cands;
+  const int s = blockIdx.z, h = blockIdx.y, chunk = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const Row r = row_of(a, s);
+  if (r.m == 0 || (int64_t)chunk * kChunk >= r.len) return;
+  const int64_t row = (int64_t)s * a.kv_heads + h, at = row * a.chunks + chunk;
+  const int chunks = (r.len + kChunk - 1) / kChunk;
+  // thread t has bins kBins - 1 - 2 t and the one below: larger digits first
+  static_assert(kBins == 2 * kThreads, "two bins a thread");
+  const int bin = kBins - 1 - 2 * (int)threadIdx.x;
+  int n1 = 0, n0 = 0;
+  for (int c = 0; c < chunks; ++c) {
+    const uint2 x = *reinterpret_cast<const uint2*>(a.hist + (row * a.chunks + c) * kBins + bin - 1);
+    n0 += (int)x.x, n1 += (int)x.y;
+  }
+  int upto = n0 + n1;  // keys of this thread's bins and larger ones
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 63) slots[wave] = upto;
+  if (threadIdx.x == 0) cands = 0;
+  __syncthreads();
+  for (int i = 0; i < wave; ++i) upto += slots[i];
+  const int before = upto - n0 - n1;
+  if (before < r.m && r.m <= upto) digit_s = r.m <= before + n1 ? bin : bin - 1;
+  __syncthreads();
+  const uint32_t digit = (uint32_t)digit_s;
+  int n_above = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const uint32_t key = a.keys[at * kChunk + token_at(0, i)];
+    const bool is = key >> 21 == digit && key != 0;
+    n_above += wave_count(key >> 21 > digit);
+    const uint64_t all = __ballot(is);
+    int to = 0;
+    if (lane == 0 && all) to = atomicAdd(&cands, __popcll(all));  // their order does not matter
+    to = __builtin_amdgcn_readfirstlane(to);
+    if (is) a.candidates[at * kChunk + to + __popcll(all & ((1ull << lane) - 1))] = key;
+  }
+  __syncthreads();
+  if (lane == 0) slots[wave] = n_above;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int n = 0;
+    for (int i = 0; i < kWaves; ++i) n += slots[i];
+    a.above[at] = n;
+    a.n_cand[at] = cands;
+  }
+}
+
+// The threshold among the candidates of a row, and what each chunk has before
+// it.  One workgroup for a row; a wave takes a chunk at a time.
+__global__ __launch_bounds__(kThreads) void k_threshold(SelectArgs a) {
+  __shared__ int slots[4][kWaves];
+  const int s = blockIdx.y, h = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const Row r = row_of(a, s);
+  if (r.m == 0) return;
+  const int64_t row = (int64_t)s * a.kv_heads + h;
+  const int chunks = (r.len + kChunk - 1) / kChunk;
+  const uint32_t* cand = a.candidates + row * a.chunks * kChunk;
+  const int32_t* n_cand = a.n_cand + row * a.chunks;
+  // this wave's candidates, kMine of them in registers and the rest read again for every count
+  constexpr int kMine = 32;
+  uint32_t mine[kMine];
+  uint32_t lo = ~0u, hi = 0;
+  int above = 0, have = 0;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) mine[i] = 0;
+  auto walk = [&](auto f) {  // f(key or 0, number of the 64 in this wave's walk)
+    int k = 0;
+    for (int c = wave; c < chunks; c += kWaves) {
+      const int n = n_cand[c];
+      for (int i = 0; i < n; i += 64, ++k) f(i + lane < n ? cand[(int64_t)c * kChunk + i + lane] : 0u, k);
     }
-    for (int j0 = b0; j0 < b1; j0 += 64) {
-      const int j = j0 + lane;
-      const uint32_t key = j < b1 ? pooled_key(w, j, len, reach) : 0;
-      const bool same = j < b1 && key == prefix;
-      const uint64_t below = (1ull << lane) - 1, sames = __ballot(same);
-      const bool take = (j < b1 && key > prefix) || (same && eq_before + __popcll(sames & below) < (int)want);
-      const uint64_t takes = __ballot(take);
-      if (take) put(place + __popcll(takes & below), j);
-      place += __popcll(takes);
-      eq_before += __popcll(sames);
+    return k;
+  };
+  for (int c = wave; c < chunks; c += kWaves) above += a.above[row * a.chunks + c];
+  have = walk([&](uint32_t key, int k) {
+    if (key != 0) lo = min(lo, key), hi = max(hi, key);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) mine[i] = i == k ? key : mine[i];
+  });
+  lo = wave_extreme(lo, false), hi = wave_extreme(hi, true);
+  if (lane == 0) slots[0][wave] = (int)lo, slots[1][wave] = (int)hi, slots[2][wave] = above;
+  __syncthreads();
+  above = 0;
+  for (int i = 0; i < kWaves; ++i) {
+    lo = min(lo, (uint32_t)slots[0][i]), hi = max(hi, (uint32_t)slots[1][i]);
+    above += slots[2][i];
+  }
+  __syncthreads();
+  int turn = 0;
+  auto count = [&](uint32_t t) {
+    int n = 0;
+    if (have <= kMine) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) n += wave_count(mine[i] >= t);
+    } else {
+      walk([&](uint32_t key, int) { n += wave_count(key >= t); });
+    }
+    turn ^= 1;
+    return block_sum(n, slots[2 + turn]);
+  };
+  const uint32_t t = nth_largest(lo, hi, r.m - above, count);
+  const int want = r.m - above - (t == ~0u ? 0 : count(t + 1));
+  if (threadIdx.x == 0) a.threshold[2 * row] = t, a.threshold[2 * row + 1] = (uint32_t)want;
+  // per chunk: keys above and at the threshold, then their sums before it
+  for (int c = wave; c < chunks; c += kWaves) {
+    int gt = 0, eq = 0;
+    for (int i = 0; i < n_cand[c]; i += 64) {
+      const uint32_t key = i + lane < n_cand[c] ? cand[(int64_t)c * kChunk + i + lane] : 0u;
+      gt += wave_count(key > t), eq += wave_count(key == t);
+    }
+    if (lane == 0) a.place[row * a.chunks + c] = a.above[row * a.chunks + c] + gt, a.ties[row * a.chunks + c] = eq;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    int place = r.first, ties = 0;
+    for (int c0 = 0; c0 < chunks; c0 += 64) {
+      const int c = c0 + lane;
+      const int gt = c < chunks ? a.place[row * a.chunks + c] : 0, eq = c < chunks ? a.ties[row * a.chunks + c] : 0;
+      int ties_to = eq;
+      for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(ties_to, o);
+        if (lane >= o) ties_to += y;
+      }
+      const int mine_ties = ties + ties_to - eq, taken = gt + min(eq, max(want - mine_ties, 0));
+      int place_to = taken;
+      for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(place_to, o);
+        if (lane >= o) place_to += y;
+      }
+      if (c < chunks) a.place[row * a.chunks + c] = place + place_to - taken, a.ties[row * a.chunks + c] = mine_ties;
+      ties += __shfl(ties_to, 63);
+      place += __shfl(place_to, 63);
     }
   }
+}
+
+__global__ __launch_bounds__(kThreads) void k_keep(SelectArgs a) {
+  __shared__ int slots[2 * kWaves];
+  const int s = blockIdx.z, h = blockIdx.y, chunk = blockIdx.x;
+  const Row r = row_of(a, s);
+  if (r.m == 0 || (int64_t)chunk * kChunk >= r.len) return;
+  const int64_t row = (int64_t)s * a.kv_heads + h, at = row * a.chunks + chunk;
+  uint32_t key[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) key[i] = a.keys[at * kChunk + token_at(0, i)];
+  put_chunk(a, row, a.weights + row * a.slots, chunk, key, a.threshold[2 * row], (int)a.threshold[2 * row + 1], a.place[at],
+            a.ties[at], slots);
 }
 
 struct MoveArgs {
@@ -193,6 +464,8 @@ __global__ __launch_bounds__(kMoveThreads) void k_move(MoveArgs a) {
   }
 }
 
+size_t chunks_of(int max_len) { return ((size_t)max_len + kChunk - 1) / kChunk; }
+
 }  // namespace
 }  // namespace dllm
 
@@ -201,7 +474,9 @@ extern "C" {
 size_t dllm_cache_evict_workspace_bytes(const dllm_cache* cache, const dllm_cache_batch* batch) {
   using namespace dllm;
   if (!cache_ok(cache) || !cache_supported(cache) || !batch_ok(batch)) return 0;
-  return 256;
+  const size_t rows = (size_t)batch->S * cache->kv_heads, chunks = dllm::chunks_of(batch->max_len);
+  if (chunks == 1) return 256;
+  return rows * chunks * (2 * kChunk + kBins + 4) * sizeof(uint32_t) + rows * 2 * sizeof(uint32_t);
 }
 
 dllm_status dllm_cache_evict(const dllm_cache* cache, const dllm_cache_batch* batch, const float* weights,
@@ -220,9 +495,29 @@ dllm_status dllm_cache_evict(const dllm_cache* cache, const dllm_cache_batch* ba
   const size_t need = dllm_cache_evict_workspace_bytes(cache, batch);
   if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 255u) != 0) return DLLM_ERR_WORKSPACE;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  const SelectArgs sa = {batch->lens, batch->max_len, cache->kv_heads, weights, (int64_t)batch->table_blocks * kBlock,
-                         keep, max_keep, sink, recent, pool, lens_out, kept, weights_out, (int64_t)out_blocks * kBlock};
-  hipLaunchKernelGGL(k_select, dim3(cache->kv_heads, batch->S), dim3(kSelectThreads), 0, st, sa);
+  SelectArgs sa = {batch->lens, batch->max_len, cache->kv_heads, weights, (int64_t)batch->table_blocks * kBlock, keep,
+                   max_keep, sink, recent, pool, lens_out, kept, weights_out, (int64_t)out_blocks * kBlock};
+  const size_t rows = (size_t)batch->S * cache->kv_heads, chunks = chunks_of(batch->max_len);
+  if (chunks == 1) {
+    hipLaunchKernelGGL(k_select_one, dim3(cache->kv_heads, batch->S), dim3(kThreads), 0, st, sa);
+  } else {
+    uint32_t* p = static_cast<uint32_t*>(workspace);
+    auto take = [&](size_t n) { return std::exchange(p, p + n); };
+    sa.chunks = (int)chunks;
+    sa.keys = take(rows * chunks * kChunk);
+    sa.candidates = take(rows * chunks * kChunk);
+    sa.hist = take(rows * chunks * kBins);
+    sa.above = reinterpret_cast<int32_t*>(take(rows * chunks));
+    sa.n_cand = reinterpret_cast<int32_t*>(take(rows * chunks));
+    sa.place = reinterpret_cast<int32_t*>(take(rows * chunks));
+    sa.ties = reinterpret_cast<int32_t*>(take(rows * chunks));
+    sa.threshold = take(rows * 2);
+    const dim3 grid((unsigned)chunks, cache->kv_heads, batch->S), per_row(cache->kv_heads, batch->S);
+    hipLaunchKernelGGL(k_keys, grid, dim3(kThreads), 0, st, sa);
+    hipLaunchKernelGGL(k_split, grid, dim3(kThreads), 0, st, sa);
+    hipLaunchKernelGGL(k_threshold, per_row, dim3(kThreads), 0, st, sa);
+    hipLaunchKernelGGL(k_keep, grid, dim3(kThreads), 0, st, sa);
+  }
   if (hipGetLastError() != hipSuccess) return DLLM_ERR_HIP;
   const MoveArgs ma = {*cache, batch->table, batch->table_blocks, table_out, out_blocks, lens_out, kept, max_keep};
   const int most = max_keep < batch->max_len ? max_keep : batch->max_len;

@@ -451,6 +451,25 @@ def test_evict_ties_and_special_weights(kind):
     _evict(rng, [128, 77], [51, 40], 3, 5, 3, w=w)
 
 
+@pytest.mark.parametrize("kind", ["spread", "equal", "few values", "specials"])
+def test_evict_long_rows(kind):
+    """Rows of several selection chunks, ending on, before and behind a chunk's
+    end, one of them short; ties across chunks."""
+    rng = np.random.default_rng(44)
+    lens, keep = [20001, 8192, 8193, 100, 0], [5003, 8000, 1, 99, 4]
+    w = rng.random((5, 1, 626 * 32 + 32)).astype(np.float32)
+    if kind == "equal":
+        w[:] = 0.5
+    if kind == "few values":
+        w = rng.integers(0, 4, w.shape).astype(np.float32)
+    if kind == "specials":
+        w = rng.standard_normal(w.shape).astype(np.float32) * np.exp(20 * rng.standard_normal(w.shape)).astype(np.float32)
+        w[:, :, 3::11], w[:, :, 4::13], w[:, :, 5::17] = np.nan, np.inf, -np.inf
+    print(f"[case] evict long rows {kind}", flush=True)
+    _evict(rng, lens, keep, 4, 32, 3, heads=1, w=w)
+    _evict(rng, lens, keep, 0, 0, 63, heads=1, w=w)
+
+
 def test_evict_bad_pages_and_cut_keep():
     _evict(np.random.default_rng(42), [100, 90], [64, 60], 4, 0, 1, bad=True)
     _evict(np.random.default_rng(43), [100, 90], [64, 60], 4, 0, 1, max_keep=37)
