@@ -405,6 +405,9 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t b, float down) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x, x, 0, false) & 0xffu;
 }
 
+// 2^x, 0 below fp32's normal range (where e4m3 has long rounded to 0).
+__device__ __forceinline__ float exact_scale(int x) { return x < -126 ? 0.0f : __uint_as_float((uint32_t)(x + 127) << 23); }
+
 // One workgroup: one new block of one head, gathered from its tokens' old
 // places.
 template <int D>
@@ -414,10 +417,10 @@ __global__ __launch_bounds__(kMoveThreads) void k_move(MoveArgs a) {
   if (blk * kBlock >= n) return;
   const int to = page_of(a.table_out, a.out_blocks, a.c.pages, s, blk);
   if (to < 0) return;
-  __shared__ int64_t src[kBlock];  // the token's old block, -1: none
+  __shared__ int64_t src[kBlock];  // byte offset of the token's old block, -1: none
   __shared__ int slot[kBlock];
   __shared__ int ke[kBlock], ve[kBlock];
-  __shared__ int kmax, vmax;
+  __shared__ int kmax, vmax, kmixed, vmixed;  // largest scale bytes, and whether a token has another
   if (tid < kBlock) {
     const int t = blk * kBlock + tid;
     int64_t at = -1;
@@ -429,38 +432,57 @@ __global__ __launch_bounds__(kMoveThreads) void k_move(MoveArgs a) {
     } else {
       slot[tid] = 0;
     }
-    src[tid] = at;
+    src[tid] = at < 0 ? -1 : at * (kBlock * D);
     int k = at >= 0 ? a.c.k_scale[at] : 0, v = at >= 0 ? a.c.v_scale[at] : 0;
+    const int k_own = k, v_own = v;
     ke[tid] = k, ve[tid] = v;
     for (int o = 16; o; o >>= 1) {
       k = max(k, __shfl_xor(k, o));
       v = max(v, __shfl_xor(v, o));
     }
-    if (tid == 0) kmax = max(k, DLLM_CACHE_SCALE_MIN), vmax = max(v, DLLM_CACHE_SCALE_MIN);
+    k = max(k, DLLM_CACHE_SCALE_MIN), v = max(v, DLLM_CACHE_SCALE_MIN);
+    const bool km = __any(at >= 0 && k_own != k), vm = __any(at >= 0 && v_own != v);
+    if (tid == 0) kmax = k, vmax = v, kmixed = km, vmixed = vm;
   }
   __syncthreads();
-  const int64_t dst = block_of(a.c, to, h);
-  for (int side = 0; side < 2; ++side) {
-    const uint8_t* from = side ? a.c.v : a.c.k;
-    uint8_t* out = (side ? a.c.v : a.c.k) + dst * (kBlock * D);
-    const int top = side ? vmax : kmax;
-    for (int u = tid * 4; u < kBlock * D; u += kMoveThreads * 4) {
-      uint32_t word = 0;
+  const int64_t dst = block_of(a.c, to, h) * (kBlock * D);
+  // Pieces of 16 bytes.  Of keys a piece is 16 dims of one token; of values it is
+  // one dim of 16 tokens, 16 loads of a byte that are all in flight at once.
+  for (int u = tid; u < kBlock * D / 16; u += kMoveThreads) {
+    const int hh = (u >> 5) & 1, r = u & 31;
+    i32x4 k = {0, 0, 0, 0};
+    if (src[r] >= 0) k = *reinterpret_cast<const i32x4*>(a.c.k + src[r] + ((u & ~31) + slot[r]) * 16);
+    uint32_t b[16];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int p = u + j, hh = (p >> 9) & 1, r = (p >> 4) & 31, e = p & 15;
-        const int t = side ? 8 * (e >> 2) + 4 * hh + (e & 3) : r;
-        if (src[t] < 0) continue;
-        const int o = slot[t];
-        const int q = side ? (p & ~0x20f) | ((o >> 2) & 1) << 9 | (o >> 3) << 2 | (o & 3) : (p & ~0x1f0) | o << 4;
-        uint32_t b = from[src[t] * (kBlock * D) + q];
-        const int down = (side ? ve[t] : ke[t]) - top;
-        if (down) b = rescaled(b, down < -126 ? 0.0f : __uint_as_float((uint32_t)(down + 127) << 23));
-        word |= b << (8 * j);
-      }
-      *reinterpret_cast<uint32_t*>(out + u) = word;
+    for (int e = 0; e < 16; ++e) {
+      const int t = 8 * (e >> 2) + 4 * hh + (e & 3), o = slot[t];
+      b[e] = src[t] < 0 ? 0 : a.c.v[src[t] + ((u & ~0x20) | ((o >> 2) & 1) << 5) * 16 + ((o >> 3) << 2 | (o & 3))];
     }
-    if (tid == 0) (side ? a.c.v_scale : a.c.k_scale)[dst] = (uint8_t)top;
+    if (kmixed && ke[r] != kmax) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t x = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x |= rescaled((uint32_t)k[i] >> (8 * j) & 0xffu, exact_scale(ke[r] - kmax)) << (8 * j);
+        k[i] = (int)x;
+      }
+    }
+    if (vmixed) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int t = 8 * (e >> 2) + 4 * hh + (e & 3);
+        if (ve[t] != vmax) b[e] = rescaled(b[e], exact_scale(ve[t] - vmax));
+      }
+    }
+    i32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (int)(b[4 * i] | b[4 * i + 1] << 8 | b[4 * i + 2] << 16 | b[4 * i + 3] << 24);
+    *reinterpret_cast<i32x4*>(a.c.k + dst + u * 16) = k;
+    *reinterpret_cast<i32x4*>(a.c.v + dst + u * 16) = v;
+  }
+  if (tid == 0) {
+    a.c.k_scale[block_of(a.c, to, h)] = (uint8_t)kmax;
+    a.c.v_scale[block_of(a.c, to, h)] = (uint8_t)vmax;
   }
 }
 
