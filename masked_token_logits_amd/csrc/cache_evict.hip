@@ -77,9 +77,16 @@ __device__ __forceinline__ int token_at(int chunk, int i) {
 __device__ __forceinline__ void pooled_keys(const SelectArgs& a, const Row& r, const float* w, int chunk, uint32_t* lds,
                                             uint32_t* key) {
   const int reach = a.pool / 2, begin = chunk * kChunk - reach;
-  for (int i = threadIdx.x; i < kChunk + 2 * reach; i += kThreads) {
-    const int j = begin + i;
-    lds[i] = j >= 0 && j < r.len ? order_key(w[j]) : 0;
+  float x[kEach + 1];
+#pragma unroll
+  for (int i = 0; i <= kEach; ++i) {
+    const int at = i * kThreads + (int)threadIdx.x, j = begin + at;
+    x[i] = at < kChunk + 2 * reach && j >= 0 && j < r.len ? w[j] : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i <= kEach; ++i) {
+    const int at = i * kThreads + (int)threadIdx.x, j = begin + at;
+    if (at < kChunk + 2 * reach) lds[at] = j >= 0 && j < r.len ? order_key(x[i]) : 0;
   }
   __syncthreads();
 #pragma unroll
@@ -94,28 +101,69 @@ __device__ __forceinline__ void pooled_keys(const SelectArgs& a, const Row& r, c
 
 __device__ __forceinline__ int wave_count(bool x) { return __popcll(__ballot(x)); }
 
-// Sum over the workgroup of a value that is the same in a wave's lanes.
-// slots: kWaves ints that no wave still reads from the call before last.
-__device__ __forceinline__ int block_sum(int x, int* slots) {
-  if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = x;
+// LDS of a search for a threshold: counts of a digit, and what the thread
+// that finds the threshold's digit tells the others.
+struct Search {
+  uint32_t hist[kBins];
+  int slots[kWaves];
+  int digit, above;
+};
+
+// The digit of the want-th largest key, counted in hist (which ends cleared):
+// the thread t looks after bins kBins - 1 - 2 t and the one below it, so that
+// a scan over threads goes from large digits to small.  Returns the digit and the
+// number of keys of larger ones, the same in all threads.
+static_assert(kBins == 2 * kThreads, "two bins a thread");
+__device__ __forceinline__ int find_digit(Search& l, int want, int n1, int n0, int* above) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, bin = kBins - 1 - 2 * (int)threadIdx.x;
+  int upto = n0 + n1;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 63) l.slots[wave] = upto;
   __syncthreads();
-  int sum = 0;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) sum += slots[i];
-  return sum;
+  for (int i = 0; i < wave; ++i) upto += l.slots[i];
+  const int before = upto - n0 - n1;
+  if (before < want && want <= upto) {
+    const bool upper = want <= before + n1;
+    l.digit = upper ? bin : bin - 1;
+    l.above = upper ? before : before + n1;
+  }
+  __syncthreads();
+  *above = l.above;
+  return l.digit;
 }
 
-// The want-th largest (want >= 1) of the keys that `count` counts: count(t) is
-// the number of keys >= t in the workgroup, the same in all its threads.  The
-// bits of lo ^ hi (lo <= every key <= hi) are found from the top.
-template <class Count>
-__device__ __forceinline__ uint32_t nth_largest(uint32_t lo, uint32_t hi, int want, Count count) {
+// The want-th largest (want >= 1) of some keys, all of them in lo .. hi, and
+// the number of keys above it.  each(f) calls f(key, or 0 for none) for this
+// thread's keys.  The bits in which lo and hi differ are found 11 at a time by
+// counting digits in LDS; taking them from the first differing bit on spreads the
+// counts over the bins however narrow the weights' range is.
+template <class Each>
+__device__ __forceinline__ uint32_t nth_largest(Search& l, uint32_t lo, uint32_t hi, int want, Each each, int* above) {
+  *above = 0;
   if (lo == hi) return lo;
-  const int top = 31 - __clz(lo ^ hi);
+  int top = 31 - __clz(lo ^ hi);  // the bits above are known: t's
   uint32_t t = top == 31 ? 0 : lo >> (top + 1) << (top + 1);
-  for (int b = top; b >= 0; --b) {
-    const uint32_t trial = t | 1u << b;
-    if (count(trial) >= want) t = trial;
+  while (top >= 0) {
+    const int shift = max(top - 10, 0);
+    for (int i = threadIdx.x; i < kBins; i += kThreads) l.hist[i] = 0;
+    __syncthreads();
+    each([&](uint32_t key) {
+      const bool in = key != 0 && (top == 31 || key >> (top + 1) == t >> (top + 1));
+      if (in) atomicAdd(&l.hist[(key >> shift) & (kBins - 1)], 1u);
+    });
+    __syncthreads();
+    const int bin = kBins - 1 - 2 * (int)threadIdx.x;
+    int more;
+    const int digit = find_digit(l, want, (int)l.hist[bin], (int)l.hist[bin - 1], &more);
+    // with fewer than 11 bits left the digit holds known bits too
+    t |= ((uint32_t)digit & ((2u << (top - shift)) - 1u)) << shift;
+    want -= more;
+    *above += more;
+    top = shift - 1;
+    __syncthreads();
   }
   return t;
 }
@@ -171,12 +219,11 @@ __device__ __forceinline__ uint32_t wave_extreme(uint32_t x, bool largest) {
   return x;
 }
 
-// One workgroup: one row of at most kChunk tokens.  The keys stay in
-// registers; the threshold is found bit by bit with counts by ballot, which
-// unlike a histogram cost the same however the weights are spread.
+// One workgroup: one row of at most kChunk tokens, whose keys stay in registers.
 __global__ __launch_bounds__(kThreads) void k_select_one(SelectArgs a) {
   __shared__ uint32_t lds[kChunk + 2 * kReach];
-  __shared__ int slots[4][kWaves];
+  __shared__ int slots[2][kWaves];
+  __shared__ Search search;
   const int s = blockIdx.y, h = blockIdx.x;
   const Row r = row_of(a, s);
   const int64_t row = (int64_t)s * a.kv_heads + h;
@@ -194,16 +241,12 @@ __global__ __launch_bounds__(kThreads) void k_select_one(SelectArgs a) {
   if ((threadIdx.x & 63) == 0) slots[0][threadIdx.x >> 6] = (int)lo, slots[1][threadIdx.x >> 6] = (int)hi;
   __syncthreads();
   for (int i = 0; i < kWaves; ++i) lo = min(lo, (uint32_t)slots[0][i]), hi = max(hi, (uint32_t)slots[1][i]);
-  int turn = 0;
-  auto count = [&](uint32_t t) {
-    int n = 0;
+  int above;
+  auto each = [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) n += wave_count(key[i] >= t);
-    turn ^= 1;
-    return block_sum(n, slots[2 + turn]);
+    for (int i = 0; i < kEach; ++i) f(key[i]);
   };
-  const uint32_t t = nth_largest(lo, hi, r.m, count);
-  const int above = t == ~0u ? 0 : count(t + 1);
+  const uint32_t t = nth_largest(search, lo, hi, r.m, each, &above);
   put_chunk(a, row, w, 0, key, t, r.m - above, r.first, 0, &slots[0][0]);
 }
 
@@ -236,33 +279,21 @@ __global__ __launch_bounds__(kThreads) void k_keys(SelectArgs a) {
 
 // The threshold's first digit, and the chunk's keys of that digit.
 __global__ __launch_bounds__(kThreads) void k_split(SelectArgs a) {
-  __shared__ int slots[kWaves], digit_s, cands;
+  __shared__ Search search;
+  __shared__ int slots[kWaves], cands;
   const int s = blockIdx.z, h = blockIdx.y, chunk = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const Row r = row_of(a, s);
   if (r.m == 0 || (int64_t)chunk * kChunk >= r.len) return;
   const int64_t row = (int64_t)s * a.kv_heads + h, at = row * a.chunks + chunk;
   const int chunks = (r.len + kChunk - 1) / kChunk;
-  // thread t has bins kBins - 1 - 2 t and the one below: larger digits first
-  static_assert(kBins == 2 * kThreads, "two bins a thread");
   const int bin = kBins - 1 - 2 * (int)threadIdx.x;
-  int n1 = 0, n0 = 0;
+  int n1 = 0, n0 = 0, larger;
   for (int c = 0; c < chunks; ++c) {
     const uint2 x = *reinterpret_cast<const uint2*>(a.hist + (row * a.chunks + c) * kBins + bin - 1);
     n0 += (int)x.x, n1 += (int)x.y;
   }
-  int upto = n0 + n1;  // keys of this thread's bins and larger ones
-  for (int o = 1; o < 64; o <<= 1) {
-    const int y = __shfl_up(upto, o);
-    if (lane >= o) upto += y;
-  }
-  if (lane == 63) slots[wave] = upto;
   if (threadIdx.x == 0) cands = 0;
-  __syncthreads();
-  for (int i = 0; i < wave; ++i) upto += slots[i];
-  const int before = upto - n0 - n1;
-  if (before < r.m && r.m <= upto) digit_s = r.m <= before + n1 ? bin : bin - 1;
-  __syncthreads();
-  const uint32_t digit = (uint32_t)digit_s;
+  const uint32_t digit = (uint32_t)find_digit(search, r.m, n1, n0, &larger);
   int n_above = 0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
@@ -287,68 +318,87 @@ __global__ __launch_bounds__(kThreads) void k_split(SelectArgs a) {
 }
 
 // The threshold among the candidates of a row, and what each chunk has before
-// it.  One workgroup for a row; a wave takes a chunk at a time.
+// it.  One workgroup for a row; a wave takes a chunk at a time.  Up to kHeld
+// candidates of up to kThreads chunks are brought into LDS once, more are read
+// again for every digit.
+constexpr int kHeld = 24 * 1024;
+
 __global__ __launch_bounds__(kThreads) void k_threshold(SelectArgs a) {
-  __shared__ int slots[4][kWaves];
-  const int s = blockIdx.y, h = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ uint32_t held[kHeld];
+  __shared__ int offset[kThreads];
+  __shared__ int slots[2][kWaves];
+  __shared__ Search search;
+  const int s = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const Row r = row_of(a, s);
   if (r.m == 0) return;
   const int64_t row = (int64_t)s * a.kv_heads + h;
   const int chunks = (r.len + kChunk - 1) / kChunk;
   const uint32_t* cand = a.candidates + row * a.chunks * kChunk;
   const int32_t* n_cand = a.n_cand + row * a.chunks;
-  // this wave's candidates, kMine of them in registers and the rest read again for every count
-  constexpr int kMine = 32;
-  uint32_t mine[kMine];
-  uint32_t lo = ~0u, hi = 0;
-  int above = 0, have = 0;
-#pragma unroll
-  for (int i = 0; i < kMine; ++i) mine[i] = 0;
-  auto walk = [&](auto f) {  // f(key or 0, number of the 64 in this wave's walk)
-    int k = 0;
-    for (int c = wave; c < chunks; c += kWaves) {
-      const int n = n_cand[c];
-      for (int i = 0; i < n; i += 64, ++k) f(i + lane < n ? cand[(int64_t)c * kChunk + i + lane] : 0u, k);
-    }
-    return k;
-  };
-  for (int c = wave; c < chunks; c += kWaves) above += a.above[row * a.chunks + c];
-  have = walk([&](uint32_t key, int k) {
-    if (key != 0) lo = min(lo, key), hi = max(hi, key);
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) mine[i] = i == k ? key : mine[i];
-  });
-  lo = wave_extreme(lo, false), hi = wave_extreme(hi, true);
-  if (lane == 0) slots[0][wave] = (int)lo, slots[1][wave] = (int)hi, slots[2][wave] = above;
-  __syncthreads();
-  above = 0;
-  for (int i = 0; i < kWaves; ++i) {
-    lo = min(lo, (uint32_t)slots[0][i]), hi = max(hi, (uint32_t)slots[1][i]);
-    above += slots[2][i];
+  // candidates and larger keys of all chunks; the candidates before each chunk
+  int own = 0, larger = 0;
+  for (int c = tid; c < chunks; c += kThreads) own += n_cand[c], larger += a.above[row * a.chunks + c];
+  int upto = own;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(upto, o);
+    if (lane >= o) upto += y;
   }
+  for (int o = 32; o; o >>= 1) larger += __shfl_xor(larger, o);
+  if (lane == 63) slots[0][wave] = upto, slots[1][wave] = larger;
   __syncthreads();
-  int turn = 0;
-  auto count = [&](uint32_t t) {
-    int n = 0;
-    if (have <= kMine) {
+  int total = 0;
+  larger = 0;
+  for (int i = 0; i < kWaves; ++i) {
+    if (i < wave) upto += slots[0][i];
+    total += slots[0][i], larger += slots[1][i];
+  }
+  offset[tid] = upto - own;
+  const bool fits = total <= kHeld && chunks <= kThreads;
+  __syncthreads();
+  uint32_t lo = ~0u, hi = 0;
+  // f(key, 0 where there is none) for this wave's chunks, eight loads at a time
+  auto each_of = [&](int c, auto f) {
+    const int n = n_cand[c];
+    for (int i = 0; i < n; i += 512) {
+      uint32_t x[8];
 #pragma unroll
-      for (int i = 0; i < kMine; ++i) n += wave_count(mine[i] >= t);
-    } else {
-      walk([&](uint32_t key, int) { n += wave_count(key >= t); });
+      for (int k = 0; k < 8; ++k) x[k] = i + k * 64 + lane < n ? cand[(int64_t)c * kChunk + i + k * 64 + lane] : 0u;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f(x[k], i + k * 64 + lane);
     }
-    turn ^= 1;
-    return block_sum(n, slots[2 + turn]);
   };
-  const uint32_t t = nth_largest(lo, hi, r.m - above, count);
-  const int want = r.m - above - (t == ~0u ? 0 : count(t + 1));
-  if (threadIdx.x == 0) a.threshold[2 * row] = t, a.threshold[2 * row + 1] = (uint32_t)want;
+  for (int c = wave; c < chunks; c += kWaves)
+    each_of(c, [&](uint32_t key, int i) {
+      if (key == 0) return;
+      lo = min(lo, key), hi = max(hi, key);
+      if (fits) held[offset[c] + i] = key;
+    });
+  lo = wave_extreme(lo, false), hi = wave_extreme(hi, true);
+  __syncthreads();
+  if (lane == 0) slots[0][wave] = (int)lo, slots[1][wave] = (int)hi;
+  __syncthreads();
+  for (int i = 0; i < kWaves; ++i) lo = min(lo, (uint32_t)slots[0][i]), hi = max(hi, (uint32_t)slots[1][i]);
+  int above;
+  auto each = [&](auto f) {
+    if (fits)
+      for (int i = tid; i < total; i += kThreads) f(held[i]);
+    else
+      for (int c = wave; c < chunks; c += kWaves) each_of(c, [&](uint32_t key, int) { f(key); });
+  };
+  const uint32_t t = nth_largest(search, lo, hi, r.m - larger, each, &above);
+  const int want = r.m - larger - above;
+  if (tid == 0) a.threshold[2 * row] = t, a.threshold[2 * row + 1] = (uint32_t)want;
   // per chunk: keys above and at the threshold, then their sums before it
   for (int c = wave; c < chunks; c += kWaves) {
     int gt = 0, eq = 0;
-    for (int i = 0; i < n_cand[c]; i += 64) {
-      const uint32_t key = i + lane < n_cand[c] ? cand[(int64_t)c * kChunk + i + lane] : 0u;
-      gt += wave_count(key > t), eq += wave_count(key == t);
-    }
+    const int n = n_cand[c];
+    if (fits)
+      for (int i = 0; i < n; i += 64) {
+        const uint32_t key = i + lane < n ? held[offset[c] + i + lane] : 0u;
+        gt += wave_count(key > t), eq += wave_count(key == t);
+      }
+    else
+      each_of(c, [&](uint32_t key, int) { gt += wave_count(key > t), eq += wave_count(key == t); });
     if (lane == 0) a.place[row * a.chunks + c] = a.above[row * a.chunks + c] + gt, a.ties[row * a.chunks + c] = eq;
   }
   __syncthreads();
