@@ -14,6 +14,7 @@ constexpr int kBlock = DLLM_CACHE_BLOCK;
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short i16x2 __attribute__((ext_vector_type(2)));
 
 // One sequence of a batch, clamped to the arrays' extents.
 struct SeqView {

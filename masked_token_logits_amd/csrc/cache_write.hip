@@ -32,6 +32,7 @@ __device__ __forceinline__ uint32_t float_e4m3(float x) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x, x, 0, false) & 0xffu;
 }
 
+// The write for any strides, alignment and rotated dimensions.
 // One workgroup: one touched block of one head.  Values pass through LDS as
 // fp32 (rotated keys, values), because the cache's byte order of a block is
 // not the order of the input rows.
@@ -125,12 +126,245 @@ __global__ __launch_bounds__(kThreads) void k_write(dllm_cache c, dllm_cache_bat
   }
 }
 
+struct WriteArgs {
+  dllm_cache c;
+  dllm_cache_batch b;
+  int64_t T;
+  const uint16_t *k, *v;
+  int64_t k_token, k_head, v_token, v_head;
+  const int32_t *start, *positions;
+  dllm_rotary_plan plan;
+  int heads;  // of a workgroup
+};
+
+__device__ __forceinline__ float largest_of(const i32x4& w) {  // of 8 bf16, what is not finite left out
+  float big = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    big = fmaxf(big, finite_abs(__uint_as_float((uint32_t)w[i] << 16)));
+    big = fmaxf(big, finite_abs(__uint_as_float((uint32_t)w[i] & 0xffff0000u)));
+  }
+  return big;
+}
+
+__device__ __forceinline__ int pack_e4m3(float a, float b, float c, float d, float scale) {
+  i16x2 w = {0, 0};
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, scale, false);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, scale, true);
+  return __builtin_bit_cast(int, w);
+}
+
+// 4 e4m3 bytes times `factor`, rounded again.
+__device__ __forceinline__ int requantised(int w, float factor) {
+  const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+  int x = __builtin_amdgcn_cvt_pk_fp8_f32(lo[0] * factor, lo[1] * factor, 0, false);
+  return __builtin_amdgcn_cvt_pk_fp8_f32(hi[0] * factor, hi[1] * factor, x, true);
+}
+
+struct Scales {
+  int byte;
+  float scale, old;  // the new one's value; the old one's relative to it
+};
+
+__device__ __forceinline__ Scales scales_of(float big, int had, bool any_held) {
+  Scales s;
+  s.byte = min(max(max(scale_byte(big), any_held ? had : 0), DLLM_CACHE_SCALE_MIN), DLLM_CACHE_SCALE_MAX);
+  s.scale = scale_value(s.byte);
+  s.old = had - s.byte < -126 ? 0.0f : __uint_as_float((uint32_t)(had - s.byte + 127) << 23);
+  return s;
+}
+
+// The write for 16-byte aligned rows and rotations whose pairs fall into pairs
+// of 16-dim pieces: interleaved ones, and half layouts of a multiple of 32 dims.
+// One workgroup of 2 D threads: one touched block, a.heads heads in turn.
+// The first D threads have the keys: a token and two pieces of 16 dims that
+// are each other's partners, whose 16 angles they keep in registers for all heads
+// (an angle costs some 40 fp64 operations, a rotated pair 4).  The others have
+// the values: a token and 32 dims, turned into the cache's order through LDS.
+template <int D>
+__global__ __launch_bounds__(2 * D) void k_write_pieces(WriteArgs a) {
+  constexpr int N = 2 * D, kPer = D / 32, kWaves = N / 64;  // kPer: threads of a token
+  __shared__ __attribute__((aligned(16))) uint8_t rows[kBlock * D];
+  __shared__ __attribute__((aligned(16))) uint8_t turned[kBlock * D];
+  __shared__ float top[kWaves];
+  const int s = blockIdx.z, tid = threadIdx.x;
+  const SeqView q = seq_view(a.b, a.T, s);
+  const int64_t st = a.start[s];
+  if (st < 0 || q.rows == 0) return;
+  const int64_t blk64 = st / kBlock + blockIdx.x;
+  if (blk64 * kBlock >= st + q.rows || blk64 >= a.b.table_blocks) return;
+  const int blk = (int)blk64;
+  const int page = page_of(a.b.table, a.b.table_blocks, a.c.pages, s, blk);
+  if (page < 0) return;
+  const int h0 = blockIdx.y * a.heads, h1 = min(h0 + a.heads, a.c.kv_heads);
+  // tokens of the block: [f0, f1) are written, others below `len` are held
+  const int f0 = (int)max(st - (int64_t)blk * kBlock, (int64_t)0);
+  const int f1 = (int)min(st + q.rows - (int64_t)blk * kBlock, (int64_t)kBlock);
+  const int len = min(max(q.len - blk * kBlock, 0), kBlock);
+  const bool any_held = min(f0, len) > 0 || len > f1;
+  const bool key_side = tid < D;
+  const int u = key_side ? tid : tid - D, t = u / kPer, part = u % kPer;
+  const bool fresh = t >= f0 && t < f1, held = !fresh && t < len;
+  const int64_t token = q.q0 + ((int64_t)blk * kBlock + t - st);  // only where fresh
+  // key pieces: first dims p0, p1; pairs of this thread that are rotated (the first n_rot)
+  const int r = a.plan.turns ? a.plan.rotary_dim : 0;
+  const bool halves = a.plan.layout == DLLM_ROTARY_HALF;
+  int p0 = 32 * part, p1 = p0 + 16, n_rot = min(max(r / 2 - 16 * part, 0), 16);
+  if (halves) {
+    n_rot = 32 * part < r ? 16 : 0;
+    if (n_rot) p0 = 16 * part, p1 = r / 2 + 16 * part;
+  }
+  double2 cs[16];
+  if (key_side && fresh && n_rot) {
+    const int pos = a.positions[token];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      cs[i] = i < n_rot ? rotary_angle64(pos, a.plan.turns[16 * part + i], a.plan.magnitude) : make_double2(1.0, 0.0);
+  }
+  i32x4 x[4];  // 32 bf16
+  auto load = [&](int h) {
+    if (!fresh) return;
+    if (key_side) {
+      const i32x4* p = reinterpret_cast<const i32x4*>(a.k + token * a.k_token + h * a.k_head + p0);
+      const i32x4* z = reinterpret_cast<const i32x4*>(a.k + token * a.k_token + h * a.k_head + p1);
+      x[0] = p[0], x[1] = p[1], x[2] = z[0], x[3] = z[1];
+    } else {
+      const i32x4* p = reinterpret_cast<const i32x4*>(a.v + token * a.v_token + h * a.v_head + 32 * part);
+      x[0] = p[0], x[1] = p[1], x[2] = p[2], x[3] = p[3];
+    }
+  };
+  // bytes of a value piece that are written and held: its tokens are 8 i + 4 half + 0 .. 3
+  const int vhalf = (tid >> 5) & 1;
+  i32x4 fresh_mask, held_mask;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t f = 0, o = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int y = 8 * i + 4 * vhalf + j;
+      const bool is = y >= f0 && y < f1;
+      f |= is ? 0xffu << (8 * j) : 0u;
+      o |= !is && y < len ? 0xffu << (8 * j) : 0u;
+    }
+    fresh_mask[i] = (int)f, held_mask[i] = (int)o;
+  }
+  load(h0);
+  for (int h = h0; h < h1; ++h) {
+    const int64_t at = block_of(a.c, page, h);
+    float big = 0.0f;
+    if (fresh) big = fmaxf(fmaxf(largest_of(x[0]), largest_of(x[1])), fmaxf(largest_of(x[2]), largest_of(x[3])));
+    for (int o = 32; o; o >>= 1) big = fmaxf(big, __shfl_xor(big, o));
+    if ((tid & 63) == 0) top[tid >> 6] = big;
+    const int k_had = any_held ? a.c.k_scale[at] : 0, v_had = any_held ? a.c.v_scale[at] : 0;
+    __syncthreads();
+    float kbig = 0.0f, vbig = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWaves / 2; ++i) kbig = fmaxf(kbig, top[i]), vbig = fmaxf(vbig, top[kWaves / 2 + i]);
+    if (r) kbig *= 1.41421366f * a.plan.magnitude;
+    const Scales ks = scales_of(kbig, k_had, any_held), vs = scales_of(vbig, v_had, any_held);
+    const i32x4 in[4] = {x[0], x[1], x[2], x[3]};
+    if (h + 1 < h1) load(h + 1);
+    auto value = [&](int e) { return __uint_as_float(e & 1 ? (uint32_t)in[e / 8][e % 8 / 2] & 0xffff0000u : (uint32_t)in[e / 8][e % 8 / 2] << 16); };
+    if (key_side) {
+      uint8_t* dst = a.c.k + at * (kBlock * D);
+      i32x4* w0 = reinterpret_cast<i32x4*>(dst + ((p0 % (D / 2)) / 16 * 2 + p0 / (D / 2)) * 512 + t * 16);
+      i32x4* w1 = reinterpret_cast<i32x4*>(dst + ((p1 % (D / 2)) / 16 * 2 + p1 / (D / 2)) * 512 + t * 16);
+      i32x4 y0 = {0, 0, 0, 0}, y1 = {0, 0, 0, 0};
+      if (fresh) {
+        float z[32];
+        if (n_rot == 0) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) z[e] = value(e);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            // pair i: dims i of both pieces, or dims 2 i, 2 i + 1 of the 32
+            const float va = halves ? value(i) : value(2 * i), vb = halves ? value(16 + i) : value(2 * i + 1);
+            const double da = va, db = vb;
+            const float ra = i < n_rot ? odd_float(da * cs[i].x - db * cs[i].y) : va;
+            const float rb = i < n_rot ? odd_float(db * cs[i].x + da * cs[i].y) : vb;
+            if (halves) z[i] = ra, z[16 + i] = rb;
+            else z[2 * i] = ra, z[2 * i + 1] = rb;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y0[i] = pack_e4m3(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3], ks.scale);
+          y1[i] = pack_e4m3(z[16 + 4 * i], z[16 + 4 * i + 1], z[16 + 4 * i + 2], z[16 + 4 * i + 3], ks.scale);
+        }
+      } else if (held) {
+        y0 = *w0, y1 = *w1;
+        if (ks.byte != k_had) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y0[i] = requantised(y0[i], ks.old), y1[i] = requantised(y1[i], ks.old);
+        }
+      }
+      *w0 = y0, *w1 = y1;
+      if (tid == 0) a.c.k_scale[at] = (uint8_t)ks.byte;
+    } else if (fresh) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        i32x4 y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          y[i] = pack_e4m3(value(16 * c + 4 * i), value(16 * c + 4 * i + 1), value(16 * c + 4 * i + 2),
+                           value(16 * c + 4 * i + 3), vs.scale);
+        *reinterpret_cast<i32x4*>(rows + t * D + 32 * part + 16 * c) = y;
+      }
+    }
+    __syncthreads();
+    {
+      // 4 tokens by 4 dims: from a dword for each token to one for each dim
+      const int quad = tid % (D / 4), g = tid / (D / 4);
+      uint32_t y[4], z[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const uint32_t*>(rows + (4 * g + j) * D + 4 * quad);
+      const uint32_t a01 = __builtin_amdgcn_perm(y[1], y[0], 0x05010400u), b01 = __builtin_amdgcn_perm(y[1], y[0], 0x07030602u);
+      const uint32_t a23 = __builtin_amdgcn_perm(y[3], y[2], 0x05010400u), b23 = __builtin_amdgcn_perm(y[3], y[2], 0x07030602u);
+      z[0] = __builtin_amdgcn_perm(a23, a01, 0x05040100u), z[1] = __builtin_amdgcn_perm(a23, a01, 0x07060302u);
+      z[2] = __builtin_amdgcn_perm(b23, b01, 0x05040100u), z[3] = __builtin_amdgcn_perm(b23, b01, 0x07060302u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int d = 4 * quad + j;
+        *reinterpret_cast<uint32_t*>(turned + ((d / 32 * 2 + g % 2) * 32 + d % 32) * 16 + g / 2 * 4) = z[j];
+      }
+    }
+    __syncthreads();
+    {
+      i32x4* w = reinterpret_cast<i32x4*>(a.c.v + at * (kBlock * D) + tid * 16);
+      i32x4 y = *reinterpret_cast<const i32x4*>(turned + tid * 16) & fresh_mask;
+      if (any_held) {
+        i32x4 o = *w;
+        if (vs.byte != v_had) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = requantised(o[i], vs.old);
+        }
+        y |= o & held_mask;
+      }
+      *w = y;
+      if (tid == 0) a.c.v_scale[at] = (uint8_t)vs.byte;
+    }
+    // (the next head's first barrier stands between these reads of `turned` and its writes)
+  }
+}
+
 template <int D>
 void launch_write(const dllm_cache& c, const dllm_cache_batch& b, int64_t T, const uint16_t* k, int64_t kt, int64_t kh,
                   const uint16_t* v, int64_t vt, int64_t vh, const int32_t* start, const int32_t* positions,
                   const dllm_rotary_plan& plan, hipStream_t st) {
   const int64_t most = b.max_new < T ? b.max_new : T;
   const int64_t blocks = (most + kBlock - 2) / kBlock + 1;  // a run of n tokens touches at most this many
+  const bool rows16 = ((kt | kh | vt | vh) & 7) == 0 && (((uintptr_t)k | (uintptr_t)v) & 15u) == 0;
+  const bool pieces = !plan.turns || plan.layout == DLLM_ROTARY_INTERLEAVED || plan.rotary_dim % 32 == 0;
+  if (rows16 && pieces) {
+    // heads of a workgroup: as many as leave some 4 workgroups for every compute unit
+    int heads = c.kv_heads;
+    while (heads > 1 && blocks * b.S * ((c.kv_heads + heads - 1) / heads) < 1024) heads = (heads + 1) / 2;
+    const WriteArgs a = {c, b, T, k, v, kt, kh, vt, vh, start, positions, plan, heads};
+    hipLaunchKernelGGL(k_write_pieces<D>, dim3((unsigned)blocks, (c.kv_heads + heads - 1) / heads, b.S), dim3(2 * D), 0,
+                       st, a);
+    return;
+  }
   hipLaunchKernelGGL(k_write<D>, dim3((unsigned)blocks, c.kv_heads, b.S), dim3(kThreads), 0, st, c, b, T, k, kt, kh, v,
                      vt, vh, start, positions, plan);
 }

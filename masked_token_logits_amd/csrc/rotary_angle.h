@@ -55,14 +55,13 @@ __device__ __forceinline__ double2 rotary_angle64(int pos, double turns, double 
   return make_double2((q == 1 || q == 2 ? -cq : cq) * magnitude, (q >= 2 ? -sq : sq) * magnitude);
 }
 
-// x in fp32 with its last bit set if that is not exact (rounding to odd), so
-// that a later rounding to far fewer bits is as if made from x itself.
+// x in fp32 with 20 bits behind the first and the last of them set if that is
+// not exact (rounding to odd), so that a later rounding to far fewer bits is as if
+// made from x itself.
 __device__ __forceinline__ float odd_float(double x) {
-  const float f = (float)x;
-  const double back = (double)f;
-  uint32_t u = __float_as_uint(f);
-  if (back != x && (u & 1u) == 0 && f == f) u += fabs(back) > fabs(x) ? -1 : 1;
-  return __uint_as_float(u);
+  const uint64_t u = (uint64_t)__double_as_longlong(x);
+  const uint32_t hi = (uint32_t)(u >> 32) | min((uint32_t)u, 1u);
+  return (float)__longlong_as_double((int64_t)((uint64_t)hi << 32));
 }
 
 __device__ __forceinline__ float bf16_float(uint32_t bits) { return __uint_as_float(bits << 16); }
