@@ -178,15 +178,16 @@ __device__ __forceinline__ Scales scales_of(float big, int had, bool any_held) {
 // of 16-dim pieces: interleaved ones, and half layouts of a multiple of 32 dims.
 // One workgroup of 2 D threads: one touched block, a.heads heads in turn.
 // The first D threads have the keys: a token and two pieces of 16 dims that
-// are each other's partners, whose 16 angles they keep in registers for all heads
+// are each other's partners, whose 16 angles they keep in LDS for all heads
 // (an angle costs some 40 fp64 operations, a rotated pair 4).  The others have
 // the values: a token and 32 dims, turned into the cache's order through LDS.
 template <int D>
-__global__ __launch_bounds__(2 * D) void k_write_pieces(WriteArgs a) {
+__global__ __launch_bounds__(2 * D, 4) void k_write_pieces(WriteArgs a) {
   constexpr int N = 2 * D, kPer = D / 32, kWaves = N / 64;  // kPer: threads of a token
   __shared__ __attribute__((aligned(16))) uint8_t rows[kBlock * D];
-  __shared__ __attribute__((aligned(16))) uint8_t turned[kBlock * D];
+  uint8_t* const turned = rows;  // with arrays of their own, 40 KiB would hold three workgroups instead of four
   __shared__ float top[kWaves];
+  __shared__ double2 cs[16][D];  // the key threads' angles: in registers they would halve the waves in flight
   const int s = blockIdx.z, tid = threadIdx.x;
   const SeqView q = seq_view(a.b, a.T, s);
   const int64_t st = a.start[s];
@@ -214,12 +215,10 @@ __global__ __launch_bounds__(2 * D) void k_write_pieces(WriteArgs a) {
     n_rot = 32 * part < r ? 16 : 0;
     if (n_rot) p0 = 16 * part, p1 = r / 2 + 16 * part;
   }
-  double2 cs[16];
   if (key_side && fresh && n_rot) {
     const int pos = a.positions[token];
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      cs[i] = i < n_rot ? rotary_angle64(pos, a.plan.turns[16 * part + i], a.plan.magnitude) : make_double2(1.0, 0.0);
+#pragma unroll 4
+    for (int i = 0; i < n_rot; ++i) cs[i][u] = rotary_angle64(pos, a.plan.turns[16 * part + i], a.plan.magnitude);
   }
   i32x4 x[4];  // 32 bf16
   auto load = [&](int h) {
@@ -281,8 +280,9 @@ __global__ __launch_bounds__(2 * D) void k_write_pieces(WriteArgs a) {
             // pair i: dims i of both pieces, or dims 2 i, 2 i + 1 of the 32
             const float va = halves ? value(i) : value(2 * i), vb = halves ? value(16 + i) : value(2 * i + 1);
             const double da = va, db = vb;
-            const float ra = i < n_rot ? odd_float(da * cs[i].x - db * cs[i].y) : va;
-            const float rb = i < n_rot ? odd_float(db * cs[i].x + da * cs[i].y) : vb;
+            const double2 c = cs[i][u];
+            const float ra = i < n_rot ? odd_float(da * c.x - db * c.y) : va;
+            const float rb = i < n_rot ? odd_float(db * c.x + da * c.y) : vb;
             if (halves) z[i] = ra, z[16 + i] = rb;
             else z[2 * i] = ra, z[2 * i + 1] = rb;
           }
@@ -323,6 +323,7 @@ __global__ __launch_bounds__(2 * D) void k_write_pieces(WriteArgs a) {
       const uint32_t a23 = __builtin_amdgcn_perm(y[3], y[2], 0x05010400u), b23 = __builtin_amdgcn_perm(y[3], y[2], 0x07030602u);
       z[0] = __builtin_amdgcn_perm(a23, a01, 0x05040100u), z[1] = __builtin_amdgcn_perm(a23, a01, 0x07060302u);
       z[2] = __builtin_amdgcn_perm(b23, b01, 0x05040100u), z[3] = __builtin_amdgcn_perm(b23, b01, 0x07060302u);
+      __syncthreads();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int d = 4 * quad + j;

@@ -40,6 +40,10 @@ def _batch(bc, cu, lens, table, **kw):
     (256, 2, [77, 32], [77, 32], 256, "half"),             # a prompt from the start
     (64, 2, [40, 0, 31], [7, 0, 31], 10, "half"),          # a sequence without new tokens, few rotated dims
     (128, 2, [50, 64], [20, 32], 0, "half"),               # no rotation
+    (128, 5, [90, 31], [70, 31], 64, "half"),              # half of each head, several heads of a workgroup
+    (256, 1, [33], [33], 96, "half"),
+    (64, 3, [40], [40], 22, "interleaved"),                # pairs that end inside a piece
+    (128, 2, [45], [45], 40, "half"),                      # partners that no pieces hold
 ])
 def test_write_parity(D, heads, lens, new, r, layout):
     import torch
