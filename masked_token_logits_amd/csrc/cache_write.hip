@@ -215,11 +215,6 @@ __global__ __launch_bounds__(2 * D, 4) void k_write_pieces(WriteArgs a) {
     n_rot = 32 * part < r ? 16 : 0;
     if (n_rot) p0 = 16 * part, p1 = r / 2 + 16 * part;
   }
-  if (key_side && fresh && n_rot) {
-    const int pos = a.positions[token];
-#pragma unroll 4
-    for (int i = 0; i < n_rot; ++i) cs[i][u] = rotary_angle64(pos, a.plan.turns[16 * part + i], a.plan.magnitude);
-  }
   i32x4 x[4];  // 32 bf16
   auto load = [&](int h) {
     if (!fresh) return;
@@ -232,6 +227,12 @@ __global__ __launch_bounds__(2 * D, 4) void k_write_pieces(WriteArgs a) {
       x[0] = p[0], x[1] = p[1], x[2] = p[2], x[3] = p[3];
     }
   };
+  load(h0);
+  if (fresh && n_rot) {  // half of them by the thread that has the same token's values
+    const int pos = a.positions[token];
+#pragma unroll 2
+    for (int i = key_side ? 0 : 1; i < n_rot; i += 2) cs[i][u] = rotary_angle64(pos, a.plan.turns[16 * part + i], a.plan.magnitude);
+  }
   // bytes of a value piece that are written and held: its tokens are 8 i + 4 half + 0 .. 3
   const int vhalf = (tid >> 5) & 1;
   i32x4 fresh_mask, held_mask;
@@ -247,7 +248,6 @@ __global__ __launch_bounds__(2 * D, 4) void k_write_pieces(WriteArgs a) {
     }
     fresh_mask[i] = (int)f, held_mask[i] = (int)o;
   }
-  load(h0);
   for (int h = h0; h < h1; ++h) {
     const int64_t at = block_of(a.c, page, h);
     float big = 0.0f;
@@ -270,27 +270,30 @@ __global__ __launch_bounds__(2 * D, 4) void k_write_pieces(WriteArgs a) {
       i32x4* w1 = reinterpret_cast<i32x4*>(dst + ((p1 % (D / 2)) / 16 * 2 + p1 / (D / 2)) * 512 + t * 16);
       i32x4 y0 = {0, 0, 0, 0}, y1 = {0, 0, 0, 0};
       if (fresh) {
-        float z[32];
-        if (n_rot == 0) {
+        // four pairs at a time: dims 4 g + 0 .. 3 of both pieces, or dims 8 g + 0 .. 7 of the 32
 #pragma unroll
-          for (int e = 0; e < 32; ++e) z[e] = value(e);
-        } else {
+        for (int g = 0; g < 4; ++g) {
+          float ra[4], rb[4];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            // pair i: dims i of both pieces, or dims 2 i, 2 i + 1 of the 32
-            const float va = halves ? value(i) : value(2 * i), vb = halves ? value(16 + i) : value(2 * i + 1);
-            const double da = va, db = vb;
-            const double2 c = cs[i][u];
-            const float ra = i < n_rot ? odd_float(da * c.x - db * c.y) : va;
-            const float rb = i < n_rot ? odd_float(db * c.x + da * c.y) : vb;
-            if (halves) z[i] = ra, z[16 + i] = rb;
-            else z[2 * i] = ra, z[2 * i + 1] = rb;
+          for (int i = 0; i < 4; ++i) {
+            const int e = 4 * g + i;
+            ra[i] = halves ? value(e) : value(2 * e), rb[i] = halves ? value(16 + e) : value(2 * e + 1);
+            if (e < n_rot) {
+              const double da = ra[i], db = rb[i];
+              const double2 c = cs[e][u];
+              ra[i] = odd_float(da * c.x - db * c.y);
+              rb[i] = odd_float(db * c.x + da * c.y);
+            }
           }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y0[i] = pack_e4m3(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3], ks.scale);
-          y1[i] = pack_e4m3(z[16 + 4 * i], z[16 + 4 * i + 1], z[16 + 4 * i + 2], z[16 + 4 * i + 3], ks.scale);
+          if (halves) {
+            y0[g] = pack_e4m3(ra[0], ra[1], ra[2], ra[3], ks.scale);
+            y1[g] = pack_e4m3(rb[0], rb[1], rb[2], rb[3], ks.scale);
+          } else {
+            const int lo = pack_e4m3(ra[0], rb[0], ra[1], rb[1], ks.scale), hi = pack_e4m3(ra[2], rb[2], ra[3], rb[3], ks.scale);
+            (g < 2 ? y0 : y1)[g % 2 * 2] = lo;
+            (g < 2 ? y0 : y1)[g % 2 * 2 + 1] = hi;
+          }
+          __builtin_amdgcn_sched_barrier(0);  // not all sixteen at once: their registers would spill
         }
       } else if (held) {
         y0 = *w0, y1 = *w1;
