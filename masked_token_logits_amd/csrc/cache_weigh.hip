@@ -19,62 +19,167 @@ struct WeighArgs {
   float* weights;
 };
 
-// One wave: one block of one key/value head, against every query that may
-// see it.  The block's keys are widened to bf16 (exact, scale included) once
-// and stay in registers; queries come in as they are.
-template <int D>
-__global__ __launch_bounds__(64) void k_weigh(WeighArgs a) {
-  const int s = blockIdx.z, h = blockIdx.y, blk = blockIdx.x, lane = threadIdx.x, col = lane & 31, half = lane >> 5;
+#define LDS_AS __attribute__((address_space(3)))
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+
+// 16 values of every lane summed over the 32 lanes of its half: lane l of a
+// half ends with the sum of value l / 2.  Each round halves the values and
+// doubles the lanes that a sum covers.
+__device__ __forceinline__ float sum_columns(float* x) {
+  const int lane = threadIdx.x & 31;
+  each<0, 4>([&](auto R) {
+    constexpr int n = 8 >> decltype(R)::value, bit = 2 * n;
+    const bool upper = lane & bit;
+    each<0, n>([&](auto I) {
+      constexpr int i = decltype(I)::value;
+      const float keep = upper ? x[i + n] : x[i], give = upper ? x[i] : x[i + n];
+      x[i] = keep + __shfl_xor(give, bit);
+    });
+  });
+  return x[0] + __shfl_xor(x[0], 1);
+}
+
+// One workgroup: KW x NB blocks of 32 tokens of one key/value head, against
+// every query that may see them.  A wave widens the keys of its NB blocks to
+// bf16 once (exact, scale included) and keeps them in registers; query rows
+// (token * group + head of the group) come in tiles of 32 through LDS, in the
+// order in which the matrix instruction takes them, a step or two ahead.  KW waves
+// share a tile for different blocks; with KW = 1 the four waves take different
+// tiles of the same blocks and are summed at the end, which makes four times as
+// many workgroups where there are few blocks.
+template <int D, int NB, int KW>
+__global__ __launch_bounds__(kThreads, 2) void k_weigh(WeighArgs a) {
+  constexpr int RW = kWaves / KW, CH = D / 16;           // tiles of a step; 1 KiB chunks of a tile
+  constexpr int kStep = RW * CH * 1024, kLoads = RW * CH / kWaves;  // bytes; loads of a wave
+  constexpr int kRing = KW == 1 ? 2 : 3;                            // steps in LDS
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[kRing * kStep];
+  const int s = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kw = wave % KW, rw = wave / KW;
   const SeqView q = seq_view(a.b, a.T, s);
-  if ((int64_t)blk * kBlock >= q.len) return;
-  const int page = page_of(a.b.table, a.b.table_blocks, a.c.pages, s, blk);
-  if (page < 0) return;
-  const int64_t at = block_of(a.c, page, h);
-  const float ks = scale_value(a.c.k_scale[at]);
-  Frag k[D / 16];
-  const uint8_t* kp = a.c.k + at * (kBlock * D) + lane * 16;
+  const int first = blockIdx.x * KW * NB;  // the workgroup's first block
+  if ((int64_t)first * kBlock >= q.len) return;
+  const int rows = q.rows * a.group;
+  // a query sees tokens below len - n + its number + 1; rows before r0 see none of these
+  const int before = q.len - q.n;
+  const int64_t skip = a.causal ? (int64_t)max(first * kBlock - before, 0) * a.group : 0;
+  const int tile0 = (int)min(skip, (int64_t)rows) / 32, steps = ((rows + 31) / 32 - tile0 + RW - 1) / RW;
+  Frag k[NB][D / 16];
+  int block[NB], limit[NB];  // number; its first token, counted from len - n
+  bool ok[NB];
+  each<0, NB>([&](auto N) {
+    constexpr int b = decltype(N)::value;
+    block[b] = first + kw * NB + b;
+    const int page = (int64_t)block[b] * kBlock < q.len ? page_of(a.b.table, a.b.table_blocks, a.c.pages, s, block[b]) : -1;
+    ok[b] = page >= 0;
+    limit[b] = block[b] * kBlock - before;
+    const int64_t at = block_of(a.c, max(page, 0), h);
+    const float scale = scale_value(a.c.k_scale[at]);
+    const uint8_t* p = a.c.k + at * (kBlock * D) + lane * 16;
+    each<0, D / 32>([&](auto C) {
+      constexpr int c = decltype(C)::value;
+      widen_keys(*reinterpret_cast<const i32x4*>(p + c * 1024), scale, k[b][2 * c], k[b][2 * c + 1]);
+    });
+  });
+  float acc[NB][16];
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-    widen_keys(*reinterpret_cast<const i32x4*>(kp + i * 1024), ks, k[2 * i], k[2 * i + 1]);
-  float acc[16];
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-  const int64_t rows = (int64_t)q.rows * a.group;
-  for (int64_t row0 = 0; row0 < rows; row0 += 32) {
-    const int64_t row = min(row0 + col, rows - 1);
-    const int tok = (int)(row / a.group), head = h * a.group + (int)(row - (int64_t)tok * a.group);
-    Frag qf[D / 16];
-    load_query<D>(qf, a.q + (q.q0 + tok) * a.q_token + (int64_t)head * a.q_head, half);
-    f32x16 sc = {};
+    for (int i = 0; i < 16; ++i) acc[b][i] = 0.0f;
+  auto place = [&](int row, int& tok, int& head) {
+    row = min(row, rows - 1);
+    tok = (int)((uint32_t)row / (uint32_t)a.group);
+    head = h * a.group + (row - tok * a.group);
+  };
+  // the wave's share of a step's queries: kLoads chunks of tile (chunk / CH), each lane its own row's 16 bytes
+  auto load_step = [&](int t) {
+    each<0, kLoads>([&](auto L) {
+      const int x = wave * kLoads + decltype(L)::value, tile = x / CH, c = x % CH;
+      int tok, head;
+      place((tile0 + t * RW + tile) * 32 + col, tok, head);
+      const uint16_t* src = a.q + (q.q0 + tok) * a.q_token + (int64_t)head * a.q_head + half * (D / 2) + c * 8;
+      __builtin_amdgcn_global_load_lds((const void*)src, (LDS_AS void*)(ring + (t % kRing) * kStep + x * 1024), 16, 0, 0);
+    });
+  };
+  struct Column {
+    float neg;  // -lse in base 2; -inf where the column adds nothing
+    int tok;
+  };
+  auto column = [&](int t) {
+    const int row = (tile0 + t * RW + rw) * 32 + col;
+    int tok, head;
+    place(row, tok, head);
+    const float l = a.lse[(q.q0 + tok) * a.q_heads + head];
+    return Column{row < rows && l != -INFINITY ? -l * kLog2e : -INFINITY, tok};
+  };
+  if (steps > 0) {
+    Column now = column(0);
+    each<0, kRing - 1>([&](auto t) { load_step(decltype(t)::value); });  // behind the last step rows repeat, and columns add nothing
+    for (int t = 0; t < steps; ++t) {
+      const Column next = column(t + 1);
+      asm volatile("" ::: "memory");
+      // step t is in: only the loads of later ones and `next` may still be on their way
+      __builtin_amdgcn_s_waitcnt((((kRing - 2) * kLoads + 1) & 15) | (7 << 4) | (0 << 8));
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      load_step(t + kRing - 1);  // where step t - 1 was
+      const uint8_t* tile = ring + (t % kRing) * kStep + rw * CH * 1024 + lane * 16;
+      f32x16 sc[NB];
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[i].b, qf[i].b, sc, 0, 0, 0);
-    float l = a.lse[(q.q0 + tok) * a.q_heads + head];
-    if (row0 + col >= rows || l == -INFINITY) l = INFINITY;  // adds nothing
-    const float ref = l * kLog2e;
-    const int limit = (a.causal ? q.len - q.n + tok + 1 : q.len) - blk * kBlock;
+      for (int b = 0; b < NB; ++b) sc[b] = f32x16{};
+      each<0, CH>([&](auto C) {
+        Frag f;
+        f.w = *reinterpret_cast<const i32x4*>(tile + decltype(C)::value * 1024);
+        each<0, NB>([&](auto N) {
+          constexpr int b = decltype(N)::value;
+          sc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[b][decltype(C)::value].b, f.b, sc[b], 0, 0, 0);
+        });
+      });
+      // columns of this tile that see a block only in part
+      const int first_tok = (int)((uint32_t)min((tile0 + t * RW + rw) * 32, rows - 1) / (uint32_t)a.group);
+      each<0, NB>([&](auto N) {
+        constexpr int b = decltype(N)::value;
+        if (a.causal && limit[b] + kBlock > first_tok + 1) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i], a.scale2, -ref));
-      acc[i] += token_of(i, half) < limit ? p : 0.0f;
+          for (int i = 0; i < 16; ++i) sc[b][i] = limit[b] + token_of(i, half) <= now.tok ? sc[b][i] : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[b][i] += __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][i], a.scale2, now.neg));
+      });
+      now = next;
     }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   }
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    for (int o = 16; o; o >>= 1) acc[i] += __shfl_xor(acc[i], o);
-  float* w = a.weights + ((int64_t)s * a.c.kv_heads + h) * ((int64_t)a.b.table_blocks * kBlock) + (int64_t)blk * kBlock;
-  if (col == 0) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int t = token_of(i, half);
-      if (blk * kBlock + t < q.len) w[t] = (a.decay == 0.0f ? 0.0f : a.decay * w[t]) + acc[i];
+  float* w = a.weights + ((int64_t)s * a.c.kv_heads + h) * ((int64_t)a.b.table_blocks * kBlock);
+  float* sums = reinterpret_cast<float*>(ring);
+  each<0, NB>([&](auto N) {
+    constexpr int b = decltype(N)::value;
+    float sum = sum_columns(acc[b]);
+    const int i = col >> 1, token = block[b] * kBlock + token_of(i, half);
+    if constexpr (RW > 1) {
+      if ((col & 1) == 0) sums[(rw * NB + b) * kBlock + token_of(i, half)] = sum;
+      __syncthreads();
+      if (rw == 0)
+        for (int x = 1; x < RW; ++x) sum += sums[(x * NB + b) * kBlock + token_of(i, half)];
     }
-  }
+    if (rw == 0 && (col & 1) == 0 && ok[b] && token < q.len)
+      w[token] = (a.decay == 0.0f ? 0.0f : a.decay * w[token]) + sum;
+  });
 }
 
 template <int D>
 void launch(const WeighArgs& a, hipStream_t st) {
+  constexpr int NB = D == 256 ? 1 : 2;
   const int blocks = (a.b.max_len + kBlock - 1) / kBlock;
-  hipLaunchKernelGGL(k_weigh<D>, dim3(blocks, a.c.kv_heads, a.b.S), dim3(64), 0, st, a);
+  const int64_t wide = (int64_t)((blocks + kWaves * NB - 1) / (kWaves * NB)) * a.c.kv_heads * a.b.S;
+  if (wide >= 512)
+    hipLaunchKernelGGL((k_weigh<D, NB, kWaves>), dim3((blocks + kWaves * NB - 1) / (kWaves * NB), a.c.kv_heads, a.b.S),
+                       dim3(kThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_weigh<D, NB, 1>), dim3((blocks + NB - 1) / NB, a.c.kv_heads, a.b.S), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace
@@ -89,7 +194,7 @@ extern "C" dllm_status dllm_cache_weigh(const dllm_cache* cache, const dllm_cach
   if (q_heads < 1 || q_heads % cache->kv_heads != 0 || q_token < 0 || q_head < 0) return DLLM_ERR_INVALID_ARG;
   if (!(scale >= 1.17549435e-38f && scale <= 1.0e38f) || (causal != 0 && causal != 1)) return DLLM_ERR_INVALID_ARG;
   if (!(decay >= 0.0f && decay <= 1.0f) || !weights) return DLLM_ERR_INVALID_ARG;
-  if (!cache_supported(cache) || q_heads > (1 << 16)) return DLLM_ERR_UNSUPPORTED;
+  if (!cache_supported(cache) || T * (int64_t)q_heads >= ((int64_t)1 << 31) - 1024) return DLLM_ERR_UNSUPPORTED;
   if (T > 0 && (!q || !lse)) return DLLM_ERR_INVALID_ARG;
   if (!stride_ok(q_token) || !stride_ok(q_head) || q_token % 8 != 0 || q_head % 8 != 0 || ((uintptr_t)q & 15u) != 0)
     return DLLM_ERR_UNSUPPORTED;
