@@ -57,7 +57,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_weigh(WeighArgs a) {
   const int s = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kw = wave % KW, rw = wave / KW;
   const SeqView q = seq_view(a.b, a.T, s);
-  const int first = blockIdx.x * KW * NB;  // the workgroup's first block
+  // Early tokens are seen by more rows than late ones: every other 256
+  // workgroups go through the blocks backwards, so that a compute unit's workgroups
+  // come out alike.
+  const bool backwards = a.causal && (((blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) >> 8 & 1);
+  const int first = (int)(backwards ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * KW * NB;  // the workgroup's first block
   if ((int64_t)first * kBlock >= q.len) return;
   const int rows = q.rows * a.group;
   // a query sees tokens below len - n + its number + 1; rows before r0 see none of these
@@ -86,43 +90,46 @@ __global__ __launch_bounds__(kThreads, 2) void k_weigh(WeighArgs a) {
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[b][i] = 0.0f;
-  auto place = [&](int row, int& tok, int& head) {
-    row = min(row, rows - 1);
-    tok = (int)((uint32_t)row / (uint32_t)a.group);
-    head = h * a.group + (row - tok * a.group);
+  // Step t's row of this lane: the one whose queries it loads is also its column.
+  static_assert(KW == 1 || KW == kWaves, "a wave loads queries of its own tile");
+  struct Place {
+    int row, tok, head;
   };
-  // the wave's share of a step's queries: kLoads chunks of tile (chunk / CH), each lane its own row's 16 bytes
-  auto load_step = [&](int t) {
+  auto place = [&](int t) {
+    const int row = (tile0 + t * RW + rw) * 32 + col, real = min(row, rows - 1);
+    const int tok = (int)((uint32_t)real / (uint32_t)a.group);
+    return Place{row, tok, h * a.group + (real - tok * a.group)};
+  };
+  // The wave's share of a step's queries: kLoads chunks of its tile.
+  auto load_step = [&](int t, const Place& p) {
+    const uint16_t* src = a.q + (q.q0 + p.tok) * a.q_token + (int64_t)p.head * a.q_head + half * (D / 2);
     each<0, kLoads>([&](auto L) {
-      const int x = wave * kLoads + decltype(L)::value, tile = x / CH, c = x % CH;
-      int tok, head;
-      place((tile0 + t * RW + tile) * 32 + col, tok, head);
-      const uint16_t* src = a.q + (q.q0 + tok) * a.q_token + (int64_t)head * a.q_head + half * (D / 2) + c * 8;
-      __builtin_amdgcn_global_load_lds((const void*)src, (LDS_AS void*)(ring + (t % kRing) * kStep + x * 1024), 16, 0, 0);
+      const int x = wave * kLoads + decltype(L)::value;
+      __builtin_amdgcn_global_load_lds((const void*)(src + x % CH * 8), (LDS_AS void*)(ring + (t % kRing) * kStep + x * 1024), 16,
+                                       0, 0);
     });
   };
-  struct Column {
-    float neg;  // -lse in base 2; -inf where the column adds nothing
-    int tok;
-  };
-  auto column = [&](int t) {
-    const int row = (tile0 + t * RW + rw) * 32 + col;
-    int tok, head;
-    place(row, tok, head);
-    const float l = a.lse[(q.q0 + tok) * a.q_heads + head];
-    return Column{row < rows && l != -INFINITY ? -l * kLog2e : -INFINITY, tok};
+  // -lse of a row in base 2; -inf where it adds nothing
+  auto negative_lse = [&](const Place& p) {
+    const float l = a.lse[(q.q0 + p.tok) * a.q_heads + p.head];
+    return p.row < rows && l != -INFINITY ? -l * kLog2e : -INFINITY;
   };
   if (steps > 0) {
-    Column now = column(0);
-    each<0, kRing - 1>([&](auto t) { load_step(decltype(t)::value); });  // behind the last step rows repeat, and columns add nothing
+    Place at[kRing];  // of steps t, t + 1, ...; behind the last step rows repeat, and add nothing
+    each<0, kRing - 1>([&](auto t) {
+      at[decltype(t)::value] = place(decltype(t)::value);
+      load_step(decltype(t)::value, at[decltype(t)::value]);
+    });
+    float neg = negative_lse(at[0]);
     for (int t = 0; t < steps; ++t) {
-      const Column next = column(t + 1);
+      at[kRing - 1] = place(t + kRing - 1);
+      const float neg_next = negative_lse(at[1]);
       asm volatile("" ::: "memory");
-      // step t is in: only the loads of later ones and `next` may still be on their way
+      // step t is in: only the loads of later ones and an lse may still be on their way
       __builtin_amdgcn_s_waitcnt((((kRing - 2) * kLoads + 1) & 15) | (7 << 4) | (0 << 8));
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      load_step(t + kRing - 1);  // where step t - 1 was
+      load_step(t + kRing - 1, at[kRing - 1]);  // where step t - 1 was
       const uint8_t* tile = ring + (t % kRing) * kStep + rw * CH * 1024 + lane * 16;
       f32x16 sc[NB];
 #pragma unroll
@@ -141,12 +148,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_weigh(WeighArgs a) {
         constexpr int b = decltype(N)::value;
         if (a.causal && limit[b] + kBlock > first_tok + 1) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) sc[b][i] = limit[b] + token_of(i, half) <= now.tok ? sc[b][i] : -INFINITY;
+          for (int i = 0; i < 16; ++i) sc[b][i] = limit[b] + token_of(i, half) <= at[0].tok ? sc[b][i] : -INFINITY;
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[b][i] += __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][i], a.scale2, now.neg));
+        for (int i = 0; i < 16; ++i) acc[b][i] += __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][i], a.scale2, neg));
       });
-      now = next;
+      neg = neg_next;
+      each<0, kRing - 1>([&](auto i) { at[decltype(i)::value] = at[decltype(i)::value + 1]; });
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0);
