@@ -17,6 +17,8 @@ struct WeighArgs {
   const float* lse;
   float decay;
   float* weights;
+  uint32_t magic;  // row / group = high word of row * magic >> shift; 0: group is 1
+  int shift;
 };
 
 #define LDS_AS __attribute__((address_space(3)))
@@ -40,41 +42,56 @@ __device__ __forceinline__ float sum_columns(float* x) {
   return x[0] + __shfl_xor(x[0], 1);
 }
 
-// One workgroup: KW x NB blocks of 32 tokens of one key/value head, against
-// every query that may see them.  A wave widens the keys of its NB blocks to
+// weights[token] = decay weights[token] + sum over queries of exp(scale q.k - lse): the
+// scores of attention again, without their maximum, for lse is known.
+//
+// One workgroup: KW x 2 blocks of 32 tokens of one key/value head, against
+// every query that may see them.  A wave widens the keys of its two blocks to
 // bf16 once (exact, scale included) and keeps them in registers; query rows
-// (token * group + head of the group) come in tiles of 32 through LDS, in the
-// order in which the matrix instruction takes them, a step or two ahead.  KW waves
-// share a tile for different blocks; with KW = 1 the four waves take different
-// tiles of the same blocks and are summed at the end, which makes four times as
-// many workgroups where there are few blocks.
-template <int D, int NB, int KW>
+// (token * group + head of the group) pass in tiles of 32 through LDS, a step or two
+// ahead of their products.  With KW = 4 the waves share a tile for different blocks;
+// with KW = 1 they take different tiles of the same blocks and are summed at the
+// end, which makes four times as many workgroups where there are few blocks.
+//
+// Bound by the vector unit: 16 cycles for a score's fused multiply-add, exponential
+// and sum, next to 32 x 32 of them in CH matrix instructions of 32 cycles.  4096
+// causal queries of 32 heads of 128: 94 us (730 TFLOP/s), of which about 110 thousand
+// of 195 thousand cycles are vector instructions and 68 thousand matrix ones.  Queries in
+// 16-byte pieces straight from their rows kept the address unit as busy (104 us);
+// exponentials of one tile woven between the products of the next gained nothing (99).
+template <int D, int KW>
 __global__ __launch_bounds__(kThreads, 2) void k_weigh(WeighArgs a) {
-  constexpr int RW = kWaves / KW, CH = D / 16;           // tiles of a step; 1 KiB chunks of a tile
-  constexpr int kStep = RW * CH * 1024, kLoads = RW * CH / kWaves;  // bytes; loads of a wave
-  constexpr int kRing = KW == 1 ? 2 : 3;                            // steps in LDS
+  constexpr int NB = 2;                             // blocks of a wave
+  constexpr int RW = kWaves / KW, CH = D / 16;      // waves of different tiles; 1 KiB chunks of a tile
+  constexpr int TW = KW > 1 && D <= 128 ? 2 : 1;    // tiles of a wave in a step
+  constexpr int kRows = 32 * TW * RW;               // of a step
+  constexpr int kChunks = TW * RW * CH / kWaves, kLoads = kChunks + 1;  // of a wave; its loads: these and an lse
+  constexpr int kStep = kRows * (2 * D + 4);                            // bytes
+  constexpr int kRing = KW == 1 || D == 256 ? 2 : 3;                    // steps in LDS
   __shared__ __attribute__((aligned(1024))) uint8_t ring[kRing * kStep];
   const int s = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 63, col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), kw = wave % KW, rw = wave / KW;
   const SeqView q = seq_view(a.b, a.T, s);
-  // Early tokens are seen by more rows than late ones: every other 256
-  // workgroups go through the blocks backwards, so that a compute unit's workgroups
-  // come out alike.
-  const bool backwards = a.causal && (((blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) >> 8 & 1);
-  const int first = (int)(backwards ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * KW * NB;  // the workgroup's first block
-  if ((int64_t)first * kBlock >= q.len) return;
+  // Early tokens are seen by more rows than late ones under a causal mask: a wave
+  // takes blocks from both ends, and all workgroups have the same work.
+  const int blocks = (q.len + kBlock - 1) / kBlock, first = blockIdx.x * KW;  // the workgroup's first block
+  if (first * NB >= blocks) return;
   const int rows = q.rows * a.group;
-  // a query sees tokens below len - n + its number + 1; rows before r0 see none of these
+  // a query sees tokens below len - n + its number + 1; rows before see none of these
   const int before = q.len - q.n;
-  const int64_t skip = a.causal ? (int64_t)max(first * kBlock - before, 0) * a.group : 0;
-  const int tile0 = (int)min(skip, (int64_t)rows) / 32, steps = ((rows + 31) / 32 - tile0 + RW - 1) / RW;
+  auto tile_of = [&](int block) {
+    const int64_t skip = a.causal ? (int64_t)max(block * kBlock - before, 0) * a.group : 0;
+    return (int)min(skip, (int64_t)rows) / 32;
+  };
+  const int row0 = tile_of(first) * 32, steps = (rows - row0 + kRows - 1) / kRows;
+  const int lone = (tile_of(max(blocks - first - KW, first)) * 32 - row0) / kRows;  // steps before the late blocks are seen
   Frag k[NB][D / 16];
   int block[NB], limit[NB];  // number; its first token, counted from len - n
   bool ok[NB];
   each<0, NB>([&](auto N) {
     constexpr int b = decltype(N)::value;
-    block[b] = first + kw * NB + b;
-    const int page = (int64_t)block[b] * kBlock < q.len ? page_of(a.b.table, a.b.table_blocks, a.c.pages, s, block[b]) : -1;
+    block[b] = b == 0 ? first + kw : blocks - 1 - first - kw;
+    const int page = (b == 0 ? block[b] * NB < blocks : block[b] > first + kw) ? page_of(a.b.table, a.b.table_blocks, a.c.pages, s, block[b]) : -1;
     ok[b] = page >= 0;
     limit[b] = block[b] * kBlock - before;
     const int64_t at = block_of(a.c, max(page, 0), h);
@@ -90,71 +107,91 @@ __global__ __launch_bounds__(kThreads, 2) void k_weigh(WeighArgs a) {
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[b][i] = 0.0f;
-  // Step t's row of this lane: the one whose queries it loads is also its column.
-  static_assert(KW == 1 || KW == kWaves, "a wave loads queries of its own tile");
-  struct Place {
-    int row, tok, head;
-  };
-  auto place = [&](int t) {
-    const int row = (tile0 + t * RW + rw) * 32 + col, real = min(row, rows - 1);
-    const int tok = (int)((uint32_t)real / (uint32_t)a.group);
-    return Place{row, tok, h * a.group + (real - tok * a.group)};
-  };
-  // The wave's share of a step's queries: kLoads chunks of its tile.
-  auto load_step = [&](int t, const Place& p) {
-    const uint16_t* src = a.q + (q.q0 + p.tok) * a.q_token + (int64_t)p.head * a.q_head + half * (D / 2);
-    each<0, kLoads>([&](auto L) {
-      const int x = wave * kLoads + decltype(L)::value;
-      __builtin_amdgcn_global_load_lds((const void*)(src + x % CH * 8), (LDS_AS void*)(ring + (t % kRing) * kStep + x * 1024), 16,
-                                       0, 0);
+  auto token_of_row = [&](int row) { return a.magic ? (int)(__umulhi((uint32_t)row, a.magic) >> a.shift) : row; };
+  // The wave's share of a step's queries and of their lse.  A load takes 1 KiB of
+  // whole rows, so that its lanes read whole lines; each lane finds one row's place and
+  // hands it to the lanes that load it.  In a row's place in LDS its 16-byte units are
+  // swapped by the row's number, so that lanes that read the same unit of 32 rows meet
+  // in no bank.
+  constexpr int kUnits = D / 8, kSwap = kUnits < 16 ? kUnits - 1 : 15, kPer = 64 / kUnits;  // kPer: rows of a load
+  const int from = (KW == 1 ? 0 : wave * kChunks * kPer) + lane / kUnits;
+  const int own = KW == 1 ? rw * 32 + col : lane % kRows;  // row of a step that this lane finds
+  auto load_step = [&](int t) {
+    uint8_t* to = ring + (t % kRing) * kStep;
+    const int row = min(row0 + t * kRows + own, rows - 1);  // behind the last row it repeats, and adds nothing
+    const int tok = token_of_row(row), head = h * a.group + (row - tok * a.group);
+    const uint64_t src = (uint64_t)(a.q + (q.q0 + tok) * a.q_token + (int64_t)head * a.q_head);
+    each<0, kChunks>([&](auto L) {
+      constexpr int l = decltype(L)::value;
+      const uint32_t lo = __shfl((uint32_t)src, from + l * kPer), hi = __shfl((uint32_t)(src >> 32), from + l * kPer);
+      const uint32_t unit = (lane % kUnits) ^ ((from + l * kPer) & kSwap);
+      __builtin_amdgcn_global_load_lds((const void*)((((uint64_t)hi << 32) | lo) + unit * 16),
+                                       (LDS_AS void*)(to + (wave * kChunks + l) * 1024), 16, 0, 0);
     });
-  };
-  // -lse of a row in base 2; -inf where it adds nothing
-  auto negative_lse = [&](const Place& p) {
-    const float l = a.lse[(q.q0 + p.tok) * a.q_heads + p.head];
-    return p.row < rows && l != -INFINITY ? -l * kLog2e : -INFINITY;
+    if (lane * KW / (32 * TW) == kw)
+      __builtin_amdgcn_global_load_lds((const void*)(a.lse + (q.q0 + tok) * a.q_heads + head),
+                                       (LDS_AS void*)(to + kRows * 2 * D + rw * 128), 4, 0, 0);
   };
   if (steps > 0) {
-    Place at[kRing];  // of steps t, t + 1, ...; behind the last step rows repeat, and add nothing
-    each<0, kRing - 1>([&](auto t) {
-      at[decltype(t)::value] = place(decltype(t)::value);
-      load_step(decltype(t)::value, at[decltype(t)::value]);
-    });
-    float neg = negative_lse(at[0]);
-    for (int t = 0; t < steps; ++t) {
-      at[kRing - 1] = place(t + kRing - 1);
-      const float neg_next = negative_lse(at[1]);
-      asm volatile("" ::: "memory");
-      // step t is in: only the loads of later ones and an lse may still be on their way
-      __builtin_amdgcn_s_waitcnt((((kRing - 2) * kLoads + 1) & 15) | (7 << 4) | (0 << 8));
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      load_step(t + kRing - 1, at[kRing - 1]);  // where step t - 1 was
-      const uint8_t* tile = ring + (t % kRing) * kStep + rw * CH * 1024 + lane * 16;
-      f32x16 sc[NB];
+    each<0, kRing - 1>([&](auto t) { load_step(decltype(t)::value); });
+    // Tiles j to j + M of the wave's in step t, with its first N blocks
+    auto scores = [&](int t, int j, auto m, auto n) {
+      constexpr int M = decltype(m)::value, N = decltype(n)::value;
+      const uint8_t* slot = ring + (t % kRing) * kStep;
+      const int tile = rw * TW + j;
+      f32x16 sc[M][N];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) sc[b] = f32x16{};
+      for (int i = 0; i < M; ++i)
+#pragma unroll
+        for (int b = 0; b < N; ++b) sc[i][b] = f32x16{};
       each<0, CH>([&](auto C) {
-        Frag f;
-        f.w = *reinterpret_cast<const i32x4*>(tile + decltype(C)::value * 1024);
-        each<0, NB>([&](auto N) {
-          constexpr int b = decltype(N)::value;
-          sc[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[b][decltype(C)::value].b, f.b, sc[b], 0, 0, 0);
+        constexpr int c = decltype(C)::value;
+        each<0, M>([&](auto I) {
+          constexpr int i = decltype(I)::value;
+          Frag f;
+          f.w = *reinterpret_cast<const i32x4*>(slot + ((tile + i) * 32 + col) * (2 * D) +
+                                                ((half * (kUnits / 2) + c) ^ (col & kSwap)) * 16);
+          each<0, N>([&](auto B) {
+            constexpr int b = decltype(B)::value;
+            sc[i][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[b][c].b, f.b, sc[i][b], 0, 0, 0);
+          });
         });
       });
-      // columns of this tile that see a block only in part
-      const int first_tok = (int)((uint32_t)min((tile0 + t * RW + rw) * 32, rows - 1) / (uint32_t)a.group);
-      each<0, NB>([&](auto N) {
-        constexpr int b = decltype(N)::value;
-        if (a.causal && limit[b] + kBlock > first_tok + 1) {
+      each<0, M>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        const int at = row0 + t * kRows + (tile + i) * 32, row = at + col;
+        const float lse = reinterpret_cast<const float*>(slot + kRows * 2 * D)[(tile + i) * 32 + col];
+        const float neg = row < rows && lse != -INFINITY ? -lse * kLog2e : -INFINITY;  // -inf where it adds nothing
+        const int first_tok = token_of_row(min(at, rows - 1));
+        each<0, N>([&](auto B) {
+          constexpr int b = decltype(B)::value;
+          if (a.causal && limit[b] + kBlock > first_tok + 1) {  // columns of this tile that see a block only in part
+            const int tok = token_of_row(min(row, rows - 1));
 #pragma unroll
-          for (int i = 0; i < 16; ++i) sc[b][i] = limit[b] + token_of(i, half) <= at[0].tok ? sc[b][i] : -INFINITY;
-        }
+            for (int x = 0; x < 16; ++x) sc[i][b][x] = limit[b] + token_of(x, half) <= tok ? sc[i][b][x] : -INFINITY;
+          }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[b][i] += __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][i], a.scale2, neg));
+          for (int x = 0; x < 16; ++x) acc[b][x] += __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i][b][x], a.scale2, neg));
+        });
       });
-      neg = neg_next;
-      each<0, kRing - 1>([&](auto i) { at[decltype(i)::value] = at[decltype(i)::value + 1]; });
+    };
+    auto next = [&](int t) {
+      asm volatile("" ::: "memory");
+      // step t is in: only the loads of later ones may still be on their way
+      __builtin_amdgcn_s_waitcnt(((kRing - 2) * kLoads & 15) | (7 << 4) | (0 << 8));
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      load_step(t + kRing - 1);  // where step t - 1 was
+    };
+    int t = 0;
+    for (; t < lone; ++t) {
+      next(t);
+      scores(t, 0, Const<TW>{}, Const<1>{});
+    }
+    for (; t < steps; ++t) {
+      next(t);
+      for (int j = 0; j < TW; ++j)
+        if (j == 0 || row0 + t * kRows + j * 32 < rows) scores(t, j, Const<1>{}, Const<NB>{});
     }
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0);
@@ -180,14 +217,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_weigh(WeighArgs a) {
 
 template <int D>
 void launch(const WeighArgs& a, hipStream_t st) {
-  constexpr int NB = D == 256 ? 1 : 2;
-  const int blocks = (a.b.max_len + kBlock - 1) / kBlock;
-  const int64_t wide = (int64_t)((blocks + kWaves * NB - 1) / (kWaves * NB)) * a.c.kv_heads * a.b.S;
-  if (wide >= 512)
-    hipLaunchKernelGGL((k_weigh<D, NB, kWaves>), dim3((blocks + kWaves * NB - 1) / (kWaves * NB), a.c.kv_heads, a.b.S),
-                       dim3(kThreads), 0, st, a);
+  // With 256 workgroups of eight blocks every compute unit has one; below, four times
+  // as many of two blocks fill it better, though each reads the queries again.  At 256
+  // (2048 queries and tokens, 32 heads of 128) 45 us against 56, at 128 (1024 of
+  // them) 24 against 21, at 64 with four queries to a key (2048) 136 against 69.
+  const int blocks = (a.b.max_len + kBlock - 1) / kBlock, wide = (blocks + 2 * kWaves - 1) / (2 * kWaves);
+  if ((int64_t)wide * a.c.kv_heads * a.b.S >= 256)
+    hipLaunchKernelGGL((k_weigh<D, kWaves>), dim3(wide, a.c.kv_heads, a.b.S), dim3(kThreads), 0, st, a);
   else
-    hipLaunchKernelGGL((k_weigh<D, NB, 1>), dim3((blocks + NB - 1) / NB, a.c.kv_heads, a.b.S), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((k_weigh<D, 1>), dim3((blocks + 1) / 2, a.c.kv_heads, a.b.S), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace
@@ -206,8 +244,15 @@ extern "C" dllm_status dllm_cache_weigh(const dllm_cache* cache, const dllm_cach
   if (T > 0 && (!q || !lse)) return DLLM_ERR_INVALID_ARG;
   if (!stride_ok(q_token) || !stride_ok(q_head) || q_token % 8 != 0 || q_head % 8 != 0 || ((uintptr_t)q & 15u) != 0)
     return DLLM_ERR_UNSUPPORTED;
-  const WeighArgs a = {*cache, *batch, T, q, q_token, q_head, q_heads, q_heads / cache->kv_heads, scale * kLog2e,
-                       causal, lse, decay, weights};
+  WeighArgs a = {*cache, *batch, T, q, q_token, q_head, q_heads, q_heads / cache->kv_heads, scale * kLog2e,
+                 causal, lse, decay, weights, 0, 0};
+  if (a.group > 1) {
+    // magic = ceil(2^(31 + l) / group) < 2^32 with l = ceil(log2 group): exact below 2^31
+    int l = 1;
+    while ((1 << l) < a.group) ++l;
+    a.magic = (uint32_t)((((uint64_t)1 << (31 + l)) + (uint64_t)a.group - 1) / (uint64_t)a.group);
+    a.shift = l - 1;
+  }
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (cache->head_dim == 64) launch<64>(a, st);
   else if (cache->head_dim == 128) launch<128>(a, st);
