@@ -680,93 +680,88 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
 
 // ---- joining a tile's parts -------------------------------------------------------------------------------------
 
-// One workgroup for each 8 stretches and 32-row, 32-dim piece of a tile: where
+// One workgroup for each few stretches and 32-row, 32-dim piece of a tile: where
 // stretch w is the first to begin inside its tile, the piece is joined here from
-// w - 1's last part and the first parts of w, w + 1, ...  The waves take the parts
-// in turn, a few in flight at a time, and their shares are added in order.
-// (With a workgroup for every stretch, most of them only to find no work, this
-// kernel took 16 us where it now takes 6.)
-constexpr int kJoinStretches = 8;
-constexpr int kJoinThreads = 256, kJoinTurns = kJoinThreads / 64, kJoinFlight = 4;
+// w - 1's last part and the first parts of w, w + 1, ...  First the largest reference and
+// value scale of all parts, then their sums under these: the waves take the parts
+// in turn, a few in flight at a time, and what they have is added in order, so that the
+// same call has the same result.  (Rescaling what was there for each part, a chain of
+// dependent steps, took 28 us for 4 tiles of 64 parts where this takes XX; with a
+// workgroup for every stretch, most of them only to find no work, XX more.)
+constexpr int kJoinFlight = 4;
 
-// o, sum of a column under reference ref and value scale v.
-struct Share {
-  float o[16];
-  float ref, sum;
-  int v;
-};
-
-__device__ __forceinline__ void add_share(Share& a, const float4* x, float ref, float sum, int v) {
-  const float to = fmaxf(a.ref, ref);
-  const int v_to = max(a.v, v);
-  const float mine = part_of_ref(a.ref, to), theirs = part_of_ref(ref, to);
-  a.sum = a.sum * mine + sum * theirs;
-  const float m = mine * exact_power(a.v - v_to), t = theirs * exact_power(v - v_to);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    a.o[4 * i] = a.o[4 * i] * m + x[i].x * t;
-    a.o[4 * i + 1] = a.o[4 * i + 1] * m + x[i].y * t;
-    a.o[4 * i + 2] = a.o[4 * i + 2] * m + x[i].z * t;
-    a.o[4 * i + 3] = a.o[4 * i + 3] * m + x[i].w * t;
-  }
-  a.ref = to;
-  a.v = v_to;
-}
-
-template <int D, int BM>
-__global__ __launch_bounds__(kJoinThreads) void k_join(AttendArgs a) {
-  __shared__ float o_lds[kJoinTurns][4][64][4];
-  __shared__ float ref_lds[kJoinTurns][32], sum_lds[kJoinTurns][32];
-  __shared__ int v_lds[kJoinTurns];
-  const int sub = blockIdx.y, chunk = blockIdx.z;
+template <int D, int BM, int kTurns, int kStretches>
+__global__ __launch_bounds__(kTurns * 64) void k_join(AttendArgs a) {
+  __shared__ float o_lds[kTurns][4][64][4];
+  __shared__ float ref_lds[kTurns][32], sum_lds[kTurns][32];
+  __shared__ int v_lds[kTurns];
+  const int chunk = blockIdx.x, sub = blockIdx.y, stretch0 = blockIdx.z * kStretches;
   const int lane = threadIdx.x & 63, turn = threadIdx.x >> 6, col = lane & 31, half = lane >> 5;
-  const Stretch* all = reinterpret_cast<const Stretch*>(a.ws) + blockIdx.x * kJoinStretches;
-  uint64_t todo = __ballot(lane < kJoinStretches && all[lane].parts > 0);
-  for (bool again = false; todo; todo &= todo - 1) {
-    const int w0 = __ffsll((unsigned long long)todo) - 1, w = blockIdx.x * kJoinStretches + w0;
+  const Stretch* all = reinterpret_cast<const Stretch*>(a.ws) + stretch0;
+  uint64_t todo = __ballot(lane < kStretches && all[lane].parts > 0);
+  for (; todo; todo &= todo - 1) {
+    const int w0 = __ffsll((unsigned long long)todo) - 1, w = stretch0 + w0;
     const Stretch me = all[w0];
     const int row0 = me.rt * BM + sub * 32, parts = me.parts;
     if (row0 >= me.rows * a.group) continue;
-    if (again) __syncthreads();  // the shares of the one before are no longer read
-    again = true;
     const Row r = row_of(a, me.q0, me.rows, me.h, row0 + col);
-    Share mine;
-    mine.ref = -INFINITY, mine.sum = 0.0f, mine.v = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) mine.o[i] = 0.0f;
-    for (int i0 = turn; i0 < parts; i0 += kJoinTurns * kJoinFlight) {
-      float4 x[kJoinFlight][4];
-      float ref[kJoinFlight], sum[kJoinFlight];
-      int v[kJoinFlight];
-      each<0, kJoinFlight>([&](auto F) {
-        constexpr int f = decltype(F)::value;
-        const int i = i0 + f * kJoinTurns;
-        if (i < parts) {
-          const PartRows<D>* p = part_of<D>(a, BM / 32, i == 0 ? w - 1 : w + i - 1, i == 0 ? 1 : 0) + sub;
-          each<0, 4>([&](auto c) { x[f][decltype(c)::value] = *reinterpret_cast<const float4*>(p->o[chunk][decltype(c)::value][lane]); });
-          ref[f] = p->ref[col], sum[f] = p->sum[col], v[f] = p->v_ref;
-        }
-      });
-      each<0, kJoinFlight>([&](auto F) {
-        constexpr int f = decltype(F)::value;
-        if (i0 + f * kJoinTurns < parts) add_share(mine, x[f], ref[f], sum[f], v[f]);
-      });
+    auto part = [&](int i) { return part_of<D>(a, BM / 32, i == 0 ? w - 1 : w + i - 1, i == 0 ? 1 : 0) + sub; };
+    float ref = -INFINITY, sum = 0.0f;
+    int v = 0;
+    for (int i = 2 * turn + half; i < parts; i += 2 * kTurns) {
+      const PartRows<D>* p = part(i);
+      ref = fmaxf(ref, p->ref[col]), v = max(v, p->v_ref);
     }
-    if (half == 0) ref_lds[turn][col] = mine.ref, sum_lds[turn][col] = mine.sum;
-    if (lane == 0) v_lds[turn] = mine.v;
+    ref = fmaxf(ref, __shfl_xor(ref, 32)), v = max(v, __shfl_xor(v, 32));
+    if (half == 0) ref_lds[turn][col] = ref;
+    if (lane == 0) v_lds[turn] = v;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) ref = fmaxf(ref, ref_lds[i][col]), v = max(v, v_lds[i]);
+    float o[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = 0.0f;
+    if (r.real)
+      for (int i0 = turn; i0 < parts; i0 += kTurns * kJoinFlight) {
+        float4 x[kJoinFlight][4];
+        float part_ref[kJoinFlight], part_sum[kJoinFlight];
+        int part_v[kJoinFlight];
+        each<0, kJoinFlight>([&](auto F) {
+          constexpr int f = decltype(F)::value;
+          const PartRows<D>* p = part(min(i0 + f * kTurns, parts - 1));  // the last one again adds nothing
+          each<0, 4>([&](auto c) { x[f][decltype(c)::value] = *reinterpret_cast<const float4*>(p->o[chunk][decltype(c)::value][lane]); });
+          part_ref[f] = p->ref[col], part_sum[f] = p->sum[col], part_v[f] = p->v_ref;
+        });
+        each<0, kJoinFlight>([&](auto F) {
+          constexpr int f = decltype(F)::value;
+          if (i0 + f * kTurns < parts) {
+            const float m = part_of_ref(part_ref[f], ref), t = m * exact_power(part_v[f] - v);
+            sum += m * part_sum[f];
+            each<0, 4>([&](auto C) {
+              constexpr int c = decltype(C)::value;
+              o[4 * c] += x[f][c].x * t, o[4 * c + 1] += x[f][c].y * t;
+              o[4 * c + 2] += x[f][c].z * t, o[4 * c + 3] += x[f][c].w * t;
+            });
+          }
+        });
+      }
+    if (half == 0) sum_lds[turn][col] = sum;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<float4*>(o_lds[turn][c][lane]) =
-          make_float4(mine.o[4 * c], mine.o[4 * c + 1], mine.o[4 * c + 2], mine.o[4 * c + 3]);
+      *reinterpret_cast<float4*>(o_lds[turn][c][lane]) = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
     __syncthreads();
-    if (turn != 0) continue;
-    for (int i = 1; i < min(parts, kJoinTurns); ++i) {
-      float4 x[4];
+    if (turn == 0) {
+      for (int i = 1; i < min(parts, kTurns); ++i) {
+        sum += sum_lds[i][col];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const float4*>(o_lds[i][c][lane]);
-      add_share(mine, x, ref_lds[i][col], sum_lds[i][col], v_lds[i]);
+        for (int c = 0; c < 4; ++c) {
+          const float4 x = *reinterpret_cast<const float4*>(o_lds[i][c][lane]);
+          o[4 * c] += x.x, o[4 * c + 1] += x.y, o[4 * c + 2] += x.z, o[4 * c + 3] += x.w;
+        }
+      }
+      write_rows<D>(a, r, chunk, o, ref, sum, v);
     }
-    write_rows<D>(a, r, chunk, mine.o, mine.ref, mine.sum, mine.v);
+    __syncthreads();  // before the next one's shares
   }
 }
 
@@ -784,12 +779,12 @@ void launch(AttendArgs a, hipStream_t st) {
     a.parts = kManyParts;
     a.min_steps = 2;
     hipLaunchKernelGGL((k_attend_many<D, RG>), dim3(a.parts), dim3(kThreads), 0, st, a);
-    hipLaunchKernelGGL((k_join<D, BM>), dim3(a.parts / kJoinStretches, BM / 32, D / 32), dim3(kJoinThreads), 0, st, a);
+    hipLaunchKernelGGL((k_join<D, BM, 8, 8>), dim3(D / 32, BM / 32, a.parts / 8), dim3(8 * 64), 0, st, a);
   } else {
     a.parts = kNarrowParts;
     a.min_steps = kWaves;
     hipLaunchKernelGGL(k_attend_few<D>, dim3(a.parts), dim3(kThreads), 0, st, a);
-    hipLaunchKernelGGL((k_join<D, 32>), dim3(a.parts / kJoinStretches, 1, D / 32), dim3(kJoinThreads), 0, st, a);
+    hipLaunchKernelGGL((k_join<D, 32, 4, 4>), dim3(D / 32, 1, a.parts / 4), dim3(4 * 64), 0, st, a);
   }
 }
 
