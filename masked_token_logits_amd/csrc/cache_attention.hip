@@ -5,6 +5,8 @@
 #include "persistent_sched.h"
 #include "rotary_angle.h"
 
+#include <algorithm>
+
 namespace dllm {
 namespace {
 
@@ -150,24 +152,27 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void k_attend_few(Atten
     int kb, vb;
     int j = at.begin + wave;
     const int clean = min(last, whole);  // blocks below need no mask
+    auto add = [&](const i32x4* k, const i32x4* v, int kb, int vb) {
+      const f32x16 sc = scores<D>(qf, k, scale_value(kb));
+      cover<D>(acc, largest(sc), a.scale2);
+      Frag p[2];
+      probabilities<D>(acc, sc, a.scale2, p);
+      add_values<D>(acc, p, v, cover_values<D>(acc, vb));
+    };
     if (j < clean) {
+      // two blocks in turn, each in registers of its own: copying the one in flight
+      // to the other would wait for it
+      i32x4 k2[D / 32], v2[D / 32];
+      int kb2, vb2;
       bool ok = walk.fetch(j, k, v, kb, vb);
-      do {
-        i32x4 k_next[D / 32], v_next[D / 32];
-        int kb_next, vb_next;
-        const bool ok_next = walk.fetch(min(j + kWaves, clean - 1), k_next, v_next, kb_next, vb_next);
-        if (ok) {
-          const f32x16 sc = scores<D>(qf, k, scale_value(kb));
-          cover<D>(acc, largest(sc), a.scale2);
-          Frag p[2];
-          probabilities<D>(acc, sc, a.scale2, p);
-          add_values<D>(acc, p, v, cover_values<D>(acc, vb));
-        }
-        ok = ok_next, kb = kb_next, vb = vb_next;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) k[c] = k_next[c], v[c] = v_next[c];
-        j += kWaves;
-      } while (j < clean);
+      for (;;) {
+        const bool ok2 = walk.fetch(min(j + kWaves, clean - 1), k2, v2, kb2, vb2);
+        if (ok) add(k, v, kb, vb);
+        if ((j += kWaves) >= clean) break;
+        ok = walk.fetch(min(j + kWaves, clean - 1), k, v, kb, vb);
+        if (ok2) add(k2, v2, kb2, vb2);
+        if ((j += kWaves) >= clean) break;
+      }
     }
     for (; j < last; j += kWaves) {
       if (!walk.fetch(j, k, v, kb, vb)) continue;
@@ -686,8 +691,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
 // value scale of all parts, then their sums under these: the waves take the parts
 // in turn, a few in flight at a time, and what they have is added in order, so that the
 // same call has the same result.  (Rescaling what was there for each part, a chain of
-// dependent steps, took 28 us for 4 tiles of 64 parts where this takes XX; with a
-// workgroup for every stretch, most of them only to find no work, XX more.)
+// dependent steps, was slower, and so was a workgroup for every stretch, most of them
+// only to find no work.  The pieces of one tile are neighbours in the grid, for then
+// they spread over the 8 chips: 4 tiles of 64 parts, 29 MB, take 11.5 us, all on
+// one chip 31.)
 constexpr int kJoinFlight = 4;
 
 template <int D, int BM, int kTurns, int kStretches>
@@ -765,8 +772,11 @@ __global__ __launch_bounds__(kTurns * 64) void k_join(AttendArgs a) {
   }
 }
 
-// Row tiles of more than this many rows take the kernel for many.
-constexpr int kFewRows = 32;
+// A head with more rows than this takes the kernel for many.  For head_dim 128 and few /
+// many: 64 rows of 32 heads over 4096 tokens 24 / 36 us, 128 rows 27 / 38, 64 rows of 8
+// heads of 16 such sequences 40 / 91; 224 rows of 32 heads 41 / 42, of 4 heads over
+// 131072 tokens 144 / 84.  Where 128 rows read 131072 tokens, 95 / 80, the rule is late.
+constexpr int kFewRows = 128;
 
 constexpr int many_groups(int D) { return D == 256 ? 1 : 2; }
 
@@ -782,7 +792,7 @@ void launch(AttendArgs a, hipStream_t st) {
     hipLaunchKernelGGL((k_join<D, BM, 8, 8>), dim3(D / 32, BM / 32, a.parts / 8), dim3(8 * 64), 0, st, a);
   } else {
     a.parts = kNarrowParts;
-    a.min_steps = kWaves;
+    a.min_steps = std::min(kWaves, (a.b.max_len + kBlock - 1) / kBlock);  // a short tile's waves wait for nobody else's
     hipLaunchKernelGGL(k_attend_few<D>, dim3(a.parts), dim3(kThreads), 0, st, a);
     hipLaunchKernelGGL((k_join<D, 32, 4, 4>), dim3(D / 32, 1, a.parts / 4), dim3(4 * 64), 0, st, a);
   }

@@ -77,13 +77,20 @@ __device__ __forceinline__ int64_t head_steps(const AttendArgs& a, const SeqView
   return n;
 }
 
-// Inclusive sum over the workgroup's 256 threads.
-__device__ __forceinline__ int64_t scan(int64_t x, int64_t* lds) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Inclusive sum over the wave's lanes.
+__device__ __forceinline__ int64_t scan_wave(int64_t x) {
+  const int lane = threadIdx.x & 63;
   for (int o = 1; o < 64; o <<= 1) {
     const int64_t y = __shfl_up(x, o);
     if (lane >= o) x += y;
   }
+  return x;
+}
+
+// Inclusive sum over the workgroup's 256 threads.
+__device__ __forceinline__ int64_t scan(int64_t x, int64_t* lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  x = scan_wave(x);
   __syncthreads();
   if (lane == 63) lds[wave] = x;
   __syncthreads();
@@ -105,7 +112,18 @@ __device__ Stretch find_stretch(const AttendArgs& a, int64_t* lds, int* number, 
   int& found_s = *reinterpret_cast<int*>(lds + kScheduleThreads / 64 + 1);
   const int tid = threadIdx.x;
   int64_t total = 0, mine = 0, upto = 0;
-  if (a.b.S == 1) {
+  // Up to 64 sequences, where rows are few, every wave looks through by itself, one to
+  // a lane: with no barrier, and no second look at the sequence that it finds (it saves 0.5
+  // to 1 us; where rows are many the registers cost more).
+  const bool by_wave = BM == 32 && a.b.S > 1 && a.b.S <= 64;
+  SeqView lanes;
+  if (by_wave) {
+    const int lane = tid & 63;
+    lanes = seq_view(a.b, a.T, min(lane, a.b.S - 1));
+    mine = lane < a.b.S ? head_steps<BM, KEYS>(a, lanes) * a.c.kv_heads : 0;
+    upto = scan_wave(mine);
+    total = __shfl(upto, 63);
+  } else if (a.b.S == 1) {
     total = head_steps<BM, KEYS>(a, seq_view(a.b, a.T, 0)) * a.c.kv_heads;
   } else {
     for (int s0 = 0; s0 < a.b.S; s0 += kScheduleThreads) {
@@ -127,7 +145,16 @@ __device__ Stretch find_stretch(const AttendArgs& a, int64_t* lds, int* number, 
   const int64_t lo = quotient(total * w, parts), hi = quotient(total * (w + 1), parts);
   *steps = hi - lo;
   int64_t at = 0;  // the line up to sequence r.s
-  if (a.b.S > 1) {
+  SeqView q;
+  if (by_wave) {
+    const int found = __ffsll((unsigned long long)__ballot(upto - mine <= lo && lo < upto)) - 1;
+    r.s = __builtin_amdgcn_readfirstlane(found);
+    at = __shfl(upto - mine, found);
+    q.q0 = __builtin_amdgcn_readlane((int)lanes.q0, r.s);
+    q.n = __builtin_amdgcn_readlane(lanes.n, r.s);
+    q.rows = __builtin_amdgcn_readlane(lanes.rows, r.s);
+    q.len = __builtin_amdgcn_readlane(lanes.len, r.s);
+  } else if (a.b.S > 1) {
     for (int s0 = 0; s0 < a.b.S; s0 += kScheduleThreads) {
       if (a.b.S > kScheduleThreads) {
         mine = s0 + tid < a.b.S ? head_steps<BM, KEYS>(a, seq_view(a.b, a.T, s0 + tid)) * a.c.kv_heads : 0;
@@ -145,7 +172,7 @@ __device__ Stretch find_stretch(const AttendArgs& a, int64_t* lds, int* number, 
     r.s = found_s;
     at = found_at;
   }
-  const SeqView q = seq_view(a.b, a.T, r.s);
+  if (!by_wave) q = seq_view(a.b, a.T, r.s);
   r.q0 = q.q0, r.rows = q.rows;
   const int64_t per_head = head_steps<BM, KEYS>(a, q);
   r.h = (int)quotient(lo - at, per_head);
