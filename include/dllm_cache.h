@@ -137,6 +137,8 @@ size_t dllm_cache_attention_workspace_bytes(const dllm_cache *cache, const dllm_
  *   scale    finite, > 0 (a normal float32)
  *   out      [T, q_heads, D] bf16, 16-byte aligned
  *   lse      [T, q_heads] float32, or NULL
+ * out and lse overlap no input and not each other; T * q_heads < 2^31 - 1024
+ * (else DLLM_ERR_UNSUPPORTED; the same for dllm_cache_weigh).
  * A query that sees no token gets out = 0 and lse = -inf.
  * Sums are fp32.  For its product with v a probability is rounded to fp16
  * (its own sum takes it unrounded), and a value counts to within 2^-33 of the

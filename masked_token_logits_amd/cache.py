@@ -136,7 +136,7 @@ class Rotary(_Queued):
                                            positions.data_ptr(), 1 if transpose else 0, y.data_ptr(), y.stride(0),
                                            y.stride(1), stream)
 
-        self._call("dllm_rotary", (x, positions, out), make)
+        self._call("dllm_rotary", (x, positions, out, self.turns), make)
         return box[0]
 
 
@@ -167,7 +167,9 @@ class CacheBatch:
         self.cu, self.lens, self.table = cu, lens, table
         self.struct = _abi.dllm_cache_batch(cu.data_ptr(), lens.data_ptr(), table.data_ptr(), self.S, self.blocks,
                                             self.max_new or (1 << 31) - 1, max_len)
-        self._ws = {}
+
+    def _tensors(self):
+        return self.cu, self.lens, self.table
 
 
 class BlockCache(_Queued):
@@ -209,6 +211,9 @@ class BlockCache(_Queued):
         self.struct = _abi.dllm_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.pages,
                                       self.kv_heads, self.head_dim)
 
+    def _buffers(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
     def batch(self, cu, lens, table, max_new: int | None = None, max_len: int | None = None) -> CacheBatch:
         return CacheBatch(cu, lens, table, max_new, max_len, self.device)
 
@@ -247,7 +252,8 @@ class BlockCache(_Queued):
                 v.stride(0), v.stride(1), start.data_ptr(), positions.data_ptr() if positions is not None else None,
                 plan, stream)
 
-        self._call("dllm_cache_write", (k, v, start, positions), make)
+        self._call("dllm_cache_write", (k, v, start, positions, rotary.turns if rotary is not None else None,
+                                        *self._buffers(), *batch._tensors()), make)
 
     def attend(self, batch: CacheBatch, q, scale: float | None = None, causal: bool = False, out=None, lse=False):
         """Queue attention of ``q`` [T, q_heads, head_dim] over the cache;
@@ -264,11 +270,9 @@ class BlockCache(_Queued):
         if given is not None:
             _need(given, "lse", (torch.float32,), (T, H), self.device)
         want = given is not None or bool(lse)
-        nbytes = batch._ws.get((id(self), H))
-        if nbytes is None:
-            nbytes = _abi.dllm_cache_attention_workspace_bytes(self.struct, batch.struct, H)
-            if nbytes == 0:
-                raise DllmError(DLLM_ERR_INVALID_ARG, "dllm_cache_attention_workspace_bytes")
+        nbytes = _abi.dllm_cache_attention_workspace_bytes(self.struct, batch.struct, H)
+        if nbytes == 0:
+            raise DllmError(DLLM_ERR_INVALID_ARG, "dllm_cache_attention_workspace_bytes")
         box = [out, given]
 
         def make(stream):
@@ -283,7 +287,7 @@ class BlockCache(_Queued):
                 1 if causal else 0, o.data_ptr(), l.data_ptr() if l is not None else None, ws.data_ptr(), nbytes,
                 stream)
 
-        self._call("dllm_cache_attention", (q, out, given), make)
+        self._call("dllm_cache_attention", (q, out, given, *self._buffers(), *batch._tensors()), make)
         return (box[0], box[1]) if want else box[0]
 
     def weigh(self, batch: CacheBatch, q, lse, weights, scale: float | None = None, causal: bool = False,
@@ -303,7 +307,7 @@ class BlockCache(_Queued):
                 C.byref(self.struct), C.byref(batch.struct), T, q.data_ptr(), q.stride(0), q.stride(1), H, scale,
                 1 if causal else 0, lse.data_ptr(), decay, weights.data_ptr(), stream)
 
-        self._call("dllm_cache_weigh", (q, lse, weights), make)
+        self._call("dllm_cache_weigh", (q, lse, weights, *self._buffers(), *batch._tensors()), make)
 
     def evict(self, batch: CacheBatch, weights, keep, table_out, sink: int = 0, recent: int = 0, pool: int = 1,
               lens_out=None, kept=None, weights_out=None):
@@ -351,5 +355,6 @@ class BlockCache(_Queued):
                 pool, table_out.data_ptr(), blocks, box[0].data_ptr(), box[1].data_ptr(), box[2].data_ptr(),
                 ws.data_ptr(), nbytes, stream)
 
-        self._call("dllm_cache_evict", (weights, keep, table_out, lens_out, kept, weights_out), make)
+        self._call("dllm_cache_evict", (weights, keep, table_out, lens_out, kept, weights_out, *self._buffers(),
+                                        *batch._tensors()), make)
         return tuple(box)

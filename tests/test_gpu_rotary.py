@@ -169,3 +169,27 @@ def test_rotary_no_tokens():
     import masked_token_logits_amd as mtl
     x = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
     assert mtl.Rotary(64)(x, dev_i32([])).shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("T,H,D,r", [(5, 1, 64, 32), (9, 3, 128, 128), (3, 40, 64, 64), (17, 2, 512, 512), (2, 5, 256, 48),
+                                     (11, 7, 72, 16)])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rotary_alignment_changes_nothing(T, H, D, r, layout):
+    """Aligned heads go in 16-byte pieces, several tokens to a workgroup where heads are few; the same values
+    one element off go one by one, to the same bits."""
+    import torch
+
+    import masked_token_logits_amd as mtl
+    g = torch.Generator(device="cuda").manual_seed(T + D)
+    rot = mtl.Rotary(D, r, layout=layout)
+    x = torch.randn(T, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    pos = torch.randint(-1000, 200000, (T,), generator=g, device="cuda", dtype=torch.int32)
+    off = torch.empty(T * H * D + 1, dtype=torch.bfloat16, device="cuda")[1:].view(T, H, D)
+    off.copy_(x)
+    for transpose in (False, True):
+        y = rot(x, pos, transpose=transpose)
+        z = rot(off, pos, out=torch.empty(T * H * D + 1, dtype=torch.bfloat16, device="cuda")[1:].view(T, H, D),
+                transpose=transpose)
+        assert torch.equal(y, z)
+        inplace = x.clone()
+        assert rot(inplace, pos, out=inplace, transpose=transpose) is inplace and torch.equal(inplace, y)
