@@ -98,8 +98,8 @@ dllm_status dllm_rotary_frequencies(int32_t rotary_dim, double base, int32_t sca
  *               y to the gradient of x
  * rotary_dim <= D <= DLLM_ROTARY_DIM_MAX.  T = 0 queues nothing.  Pointers
  * and strides need no alignment beyond the element's 2 bytes; the fast path
- * takes 16-byte aligned pointers, strides and D in multiples of 8, and
- * rotary_dim in multiples of 16.
+ * takes 16-byte aligned pointers, strides and D in multiples of 8, and in the
+ * layout HALF a rotary_dim in multiples of 16.
  */
 dllm_status dllm_rotary(const dllm_rotary_plan *plan, const uint16_t *x, int64_t T, int32_t H, int32_t D,
                         int64_t x_token, int64_t x_head, const int32_t *positions, int32_t transpose,

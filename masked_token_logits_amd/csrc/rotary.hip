@@ -76,7 +76,7 @@ struct PieceArgs {
 // take 14.0.
 __global__ __launch_bounds__(kThreads) void k_rotary_pieces(PieceArgs a) {
   __shared__ float4 cs[kTokens][DLLM_ROTARY_DIM_MAX / 4];  // two pairs' (cos, sin)
-  const int half = a.plan.rotary_dim / 2, rotated = a.plan.rotary_dim / 16, of_token = a.H * a.pieces;
+  const int half = a.plan.rotary_dim / 2, rotated = (a.plan.rotary_dim + 15) / 16, of_token = a.H * a.pieces;
   const bool halves = a.plan.layout == DLLM_ROTARY_HALF;
   for (int64_t t0 = (int64_t)blockIdx.x * a.tokens; t0 < a.T; t0 += (int64_t)gridDim.x * a.tokens) {
     const int tokens = (int)min(a.T - t0, (int64_t)a.tokens), all = tokens * of_token;
@@ -126,7 +126,8 @@ __global__ __launch_bounds__(kThreads) void k_rotary_pieces(PieceArgs a) {
             const float2 ci = i % 2 ? make_float2(c[i / 2].z, c[i / 2].w) : make_float2(c[i / 2].x, c[i / 2].y);
             uint32_t& w = i < 4 ? w0[i] : w1[i - 4];
             const float xa = bf16_float(w & 0xffff), xb = bf16_float(w >> 16);
-            w = float_bf16(rotated_a(xa, xb, ci)) | float_bf16(rotated_b(xa, xb, ci)) << 16;
+            const uint32_t y = float_bf16(rotated_a(xa, xb, ci)) | float_bf16(rotated_b(xa, xb, ci)) << 16;
+            w = 8 * piece + i < half ? y : w;  // the last piece may hold dimensions behind the rotated ones
           }
         }
       }
@@ -188,8 +189,8 @@ dllm_status dllm_rotary(const dllm_rotary_plan* plan, const uint16_t* x, int64_t
   if (x == y && (x_token != y_token || x_head != y_head)) return DLLM_ERR_INVALID_ARG;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const bool aligned = (((uintptr_t)x | (uintptr_t)y) & 15u) == 0 && (x_token | x_head | y_token | y_head | D) % 8 == 0;
-  if (aligned && plan->rotary_dim % 16 == 0) {
-    const int pieces = plan->rotary_dim / 16 + (D - plan->rotary_dim + 15) / 16, all = H * pieces;
+  if (aligned && (plan->rotary_dim % 16 == 0 || plan->layout == DLLM_ROTARY_INTERLEAVED)) {
+    const int rotated = (plan->rotary_dim + 15) / 16, pieces = rotated + (D - 16 * rotated + 15) / 16, all = H * pieces;
     const int fit = dllm::kThreads / all, tokens = fit < 1 ? 1 : fit < dllm::kTokens ? fit : dllm::kTokens;
     const auto per = [](int d) { return (uint32_t)((((uint64_t)1 << 32) + d - 1) / d); };
     const dllm::PieceArgs a = {*plan, x, T, (int)H, (int)D, x_token, x_head, positions, (int)transpose, y, y_token, y_head,

@@ -172,7 +172,7 @@ def test_rotary_no_tokens():
 
 
 @pytest.mark.parametrize("T,H,D,r", [(5, 1, 64, 32), (9, 3, 128, 128), (3, 40, 64, 64), (17, 2, 512, 512), (2, 5, 256, 48),
-                                     (11, 7, 72, 16)])
+                                     (11, 7, 72, 16), (6, 3, 72, 70), (4, 5, 64, 2), (3, 33, 128, 50)])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 def test_rotary_alignment_changes_nothing(T, H, D, r, layout):
     """Aligned heads go in 16-byte pieces, several tokens to a workgroup where heads are few; the same values
