@@ -18,6 +18,9 @@ import torch
 from . import _abi
 from ._abi import DLLM_ERR_INVALID_ARG, DLLM_OK, DllmError
 
+# The current stream's handle: without the Stream object, a fifth of a small call's time.
+_stream_handle = torch._C._cuda_getCurrentRawStream
+
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # bf16 data or its bit pattern
 _BLOCK = _abi.DLLM_CACHE_BLOCK
 
@@ -57,7 +60,7 @@ class _Queued:
         if dev.type != "cuda":
             st = make(None)   # no device: the library's own checks answer
         elif self.stream is None and torch.cuda.current_device() == dev.index:
-            st = make(torch.cuda.current_stream(dev).cuda_stream)
+            st = make(_stream_handle(dev.index))
         else:
             with torch.cuda.device(dev):
                 stream = self.stream if self.stream is not None else torch.cuda.current_stream(dev)
