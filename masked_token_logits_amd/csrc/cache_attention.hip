@@ -12,7 +12,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kNarrowParts = 512;  // two workgroups to a compute unit
+constexpr int kNarrowParts = 256;  // a workgroup to a compute unit
 
 // ---- parts of a tile, in the workspace -------------------------------------------------------------------------
 
@@ -90,31 +90,50 @@ struct Walk {
   __device__ Walk(const AttendArgs& a_, int s_, int h_, int first, int last_, int len)
       : a(a_), s(s_), h(h_), base(first - 64), last(last_), have(len) {}
 
-  // Block j's scale bytes, and its keys and values on their way; false if it
-  // has no page.
-  __device__ __forceinline__ bool fetch(int j, i32x4* k, i32x4* v, int& kb, int& vb) {
-    const int lane = threadIdx.x & 63;
-    if (j >= base + 64 || j < base) {
-      base = j;
-      const int b = base + lane;
-      page = b < last ? page_of(a.b.table, a.b.table_blocks, a.c.pages, s, b) : -1;
-      const int64_t at = block_of(a.c, max(page, 0), h);
-      k_byte = a.c.k_scale[at];
-      v_byte = a.c.v_scale[at];
-      // wait for them here: behind the branch the wait would be for every load
-      // in flight, at every use
-      asm volatile("" : "+v"(page), "+v"(k_byte), "+v"(v_byte));
-    }
-    const int i = j - base;
-    const int p = __builtin_amdgcn_readlane(page, i);
-    kb = __builtin_amdgcn_readlane(k_byte, i);
-    vb = __builtin_amdgcn_readlane(v_byte, i);
-    const int64_t at = block_of(a.c, max(p, 0), h) * (kBlock * D) + lane * 16;
+  // Pages of 64 blocks from j on, and their scales on their way.
+  __device__ __forceinline__ void look(int j) {
+    base = j;
+    const int b = base + (threadIdx.x & 63);
+    page = b < last ? page_of(a.b.table, a.b.table_blocks, a.c.pages, s, b) : -1;
+    const int64_t at = block_of(a.c, max(page, 0), h);
+    k_byte = a.c.k_scale[at];
+    v_byte = a.c.v_scale[at];
+  }
+
+  // Wait for them here: behind a branch the wait would be for every load in
+  // flight, at every use.
+  __device__ __forceinline__ void looked() { asm volatile("" : "+v"(page), "+v"(k_byte), "+v"(v_byte)); }
+
+  // Block j's keys and values on their way; false if it has no page.
+  __device__ __forceinline__ bool load(int j, i32x4* k, i32x4* v) {
+    const int p = __builtin_amdgcn_readlane(page, j - base);
+    const int64_t at = block_of(a.c, max(p, 0), h) * (kBlock * D) + (threadIdx.x & 63) * 16;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) k[c] = *reinterpret_cast<const i32x4*>(a.c.k + at + c * 1024);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) v[c] = *reinterpret_cast<const i32x4*>(a.c.v + at + c * 1024);
     return p >= 0;
+  }
+
+  // The first look-up, with the block's loads behind it at once.
+  __device__ __forceinline__ bool first(int j, i32x4* k, i32x4* v, int& kb, int& vb) {
+    look(j);
+    const bool ok = load(j, k, v);
+    looked();
+    kb = __builtin_amdgcn_readlane(k_byte, 0), vb = __builtin_amdgcn_readlane(v_byte, 0);
+    return ok;
+  }
+
+  // Block j's scale bytes, and its keys and values on their way; false if it
+  // has no page.
+  __device__ __forceinline__ bool fetch(int j, i32x4* k, i32x4* v, int& kb, int& vb) {
+    if (j >= base + 64 || j < base) {
+      look(j);
+      looked();
+    }
+    kb = __builtin_amdgcn_readlane(k_byte, j - base);
+    vb = __builtin_amdgcn_readlane(v_byte, j - base);
+    return load(j, k, v);
   }
 };
 
@@ -123,7 +142,7 @@ struct Walk {
 // into registers with the next block in flight; at a tile's end their states
 // are joined through LDS.
 template <int D>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void k_attend_few(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, 1) void k_attend_few(AttendArgs a) {
   __shared__ __attribute__((aligned(16))) float o_lds[kWaves][D / 32][4][64][4];
   __shared__ float ref_lds[kWaves][32], sum_lds[kWaves][32];
   __shared__ int v_lds[kWaves];
@@ -164,7 +183,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void k_attend_few(Atten
       // to the other would wait for it
       i32x4 k2[D / 32], v2[D / 32];
       int kb2, vb2;
-      bool ok = walk.fetch(j, k, v, kb, vb);
+      bool ok = walk.first(j, k, v, kb, vb);
       for (;;) {
         const bool ok2 = walk.fetch(min(j + kWaves, clean - 1), k2, v2, kb2, vb2);
         if (ok) add(k, v, kb, vb);
@@ -772,20 +791,31 @@ __global__ __launch_bounds__(kTurns * 64) void k_join(AttendArgs a) {
   }
 }
 
-// A head with more rows than this takes the kernel for many.  For head_dim 128 and few /
-// many: 64 rows of 32 heads over 4096 tokens 24 / 36 us, 128 rows 27 / 38, 64 rows of 8
-// heads of 16 such sequences 40 / 91; 224 rows of 32 heads 41 / 42, of 4 heads over
-// 131072 tokens 144 / 84.  Where 128 rows read 131072 tokens, 95 / 80, the rule is late.
+// The kernel for few rows takes calls of at most kFewRows rows of a head, and of more
+// where they are small: its steps are 32 rows by 32 tokens, read from memory for each 32
+// rows, where the other's start and parts cost about 25 us more.  Few / many, us, in
+// steps times head_dim (a call is small up to kFewWork):
+//   128 rows, 32 heads of 128, 4096 tokens: 21 / 38;  4 heads, 131072 tokens: 61 / 80
+//   224 rows, 4 heads of 128: 4096 tokens (2^18.8) 19 / 27, 131072 tokens (2^23.8) 140 / 83
+//   1024 rows, 1024 tokens, 32 heads of 128 (2^22): 44 / 53;  of 64 (2^21) 32 / 36
+//   256 rows, 16384 tokens, 16 heads of 128 (2^23): 60 / 53
+//   16 heads of 256: 1024 rows, 1024 tokens (2^22) 36 / 52;  4 heads, 448 rows, 16384 (2^22.8) 81 / 52
 constexpr int kFewRows = 128;
+constexpr double kFewWork = 4194304.0;
 
 constexpr int many_groups(int D) { return D == 256 ? 1 : 2; }
 
-int64_t rows_bound(const dllm_cache_batch& b, int64_t T, int group) { return (b.max_new < T ? b.max_new : T) * group; }
+// From the host's bounds on what the device holds.
+bool few_rows(const AttendArgs& a) {
+  const int64_t rows = (int64_t)std::min<int64_t>(a.b.max_new, a.T) * a.group;
+  const double tiles = (double)((a.T * a.group + 31) / 32 + a.b.S - 1), blocks = (a.b.max_len + kBlock - 1) / kBlock;
+  return rows <= kFewRows || tiles * a.c.kv_heads * blocks * a.c.head_dim <= kFewWork;
+}
 
 template <int D>
 void launch(AttendArgs a, hipStream_t st) {
   constexpr int RG = many_groups(D), BM = kWaves * 32 * RG;
-  if (rows_bound(a.b, a.T, a.group) > kFewRows) {
+  if (!few_rows(a)) {
     a.parts = kManyParts;
     a.min_steps = 2;
     hipLaunchKernelGGL((k_attend_many<D, RG>), dim3(a.parts), dim3(kThreads), 0, st, a);

@@ -15,9 +15,10 @@ from test_gpu_cache import _batch, _check_attention, _dS
 pytestmark = pytest.mark.gpu
 
 
-def _attend_against_oracle(rng, D, heads, Hq, lens, new, causal, where, change=None, std=1.0):
+def _attend_against_oracle(rng, D, heads, Hq, lens, new, causal, where, change=None, extra=0):
     import torch
     table, pages = tables(rng, lens)
+    table = np.concatenate([table, np.full((len(lens), extra), -1, np.int32)], 1)
     if change == "holes":
         table[:, 1::3] = -1
     c = cache(rng, pages, heads, D, lens, table)
@@ -27,7 +28,7 @@ def _attend_against_oracle(rng, D, heads, Hq, lens, new, causal, where, change=N
                 if 0 <= table[s, j] < pages:
                     c["v_scale"][table[s, j]] = 100 + min(2 * j, 40)
     T = sum(new)
-    q, qf = bf16(rng, (T, Hq, D), std)
+    q, qf = bf16(rng, (T, Hq, D))
     bc = on_gpu(c)
     b = _batch(bc, cu_of(new), lens, table)
     o, l = bc.attend(b, dev_bf16(q), causal=causal, lse=True)
@@ -52,13 +53,18 @@ def _attend_against_oracle(rng, D, heads, Hq, lens, new, causal, where, change=N
     (64, 2, 2, [1999], [97], True, None),
     (256, 2, 4, [1500], [30], True, None),
 ])
-def test_attention_in_parts(D, heads, Hq, lens, new, causal, change):
-    print(f"[case] parts D={D} heads={heads}/{Hq} lens={lens} new={new} causal={causal} {change}", flush=True)
-    _attend_against_oracle(np.random.default_rng(D + sum(lens) + sum(new)), D, heads, Hq, lens, new, causal, "parts", change)
+@pytest.mark.parametrize("extra", [0, 30000])
+def test_attention_in_parts(D, heads, Hq, lens, new, causal, change, extra):
+    """With room in the table for a million tokens a call of more than 128 rows of a head is
+    taken for a large one, without it for a small one."""
+    print(f"[case] parts D={D} heads={heads}/{Hq} lens={lens} new={new} causal={causal} {change} {extra}", flush=True)
+    _attend_against_oracle(np.random.default_rng(D + sum(lens) + sum(new)), D, heads, Hq, lens, new, causal, "parts", change,
+                           extra)
 
 
-@pytest.mark.parametrize("S,n", [(63, 1), (64, 1), (65, 1), (300, 1), (300, 9)])
-def test_attention_many_sequences(S, n):
+@pytest.mark.parametrize("S,n,extra", [(63, 1, 0), (64, 1, 0), (65, 1, 0), (300, 1, 0), (300, 9, 0), (65, 9, 1000),
+                                       (300, 9, 1000)])
+def test_attention_many_sequences(S, n, extra):
     """Around the number of sequences that one wave, or one workgroup, looks through at
     a time; some have no tokens or no queries; 9 queries of 16 heads make 144 rows."""
     rng = np.random.default_rng(S + n)
@@ -67,7 +73,7 @@ def test_attention_many_sequences(S, n):
     lens[0] = new[1] = 0
     new[S - 1], lens[S - 1] = n, 90
     print(f"[case] sequences S={S} n={n}", flush=True)
-    _attend_against_oracle(rng, 64, 1, 16, lens, new, n > 1, "sequences")
+    _attend_against_oracle(rng, 64, 1, 16, lens, new, n > 1, "sequences", extra=extra)
 
 
 @pytest.mark.parametrize("D,heads,Hq,S,causal", [(64, 16, 16, 17, True), (64, 16, 48, 17, False), (128, 32, 32, 8, True),
