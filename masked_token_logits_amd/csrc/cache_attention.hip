@@ -2,7 +2,6 @@
 #include "cache_common.h"
 #include "cache_schedule.h"
 #include "cache_tiles.h"
-#include "persistent_sched.h"
 #include "rotary_angle.h"
 
 #include <algorithm>
@@ -141,6 +140,13 @@ struct Walk {
 // hold the same rows and take the blocks in turn, each straight from memory
 // into registers with the next block in flight; at a tile's end their states
 // are joined through LDS.
+//
+// Bound by memory, and where that takes little by what comes one after the other:
+// schedule, pages, blocks, join.  One token of 16 sequences of up to 4096 tokens, 8 heads
+// of 128: 20 us for 86 MB (4.3 TB/s), k_join 5.5; a 32-token block of 32 heads over
+// 4096 tokens 12 us for 34 MB, k_join 4.5.  One workgroup to a compute unit: two, whose
+// waves have half the registers and spill, took 26 and 17 us and made twice the
+// parts; three blocks in a wave's registers instead of two 21 and 13.
 template <int D>
 __global__ __launch_bounds__(kThreads, 1) void k_attend_few(AttendArgs a) {
   __shared__ __attribute__((aligned(16))) float o_lds[kWaves][D / 32][4][64][4];
@@ -316,6 +322,12 @@ __device__ __forceinline__ bool has_page(int info) { return info >> 16 != 0; }
 // the loop the products of three blocks are in flight, independent of each other:
 // the scores of block b + 1, the probabilities of block b and the output of
 // block b - 1, so that the matrix pipe and the VALU work at the same time.
+//
+// Bound by instruction issue: of 8192 queries over 8192 tokens, 28 heads of 128 on 4 (962
+// GFLOP, 820 us, 1170 TFLOP/s where a bf16 product of 8192^3 reaches 1487), a SIMD's
+// cycles are 57% matrix and 64% vector instructions, side by side: a score's
+// exponential, scaling, sum, maximum and rounding and a widened key's and value's
+// conversions.  Two groups of 32 rows to a wave halve the widening; a third has no registers.
 template <int D, int RG>
 __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {
   constexpr int BM = kWaves * 32 * RG, KEYS = kBlock * kManyBlocks;
@@ -824,7 +836,7 @@ void launch(AttendArgs a, hipStream_t st) {
     a.parts = kNarrowParts;
     a.min_steps = std::min(kWaves, (a.b.max_len + kBlock - 1) / kBlock);  // a short tile's waves wait for nobody else's
     hipLaunchKernelGGL(k_attend_few<D>, dim3(a.parts), dim3(kThreads), 0, st, a);
-    hipLaunchKernelGGL((k_join<D, 32, 4, 4>), dim3(D / 32, 1, a.parts / 4), dim3(4 * 64), 0, st, a);
+    hipLaunchKernelGGL((k_join<D, 32, 4, 2>), dim3(D / 32, 1, a.parts / 2), dim3(4 * 64), 0, st, a);
   }
 }
 
