@@ -2,6 +2,7 @@
 #include "cache_common.h"
 #include "cache_schedule.h"
 #include "cache_tiles.h"
+#include "persistent_sched.h"
 #include "rotary_angle.h"
 
 #include <algorithm>
