@@ -8,6 +8,10 @@ margin or negative entropy (top-k, or every position above a threshold).  The wo
 in hand-written HIP kernels behind the C ABI in include/dllm_readout.h;
 this package is its thin Python binding.  PyTorch only provides device
 memory and streams.
+
+Beside it: the sequence-chunked SwiGLU FFN (SwiGLUFFN), rotary positions
+(Rotary) and an 8-bit paged cache of keys and values with attention over it
+and eviction by attention weight (BlockCache).
 """
 from __future__ import annotations
 
