@@ -83,6 +83,13 @@ def _device(device) -> torch.device:
     return dev
 
 
+def _stream(stream, device):
+    """The stream an object queues on: one of its device's, or None."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, expected {device}")
+    return stream
+
+
 class Rotary(_Queued):
     """Rotary positions of heads whose first ``rotary_dim`` dimensions
     (default: all of ``head_dim``) are rotated.
@@ -113,7 +120,8 @@ class Rotary(_Queued):
         if not 0.0 < magnitude < 3e38:
             raise ValueError(f"magnitude {magnitude} is not a positive float32")
         self.head_dim, self.rotary_dim, self.magnitude = int(head_dim), r, float(magnitude)
-        self.device, self.stream = _device(device), stream
+        self.device = _device(device)
+        self.stream = _stream(stream, self.device)
         self.turns = torch.tensor(turns, dtype=torch.float64, device=self.device)
         self.plan = _abi.dllm_rotary_plan(self.turns.data_ptr(), self.magnitude, r, _abi.ROTARY_LAYOUTS[layout])
 
@@ -210,7 +218,7 @@ class BlockCache(_Queued):
         _need(v_scale, "v_scale", u8, (pages, heads), k.device)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.kv_heads, self.head_dim = int(pages), int(heads), int(k.shape[2]) // _BLOCK
-        self.device, self.stream = k.device, stream
+        self.device, self.stream = k.device, _stream(stream, k.device)
         self.struct = _abi.dllm_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.pages,
                                       self.kv_heads, self.head_dim)
 

@@ -66,15 +66,41 @@ __device__ __forceinline__ int row_tiles(const AttendArgs& a, const SeqView& q) 
   return (q.rows * a.group + BM - 1) / BM;
 }
 
-// Steps of one head of a sequence.
+// sum over i in 0 .. n - 1 of floor((x i + y) / m), for x, y >= 0: the whole parts
+// leave x, y < m, and then the points below a line are those beside it, with the
+// axes exchanged (Euclid's steps).
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t x, int64_t y) {
+  int64_t sum = 0;
+  for (;;) {
+    const int64_t whole_x = quotient(x, m), whole_y = quotient(y, m);
+    sum += n * (n - 1) / 2 * whole_x + n * whole_y;
+    x -= whole_x * m, y -= whole_y * m;
+    const int64_t top = x * n + y;
+    if (top < m) return sum;
+    n = quotient(top, m);
+    y = top - n * m;
+    const int64_t was = m;
+    m = x, x = was;
+  }
+}
+
+// Steps of one head of a sequence.  Under a causal mask tile i < tiles - 1 whose last
+// row sees c + l + 1 >= 1 tokens (c = len - n, l = floor(((i + 1) BM - 1) / group)) has
+//   ceil((c + l + 1) / KEYS) = floor(((i + 1) BM - 1 + group (c + KEYS)) / (group KEYS)),
+// the ones before it have 1.
 template <int BM, int KEYS>
 __device__ __forceinline__ int64_t head_steps(const AttendArgs& a, const SeqView& q) {
   const int tiles = row_tiles<BM>(a, q);
   if (tiles == 0) return 0;
   if (!a.causal) return (int64_t)tiles * tile_steps<BM, KEYS>(a, q, 0);
-  int64_t n = 0;
-  for (int i = 0; i < tiles; ++i) n += tile_steps<BM, KEYS>(a, q, i);
-  return n;
+  const int64_t c = (int64_t)q.len - q.n, g = a.group;
+  const int blind = c >= 0 ? 0 : (int)min((-c * g + BM) / BM - 1, (int64_t)tiles - 1), rest = tiles - 1 - blind;
+  int64_t steps = blind + tile_steps<BM, KEYS>(a, q, tiles - 1);
+  if (rest > 0) {
+    const int64_t e = (c + KEYS) >> __builtin_ctz(KEYS), f = (c + KEYS) & (KEYS - 1);  // c + KEYS = e KEYS + f
+    steps += e * rest + floor_sum(rest, g * KEYS, BM, (int64_t)BM * (blind + 1) - 1 + g * f);
+  }
+  return steps;
 }
 
 // Inclusive sum over the wave's lanes.
@@ -182,6 +208,15 @@ __device__ Stretch find_stretch(const AttendArgs& a, int64_t* lds, int* number, 
     r.rt = (int)quotient(lo - at, n);
     at += (int64_t)r.rt * n;
   } else {
+    // each lane a run of tiles, then along the run that the place is in
+    const int lane = tid & 63, tiles = row_tiles<BM>(a, q), run = (tiles + 63) / 64;
+    int64_t own = 0;
+    for (int i = lane * run; i < min((lane + 1) * run, tiles); ++i) own += tile_steps<BM, KEYS>(a, q, i);
+    const int64_t run_end = scan_wave(own);
+    const int found = __ffsll((unsigned long long)__ballot(run_end - own <= lo - at && lo - at < run_end)) - 1;
+    at += __shfl(run_end - own, found);
+    r.rt = __builtin_amdgcn_readfirstlane(found * run);
+    n = tile_steps<BM, KEYS>(a, q, r.rt);
     while (lo >= at + n) {
       at += n;
       n = tile_steps<BM, KEYS>(a, q, ++r.rt);
