@@ -189,6 +189,17 @@ def test_rotary_object_checks():
             rot(*a)
 
 
+def test_streams_of_another_device_refused():
+    import types
+    other = types.SimpleNamespace(device=torch.device("cuda", 1))
+    c = mtl.BlockCache(4, 2, 64, device="cpu")
+    for make in (lambda: mtl.Rotary(64, device="cpu", stream=other),
+                 lambda: mtl.BlockCache(4, 2, 64, device="cpu", stream=other),
+                 lambda: mtl.BlockCache.over(c.k, c.v, c.k_scale, c.v_scale, stream=other)):
+        with pytest.raises(ValueError):
+            make()
+
+
 def test_batch_checks():
     cache, _, i = _objects()
     t = torch.zeros((2, 3), dtype=torch.int32)
