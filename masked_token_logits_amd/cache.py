@@ -142,7 +142,7 @@ class Rotary(_Queued):
         def make(stream):
             y = box[0]
             if y is None:
-                y = box[0] = torch.empty((T, H, D), dtype=x.dtype, device=self.device)
+                y = box[0] = x.new_empty((T, H, D))
             return _abi.load().dllm_rotary(C.byref(self.plan), x.data_ptr(), T, H, D, x.stride(0), x.stride(1),
                                            positions.data_ptr(), 1 if transpose else 0, y.data_ptr(), y.stride(0),
                                            y.stride(1), stream)
@@ -178,6 +178,7 @@ class CacheBatch:
         self.cu, self.lens, self.table = cu, lens, table
         self.struct = _abi.dllm_cache_batch(cu.data_ptr(), lens.data_ptr(), table.data_ptr(), self.S, self.blocks,
                                             self.max_new or (1 << 31) - 1, max_len)
+        self._bytes = {}
 
     def _tensors(self):
         return self.cu, self.lens, self.table
@@ -227,6 +228,17 @@ class BlockCache(_Queued):
 
     def batch(self, cu, lens, table, max_new: int | None = None, max_len: int | None = None) -> CacheBatch:
         return CacheBatch(cu, lens, table, max_new, max_len, self.device)
+
+    def _workspace(self, batch, name, *args):
+        """Bytes of workspace: by sizes alone, so each is asked for once."""
+        key = (name, self.kv_heads, self.head_dim, *args)
+        nbytes = batch._bytes.get(key)
+        if nbytes is None:
+            nbytes = getattr(_abi, name)(self.struct, batch.struct, *args)
+            if nbytes == 0:
+                raise DllmError(DLLM_ERR_INVALID_ARG, name)
+            batch._bytes[key] = nbytes
+        return nbytes
 
     def _queries(self, batch, q):
         if not isinstance(batch, CacheBatch):
@@ -281,18 +293,16 @@ class BlockCache(_Queued):
         if given is not None:
             _need(given, "lse", (torch.float32,), (T, H), self.device)
         want = given is not None or bool(lse)
-        nbytes = _abi.dllm_cache_attention_workspace_bytes(self.struct, batch.struct, H)
-        if nbytes == 0:
-            raise DllmError(DLLM_ERR_INVALID_ARG, "dllm_cache_attention_workspace_bytes")
+        nbytes = self._workspace(batch, "dllm_cache_attention_workspace_bytes", H)
         box = [out, given]
 
         def make(stream):
             o, l = box
             if o is None:
-                o = box[0] = torch.empty((T, H, D), dtype=q.dtype, device=self.device)
+                o = box[0] = q.new_empty((T, H, D))
             if l is None and want:
-                l = box[1] = torch.empty((T, H), dtype=torch.float32, device=self.device)
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+                l = box[1] = q.new_empty((T, H), dtype=torch.float32)
+            ws = self.k.new_empty(nbytes)
             return _abi.load().dllm_cache_attention(
                 C.byref(self.struct), C.byref(batch.struct), T, q.data_ptr(), q.stride(0), q.stride(1), H, scale,
                 1 if causal else 0, o.data_ptr(), l.data_ptr() if l is not None else None, ws.data_ptr(), nbytes,
@@ -348,9 +358,7 @@ class BlockCache(_Queued):
             _need(lens_out, "lens_out", i32, (S,), dev)
         if weights_out is not None:
             _need(weights_out, "weights_out", f32, (S, H, blocks * _BLOCK), dev)
-        nbytes = _abi.dllm_cache_evict_workspace_bytes(self.struct, batch.struct)
-        if nbytes == 0:
-            raise DllmError(DLLM_ERR_INVALID_ARG, "dllm_cache_evict_workspace_bytes")
+        nbytes = self._workspace(batch, "dllm_cache_evict_workspace_bytes")
         box = [lens_out, kept, weights_out]
 
         def make(stream):
@@ -360,7 +368,7 @@ class BlockCache(_Queued):
                 box[1] = torch.empty((S, H, most), dtype=torch.int32, device=dev)
             if box[2] is None:
                 box[2] = torch.empty((S, H, blocks * _BLOCK), dtype=torch.float32, device=dev)
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            ws = self.k.new_empty(nbytes)
             return _abi.load().dllm_cache_evict(
                 C.byref(self.struct), C.byref(batch.struct), weights.data_ptr(), keep.data_ptr(), most, sink, recent,
                 pool, table_out.data_ptr(), blocks, box[0].data_ptr(), box[1].data_ptr(), box[2].data_ptr(),
