@@ -168,15 +168,15 @@ __device__ __forceinline__ uint32_t nth_largest(Search& l, uint32_t lo, uint32_t
   return t;
 }
 
-__device__ __forceinline__ void put(const SelectArgs& a, int64_t row, const float* w, int place, int j) {
+__device__ __forceinline__ void put(const SelectArgs& a, int64_t row, float weight, int place, int j) {
   a.kept[row * a.max_keep + place] = j;
-  if (a.weights_out) a.weights_out[row * a.out_slots + place] = w[j];
+  if (a.weights_out) a.weights_out[row * a.out_slots + place] = weight;
 }
 
 // The tokens kept unconditionally.
 __device__ __forceinline__ void put_ends(const SelectArgs& a, const Row& r, int64_t row, const float* w) {
-  for (int j = threadIdx.x; j < r.first; j += kThreads) put(a, row, w, j, j);
-  for (int j = threadIdx.x; j < r.last; j += kThreads) put(a, row, w, r.n - r.last + j, r.len - r.last + j);
+  for (int j = threadIdx.x; j < r.first; j += kThreads) put(a, row, w[j], j, j);
+  for (int j = threadIdx.x; j < r.last; j += kThreads) put(a, row, w[r.len - r.last + j], r.n - r.last + j, r.len - r.last + j);
 }
 
 // The chunk's kept tokens in order: those above the threshold, and of those at
@@ -187,6 +187,9 @@ __device__ __forceinline__ void put_chunk(const SelectArgs& a, int64_t row, cons
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint64_t below = (1ull << lane) - 1;
   int n_gt = 0, n_eq = 0;
+  float weight[kEach];  // all on their way at once, not one after another as they are put
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) weight[i] = key[i] >= threshold ? w[token_at(chunk, i)] : 0.0f;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     n_gt += wave_count(key[i] > threshold);
@@ -205,7 +208,7 @@ __device__ __forceinline__ void put_chunk(const SelectArgs& a, int64_t row, cons
     const uint64_t sames = __ballot(same);
     const bool take = key[i] > threshold || (same && ties + __popcll(sames & below) < want);
     const uint64_t takes = __ballot(take);
-    if (take) put(a, row, w, place + __popcll(takes & below), token_at(chunk, i));
+    if (take) put(a, row, weight[i], place + __popcll(takes & below), token_at(chunk, i));
     place += __popcll(takes);
     ties += __popcll(sames);
   }
