@@ -208,15 +208,6 @@ __device__ Stretch find_stretch(const AttendArgs& a, int64_t* lds, int* number, 
     r.rt = (int)quotient(lo - at, n);
     at += (int64_t)r.rt * n;
   } else {
-    // each lane a run of tiles, then along the run that the place is in
-    const int lane = tid & 63, tiles = row_tiles<BM>(a, q), run = (tiles + 63) / 64;
-    int64_t own = 0;
-    for (int i = lane * run; i < min((lane + 1) * run, tiles); ++i) own += tile_steps<BM, KEYS>(a, q, i);
-    const int64_t run_end = scan_wave(own);
-    const int found = __ffsll((unsigned long long)__ballot(run_end - own <= lo - at && lo - at < run_end)) - 1;
-    at += __shfl(run_end - own, found);
-    r.rt = __builtin_amdgcn_readfirstlane(found * run);
-    n = tile_steps<BM, KEYS>(a, q, r.rt);
     while (lo >= at + n) {
       at += n;
       n = tile_steps<BM, KEYS>(a, q, ++r.rt);
