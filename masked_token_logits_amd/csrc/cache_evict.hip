@@ -471,19 +471,18 @@ __device__ __forceinline__ float exact_scale(int x) { return x < -126 ? 0.0f : _
 template <int D>
 __global__ __launch_bounds__(kMoveThreads) void k_move(MoveArgs a) {
   const int s = blockIdx.z, h = blockIdx.y, blk = blockIdx.x, tid = threadIdx.x;
-  const int n = a.lens_out[s];
-  if (blk * kBlock >= n) return;
-  const int to = page_of(a.table_out, a.out_blocks, a.c.pages, s, blk);
-  if (to < 0) return;
+  const int t = blk * kBlock + (tid & (kBlock - 1));
+  int n = a.lens_out[s], to = page_of(a.table_out, a.out_blocks, a.c.pages, s, blk);
+  int j = t < a.max_keep ? a.kept[((int64_t)s * a.c.kv_heads + h) * a.max_keep + t] : 0;  // of use where t < n
+  asm volatile("" : "+v"(n), "+v"(to), "+v"(j));  // the three on their way at once, not one behind the other's branch
+  if (blk * kBlock >= n || to < 0) return;
   __shared__ int64_t src[kBlock];  // byte offset of the token's old block, -1: none
   __shared__ int slot[kBlock];
   __shared__ int ke[kBlock], ve[kBlock];
   __shared__ int kmax, vmax, kmixed, vmixed;  // largest scale bytes, and whether a token has another
   if (tid < kBlock) {
-    const int t = blk * kBlock + tid;
     int64_t at = -1;
     if (t < n) {
-      const int j = a.kept[((int64_t)s * a.c.kv_heads + h) * a.max_keep + t];
       const int page = page_of(a.table, a.table_blocks, a.c.pages, s, j / kBlock);
       if (page >= 0) at = block_of(a.c, page, h);
       slot[tid] = j % kBlock;
