@@ -325,8 +325,8 @@ __device__ __forceinline__ bool has_page(int info) { return info >> 16 != 0; }
 // block b - 1, so that the matrix pipe and the VALU work at the same time.
 //
 // Bound by instruction issue: of 8192 queries over 8192 tokens, 28 heads of 128 on 4 (962
-// GFLOP, 820 us, 1170 TFLOP/s where a bf16 product of 8192^3 reaches 1487), a SIMD's
-// cycles are 57% matrix and 64% vector instructions, side by side: a score's
+// GFLOP, 820 to 870 us by the card's clock, 1110 to 1170 TFLOP/s where a bf16 product of
+// 8192^3 reaches 1487), a SIMD's cycles are 58% matrix and 64% vector instructions, side by side: a score's
 // exponential, scaling, sum, maximum and rounding and a widened key's and value's
 // conversions.  Two groups of 32 rows to a wave halve the widening; a third has no registers.
 template <int D, int RG>
