@@ -326,8 +326,8 @@ __device__ __forceinline__ bool has_page(int info) { return info >> 16 != 0; }
 //
 // Bound by instruction issue: of 8192 queries over 8192 tokens, 28 heads of 128 on 4 (962
 // GFLOP, 820 to 870 us by the card's clock, 1110 to 1170 TFLOP/s where a bf16 product of
-// 8192^3 reaches 1487), a SIMD's cycles are 58% matrix and 64% vector instructions, side by side: a score's
-// exponential, scaling, sum, maximum and rounding and a widened key's and value's
+// 8192^3 reaches 1487), a SIMD's cycles are 58% matrix and 64% vector instructions,
+// side by side: a score's exponential, scaling, sum, maximum and rounding and a widened key's and value's
 // conversions.  Two groups of 32 rows to a wave halve the widening; a third has no registers.
 template <int D, int RG>
 __global__ __launch_bounds__(kThreads, 1) void k_attend_many(AttendArgs a) {

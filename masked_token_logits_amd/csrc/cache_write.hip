@@ -364,6 +364,8 @@ void launch_write(const dllm_cache& c, const dllm_cache_batch& b, int64_t T, con
   const int64_t blocks = (most + kBlock - 2) / kBlock + 1;  // a run of n tokens touches at most this many
   const bool rows16 = ((kt | kh | vt | vh) & 7) == 0 && (((uintptr_t)k | (uintptr_t)v) & 15u) == 0;
   const bool pieces = !plan.turns || plan.layout == DLLM_ROTARY_INTERLEAVED || plan.rotary_dim % 32 == 0;
+  // In pieces wherever they can be: one token of 64 sequences, 8 heads of 128, 9.3 us against
+  // 12.6 in the general kernel, 2048 tokens of one 11.9 against 20.8, 32768 53 against 165.
   if (rows16 && pieces) {
     // heads of a workgroup: as many as leave some 4 workgroups for every compute unit
     int heads = c.kv_heads;
