@@ -289,6 +289,8 @@ class BlockCache(_Queued):
             scale = D ** -0.5
         if out is not None:
             _need(out, "out", (q.dtype,), (T, H, D), self.device)
+            if T and out.data_ptr() == q.data_ptr():
+                raise ValueError("out: must not be q, which is read to the end")
         given = lse if isinstance(lse, torch.Tensor) else None
         if given is not None:
             _need(given, "lse", (torch.float32,), (T, H), self.device)

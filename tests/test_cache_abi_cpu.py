@@ -189,6 +189,13 @@ def test_rotary_object_checks():
             rot(*a)
 
 
+def test_attention_in_place_refused():
+    cache, batch, _ = _objects()
+    q = torch.zeros((5, 4, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        cache.attend(batch, q, out=q)
+
+
 def test_streams_of_another_device_refused():
     import types
     other = types.SimpleNamespace(device=torch.device("cuda", 1))
