@@ -59,10 +59,13 @@ struct PieceArgs {
   uint16_t* y;
   int64_t y_token, y_head;
   int pieces;          // of a head
-  uint32_t per_piece;  // n / pieces = high word of n * per_piece: exact for n * pieces < 2^32
+  uint32_t per_piece;  // n / pieces = high word of n * per_piece: exact for n * pieces < 2^32; 0 where pieces is 1
   int tokens;          // of a workgroup
-  uint32_t per_token;  // likewise n / (H * pieces), where there is more than one
+  uint32_t per_token;  // likewise n / (H * pieces), where there is more than one token
 };
+
+// n / d by d's reciprocal, which is 2^32 for d = 1 and does not fit: 0 stands for it.
+__device__ __forceinline__ int divided(int n, uint32_t per) { return per ? (int)__umulhi((uint32_t)n, per) : n; }
 
 // Heads in pieces of two units of 16 bytes: eight pairs, or what lies behind the
 // rotated dimensions.  A workgroup takes as many tokens as give each thread a piece; its
@@ -84,10 +87,10 @@ __global__ __launch_bounds__(kThreads) void k_rotary_pieces(PieceArgs a) {
     int t = 0, h = 0, piece = 0, first = 0, second = 0;  // the piece's token, head and number, its units' first dimensions
     auto load = [&](int n) {
       if (a.tokens > 1) {
-        t = (int)__umulhi((uint32_t)n, a.per_token);
+        t = divided(n, a.per_token);
         n -= t * of_token;
       }
-      h = (int)__umulhi((uint32_t)n, a.per_piece);
+      h = divided(n, a.per_piece);
       piece = n - h * a.pieces;
       first = halves && piece < rotated ? 8 * piece : 16 * piece;
       second = halves && piece < rotated ? first + half : first + 8;
@@ -192,7 +195,7 @@ dllm_status dllm_rotary(const dllm_rotary_plan* plan, const uint16_t* x, int64_t
   if (aligned && (plan->rotary_dim % 16 == 0 || plan->layout == DLLM_ROTARY_INTERLEAVED)) {
     const int rotated = (plan->rotary_dim + 15) / 16, pieces = rotated + (D - 16 * rotated + 15) / 16, all = H * pieces;
     const int fit = dllm::kThreads / all, tokens = fit < 1 ? 1 : fit < dllm::kTokens ? fit : dllm::kTokens;
-    const auto per = [](int d) { return (uint32_t)((((uint64_t)1 << 32) + d - 1) / d); };
+    const auto per = [](int d) { return d == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + d - 1) / d); };
     const dllm::PieceArgs a = {*plan, x, T, (int)H, (int)D, x_token, x_head, positions, (int)transpose, y, y_token, y_head,
                                pieces, per(pieces), tokens, per(all)};
     const int64_t groups = (T + tokens - 1) / tokens;

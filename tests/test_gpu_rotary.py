@@ -193,3 +193,35 @@ def test_rotary_alignment_changes_nothing(T, H, D, r, layout):
         assert torch.equal(y, z)
         inplace = x.clone()
         assert rot(inplace, pos, out=inplace, transpose=transpose) is inplace and torch.equal(inplace, y)
+
+
+@pytest.mark.parametrize("T,H,D,r", [(9, 1, 8, 8), (300, 1, 16, 16), (5, 8, 8, 4), (3, 33, 16, 16), (70, 3, 16, 2),
+                                     (1, 300, 8, 8), (11, 2, 24, 16), (4, 5, 24, 24)])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rotary_small_heads(T, H, D, r, layout):
+    """Heads of one 16-byte unit, of one piece of two and of a piece and a half, one head and several tokens to a
+    workgroup: the oracle's values both ways, the element path's bits, and nothing written around the output."""
+    import torch
+
+    import masked_token_logits_amd as mtl
+    rng = np.random.default_rng(T * 1000 + H * 100 + D + r)
+    print(f"[case] rotary small T={T} H={H} D={D} r={r} {layout}", flush=True)
+    x, xf = bf16(rng, (T, H, D))
+    pos = rng.integers(-1000, 131072, T)
+    rot = mtl.Rotary(D, r, layout=layout)
+    n = T * H * D
+    tx, tp = dev_bf16(x), dev_i32(pos)
+    off = torch.zeros(n + 1, dtype=torch.bfloat16, device="cuda")[1:].view(T, H, D)
+    off.copy_(tx)
+    for transpose in (False, True):
+        flat = torch.full((n + 128,), 7.0, dtype=torch.bfloat16, device="cuda")
+        y = rot(tx, tp, out=flat[64:64 + n].view(T, H, D), transpose=transpose)
+        torch.cuda.synchronize()
+        want, size = oc.rotate(xf, pos, oc.rotary_theta(r), layout, transpose=transpose)
+        _close(_f64(y), want, size, "small heads")
+        assert np.array_equal(_f64(y)[..., r:], xf[..., r:])
+        assert torch.all(flat[:64] == 7) and torch.all(flat[64 + n:] == 7)
+        z = torch.empty(n + 1, dtype=torch.bfloat16, device="cuda")[1:].view(T, H, D)
+        assert torch.equal(rot(off, tp, out=z, transpose=transpose), y)
+        inplace = tx.clone()
+        assert torch.equal(rot(inplace, tp, out=inplace, transpose=transpose), y)
