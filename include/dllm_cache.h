@@ -106,12 +106,14 @@ typedef struct {
  *   plan        rotation of k before it is stored (rotary_dim <= head_dim);
  *               NULL: k is stored as it is
  * Every touched block gets the smallest scale 2^e with
- * g * max |x| <= 448 * 2^e over its new tokens' finite values
- * (g = 1.41421366 * magnitude for rotated keys, which no rotation exceeds,
- * else 1), but at least the scale it had if it holds other tokens of the
- * sequence; those are requantised when it grows.  Values are rounded once,
- * to nearest even, from an fp64 rotation.  What is not finite is stored as
- * NaN.  Slots of touched blocks at or behind lens[s] are cleared.  A page
+ * g * max |x| <= 448 * 2^e over its new tokens' finite values, but at least
+ * the scale it had if it holds other tokens of the sequence; those are
+ * requantised when it grows.  g covers what a rotation can grow a value by:
+ * 1.41421366 * magnitude for keys rotated in all dimensions, the larger of
+ * that and 1 for keys rotated in some (the others stay as they are), else 1.
+ * Values are rounded once, to nearest even, from an fp64 rotation.  What is
+ * not finite, a key that its rotation takes beyond float32 among it, is
+ * stored as NaN.  Slots of touched blocks at or behind lens[s] are cleared.  A page
  * may be written through one table entry of a call only.
  */
 dllm_status dllm_cache_write(const dllm_cache *cache, const dllm_cache_batch *batch, int64_t T, const uint16_t *k,

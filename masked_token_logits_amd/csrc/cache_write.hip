@@ -18,6 +18,13 @@ __device__ __forceinline__ int scale_byte(float big) {
   return x - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0) + 127;
 }
 
+// What a block's largest key may grow by: a rotated pair by sqrt 2 times the magnitude,
+// the dimensions behind the rotated ones not at all.
+__device__ __forceinline__ float key_gain(const dllm_rotary_plan& plan, int D) {
+  const float g = 1.41421366f * plan.magnitude;
+  return plan.rotary_dim < D ? fmaxf(g, 1.0f) : g;
+}
+
 __device__ __forceinline__ float finite_abs(float x) {
   const float a = fabsf(x);
   return a <= 3.4028235e38f ? a : 0.0f;
@@ -80,7 +87,7 @@ __global__ __launch_bounds__(kThreads) void k_write(dllm_cache c, dllm_cache_bat
     if ((tid & 63) == 0) top[tid >> 6] = big;
     const int any_held = __syncthreads_or(held);
     big = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-    if (side == 0 && half) big *= 1.41421366f * plan.magnitude;
+    if (side == 0 && half) big *= key_gain(plan, D);
     const int had = *scale;
     int byte = max(scale_byte(big), any_held ? had : 0);
     byte = min(max(byte, DLLM_CACHE_SCALE_MIN), DLLM_CACHE_SCALE_MAX);
@@ -263,7 +270,7 @@ __global__ __launch_bounds__(2 * D, 4) void k_write_pieces(WriteArgs a) {
     float kbig = 0.0f, vbig = 0.0f;
 #pragma unroll
     for (int i = 0; i < kWaves / 2; ++i) kbig = fmaxf(kbig, top[i]), vbig = fmaxf(vbig, top[kWaves / 2 + i]);
-    if (r) kbig *= 1.41421366f * a.plan.magnitude;
+    if (r) kbig *= key_gain(a.plan, D);
     const Scales ks = scales_of(kbig, k_had, any_held), vs = scales_of(vbig, v_had, any_held);
     const i32x4 in[4] = {x[0], x[1], x[2], x[3]};
     if (h + 1 < h1) load(h + 1);

@@ -68,11 +68,15 @@ E4M3 = _e4m3_values()
 
 def e4m3_bytes(x: np.ndarray) -> np.ndarray:
     """Bytes of the e4m3 values nearest to x, ties to the even byte; NaN for
-    what is not finite.  |x| <= 448 up to rounding."""
+    what is not finite.  |x| <= 448 up to the roundings of a scale's bound:
+    what is larger was given a scale that does not hold it."""
     x = np.asarray(x, dtype=np.float64)
     out = np.full(x.shape, 0x7F, np.uint8)
     ok = np.isfinite(x)
-    a = np.minimum(np.abs(x[ok]), 448.0)
+    a = np.abs(x[ok])
+    if a.max(initial=0) > 448.0 * (1 + 2.0 ** -20):
+        raise ValueError(f"{a.max()} is beyond e4m3's largest value")
+    a = np.minimum(a, 448.0)
     grid = E4M3[:127]                                     # ascending
     i = np.clip(np.searchsorted(grid, a), 1, 126)
     lo, hi = grid[i - 1], grid[i]
@@ -145,7 +149,11 @@ def write(cache: dict, cu, lens, table, start, k: np.ndarray, v: np.ndarray, pos
     heads, D = k.shape[1:]
     loose = np.zeros(cache["k"].shape, bool)
     yk, size = (rotate(k, pos, theta, layout, magnitude) if theta is not None else (k, np.zeros_like(k)))
-    gain = np.float32(ROOT2 * np.float32(magnitude)) if theta is not None else np.float32(1)
+    gain = np.float32(1)
+    if theta is not None:
+        gain = np.float32(ROOT2 * np.float32(magnitude))
+        if 2 * len(theta) < D:                 # some dimensions are stored as they are
+            gain = max(gain, np.float32(1))
     for s in range(len(lens)):
         n, st = int(cu[s + 1] - cu[s]), int(start[s])
         if st < 0 or n == 0:

@@ -307,3 +307,9 @@ def test_oracle_select():
     assert oc.select(w, 4, 1, 2, 1).tolist() == [0, 3, 8, 9]
     assert oc.select(np.ones(6), 3, 0, 0, 1).tolist() == [0, 1, 2]
     assert oc.select(w, 99, 2, 2, 3).tolist() == list(range(10))
+
+
+def test_oracle_refuses_what_a_scale_does_not_hold():
+    oc.e4m3_bytes(np.array([448.0, -448.0 * (1 + 2.0 ** -21), np.inf, np.nan]))
+    with pytest.raises(ValueError):
+        oc.e4m3_bytes(np.array([1.0, -449.0]))

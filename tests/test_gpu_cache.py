@@ -173,6 +173,52 @@ def test_write_strided_inputs():
     g = host(bc)
     np.testing.assert_array_equal(g["k"][table[0, :2], 0], g["k"][table[0, :2], 1])
 
+@pytest.mark.parametrize("D,heads,lens,new,r,layout", [
+    (128, 2, [45, 64], [40, 30], 64, "half"),              # in pieces, tokens of the first block held
+    (64, 3, [40], [33], 22, "interleaved"),                # pairs that end inside a piece
+    (128, 2, [45], [45], 40, "half"),                      # the general kernel
+    (64, 1, [33], [33], 64, "half"),                       # nothing behind the rotated dimensions
+])
+@pytest.mark.parametrize("magnitude", [0.25, 0.5, 1.25])
+def test_write_magnitude(D, heads, lens, new, r, layout, magnitude):
+    """A magnitude shrinks or stretches only the rotated dimensions: those behind them, here the loudest, fit
+    the block's scale as they are.  Besides parity, every finite key is read back to within half a step of e4m3
+    (2^-4 of it, or 2^-10 of the scale below its normal range)."""
+    import torch
+
+    import masked_token_logits_amd as mtl
+    rng = np.random.default_rng(D + heads + sum(lens))
+    print(f"[case] write magnitude={magnitude} D={D} heads={heads} lens={lens} new={new} r={r} {layout}", flush=True)
+    table, pages = tables(rng, lens, extra=1)
+    old = [a - b for a, b in zip(lens, new)]
+    c = cache(rng, pages, heads, D, old, table)
+    cu, T = cu_of(new), sum(new)
+    k, kf = bf16(rng, (T, heads, D), 2.0)
+    if r < D:
+        k[..., D - 1], kf[..., D - 1] = 0x4416, 600.0
+    v, vf = bf16(rng, (T, heads, D), 0.3)
+    pos = rng.integers(0, 131072, T)
+    bc = on_gpu(c)
+    rot = mtl.Rotary(D, r, layout=layout, magnitude=magnitude)
+    bc.write(_batch(bc, cu, lens, table), dev_bf16(k), dev_bf16(v), dev_i32(old), positions=dev_i32(pos), rotary=rot)
+    torch.cuda.synchronize()
+    got = host(bc)
+    y, size = oc.rotate(kf, pos, oc.rotary_theta(r), layout, magnitude)
+    for s, (n, st) in enumerate(zip(new, old)):
+        for h in range(heads):
+            x, _ = oc.read_tokens(got, "k", table[s], h, lens[s])
+            at = slice(int(cu[s]), int(cu[s]) + n)
+            e = 2.0 ** (got["k_scale"][table[s, np.arange(st, lens[s]) // 32], h].astype(float) - 127)[:, None]
+            err, tol = np.abs(x[st:] - y[at, h]), np.maximum(2.0 ** -4 * np.abs(y[at, h]), 2.0 ** -10 * e) + 2.0 ** -20 * size[at, h]
+            assert np.all(err <= tol), f"sequence {s} head {h}: {np.argwhere(~(err <= tol))[:3].tolist()}"
+    want, loose = oc.write(c, cu, lens, table, old, kf, vf, pos, oc.rotary_theta(r), layout, magnitude)
+    np.testing.assert_array_equal(got["k_scale"], want["k_scale"])
+    np.testing.assert_array_equal(got["v_scale"], want["v_scale"])
+    np.testing.assert_array_equal(got["v"], want["v"])
+    off = got["k"] != want["k"]
+    assert not np.any(off & ~loose), np.argwhere(off & ~loose)[:5].tolist()
+    assert off.sum() <= max(2, 1e-3 * off.size)
+
 
 # ---- attention ------------------------------------------------------------------------------------------------
 
