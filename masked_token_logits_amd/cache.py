@@ -196,6 +196,8 @@ class BlockCache(_Queued):
         data = [torch.zeros((pages, kv_heads, _BLOCK * head_dim), **u8) for _ in range(2)]
         scale = [torch.full((pages, kv_heads), 127, **u8) for _ in range(2)]
         self._adopt(*data, *scale, stream)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream(dev))   # for these fills
 
     @classmethod
     def over(cls, k, v, k_scale, v_scale, stream=None) -> "BlockCache":

@@ -370,3 +370,29 @@ def test_nothing_to_do():
     got = host(bc)
     for name in c:
         np.testing.assert_array_equal(got[name], c[name], err_msg=name)
+
+
+def test_a_new_cache_is_filled_before_its_stream_writes():
+    """A cache made with a stream while the current one is busy: the first write, queued at once, comes behind the
+    fill of the pool."""
+    import torch
+
+    import masked_token_logits_amd as mtl
+    rng = np.random.default_rng(92)
+    D, H, pages = 64, 2, 4096
+    k, v = (dev_bf16(bf16(rng, (40, H, D))[0]) for _ in "kv")
+    cu, lens, table, start = dev_i32([0, 40]), dev_i32([40]), dev_i32([[pages - 1, 0]]), dev_i32([0])
+    busy = torch.randn(4096, 4096, device="cuda").to(torch.bfloat16)
+    s = torch.cuda.Stream()
+    res = []
+    for stream in (None, s):
+        torch.cuda.synchronize()
+        if stream is not None:
+            for _ in range(30):
+                busy = torch.mm(busy, busy).clamp_(-1, 1)
+        bc = mtl.BlockCache(pages, H, D, stream=stream)
+        bc.write(bc.batch(cu, lens, table), k, v, start)
+        torch.cuda.synchronize()
+        res.append([t.clone() for t in (bc.k, bc.v, bc.k_scale, bc.v_scale)])
+    assert _same(*res)
+    assert torch.any(res[0][0][pages - 1]) and not torch.any(res[0][0][1:pages - 1]) and torch.all(res[0][2][1:pages - 1] == 127)
