@@ -7,6 +7,9 @@ allocates (outputs that are not given, workspaces) belongs to the stream it
 runs on, and tensors passed to a call on another stream than the current
 one are kept alive until that stream is done with them.  Ordering between
 streams is the caller's.
+
+Objects of another device than a GPU take their checks, but run nothing: a
+valid call raises DLLM_ERR_UNSUPPORTED.
 """
 from __future__ import annotations
 
@@ -16,7 +19,7 @@ import math
 import torch
 
 from . import _abi
-from ._abi import DLLM_ERR_INVALID_ARG, DLLM_OK, DllmError
+from ._abi import DLLM_ERR_INVALID_ARG, DLLM_ERR_UNSUPPORTED, DLLM_OK, DllmError
 
 # The current stream's handle: without the Stream object, a fifth of a small call's time.
 _stream_handle = torch._C._cuda_getCurrentRawStream
@@ -58,8 +61,9 @@ class _Queued:
         """``make(stream)`` queues the call and returns its status."""
         dev = self.device
         if dev.type != "cuda":
-            st = make(None)   # no device: the library's own checks answer
-        elif self.stream is None and torch.cuda.current_device() == dev.index:
+            # a GPU, where there is one, would take these pointers for its own
+            raise DllmError(DLLM_ERR_UNSUPPORTED, f"{where} on {dev}")
+        if self.stream is None and torch.cuda.current_device() == dev.index:
             st = make(_stream_handle(dev.index))
         else:
             with torch.cuda.device(dev):

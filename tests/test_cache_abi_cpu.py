@@ -313,3 +313,40 @@ def test_oracle_refuses_what_a_scale_does_not_hold():
     oc.e4m3_bytes(np.array([448.0, -448.0 * (1 + 2.0 ** -21), np.inf, np.nan]))
     with pytest.raises(ValueError):
         oc.e4m3_bytes(np.array([1.0, -449.0]))
+
+
+class _Library:
+    """Stands in for the loaded library: workspace sizes are 256, and kernel launches are noted."""
+
+    def __init__(self):
+        self.launched = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            if name.endswith("_bytes"):
+                return 256
+            self.launched.append(name)
+            return E.DLLM_OK
+        return call
+
+
+def test_objects_off_the_gpu_launch_nothing(monkeypatch):
+    """Objects of another device than a GPU are refused before the library gets their pointers, whether or not there is a
+    GPU whose kernels would take them for their own."""
+    cache, batch, i = _objects()
+    rot = mtl.Rotary(64, device="cpu")
+    k, q = torch.zeros((5, 2, 64), dtype=torch.bfloat16), torch.zeros((5, 4, 64), dtype=torch.bfloat16)
+    w, lse, to = torch.zeros((2, 2, 96)), torch.zeros((5, 4)), torch.zeros((2, 2), dtype=torch.int32)
+    lib = _Library()
+    with monkeypatch.context() as m:
+        m.setattr(_abi, "load", lambda *a: lib)
+        m.setattr(_abi, "dllm_status_string", str)
+        for f in (lambda: rot(k, i(0, 1, 2, 3, 4)), lambda: rot(k, i(0, 1, 2, 3, 4), out=k, transpose=True),
+                  lambda: cache.write(batch, k, k, i(0, 0)),
+                  lambda: cache.write(batch, k, k, i(0, 0), positions=i(0, 1, 2, 3, 4), rotary=rot),
+                  lambda: cache.attend(batch, q, lse=True), lambda: cache.weigh(batch, q, lse, w),
+                  lambda: cache.evict(batch, w, i(1, 1), to)):
+            with pytest.raises(mtl.DllmError) as e:
+                f()
+            assert e.value.status == E.DLLM_ERR_UNSUPPORTED
+    assert lib.launched == []
