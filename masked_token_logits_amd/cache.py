@@ -179,7 +179,7 @@ class CacheBatch:
             raise ValueError(f"max_new {max_new} is not positive")
         self.S, self.blocks, self.max_len = int(S), int(blocks), max_len
         self.max_new = None if max_new is None else int(max_new)
-        self.cu, self.lens, self.table = cu, lens, table
+        self.cu, self.lens, self.table, self.device = cu, lens, table, device
         self.struct = _abi.dllm_cache_batch(cu.data_ptr(), lens.data_ptr(), table.data_ptr(), self.S, self.blocks,
                                             self.max_new or (1 << 31) - 1, max_len)
         self._bytes = {}
@@ -246,9 +246,14 @@ class BlockCache(_Queued):
             batch._bytes[key] = nbytes
         return nbytes
 
-    def _queries(self, batch, q):
+    def _check_batch(self, batch):
         if not isinstance(batch, CacheBatch):
             raise TypeError("batch: a CacheBatch (BlockCache.batch) is expected")
+        if batch.device != self.device:
+            raise ValueError(f"batch: made for {batch.device}, expected {self.device}")
+
+    def _queries(self, batch, q):
+        self._check_batch(batch)
         _heads(q, "q", None, self.head_dim, self.device)
         if q.shape[1] < 1 or q.shape[1] % self.kv_heads != 0:
             raise ValueError(f"q: {q.shape[1]} heads, a multiple of {self.kv_heads} is expected")
@@ -258,8 +263,7 @@ class BlockCache(_Queued):
         head_dim] (any strides) to slots ``start`` [S] onwards; ``rotary``
         rotates k to ``positions`` [T] first.  ``batch.lens`` counts the new
         tokens already."""
-        if not isinstance(batch, CacheBatch):
-            raise TypeError("batch: a CacheBatch (BlockCache.batch) is expected")
+        self._check_batch(batch)
         _heads(k, "k", self.kv_heads, self.head_dim, self.device)
         _heads(v, "v", self.kv_heads, self.head_dim, self.device)
         T = k.shape[0]
@@ -347,8 +351,7 @@ class BlockCache(_Queued):
         out_blocks * 32).  Returns (lens_out [S], kept, weights_out [S,
         kv_heads, out_blocks * 32]), new unless given; places behind a
         sequence's new length are not written."""
-        if not isinstance(batch, CacheBatch):
-            raise TypeError("batch: a CacheBatch (BlockCache.batch) is expected")
+        self._check_batch(batch)
         S, H, dev = batch.S, self.kv_heads, self.device
         i32, f32 = (torch.int32,), (torch.float32,)
         _need(weights, "weights", f32, (S, H, batch.blocks * _BLOCK), dev)

@@ -350,3 +350,16 @@ def test_objects_off_the_gpu_launch_nothing(monkeypatch):
                 f()
             assert e.value.status == E.DLLM_ERR_UNSUPPORTED
     assert lib.launched == []
+
+
+def test_batch_of_another_device_refused():
+    cache, _, i = _objects()
+    other = mtl.BlockCache(12, 2, 64, device="meta")
+    meta = lambda *s: torch.zeros(s, dtype=torch.int32, device="meta")  # noqa: E731
+    batch = other.batch(meta(3), meta(2), meta(2, 3))
+    k, q = torch.zeros((5, 2, 64), dtype=torch.bfloat16), torch.zeros((5, 4, 64), dtype=torch.bfloat16)
+    w, lse, to = torch.zeros((2, 2, 96)), torch.zeros((5, 4)), torch.zeros((2, 2), dtype=torch.int32)
+    for f in (lambda: cache.write(batch, k, k, i(0, 0)), lambda: cache.attend(batch, q),
+              lambda: cache.weigh(batch, q, lse, w), lambda: cache.evict(batch, w, i(1, 1), to)):
+        with pytest.raises(ValueError, match="batch"):
+            f()
