@@ -158,6 +158,8 @@ dllm_status dllm_cache_attention(const dllm_cache *cache, const dllm_cache_batch
  * see token j, for every j < lens[s]; the rest of weights stays as it was.
  *   lse      [T, q_heads] float32 as dllm_cache_attention wrote it for the
  *            same q, scale and causal
+ *            (-inf: the query adds nothing; NaN: the tokens that it sees, and
+ *            no others, become NaN)
  *   decay    0 <= decay <= 1; with 0 the old weights are not read
  *   weights  [S, kv_heads, table_blocks * 32] float32
  */

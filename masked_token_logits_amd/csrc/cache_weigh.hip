@@ -161,12 +161,19 @@ __global__ __launch_bounds__(kThreads, 2) void k_weigh(WeighArgs a) {
         constexpr int i = decltype(I)::value;
         const int at = row0 + t * kRows + (tile + i) * 32, row = at + col;
         const float lse = reinterpret_cast<const float*>(slot + kRows * 2 * D)[(tile + i) * 32 + col];
-        const float neg = row < rows && lse != -INFINITY ? -lse * kLog2e : -INFINITY;  // -inf where it adds nothing
+        float neg = row < rows && lse != -INFINITY ? -lse * kLog2e : -INFINITY;  // -inf where it adds nothing
         const int first_tok = token_of_row(min(at, rows - 1));
         each<0, N>([&](auto B) {
           constexpr int b = decltype(B)::value;
           if (a.causal && limit[b] + kBlock > first_tok + 1) {  // columns of this tile that see a block only in part
             const int tok = token_of_row(min(row, rows - 1));
+            if (__builtin_expect(__any(neg != neg), 0)) {
+              // a NaN lse goes into its column's scores: added behind the mask, it would reach tokens that the
+              // query does not see
+              const float nan = neg != neg ? neg : 0.0f;
+              each<b, N>([&](auto L) { sc[i][decltype(L)::value] += nan; });
+              neg = neg != neg ? 0.0f : neg;
+            }
 #pragma unroll
             for (int x = 0; x < 16; ++x) sc[i][b][x] = limit[b] + token_of(x, half) <= tok ? sc[i][b][x] : -INFINITY;
           }

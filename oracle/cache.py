@@ -234,7 +234,7 @@ def weigh(cache: dict, cu, lens, table, q: np.ndarray, lse: np.ndarray, scale: f
                 see = ok & (np.arange(length) <= length - n + i) if causal else ok
                 for g in range(group):
                     t, hq = int(cu[s]) + i, h * group + g
-                    if np.isfinite(lse[t, hq]):
+                    if lse[t, hq] != -np.inf:
                         got[see] += np.exp(scale * (k[see] @ q[t, hq]) - float(lse[t, hq]))
             old = decay * out[s, h, :length] if decay else 0.0
             out[s, h, :length] = np.where(ok, old + got, out[s, h, :length])

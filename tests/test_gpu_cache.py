@@ -425,6 +425,44 @@ def test_weigh_parity(D, heads, Hq, lens, new, causal, decay):
         same = np.isnan(x) & np.isnan(y)                # the hole, where decay is 0
         assert np.all(same | (np.abs(x - y) <= tol)), f"sequence {s}"
 
+@pytest.mark.parametrize("D,heads,Hq,S", [(64, 2, 4, 2), (128, 1, 3, 2), (256, 1, 1, 2),   # few workgroups
+                                          (64, 16, 16, 16), (128, 32, 32, 8)])             # of eight blocks
+def test_weigh_nan_queries_reach_what_they_see(D, heads, Hq, S):
+    """Under a causal mask a NaN query (whose lse is NaN) makes the tokens that it sees NaN, in its key head, and
+    leaves the others to the queries that see them."""
+    import torch
+    rng = np.random.default_rng(51 + D)
+    lens = [80] * S
+    new = [70] * (S - 1) + [80]
+    print(f"[case] weigh nan D={D} heads={heads}/{Hq} S={S}", flush=True)
+    table, pages = tables(rng, lens)
+    c = cache(rng, pages, heads, D, lens, table)
+    q, qf = bf16(rng, (sum(new), Hq, D))
+    cu = cu_of(new)
+    hit = [(0, 20, 0), (0, 50, Hq - 1), (S - 1, 3, 0)]            # sequence, query, head
+    for s, i, h in hit:
+        q[cu[s] + i, h, 5], qf[cu[s] + i, h, 5] = 0x7FC0, np.nan
+    w0 = rng.random((S, heads, table.shape[1] * 32)).astype(np.float32)
+    bc = on_gpu(c)
+    b = _batch(bc, cu, lens, table, max_len=96)
+    _, lse = bc.attend(b, dev_bf16(q), causal=True, lse=True)
+    w = torch.from_numpy(w0.copy()).cuda()
+    bc.weigh(b, dev_bf16(q), lse, w, causal=True)
+    torch.cuda.synchronize()
+    lh = lse.cpu().numpy()
+    scale = float(np.float32(D ** -0.5))
+    want = oc.weigh(c, cu, lens, table, qf, lh, scale, True, w0, 1.0)
+    r = oc.attend(c, cu, lens, table, qf, scale, True)
+    rel = np.nanmax(np.where(np.isfinite(r["lse"]), _dS(r, D) + 2.0 ** -21 * (np.abs(r["lse"]) + r["A"] + 1), 0))
+    got = w.cpu().numpy().astype(np.float64)
+    nan = np.zeros((S, heads, 80), bool)
+    for s, i, h in hit:
+        nan[s, h // (Hq // heads), :80 - new[s] + i + 1] = True
+    np.testing.assert_array_equal(np.isnan(got[..., :80]), nan)
+    x, y = got[..., :80][~nan], want[..., :80][~nan]
+    tol = (rel + sum(new) * Hq * 2.0 ** -24) * np.abs(y - w0[..., :80][~nan]) + 2.0 ** -22 * np.abs(y)
+    assert np.all(np.abs(x - y) <= tol)
+
 
 # ---- eviction -------------------------------------------------------------------------------------------------
 
