@@ -143,8 +143,9 @@ size_t dllm_cache_attention_workspace_bytes(const dllm_cache *cache, const dllm_
  * (else DLLM_ERR_UNSUPPORTED; the same for dllm_cache_weigh).
  * A query that sees no token gets out = 0 and lse = -inf.
  * Sums are fp32.  For its product with v a probability is rounded to fp16
- * (its own sum takes it unrounded), and a value counts to within 2^-33 of the
- * head's largest.
+ * once or twice (its own sum takes it unrounded), which below 2^-21 of the
+ * largest one moves it by up to 2^-31 of that, and a value counts to within
+ * 2^-33 of the head's largest.
  */
 dllm_status dllm_cache_attention(const dllm_cache *cache, const dllm_cache_batch *batch, int64_t T, const uint16_t *q,
                                  int64_t q_token, int64_t q_head, int32_t q_heads, float scale, int32_t causal,

@@ -187,11 +187,11 @@ def write(cache: dict, cu, lens, table, start, k: np.ndarray, v: np.ndarray, pos
 
 def attend(cache: dict, cu, lens, table, q: np.ndarray, scale: float, causal: bool):
     """q [T, q_heads, D] fp64.  Returns a dict with out, lse and, for error
-    bounds, per query (and dimension): B = sum p |v| and Q = sqrt(sum p^2 v^2),
-    each over sum p, and A = scale max_j sum_i |q_i k_ji|."""
+    bounds, per query (and dimension): B = sum p |v|, Q = sqrt(sum p^2 v^2) and
+    V = (largest p) sum |v|, each over sum p, and A = scale max_j sum_i |q_i k_ji|."""
     T, Hq, D = q.shape
     heads = cache["k"].shape[1]
-    r = {n: np.full((T, Hq, D), np.nan) for n in ("out", "B", "Q")}
+    r = {n: np.full((T, Hq, D), np.nan) for n in ("out", "B", "Q", "V")}
     r["lse"], r["A"] = (np.full((T, Hq), np.nan) for _ in range(2))
     for s in range(len(lens)):
         n, length = int(cu[s + 1] - cu[s]), int(lens[s])
@@ -203,7 +203,7 @@ def attend(cache: dict, cu, lens, table, q: np.ndarray, scale: float, causal: bo
                 for g in range(Hq // heads):
                     t, hq = int(cu[s]) + i, h * (Hq // heads) + g
                     if not see.any():
-                        for name in ("out", "B", "Q"):
+                        for name in ("out", "B", "Q", "V"):
                             r[name][t, hq] = 0
                         r["lse"][t, hq], r["A"][t, hq] = -np.inf, 0
                         continue
@@ -216,6 +216,7 @@ def attend(cache: dict, cu, lens, table, q: np.ndarray, scale: float, causal: bo
                     r["lse"][t, hq] = top + math.log(tot)
                     r["B"][t, hq] = p @ np.abs(vs) / tot
                     r["Q"][t, hq] = np.sqrt((p * p) @ (vs * vs)) / tot
+                    r["V"][t, hq] = np.abs(vs).sum(0) / tot
                     r["A"][t, hq] = scale * (np.abs(ks) @ np.abs(q[t, hq])).max()
     return r
 

@@ -381,6 +381,46 @@ def test_attention_nan_stays_where_it_is_seen():
     assert bad.sum() == 1 and bad[7] and np.array_equal(np.isnan(l.cpu().numpy()[:, 0]), bad)
 
 
+def _check_faint(out, r, D, where):
+    """Outputs made by tokens of faint probability, where what fp16 has of it below its normal range counts too.
+    A probability is held in units in which the largest of its run is at least 2^7; below 2^-14 of them fp16 numbers
+    are 2^-24 apart, so that each of at most two roundings moves it by 2^-25, which is 2^-32 of the largest:
+    2^-31 V more than the tolerance above."""
+    import torch
+    out = WL.bf16_to_f32(out.cpu().view(torch.int16).numpy().view(np.uint16)).astype(np.float64)
+    tol = 6 * 2.0 ** -11 * r["Q"] + (2 * _dS(r, D)[..., None] + 2.0 ** -20) * r["B"] + 2.0 ** -8 * np.abs(r["out"])
+    err, tol = np.abs(out - r["out"]), tol + 2.0 ** -31 * r["V"]
+    assert np.all(err <= tol), f"{where}: {np.argwhere(~(err <= tol))[:3].tolist()}, {np.max(err / tol):.3g} tolerances"
+
+
+@pytest.mark.parametrize("D,Hq,new,extra", [(64, 2, 70, 80000), (128, 1, 140, 80000), (256, 5, 30, 80000),
+                                            (64, 1, 3, 0)])
+@pytest.mark.parametrize("step", [1.0, 1.875, 2.0])
+def test_attention_values_of_faint_tokens(D, Hq, new, extra, step):
+    """The most attended tokens have values of 0, and what there is comes from those of the block before them, whose
+    scores lie up to 2^-23 lower: the reference moves far while their probabilities wait for their product."""
+    import torch
+    rng = np.random.default_rng(36)
+    lens = [128]
+    print(f"[case] faint D={D} heads=1/{Hq} new={new} step={step}", flush=True)
+    table, pages = tables(rng, lens)
+    c = cache(rng, pages, 1, D)
+    q, qf = np.full((new, Hq, D), 0x3F80, np.uint16), np.ones((new, Hq, D))
+    for name in "kv":
+        c[name + "_scale"][:] = 127
+    for j, (key, loud) in enumerate(((0.0, False), (0.0, True), (step, False), (step, False))):
+        c["k"][table[0, j]] = oc.e4m3_bytes(np.array([key]))[0]
+        if not loud:
+            c["v"][table[0, j]] = 0
+    bc = on_gpu(c)
+    wide = np.concatenate([table, np.full((1, extra), -1, np.int32)], 1)
+    o, l = bc.attend(_batch(bc, cu_of([new]), lens, wide), dev_bf16(q), scale=8.0 / D, lse=True)
+    torch.cuda.synchronize()
+    r = oc.attend(c, cu_of([new]), lens, table, qf, 8.0 / D, False)
+    _check_faint(o, r, D, "faint")
+    assert np.all(np.abs(l.cpu().numpy() - r["lse"]) <= _dS(r, D) + 2.0 ** -21 * (np.abs(r["lse"]) + r["A"] + 1))
+
+
 # ---- accumulated weights --------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("decay", [1.0, 0.5, 0.0])
