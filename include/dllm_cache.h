@@ -15,9 +15,9 @@
  * token j of a sequence is token j % 32 of page table[j / 32].
  *   k, v              [pages, kv_heads, 32 * head_dim] e4m3 bytes
  *   k_scale, v_scale  [pages, kv_heads] bytes: the scale's exponent + 127
- * A value is its e4m3 byte times 2^(scale byte - 127).  The bytes of a block
- * stand in the order in which the matrix instructions read them: with
- * D = head_dim,
+ * A value is its e4m3 byte times 2^(scale byte - 127); scale bytes 0 and 255,
+ * which no call writes, count as 1 and 254.  The bytes of a block stand in the
+ * order in which the matrix instructions read them: with D = head_dim,
  *   k  [D / 32][2][32][16]: byte (c, h, t, j) is token t, dim h D/2 + 16 c + j
  *   v  [D / 32][2][32][16]: byte (c, h, r, b) is token 8 (b / 4) + 4 h + b % 4,
  *                           dim 32 c + r

@@ -96,8 +96,8 @@ struct Walk {
     const int b = base + (threadIdx.x & 63);
     page = b < last ? page_of(a.b.table, a.b.table_blocks, a.c.pages, s, b) : -1;
     const int64_t at = block_of(a.c, max(page, 0), h);
-    k_byte = a.c.k_scale[at];
-    v_byte = a.c.v_scale[at];
+    k_byte = stored_scale(a.c.k_scale, at);
+    v_byte = stored_scale(a.c.v_scale, at);
   }
 
   // Wait for them here: behind a branch the wait would be for every load in
@@ -301,7 +301,7 @@ struct Lookup {
     const int page = b < last ? page_of(a.b.table, a.b.table_blocks, a.c.pages, s, b) : -1;
     const int64_t x = block_of(a.c, max(page, 0), h);
     at = page < 0 ? -1 : x * (kBlock * D);
-    info = page < 0 ? 127 | 1 << 8 : a.c.k_scale[x] | a.c.v_scale[x] << 8 | 1 << 16;  // no page: moves no scale
+    info = page < 0 ? 127 | 1 << 8 : stored_scale(a.c.k_scale, x) | stored_scale(a.c.v_scale, x) << 8 | 1 << 16;  // no page: moves no scale
     // wait for them here: behind the branch the wait would be for every load
     // in flight, at every use
     asm volatile("" : "+v"(at), "+v"(info));

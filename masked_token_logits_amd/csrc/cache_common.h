@@ -46,6 +46,10 @@ __device__ __forceinline__ int64_t block_of(const dllm_cache& c, int page, int h
   return (int64_t)page * c.kv_heads + h;
 }
 
+// A stored scale byte: those that are not a normal float32's exponent count as the nearest
+// that is, so that 0 is free to stand for no scale at all.
+__device__ __forceinline__ int stored_scale(const uint8_t* scale, int64_t at) { return min(max((int)scale[at], 1), 254); }
+
 // 2^(byte - 127) for a scale byte of 1 .. 254.
 __device__ __forceinline__ float scale_value(int byte) { return __uint_as_float((uint32_t)byte << 23); }
 

@@ -490,7 +490,7 @@ __global__ __launch_bounds__(kMoveThreads) void k_move(MoveArgs a) {
       slot[tid] = 0;
     }
     src[tid] = at < 0 ? -1 : at * (kBlock * D);
-    int k = at >= 0 ? a.c.k_scale[at] : 0, v = at >= 0 ? a.c.v_scale[at] : 0;
+    int k = at >= 0 ? stored_scale(a.c.k_scale, at) : 0, v = at >= 0 ? stored_scale(a.c.v_scale, at) : 0;
     const int k_own = k, v_own = v;
     ke[tid] = k, ve[tid] = v;
     for (int o = 16; o; o >>= 1) {

@@ -95,7 +95,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_weigh(WeighArgs a) {
     ok[b] = page >= 0;
     limit[b] = block[b] * kBlock - before;
     const int64_t at = block_of(a.c, max(page, 0), h);
-    const float scale = scale_value(a.c.k_scale[at]);
+    const float scale = scale_value(stored_scale(a.c.k_scale, at));
     const uint8_t* p = a.c.k + at * (kBlock * D) + lane * 16;
     each<0, D / 32>([&](auto C) {
       constexpr int c = decltype(C)::value;

@@ -88,7 +88,7 @@ __global__ __launch_bounds__(kThreads) void k_write(dllm_cache c, dllm_cache_bat
     const int any_held = __syncthreads_or(held);
     big = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
     if (side == 0 && half) big *= key_gain(plan, D);
-    const int had = *scale;
+    const int had = stored_scale(scale, 0);
     int byte = max(scale_byte(big), any_held ? had : 0);
     byte = min(max(byte, DLLM_CACHE_SCALE_MIN), DLLM_CACHE_SCALE_MAX);
     const float inv = __uint_as_float((uint32_t)(254 - byte) << 23);  // 2^(127 - byte); 2^-127 at the largest byte
@@ -265,7 +265,7 @@ __global__ __launch_bounds__(2 * D, 4) void k_write_pieces(WriteArgs a) {
     if (fresh) big = fmaxf(fmaxf(largest_of(x[0]), largest_of(x[1])), fmaxf(largest_of(x[2]), largest_of(x[3])));
     for (int o = 32; o; o >>= 1) big = fmaxf(big, __shfl_xor(big, o));
     if ((tid & 63) == 0) top[tid >> 6] = big;
-    const int k_had = any_held ? a.c.k_scale[at] : 0, v_had = any_held ? a.c.v_scale[at] : 0;
+    const int k_had = any_held ? stored_scale(a.c.k_scale, at) : 0, v_had = any_held ? stored_scale(a.c.v_scale, at) : 0;
     __syncthreads();
     float kbig = 0.0f, vbig = 0.0f;
 #pragma unroll

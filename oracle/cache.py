@@ -110,11 +110,16 @@ def places(D: int, key: bool) -> np.ndarray:
     return np.array([[f(t, d, D) for d in range(D)] for t in range(BLOCK)])
 
 
+def stored_scale(cache: dict, name: str, page: int, head: int) -> int:
+    """A block's scale byte; 0 and 255 count as 1 and 254."""
+    return min(max(int(cache[name + "_scale"][page, head]), 1), 254)
+
+
 def read_block(cache: dict, name: str, page: int, head: int) -> np.ndarray:
     """[32, D] fp64."""
     D = cache[name].shape[2] // BLOCK
     raw = E4M3[cache[name][page, head]][places(D, name == "k")]
-    return raw * 2.0 ** (int(cache[name + "_scale"][page, head]) - 127)
+    return raw * 2.0 ** (stored_scale(cache, name, page, head) - 127)
 
 
 def read_tokens(cache: dict, name: str, table: np.ndarray, head: int, n: int) -> tuple[np.ndarray, np.ndarray]:
@@ -170,7 +175,7 @@ def write(cache: dict, cu, lens, table, start, k: np.ndarray, v: np.ndarray, pos
                     fin = np.where(np.isfinite(x[at, h]), np.abs(x[at, h]), 0)
                     byte = scale_byte(float(np.float32(fin.max(initial=0)) * g))
                     if held.any():
-                        byte = min(max(byte, int(cache[name + "_scale"][page, h])), SCALE_MAX)
+                        byte = min(max(byte, stored_scale(cache, name, page, h)), SCALE_MAX)
                     rows = np.zeros((BLOCK, D))
                     rows[held] = read_block(cache, name, page, h)[held] * 2.0 ** (127 - byte)
                     rows[fresh] = y[at, h] * 2.0 ** (127 - byte)
@@ -275,7 +280,7 @@ def evict(cache: dict, lens, table, weights: np.ndarray, keep, sink: int, recent
                 src = [int(table[s, j // BLOCK]) for j in js]
                 for name in "kv":
                     pl = places(D, name == "k")
-                    es = [int(cache[name + "_scale"][p, h]) if 0 <= p < pages else 0 for p in src]
+                    es = [stored_scale(cache, name, p, h) if 0 <= p < pages else 0 for p in src]
                     top = max(max(es), SCALE_MIN)
                     put = np.zeros((BLOCK, D), np.uint8)
                     for t, (j, p, e) in enumerate(zip(js, src, es)):

@@ -601,3 +601,82 @@ def test_evict_long_rows(kind):
 def test_evict_bad_pages_and_cut_keep():
     _evict(np.random.default_rng(42), [100, 90], [64, 60], 4, 0, 1, bad=True)
     _evict(np.random.default_rng(43), [100, 90], [64, 60], 4, 0, 1, max_keep=37)
+
+
+# ---- scale bytes that no write leaves ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("D,heads,Hq,lens,new,causal,extra", [
+    (64, 40, 40, [1300, 330], [1, 2], False, 0),           # few rows, several blocks to a wave
+    (128, 1, 4, [300], [9], True, 0),
+    (64, 40, 80, [700], [70], False, 1000),                # many
+    (256, 1, 5, [400], [30], True, 30000),
+])
+@pytest.mark.parametrize("kind", ["low", "high"])
+def test_attention_outermost_scale_bytes(D, heads, Hq, lens, new, causal, extra, kind):
+    """Scale bytes 0 and 255 count as 1 and 254, wherever along the cache they stand."""
+    import torch
+    rng = np.random.default_rng(34)
+    print(f"[case] scale bytes {kind} D={D} heads={heads}/{Hq} lens={lens} new={new} causal={causal} {extra}", flush=True)
+    table, pages = tables(rng, lens)
+    c = cache(rng, pages, heads, D, lens, table)
+    if kind == "low":                                      # so that runs of blocks begin with some
+        for s, n in enumerate(lens):
+            blocks = np.arange((n + 31) // 32)
+            c["v_scale"][table[s, blocks[blocks % 3 < 2]]] = 0
+            c["k_scale"][table[s, blocks[::4]]] = 0
+    else:                                                  # values within 1, for sums that bf16 holds
+        for p in range(pages):
+            c["v"][p] = np.where((c["v"][p] & 0x7F) == 0x7F, c["v"][p], (c["v"][p] & 0x87) | 0x28)
+        for s in range(len(lens)):
+            c["v_scale"][table[s, [1, 6]]] = 255
+    q, qf = bf16(rng, (sum(new), Hq, D))
+    bc = on_gpu(c)
+    wide = np.concatenate([table, np.full((len(lens), extra), -1, np.int32)], 1)
+    o, l = bc.attend(_batch(bc, cu_of(new), lens, wide), dev_bf16(q), causal=causal, lse=True)
+    torch.cuda.synchronize()
+    r = oc.attend(c, cu_of(new), lens, table, qf, float(np.float32(D ** -0.5)), causal)
+    _check_faint(o, r, D, f"scale bytes {kind}")            # the most attended tokens may be those without values
+    assert np.all(np.abs(l.cpu().numpy() - r["lse"]) <= _dS(r, D) + 2.0 ** -21 * (np.abs(r["lse"]) + r["A"] + 1))
+
+
+def test_weigh_write_and_evict_outermost_scale_bytes():
+    """The same where the other calls read them: keys of accumulated weights, the tokens that a write holds, the
+    blocks that an eviction moves."""
+    import torch
+    rng = np.random.default_rng(35)
+    D, heads, lens, new, start = 64, 2, [100, 78], [20, 11], [80, 67]
+    table, pages = tables(rng, lens)
+    table_out = (pages + np.arange(4).reshape(2, 2)).astype(np.int32)
+    c = cache(rng, pages + 4, heads, D)
+    for name in "kv":                                      # values within 1, none of them NaN
+        c[name] = (c[name] & 0x87) | 0x28
+    c["k_scale"][table[0, :3]], c["v_scale"][table[0, :4]] = 0, 0
+    q, qf = bf16(rng, (31, 2, D))
+    bc = on_gpu(c)
+    b = _batch(bc, cu_of(new), lens, table)
+    _, lse = bc.attend(b, dev_bf16(q), lse=True)
+    w = torch.zeros(2, heads, table.shape[1] * 32, device="cuda")
+    bc.weigh(b, dev_bf16(q), lse, w)
+    torch.cuda.synchronize()
+    scale = float(np.float32(D ** -0.5))
+    want = oc.weigh(c, cu_of(new), lens, table, qf, lse.cpu().numpy(), scale, False, np.zeros(w.shape, np.float32), 1.0)
+    r = oc.attend(c, cu_of(new), lens, table, qf, scale, False)
+    rel = (_dS(r, D) + 2.0 ** -21 * (np.abs(r["lse"]) + r["A"] + 1)).max() + 31 * 2.0 ** -24
+    got = w.cpu().numpy().astype(np.float64)
+    assert np.all(np.abs(got - want) <= rel * np.abs(want))
+    c["v_scale"][table[1, :3], 0], c["k_scale"][table[1, 2], 1] = 255, 255
+    bc = on_gpu(c)
+    x, xf = bf16(rng, (31, heads, D))
+    bc.write(b, dev_bf16(x), dev_bf16(x), dev_i32(start))
+    torch.cuda.synchronize()
+    want, _ = oc.write(c, cu_of(new), lens, table, start, xf, xf)
+    got = host(bc)
+    for name in want:
+        np.testing.assert_array_equal(got[name], want[name], err_msg=f"write {name}")
+    w = rng.random((2, heads, table.shape[1] * 32)).astype(np.float32)
+    bc.evict(b, torch.from_numpy(w).cuda(), dev_i32([50, 60]), dev_i32(table_out))
+    torch.cuda.synchronize()
+    moved = oc.evict(got, lens, table, w, [50, 60], 0, 0, 1, table_out)[0]
+    got = host(bc)
+    for name in moved:
+        np.testing.assert_array_equal(got[name], moved[name], err_msg=f"evict {name}")
