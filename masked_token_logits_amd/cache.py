@@ -54,6 +54,22 @@ def _heads(t, name: str, heads, dim, device):
         raise ValueError(f"{name}: on {t.device}, expected {device}")
 
 
+def _overlap(x, y) -> bool:
+    """Whether heads x [T, H, dim] of any strides share memory with contiguous y."""
+    T, H, D = x.shape
+    size, delta = x.element_size(), y.data_ptr() - x.data_ptr()
+    token, head = x.stride(0) * size if T > 1 else 0, x.stride(1) * size if H > 1 else 0
+    # a head shares some if it begins in lo + 1 .. hi - 1, counted from x's first
+    lo, hi = delta - D * size, delta + y.numel() * y.element_size()
+    if hi <= 0 or lo >= (T - 1) * token + (H - 1) * head or T * H == 0:
+        return False
+    for begin in range(0, H * head, head) if head else (0,):
+        first = max((lo - begin) // token + 1, 0) if token else 0      # the first token behind lo
+        if first < T and lo < begin + first * token < hi:
+            return True
+    return False
+
+
 class _Queued:
     """Runs library calls on the object's stream, or the current one."""
 
@@ -131,7 +147,8 @@ class Rotary(_Queued):
 
     def __call__(self, x, positions, out=None, transpose: bool = False):
         """Queue out = x [T, H, head_dim] rotated to ``positions`` [T] (int32);
-        returns out (new and contiguous unless given; may be x).
+        returns out (new and contiguous unless given; may be x, but overlaps it
+        in no other way).
         ``transpose`` turns the other way, which takes the gradient of the
         output to the gradient of x."""
         _heads(x, "x", None, self.head_dim, self.device)
@@ -299,11 +316,13 @@ class BlockCache(_Queued):
             scale = D ** -0.5
         if out is not None:
             _need(out, "out", (q.dtype,), (T, H, D), self.device)
-            if T and out.data_ptr() == q.data_ptr():
-                raise ValueError("out: must not be q, which is read to the end")
+            if _overlap(q, out):
+                raise ValueError("out: must not overlap q, which is read to the end")
         given = lse if isinstance(lse, torch.Tensor) else None
         if given is not None:
             _need(given, "lse", (torch.float32,), (T, H), self.device)
+            if _overlap(q, given) or (out is not None and _overlap(out, given)):
+                raise ValueError("lse: must not overlap q or out")
         want = given is not None or bool(lse)
         nbytes = self._workspace(batch, "dllm_cache_attention_workspace_bytes", H)
         box = [out, given]

@@ -363,3 +363,25 @@ def test_batch_of_another_device_refused():
               lambda: cache.weigh(batch, q, lse, w), lambda: cache.evict(batch, w, i(1, 1), to)):
         with pytest.raises(ValueError, match="batch"):
             f()
+
+
+def test_attention_outputs_that_overlap_the_queries_refused():
+    cache, batch, _ = _objects()
+    flat = torch.zeros(4096 * 8, dtype=torch.bfloat16)
+    n = 5 * 4 * 64
+    at = lambda i: flat[i:i + n].view(5, 4, 64)  # noqa: E731
+    fused = flat[:3 * n].view(5, 12, 64)[:, 4:8]
+    spread = flat[:5 * 6000].view(5, 6000)[:, :256].view(5, 4, 64)      # rows far apart, room between them
+    turned = flat[:n].view(4, 5, 64).transpose(0, 1)
+    one = flat[:64].view(1, 1, 64).expand(5, 4, 64)
+    f32 = flat.view(torch.float32)
+    for q, kw in ((at(0), dict(out=at(256))), (at(256), dict(out=at(0))), (fused, dict(out=at(256))),
+                  (fused, dict(out=at(768 * 4 + 448))), (spread, dict(out=at(24000 - n + 8))), (turned, dict(out=at(n - 64))),
+                  (one, dict(out=at(0))), (at(0), dict(lse=f32[100:120].view(5, 4))),
+                  (at(n), dict(out=at(4 * n), lse=f32[2 * n + 8:2 * n + 28].view(5, 4)))):
+        with pytest.raises(ValueError, match="overlap"):
+            cache.attend(batch, q, **kw)
+    for q, kw in ((at(0), dict(out=at(n))), (at(n), dict(out=at(0))), (fused, dict(out=at(768 * 4 + 512))), (spread, dict(out=at(256))),
+                  (spread, dict(out=at(6000 - n))), (one, dict(out=at(64))), (at(0), dict(lse=f32[n // 2:n // 2 + 20].view(5, 4)))):
+        with pytest.raises(mtl.DllmError):                              # on to the call, which needs a GPU
+            cache.attend(batch, q, **kw)
