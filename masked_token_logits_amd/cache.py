@@ -177,7 +177,9 @@ class CacheBatch:
     [S, blocks] (int32, on the cache's device; include/dllm_cache.h).  The
     contents may change between calls, as a decoding loop's do; ``max_new``
     and ``max_len`` are host bounds on them (defaults: any number of new
-    tokens, the table's whole capacity)."""
+    tokens, the table's whole capacity).  They choose kernels and size grids, so
+    tight ones are faster: without ``max_new`` all new tokens of a call may be
+    one sequence's."""
 
     def __init__(self, cu, lens, table, max_new: int | None, max_len: int | None, device):
         if table.dim() != 2 or table.shape[1] < 1:

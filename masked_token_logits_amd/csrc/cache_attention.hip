@@ -84,11 +84,11 @@ __device__ __forceinline__ void write_rows(const AttendArgs& a, const Row& r, in
 template <int D>
 struct Walk {
   const AttendArgs& a;
-  int s, h, base, last, have;  // base: the block that lane 0's look-up stands for
+  int s, h, base, last;  // base: the block that lane 0's look-up stands for
   int page, k_byte, v_byte;
 
-  __device__ Walk(const AttendArgs& a_, int s_, int h_, int first, int last_, int len)
-      : a(a_), s(s_), h(h_), base(first - 64), last(last_), have(len) {}
+  __device__ Walk(const AttendArgs& a_, int s_, int h_, int first, int last_)
+      : a(a_), s(s_), h(h_), base(first - 64), last(last_) {}
 
   // Pages of 64 blocks from j on, and their scales on their way.
   __device__ __forceinline__ void look(int j) {
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_attend_few(AttendArgs a) {
     const int last = min(at.begin + n, (q.len + kBlock - 1) / kBlock);
     Accumulator<D> acc;
     clear(acc);
-    Walk<D> walk(a, at.s, at.h, at.begin + wave, last, q.len);
+    Walk<D> walk(a, at.s, at.h, at.begin + wave, last);
     i32x4 k[D / 32], v[D / 32];
     int kb, vb;
     int j = at.begin + wave;
@@ -325,8 +325,8 @@ __device__ __forceinline__ bool has_page(int info) { return info >> 16 != 0; }
 // block b - 1, so that the matrix pipe and the VALU work at the same time.
 //
 // Bound by instruction issue: of 8192 queries over 8192 tokens, 28 heads of 128 on 4 (962
-// GFLOP, 820 to 870 us by the card's clock, 1110 to 1170 TFLOP/s where a bf16 product of
-// 8192^3 reaches 1487), a SIMD's cycles are 58% matrix and 64% vector instructions,
+// GFLOP, 830 to 895 us a call by the card's clock, 1075 to 1160 TFLOP/s where a bf16 product
+// of 8192^3 reaches 1487), a SIMD's cycles are 56% matrix and 63% vector instructions,
 // side by side: a score's exponential, scaling, sum, maximum and rounding and a widened key's and value's
 // conversions.  Two groups of 32 rows to a wave halve the widening; a third has no registers.
 template <int D, int RG>

@@ -466,8 +466,8 @@ __device__ __forceinline__ float exact_scale(int x) { return x < -126 ? 0.0f : _
 // One workgroup: one new block of one head, gathered from its tokens' old
 // places.  Bound by memory: a kept token's keys are pieces of 16 bytes and its values
 // single bytes of blocks that hold 32 tokens, so that the lines of a block are read
-// whole or nearly.  16385 of up to 131072 tokens of 4 sequences and heads: 261 MB read for 71
-// that are kept, 66 written, 70 us (4.7 TB/s); half of 4096 tokens, 32 heads, 16 us.
+// whole or nearly.  16385 of up to 131072 tokens of 4 sequences and heads: 267 MB read for 71
+// that are kept, 68 written, 70 us (4.8 TB/s); half of 4096 tokens, 32 heads, 16 us.
 template <int D>
 __global__ __launch_bounds__(kMoveThreads) void k_move(MoveArgs a) {
   const int s = blockIdx.z, h = blockIdx.y, blk = blockIdx.x, tid = threadIdx.x;
