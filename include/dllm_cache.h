@@ -113,8 +113,8 @@ typedef struct {
  * that and 1 for keys rotated in some (the others stay as they are), else 1.
  * Values are rounded once, to nearest even, from an fp64 rotation.  What is
  * not finite, a key that its rotation takes beyond float32 among it, is
- * stored as NaN.  Slots of touched blocks at or behind lens[s] are cleared.  A page
- * may be written through one table entry of a call only.
+ * stored as NaN.  Slots of touched blocks at or behind lens[s] are cleared.
+ * A page may be written through one table entry of a call only.
  */
 dllm_status dllm_cache_write(const dllm_cache *cache, const dllm_cache_batch *batch, int64_t T, const uint16_t *k,
                              int64_t k_token, int64_t k_head, const uint16_t *v, int64_t v_token, int64_t v_head,
