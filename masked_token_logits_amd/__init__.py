@@ -10,8 +10,10 @@ this package is its thin Python binding.  PyTorch only provides device
 memory and streams.
 
 Beside it: the sequence-chunked SwiGLU FFN (SwiGLUFFN), rotary positions
-(Rotary) and an 8-bit paged cache of keys and values with attention over it
-and eviction by attention weight (BlockCache).
+(Rotary), an 8-bit paged cache of keys and values with attention over it
+and eviction by attention weight (BlockCache), the residual update and norms
+between blocks (ResidualNorm), the token embedding (Embedding) and the loss
+of the masked positions (MaskedLoss), the last three with their gradients.
 """
 from __future__ import annotations
 
@@ -24,6 +26,7 @@ from ._abi import (  # noqa: F401
     DLLM_ERR_WORKSPACE,
     DLLM_K_MAX_LIMIT,
     DLLM_NOALLOC_SCRATCH_BYTES,
+    DLLM_NORM_DIM_MAX,
     DLLM_OK,
     DLLM_ROTARY_DIM_MAX,
     DLLM_SCORE_CONF,
@@ -40,9 +43,17 @@ from ._abi import (  # noqa: F401
     dllm_cache_evict_workspace_bytes,
     dllm_cache_weigh,
     dllm_cache_write,
+    dllm_embed,
+    dllm_embed_backward,
+    dllm_embed_backward_workspace_bytes,
     dllm_ffn_pack_gate_up,
     dllm_ffn_swiglu_chunked,
     dllm_ffn_workspace_bytes,
+    dllm_loss,
+    dllm_loss_backward,
+    dllm_loss_backward_workspace_bytes,
+    dllm_loss_forward,
+    dllm_loss_forward_workspace_bytes,
     dllm_masked_readout_create,
     dllm_masked_readout_destroy,
     dllm_masked_readout_set_gemm_events,
@@ -52,10 +63,14 @@ from ._abi import (  # noqa: F401
     dllm_masked_readout_step_ex,
     dllm_masked_readout_step_noalloc,
     dllm_masked_readout_workspace_bytes,
+    dllm_norm,
     dllm_probe_gemm_mix,
     dllm_probe_source_bytes,
     dllm_probe_wall_clock_khz,
     dllm_policy,
+    dllm_residual_norm,
+    dllm_residual_norm_backward,
+    dllm_residual_norm_backward_workspace_bytes,
     dllm_rotary,
     dllm_rotary_frequencies,
     dllm_rotary_plan,
@@ -264,3 +279,4 @@ class MaskedReadout:
 
 
 from .cache import BlockCache, CacheBatch, Rotary  # noqa: E402,F401
+from .layers import Embedding, MaskedLoss, ResidualNorm  # noqa: E402,F401

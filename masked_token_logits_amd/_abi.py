@@ -52,6 +52,16 @@ EXPORTED = (
     "dllm_cache_weigh",
     "dllm_cache_evict_workspace_bytes",
     "dllm_cache_evict",
+    "dllm_residual_norm",
+    "dllm_residual_norm_backward_workspace_bytes",
+    "dllm_residual_norm_backward",
+    "dllm_embed",
+    "dllm_embed_backward_workspace_bytes",
+    "dllm_embed_backward",
+    "dllm_loss_forward_workspace_bytes",
+    "dllm_loss_forward",
+    "dllm_loss_backward_workspace_bytes",
+    "dllm_loss_backward",
 )
 
 DLLM_ROTARY_HALF = 0
@@ -65,6 +75,7 @@ ROTARY_SCALINGS = {"none": DLLM_ROTARY_PLAIN, "linear": DLLM_ROTARY_LINEAR, "bas
                    "ramp": DLLM_ROTARY_RAMP}
 DLLM_ROTARY_DIM_MAX = 512
 DLLM_CACHE_BLOCK = 32
+DLLM_NORM_DIM_MAX = 8192
 
 
 class dllm_step_out(C.Structure):
@@ -129,6 +140,29 @@ class dllm_cache_batch(C.Structure):
         ("table_blocks", C.c_int32),
         ("max_new", C.c_int32),
         ("max_len", C.c_int32),
+    ]
+
+
+class dllm_norm(C.Structure):
+    _fields_ = [
+        ("pre", C.c_void_p),
+        ("post", C.c_void_p),
+        ("d", C.c_int64),
+        ("eps", C.c_float),
+        ("scale", C.c_float),
+    ]
+
+
+class dllm_loss(C.Structure):
+    _fields_ = [
+        ("W_lm", C.c_void_p),
+        ("hidden", C.c_void_p),
+        ("mask", C.c_void_p),
+        ("targets", C.c_void_p),
+        ("weights", C.c_void_p),
+        ("V", C.c_int64),
+        ("d", C.c_int64),
+        ("L", C.c_int64),
     ]
 
 
@@ -215,6 +249,27 @@ def load(path: str = LIB_PATH):
     lib.dllm_cache_evict_workspace_bytes.argtypes = [cache_p, batch_p]
     lib.dllm_cache_evict.restype = C.c_int
     lib.dllm_cache_evict.argtypes = [cache_p, batch_p, P, P, i32, i32, i32, i32, P, i32, P, P, P, P, C.c_size_t, P]
+    norm_p, loss_p, size = C.POINTER(dllm_norm), C.POINTER(dllm_loss), C.c_size_t
+    lib.dllm_residual_norm.restype = C.c_int
+    lib.dllm_residual_norm.argtypes = [norm_p, P, P, i64, P, i64, P, P, P]
+    lib.dllm_residual_norm_backward_workspace_bytes.restype = size
+    lib.dllm_residual_norm_backward_workspace_bytes.argtypes = [norm_p, i64, i64]
+    lib.dllm_residual_norm_backward.restype = C.c_int
+    lib.dllm_residual_norm_backward.argtypes = [norm_p, P, P, i64, P, i64, P, P, P, P, P, P, P, P, size, P]
+    lib.dllm_embed.restype = C.c_int
+    lib.dllm_embed.argtypes = [P, i64, i64, P, i64, f32, P, P]
+    lib.dllm_embed_backward_workspace_bytes.restype = size
+    lib.dllm_embed_backward_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.dllm_embed_backward.restype = C.c_int
+    lib.dllm_embed_backward.argtypes = [P, i64, P, i64, i64, f32, i32, P, P, size, P]
+    lib.dllm_loss_forward_workspace_bytes.restype = size
+    lib.dllm_loss_forward_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.dllm_loss_forward.restype = C.c_int
+    lib.dllm_loss_forward.argtypes = [loss_p, P, P, P, P, size, P]
+    lib.dllm_loss_backward_workspace_bytes.restype = size
+    lib.dllm_loss_backward_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    lib.dllm_loss_backward.restype = C.c_int
+    lib.dllm_loss_backward.argtypes = [loss_p, P, P, P, P, i32, i64, P, size, P]
     _lib = lib
     return lib
 
@@ -407,3 +462,52 @@ def dllm_cache_evict(cache, batch, weights, keep, max_keep: int, sink: int, rece
     return load().dllm_cache_evict(_ref(cache), _ref(batch), _ptr(weights), _ptr(keep), max_keep, sink, recent, pool,
                                    _ptr(table_out), out_blocks, _ptr(lens_out), _ptr(kept), _ptr(weights_out),
                                    _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def dllm_residual_norm(norm, x, y, T: int, gate, groups: int, x_out, n, stream=None) -> int:
+    return load().dllm_residual_norm(_ref(norm), _ptr(x), _ptr(y), T, _ptr(gate), groups, _ptr(x_out), _ptr(n),
+                                     _stream(stream))
+
+
+def dllm_residual_norm_backward_workspace_bytes(norm, T: int, groups: int) -> int:
+    return int(load().dllm_residual_norm_backward_workspace_bytes(_ref(norm), T, groups))
+
+
+def dllm_residual_norm_backward(norm, x, y, T: int, gate, groups: int, d_n, d_x_out, d_x, d_y, d_pre, d_post, d_gate,
+                                workspace, workspace_bytes: int, stream=None) -> int:
+    return load().dllm_residual_norm_backward(_ref(norm), _ptr(x), _ptr(y), T, _ptr(gate), groups, _ptr(d_n),
+                                              _ptr(d_x_out), _ptr(d_x), _ptr(d_y), _ptr(d_pre), _ptr(d_post),
+                                              _ptr(d_gate), _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def dllm_embed(table, V: int, d: int, tokens, T: int, scale: float, out, stream=None) -> int:
+    return load().dllm_embed(_ptr(table), V, d, _ptr(tokens), T, scale, _ptr(out), _stream(stream))
+
+
+def dllm_embed_backward_workspace_bytes(V: int, d: int, T: int) -> int:
+    return int(load().dllm_embed_backward_workspace_bytes(V, d, T))
+
+
+def dllm_embed_backward(tokens, T: int, d_out, V: int, d: int, scale: float, accumulate: int, d_table, workspace,
+                        workspace_bytes: int, stream=None) -> int:
+    return load().dllm_embed_backward(_ptr(tokens), T, _ptr(d_out), V, d, scale, accumulate, _ptr(d_table),
+                                      _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def dllm_loss_forward_workspace_bytes(V: int, d: int, L: int) -> int:
+    return int(load().dllm_loss_forward_workspace_bytes(V, d, L))
+
+
+def dllm_loss_forward(p, loss, losses, lse, workspace, workspace_bytes: int, stream=None) -> int:
+    return load().dllm_loss_forward(_ref(p), _ptr(loss), _ptr(losses), _ptr(lse), _ptr(workspace), workspace_bytes,
+                                    _stream(stream))
+
+
+def dllm_loss_backward_workspace_bytes(V: int, d: int, L: int, piece: int = 0) -> int:
+    return int(load().dllm_loss_backward_workspace_bytes(V, d, L, piece))
+
+
+def dllm_loss_backward(p, lse, grad, d_hidden, d_W, accumulate: int, piece: int, workspace, workspace_bytes: int,
+                       stream=None) -> int:
+    return load().dllm_loss_backward(_ref(p), _ptr(lse), _ptr(grad), _ptr(d_hidden), _ptr(d_W), accumulate, piece,
+                                     _ptr(workspace), workspace_bytes, _stream(stream))

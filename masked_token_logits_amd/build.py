@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdllm_readout.so")
 SOURCES = ["readout.hip", "mask_compact.hip", "gemm_online.hip", "gemm_persistent.hip", "merge_select.hip",
            "ffn.hip", "probe.hip", "rotary.hip", "cache_write.hip", "cache_attention.hip", "cache_weigh.hip",
-           "cache_evict.hip"]
+           "cache_evict.hip", "norm.hip", "embed.hip", "loss.hip", "loss_gemm.hip"]
 ARCH = "gfx950"
 # Matrix results in ordinary registers where they are used as such: a kernel of
 # more than 256 registers otherwise gets all of them in accumulation registers and

@@ -1,0 +1,318 @@
+// Host side and row kernels of the masked cross entropy (include/dllm_loss.h).
+//
+// Forward is the readout's projection: the counted rows are compacted, the
+// LM-head GEMM folds each row's logits into a running maximum and sum per
+// vocabulary slice, and a wave for each row joins the slices and takes the
+// target's logit.  Backward walks the vocabulary in pieces (loss_gemm.hip).
+#include "dllm_loss.h"
+
+#include <math.h>
+
+#include "bf16.h"
+#include "loss_internal.h"
+#include "online_state.h"
+#include "readout_internal.h"
+
+namespace dllm {
+namespace {
+
+// Which positions count; zeros for the others' outputs.
+__global__ __launch_bounds__(256) void k_loss_counted(const uint8_t* __restrict__ mask,
+                                                      const int32_t* __restrict__ targets, int L, int V,
+                                                      uint8_t* __restrict__ counted, float* __restrict__ losses,
+                                                      float* __restrict__ lse) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < L; i += (int64_t)gridDim.x * 256) {
+    const int t = targets[i];
+    const bool yes = mask[i] != 0 && t >= 0 && t < V;
+    counted[i] = yes ? 1 : 0;
+    if (!yes && losses) {
+      losses[i] = 0.f;
+      lse[i] = 0.f;
+    }
+  }
+}
+
+// One wave for each row: the slices' partials joined, and the target's logit.
+__global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* __restrict__ W, const uint16_t* __restrict__ H,
+                                                   int d, int L, const int32_t* __restrict__ targets,
+                                                   const float* __restrict__ weights,
+                                                   const int32_t* __restrict__ idx, const int32_t* __restrict__ ctr,
+                                                   Partials p, float* __restrict__ terms, float* __restrict__ losses,
+                                                   float* __restrict__ lse) {
+  const int M = min(ctr[0], L), slices = ctr[3];
+  const int lane = threadIdx.x & 63;
+  for (int row = blockIdx.x * 4 + (threadIdx.x >> 6); row < M; row += gridDim.x * 4) {
+    const int pos = idx[row];
+    const uint16_t *h = H + (int64_t)pos * d, *w = W + (int64_t)targets[pos] * d;
+    float z = 0.f;
+    for (int c = 8 * lane; c < d; c += 8 * 64) {
+      float x[8], y[8];
+      unpack8(*reinterpret_cast<const uint4*>(h + c), x);
+      unpack8(*reinterpret_cast<const uint4*>(w + c), y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z = fmaf(x[j], y[j], z);
+    }
+    RowState r = row_state_empty();
+    const size_t base = (size_t)row * (size_t)slices;
+    for (int j = lane; j < slices; j += 64) {
+      RowState y = row_state_empty();
+      y.m = p.m[base + j];
+      y.a = p.a[base + j];
+      y.s = p.s[base + j];
+      row_merge<false>(r, y);
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+      z += __shfl_xor(z, off);
+      row_merge<false>(r, shfl_xor_state(r, off));
+    }
+    if (lane == 0) {
+      const float l = row_finish<false>(r).lse;
+      losses[pos] = l - z;
+      lse[pos] = l;
+      terms[row] = (l - z) * (weights ? weights[pos] : 1.f);
+    }
+  }
+}
+
+// The weighted sum, in fp64 and a fixed order.
+__global__ __launch_bounds__(1024) void k_loss_total(const float* __restrict__ terms, const int32_t* __restrict__ ctr,
+                                                     int L, float* __restrict__ loss) {
+  __shared__ double part[16];
+  const int M = min(ctr[0], L);
+  double s = 0.0;
+  for (int i = threadIdx.x; i < M; i += 1024) s += (double)terms[i];
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+    for (int w = 0; w < 16; ++w) t += part[w];
+    *loss = (float)t;
+  }
+}
+
+// What backward keeps of each counted row, and zeros for the rows of d_hidden
+// that do not count.
+__global__ __launch_bounds__(256) void k_loss_prepare(const uint8_t* __restrict__ counted,
+                                                      const int32_t* __restrict__ targets,
+                                                      const float* __restrict__ weights,
+                                                      const float* __restrict__ grad, const float* __restrict__ lse,
+                                                      const int32_t* __restrict__ idx,
+                                                      const int32_t* __restrict__ ctr, int L, int d,
+                                                      float* __restrict__ row_lse, float* __restrict__ coef,
+                                                      int32_t* __restrict__ tgt, uint16_t* __restrict__ d_hidden) {
+  const int M = min(ctr[0], L);
+  for (int i = blockIdx.x; i < L; i += gridDim.x) {
+    if (threadIdx.x == 0 && i < M) {
+      const int pos = idx[i];
+      row_lse[i] = lse[pos];
+      coef[i] = (weights ? weights[pos] : 1.f) * (grad ? *grad : 1.f);
+      tgt[i] = targets[pos];
+    }
+    if (d_hidden && !counted[i])
+      for (int c = 8 * threadIdx.x; c < d; c += 8 * 256)
+        *reinterpret_cast<uint4*>(d_hidden + (int64_t)i * d + c) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+bool sizes_ok(int64_t V, int64_t d, int64_t L) {
+  return V >= 1 && V < ((int64_t)1 << 31) - 1024 && d >= 1 && L >= 1 && L < ((int64_t)1 << 31) - 1024;
+}
+bool supported(int64_t d) { return d % 8 == 0 && d < ((int64_t)1 << 20); }
+
+int64_t part_cap(int64_t L) { return (L + kLargeBM - 1) / kLargeBM * kLargeBM * kMaxLargeSlices; }
+
+struct Rows {
+  uint8_t* counted;
+  int32_t *idx, *ctr;
+  float* terms;
+  Partials part;
+  float *row_lse, *coef;
+  int32_t* tgt;
+  uint16_t* dz;
+  float* acc;
+};
+
+// Workspace of both directions; returns its size.
+size_t carve(int64_t d, int64_t L, int64_t piece, uint8_t* base, Rows* r) {
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = up256(off + bytes);
+    return base ? base + o : nullptr;
+  };
+  Rows x = {};
+  x.counted = take((size_t)L);
+  x.idx = reinterpret_cast<int32_t*>(take((size_t)L * 4));
+  x.ctr = reinterpret_cast<int32_t*>(take(16 * 4));
+  if (piece == 0) {
+    x.terms = reinterpret_cast<float*>(take((size_t)L * 4));
+    x.part.m = reinterpret_cast<float*>(take((size_t)part_cap(L) * 4));
+    x.part.a = reinterpret_cast<int32_t*>(take((size_t)part_cap(L) * 4));
+    x.part.s = reinterpret_cast<float*>(take((size_t)part_cap(L) * 4));
+  } else {
+    const size_t rows = (size_t)(L + kLossPad - 1) / kLossPad * kLossPad;
+    x.row_lse = reinterpret_cast<float*>(take((size_t)L * 4));
+    x.coef = reinterpret_cast<float*>(take((size_t)L * 4));
+    x.tgt = reinterpret_cast<int32_t*>(take((size_t)L * 4));
+    x.dz = reinterpret_cast<uint16_t*>(take(rows * (size_t)piece * 2));
+    x.acc = reinterpret_cast<float*>(take(rows * (size_t)d * 4));
+  }
+  if (r) *r = x;
+  return off;
+}
+
+// The piece a call works with: as given, or about 1 GiB of dz, but at least
+// 8192 entries, and never more than the vocabulary.
+int64_t piece_of(int64_t V, int64_t L, int64_t piece) {
+  if (piece == 0) {
+    piece = ((int64_t)1 << 29) / L / 256 * 256;
+    if (piece < 8192) piece = 8192;
+  }
+  const int64_t all = (V + 255) / 256 * 256;
+  return piece < all ? piece : all;
+}
+
+dllm_status check(const dllm_loss* p) {
+  if (!p || !sizes_ok(p->V, p->d, p->L)) return DLLM_ERR_INVALID_ARG;
+  if (!supported(p->d)) return DLLM_ERR_UNSUPPORTED;
+  if (!p->W_lm || !p->hidden || !p->mask || !p->targets) return DLLM_ERR_INVALID_ARG;
+  if (!aligned(p->W_lm, 16) || !aligned(p->hidden, 16) || !aligned(p->targets, 4) || !aligned(p->weights, 4))
+    return DLLM_ERR_UNSUPPORTED;
+  return DLLM_OK;
+}
+
+// Whether an output shares memory with an input.
+bool over_inputs(const dllm_loss* p, const void* out, size_t n) {
+  const size_t L = (size_t)p->L, row = (size_t)p->d * 2;
+  return overlaps(out, n, p->W_lm, (size_t)p->V * row) || overlaps(out, n, p->hidden, L * row) ||
+         overlaps(out, n, p->mask, L) || overlaps(out, n, p->targets, L * 4) || overlaps(out, n, p->weights, L * 4);
+}
+
+int device_cus() {
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return 0;
+  if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
+  return cus;
+}
+
+unsigned grid_for(int64_t n, int64_t most) { return (unsigned)(n < most ? n : most); }
+
+}  // namespace
+}  // namespace dllm
+
+extern "C" {
+
+size_t dllm_loss_forward_workspace_bytes(int64_t V, int64_t d, int64_t L) {
+  if (!dllm::sizes_ok(V, d, L) || !dllm::supported(d)) return 0;
+  return dllm::carve(d, L, 0, nullptr, nullptr);
+}
+
+dllm_status dllm_loss_forward(const dllm_loss* p, float* loss, float* losses, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  const dllm_status ok = dllm::check(p);
+  if (ok != DLLM_OK) return ok;
+  if (!loss || !losses || !lse) return DLLM_ERR_INVALID_ARG;
+  if (!dllm::aligned(loss, 4) || !dllm::aligned(losses, 4) || !dllm::aligned(lse, 4)) return DLLM_ERR_UNSUPPORTED;
+  const int64_t L = p->L;
+  const size_t n = (size_t)L * 4, need = dllm::carve(p->d, L, 0, nullptr, nullptr);
+  if (!workspace || workspace_bytes < need || !dllm::aligned(workspace, 256)) return DLLM_ERR_WORKSPACE;
+  if (dllm::over_inputs(p, loss, 4) || dllm::over_inputs(p, losses, n) || dllm::over_inputs(p, lse, n) ||
+      dllm::over_inputs(p, workspace, need) || dllm::overlaps(losses, n, lse, n) || dllm::overlaps(loss, 4, losses, n) ||
+      dllm::overlaps(loss, 4, lse, n) || dllm::overlaps(workspace, need, loss, 4) ||
+      dllm::overlaps(workspace, need, losses, n) || dllm::overlaps(workspace, need, lse, n))
+    return DLLM_ERR_INVALID_ARG;
+  const int cus = dllm::device_cus();
+  if (cus <= 0) return DLLM_ERR_HIP;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  dllm::Rows r;
+  dllm::carve(p->d, L, 0, reinterpret_cast<uint8_t*>(workspace), &r);
+  hipLaunchKernelGGL(dllm::k_loss_counted, dim3(dllm::grid_for((L + 255) / 256, 4096)), dim3(256), 0, st, p->mask,
+                     p->targets, (int)L, (int)p->V, r.counted, losses, lse);
+  // as the readout chooses it: the persistent GEMM where its 32-bit offsets reach, else the streaming one
+  const int64_t n_vt = (p->V + dllm::kLargeBN - 1) / dllm::kLargeBN, n_rt = (L + dllm::kLargeBM - 1) / dllm::kLargeBM;
+  const bool persistent = p->d % dllm::kPersistBK == 0 && (int64_t)dllm::kPersistBN * p->d * 2 < ((int64_t)1 << 32) &&
+                          (p->d % dllm::kPersistWideBK == 0 || L * p->d * 2 < ((int64_t)1 << 32));
+  dllm::PlanParams plan = {};
+  plan.tile_rows = dllm::kLargeBM;
+  plan.n_vt = (int)n_vt;
+  plan.grid = cus;
+  plan.max_slices = 1024;
+  plan.part_cap = dllm::part_cap(L);
+  if (!persistent) {
+    int64_t s = (4 * (int64_t)cus + n_rt - 1) / n_rt;
+    if (s > dllm::kMaxLargeSlices) s = dllm::kMaxLargeSlices;
+    plan.fixed_slices = (int)(s < n_vt ? s : n_vt);
+  }
+  if (dllm::launch_mask_compact(r.counted, 0, L, 0, plan, r.idx, r.ctr, st) != hipSuccess) return DLLM_ERR_HIP;
+  const hipError_t e =
+      persistent ? dllm::launch_gemm_persistent(p->W_lm, p->hidden, (int)p->d, (int)p->V, r.idx, r.ctr, cus, r.part, st)
+                 : dllm::launch_gemm_large(p->W_lm, p->hidden, (int)p->d, (int)p->V, r.idx, r.ctr, (int)n_rt,
+                                           plan.fixed_slices, r.part, st);
+  if (e != hipSuccess) return DLLM_ERR_HIP;
+  hipLaunchKernelGGL(dllm::k_loss_rows, dim3(dllm::grid_for((L + 3) / 4, 65536)), dim3(256), 0, st, p->W_lm, p->hidden,
+                     (int)p->d, (int)L, p->targets, p->weights, r.idx, r.ctr, r.part, r.terms, losses, lse);
+  hipLaunchKernelGGL(dllm::k_loss_total, dim3(1), dim3(1024), 0, st, r.terms, r.ctr, (int)L, loss);
+  return hipGetLastError() == hipSuccess ? DLLM_OK : DLLM_ERR_HIP;
+}
+
+size_t dllm_loss_backward_workspace_bytes(int64_t V, int64_t d, int64_t L, int64_t piece) {
+  if (!dllm::sizes_ok(V, d, L) || !dllm::supported(d) || piece < 0 || piece % 256 != 0) return 0;
+  return dllm::carve(d, L, dllm::piece_of(V, L, piece), nullptr, nullptr);
+}
+
+dllm_status dllm_loss_backward(const dllm_loss* p, const float* lse, const float* grad, uint16_t* d_hidden,
+                               uint16_t* d_W, int32_t accumulate, int64_t piece, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  const dllm_status ok = dllm::check(p);
+  if (ok != DLLM_OK) return ok;
+  if (!lse || (!d_hidden && !d_W) || (accumulate != 0 && accumulate != 1) || piece < 0 || piece % 256 != 0)
+    return DLLM_ERR_INVALID_ARG;
+  if (!dllm::aligned(lse, 4) || !dllm::aligned(grad, 4) || !dllm::aligned(d_hidden, 16) || !dllm::aligned(d_W, 16))
+    return DLLM_ERR_UNSUPPORTED;
+  const int64_t L = p->L, d = p->d, V = p->V;
+  piece = dllm::piece_of(V, L, piece);
+  const size_t need = dllm::carve(d, L, piece, nullptr, nullptr);
+  if (!workspace || workspace_bytes < need || !dllm::aligned(workspace, 256)) return DLLM_ERR_WORKSPACE;
+  const size_t nh = (size_t)L * (size_t)d * 2, nw = (size_t)V * (size_t)d * 2;
+  const void* out[] = {d_hidden, d_W, workspace};
+  const size_t size[] = {nh, nw, need};
+  for (int i = 0; i < 3; ++i) {
+    if (dllm::over_inputs(p, out[i], size[i]) || dllm::overlaps(out[i], size[i], lse, (size_t)L * 4) ||
+        dllm::overlaps(out[i], size[i], grad, 4))
+      return DLLM_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (dllm::overlaps(out[i], size[i], out[j], size[j])) return DLLM_ERR_INVALID_ARG;
+  }
+  const int cus = dllm::device_cus();
+  if (cus <= 0) return DLLM_ERR_HIP;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  dllm::Rows r;
+  dllm::carve(d, L, piece, reinterpret_cast<uint8_t*>(workspace), &r);
+  hipLaunchKernelGGL(dllm::k_loss_counted, dim3(dllm::grid_for((L + 255) / 256, 4096)), dim3(256), 0, st, p->mask,
+                     p->targets, (int)L, (int)V, r.counted, nullptr, nullptr);
+  dllm::PlanParams plan = {};
+  plan.fixed_slices = 1;
+  plan.tile_rows = dllm::kLargeBM;
+  if (dllm::launch_mask_compact(r.counted, 0, L, 0, plan, r.idx, r.ctr, st) != hipSuccess) return DLLM_ERR_HIP;
+  hipLaunchKernelGGL(dllm::k_loss_prepare, dim3(dllm::grid_for(L, 65536)), dim3(256), 0, st, r.counted, p->targets,
+                     p->weights, grad, lse, r.idx, r.ctr, (int)L, (int)d, r.row_lse, r.coef, r.tgt, d_hidden);
+  dllm::GradArgs a = {p->W_lm, p->hidden, r.idx, r.ctr, r.row_lse, r.coef, r.tgt, r.dz, r.acc, d_hidden, d_W, piece,
+                      (int)V, (int)d, (int)L, 0, 0, 0, 0, accumulate};
+  for (int64_t v = 0; v < V; v += piece) {
+    a.v0 = (int)v;
+    a.n = (int)(V - v < piece ? V - v : piece);
+    a.first = v == 0;
+    a.last = v + piece >= V;
+    if (dllm::launch_loss_dz(a, 8 * cus, st) != hipSuccess) return DLLM_ERR_HIP;
+    if (d_hidden && dllm::launch_loss_d_hidden(a, 8 * cus, st) != hipSuccess) return DLLM_ERR_HIP;
+    if (d_W && dllm::launch_loss_d_W(a, 8 * cus, st) != hipSuccess) return DLLM_ERR_HIP;
+  }
+  return hipGetLastError() == hipSuccess ? DLLM_OK : DLLM_ERR_HIP;
+}
+
+}  // extern "C"

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "bf16.h"
 #include "dllm_rotary.h"
 
 namespace dllm {
@@ -62,16 +63,6 @@ __device__ __forceinline__ float odd_float(double x) {
   const uint64_t u = (uint64_t)__double_as_longlong(x);
   const uint32_t hi = (uint32_t)(u >> 32) | min((uint32_t)u, 1u);
   return (float)__longlong_as_double((int64_t)((uint64_t)hi << 32));
-}
-
-__device__ __forceinline__ float bf16_float(uint32_t bits) { return __uint_as_float(bits << 16); }
-
-// bf16 bits of x, nearest with ties to even; NaN stays NaN.
-__device__ __forceinline__ uint32_t float_bf16(float x) {
-  const __bf16 b = (__bf16)x;
-  uint16_t u;
-  __builtin_memcpy(&u, &b, 2);
-  return u;
 }
 
 inline bool rotary_plan_ok(const dllm_rotary_plan* p, int64_t head_dim) {
