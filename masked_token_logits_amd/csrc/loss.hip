@@ -93,27 +93,43 @@ __global__ __launch_bounds__(1024) void k_loss_total(const float* __restrict__ t
   }
 }
 
-// What backward keeps of each counted row, and zeros for the rows of d_hidden
-// that do not count.
-__global__ __launch_bounds__(256) void k_loss_prepare(const uint8_t* __restrict__ counted,
-                                                      const int32_t* __restrict__ targets,
-                                                      const float* __restrict__ weights,
-                                                      const float* __restrict__ grad, const float* __restrict__ lse,
-                                                      const int32_t* __restrict__ idx,
-                                                      const int32_t* __restrict__ ctr, int L, int d,
-                                                      float* __restrict__ row_lse, float* __restrict__ coef,
-                                                      int32_t* __restrict__ tgt, uint16_t* __restrict__ d_hidden) {
-  const int M = min(ctr[0], L);
-  for (int i = blockIdx.x; i < L; i += gridDim.x) {
-    if (threadIdx.x == 0 && i < M) {
-      const int pos = idx[i];
-      row_lse[i] = lse[pos];
-      coef[i] = (weights ? weights[pos] : 1.f) * (grad ? *grad : 1.f);
-      tgt[i] = targets[pos];
+// What backward keeps of each counted row, in order: its hidden state and
+// scalars, filled up with rows and columns of zeros; and zeros for the rows of
+// d_hidden that do not count.
+struct PrepareArgs {
+  const uint16_t* H;
+  const uint8_t* counted;
+  const int32_t* targets;
+  const float *weights, *grad, *lse;
+  const int32_t *idx, *ctr;
+  int L, d, dp;
+  uint16_t *rows, *zeros;
+  float *row_lse, *coef;
+  int32_t* tgt;
+  uint16_t* d_hidden;
+};
+
+__global__ __launch_bounds__(256) void k_loss_prepare(PrepareArgs a) {
+  const int M = min(a.ctr[0], a.L), Mp = (M + kLossStep - 1) / kLossStep * kLossStep;
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<uint4*>(a.zeros) = none;
+  for (int i = blockIdx.x; i < max(a.L, Mp); i += gridDim.x) {
+    if (i < Mp) {
+      const int pos = i < M ? a.idx[i] : 0;
+      if (threadIdx.x == 0) {
+        a.row_lse[i] = i < M ? a.lse[pos] : 0.f;
+        a.coef[i] = i < M ? (a.weights ? a.weights[pos] : 1.f) * (a.grad ? *a.grad : 1.f) : 0.f;
+        a.tgt[i] = i < M ? a.targets[pos] : -1;
+      }
+      for (int c = 8 * threadIdx.x; c < a.dp; c += 8 * 256) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (i < M && c < a.d) u = *reinterpret_cast<const uint4*>(a.H + (int64_t)pos * a.d + c);
+        *reinterpret_cast<uint4*>(a.rows + (int64_t)i * a.dp + c) = u;
+      }
     }
-    if (d_hidden && !counted[i])
-      for (int c = 8 * threadIdx.x; c < d; c += 8 * 256)
-        *reinterpret_cast<uint4*>(d_hidden + (int64_t)i * d + c) = make_uint4(0, 0, 0, 0);
+    if (a.d_hidden && i < a.L && !a.counted[i])
+      for (int c = 8 * threadIdx.x; c < a.d; c += 8 * 256)
+        *reinterpret_cast<uint4*>(a.d_hidden + (int64_t)i * a.d + c) = none;
   }
 }
 
@@ -133,7 +149,7 @@ struct Rows {
   Partials part;
   float *row_lse, *coef;
   int32_t* tgt;
-  uint16_t* dz;
+  uint16_t *zeros, *rows, *dz;
   float* acc;
 };
 
@@ -155,16 +171,21 @@ size_t carve(int64_t d, int64_t L, int64_t piece, uint8_t* base, Rows* r) {
     x.part.a = reinterpret_cast<int32_t*>(take((size_t)part_cap(L) * 4));
     x.part.s = reinterpret_cast<float*>(take((size_t)part_cap(L) * 4));
   } else {
-    const size_t rows = (size_t)(L + kLossPad - 1) / kLossPad * kLossPad;
-    x.row_lse = reinterpret_cast<float*>(take((size_t)L * 4));
-    x.coef = reinterpret_cast<float*>(take((size_t)L * 4));
-    x.tgt = reinterpret_cast<int32_t*>(take((size_t)L * 4));
+    const size_t rows = (size_t)loss_padded(L);
+    x.row_lse = reinterpret_cast<float*>(take(rows * 4));
+    x.coef = reinterpret_cast<float*>(take(rows * 4));
+    x.tgt = reinterpret_cast<int32_t*>(take(rows * 4));
+    x.zeros = reinterpret_cast<uint16_t*>(take(16));
+    x.rows = reinterpret_cast<uint16_t*>(take(rows * (size_t)loss_padded(d) * 2));
     x.dz = reinterpret_cast<uint16_t*>(take(rows * (size_t)piece * 2));
-    x.acc = reinterpret_cast<float*>(take(rows * (size_t)d * 4));
+    x.acc = reinterpret_cast<float*>(take((size_t)loss_shares(L, d, piece) * kLossTile * kLossTile * 4));
   }
   if (r) *r = x;
   return off;
 }
+
+// A tile of dz is addressed by 32-bit byte offsets: 256 rows of a piece.
+constexpr int64_t kMostPiece = (int64_t)1 << 22;
 
 // The piece a call works with: as given, or about 1 GiB of dz, but at least
 // 8192 entries, and never more than the vocabulary.
@@ -174,6 +195,7 @@ int64_t piece_of(int64_t V, int64_t L, int64_t piece) {
     if (piece < 8192) piece = 8192;
   }
   const int64_t all = (V + 255) / 256 * 256;
+  if (piece > kMostPiece) piece = kMostPiece;
   return piece < all ? piece : all;
 }
 
@@ -299,19 +321,21 @@ dllm_status dllm_loss_backward(const dllm_loss* p, const float* lse, const float
   plan.fixed_slices = 1;
   plan.tile_rows = dllm::kLargeBM;
   if (dllm::launch_mask_compact(r.counted, 0, L, 0, plan, r.idx, r.ctr, st) != hipSuccess) return DLLM_ERR_HIP;
-  hipLaunchKernelGGL(dllm::k_loss_prepare, dim3(dllm::grid_for(L, 65536)), dim3(256), 0, st, r.counted, p->targets,
-                     p->weights, grad, lse, r.idx, r.ctr, (int)L, (int)d, r.row_lse, r.coef, r.tgt, d_hidden);
-  dllm::GradArgs a = {p->W_lm, p->hidden, r.idx, r.ctr, r.row_lse, r.coef, r.tgt, r.dz, r.acc, d_hidden, d_W, piece,
-                      (int)V, (int)d, (int)L, 0, 0, 0, 0, accumulate};
+  const int dp = (int)dllm::loss_padded(d), grid = cus < dllm::kLossGrid ? cus : dllm::kLossGrid;
+  const dllm::PrepareArgs pa = {p->hidden, r.counted, p->targets, p->weights, grad,      lse,    r.idx, r.ctr,   (int)L,
+                                (int)d,    dp,        r.rows,     r.zeros,    r.row_lse, r.coef, r.tgt, d_hidden};
+  hipLaunchKernelGGL(dllm::k_loss_prepare, dim3(dllm::grid_for(dllm::loss_padded(L), 65536)), dim3(256), 0, st, pa);
+  dllm::GradArgs a = {p->W_lm, r.zeros,  r.rows, r.idx, r.ctr,  r.row_lse, r.coef, r.tgt, r.dz, r.acc,
+                      d_hidden, d_W,     piece,  (int)V, (int)d, dp,       (int)L, 0,     0,    0,     accumulate};
   for (int64_t v = 0; v < V; v += piece) {
     a.v0 = (int)v;
     a.n = (int)(V - v < piece ? V - v : piece);
     a.first = v == 0;
-    a.last = v + piece >= V;
-    if (dllm::launch_loss_dz(a, 8 * cus, st) != hipSuccess) return DLLM_ERR_HIP;
-    if (d_hidden && dllm::launch_loss_d_hidden(a, 8 * cus, st) != hipSuccess) return DLLM_ERR_HIP;
-    if (d_W && dllm::launch_loss_d_W(a, 8 * cus, st) != hipSuccess) return DLLM_ERR_HIP;
+    if (dllm::launch_loss_dz(a, grid, st) != hipSuccess) return DLLM_ERR_HIP;
+    if (d_hidden && dllm::launch_loss_d_hidden(a, grid, st) != hipSuccess) return DLLM_ERR_HIP;
+    if (d_W && dllm::launch_loss_d_W(a, grid, st) != hipSuccess) return DLLM_ERR_HIP;
   }
+  if (d_hidden && dllm::launch_loss_join(a, 8 * cus, st) != hipSuccess) return DLLM_ERR_HIP;
   return hipGetLastError() == hipSuccess ? DLLM_OK : DLLM_ERR_HIP;
 }
 

@@ -8,26 +8,48 @@
 
 namespace dllm {
 
-constexpr int kLossPad = 64;  // rows and entries of dz are filled up to this
+constexpr int kLossStep = 64;   // K of a stage: rows, entries and columns are filled up to this
+constexpr int kLossTile = 256;  // rows and columns of a product's tile
+constexpr int kLossGrid = 256;  // most workgroups of a product
+
+inline int64_t loss_padded(int64_t n) { return (n + kLossStep - 1) / kLossStep * kLossStep; }
 
 // The backward pass of one vocabulary piece.  Rows are the counted positions
-// in ascending order, ctr[0] of them.
+// in ascending order, M = ctr[0] of them, filled up to Mp with rows that have
+// no gradient.
 struct GradArgs {
-  const uint16_t *W, *H;  // [V, d], [L, d]
+  const uint16_t* W;        // [V, d]
+  const uint16_t* zeros;    // 16 bytes of them
+  const uint16_t* rows;     // [Mp, dp] the counted rows of hidden, zeros behind d and M
   const int32_t *idx, *ctr;
-  const float *lse, *coef;  // per row: log-sum-exp, and grad * weight
-  const int32_t* tgt;       // per row: the target
-  uint16_t* dz;             // [rows, ldz]: the piece's gradient of the logits
-  float* acc;               // [rows, d]: the rows' gradient over the pieces so far
+  const float *lse, *coef;  // [Mp] log-sum-exp, and grad * weight; zeros behind M
+  const int32_t* tgt;       // [Mp] the target, -1 behind M
+  uint16_t* dz;             // [Mp, ldz]: the piece's gradient of the logits
+  float* acc;               // the rows' gradient over the pieces so far, in shares of a tile each
   uint16_t *d_hidden, *d_W;
-  int64_t ldz;
-  int V, d, L;
+  int64_t ldz;              // entries of a whole piece
+  int V, d, dp, L;
   int v0, n;                // the piece: entries v0 .. v0 + n - 1
-  int first, last, accumulate;
+  int first, accumulate;
 };
 
 hipError_t launch_loss_dz(const GradArgs& a, int grid, hipStream_t stream);        // dz
-hipError_t launch_loss_d_hidden(const GradArgs& a, int grid, hipStream_t stream);  // acc += dz . W, d_hidden at the last
-hipError_t launch_loss_d_W(const GradArgs& a, int grid, hipStream_t stream);       // d_W = dz^T . H
+hipError_t launch_loss_d_hidden(const GradArgs& a, int grid, hipStream_t stream);  // acc += dz . W
+hipError_t launch_loss_d_W(const GradArgs& a, int grid, hipStream_t stream);       // d_W = dz^T . rows
+hipError_t launch_loss_join(const GradArgs& a, int grid, hipStream_t stream);      // d_hidden = sum of acc's shares
+
+// How d_hidden's product is cut: its tiles' stages as one line, dealt to so
+// many workgroups, at least four stages of a whole piece to each.
+__host__ __device__ inline int64_t loss_cuts(int64_t tiles, int64_t piece) {
+  int64_t n = tiles * (piece / kLossStep) / 4;
+  if (n < tiles) n = tiles;
+  return n < kLossGrid ? n : kLossGrid;
+}
+
+// Shares of acc, a tile's floats each: workgroup g's of tile t is share g + t.
+inline int64_t loss_shares(int64_t L, int64_t d, int64_t piece) {
+  const int64_t t = (L + kLossTile - 1) / kLossTile * ((d + kLossTile - 1) / kLossTile);
+  return t + loss_cuts(t, piece);
+}
 
 }  // namespace dllm
