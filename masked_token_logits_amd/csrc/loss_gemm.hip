@@ -35,6 +35,8 @@ namespace {
 typedef short bf16x8 __attribute__((ext_vector_type(8)));
 typedef short bf16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 #define LDS_AS __attribute__((address_space(3)))
 
 constexpr int BT = kLossTile, BK = kLossStep, NT = 256;
@@ -52,15 +54,14 @@ __device__ __forceinline__ bf16x4 read_tr(LDS_AS const uint16_t* __restrict__ p,
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_AS bf16x4*)p);
 }
 
-// An operand in memory, [256 rows][K] or, by rows of K, [K][256 columns].
-// Sources outside it are drawn to its last row or piece: valid memory, whose
-// products are not stored or meet zeros.
+// An operand in memory, [256 rows][K] or, by rows of K, [K][256 columns], from
+// its first element of a tile on: the rows that exist there (of K, for one by
+// rows of K) and the columns (of K, where K is contiguous).  Sources outside it
+// are drawn to its last row or piece: valid memory, whose products are not
+// stored or meet zeros.
 struct Operand {
-  const uint16_t* p;  // the tile's first element at the first K
-  int64_t ld;         // elements from row to row
-  int64_t rows;       // rows that exist from there on (of K, for an operand by rows of K)
-  int64_t cols;       // columns that exist from there on (of K, where K is contiguous)
-  const uint16_t* zeros;
+  const uint16_t* p;
+  int rows, cols;
 };
 
 // One operand's way into LDS and from there into fragments.  TAIL: K is
@@ -74,18 +75,22 @@ template <bool TAIL>
 struct Side<false, TAIL> {
   uint32_t off[DMAS];
   const char *base, *zeros;
-  int lane_off, swz, col, cols;
-  __device__ __forceinline__ void start(const Operand& o, int wave, int lane) {
-    base = reinterpret_cast<const char*>(o.p);
-    zeros = reinterpret_cast<const char*>(o.zeros);
-    cols = (int)o.cols;
-    const int r0 = wave * 8 + (lane >> 3), piece = (lane & 7) ^ ((r0 >> 1) & 7);
-    col = piece * 8;
-    const int last = (int)min(o.rows - 1, (int64_t)(BT - 1));
-#pragma unroll
-    for (int j = 0; j < DMAS; ++j) off[j] = ((uint32_t)min(r0 + 32 * j, last) * (uint32_t)o.ld + (uint32_t)col) * 2u;
+  uint32_t ld2;  // bytes from row to row
+  int lane_off, swz, row, col, cols;
+  __device__ __forceinline__ void init(int64_t ld, const uint16_t* no_values, int wave, int lane) {
+    zeros = reinterpret_cast<const char*>(no_values);
+    ld2 = (uint32_t)ld * 2u;
+    row = wave * 8 + (lane >> 3);
+    col = ((lane & 7) ^ ((row >> 1) & 7)) * 8;
     swz = ((lane & 31) >> 1) & 7;
     lane_off = (lane & 31) * BK;
+  }
+  __device__ __forceinline__ void start(const Operand& o) {
+    base = reinterpret_cast<const char*>(o.p);
+    cols = o.cols;
+    const int last = min(o.rows - 1, BT - 1);
+#pragma unroll
+    for (int j = 0; j < DMAS; ++j) off[j] = (uint32_t)min(row + 32 * j, last) * ld2 + (uint32_t)col * 2u;
   }
   __device__ __forceinline__ const char* source(int j, int k0) const {
     const char* p = base + (size_t)k0 * 2u + off[j];
@@ -107,22 +112,24 @@ template <bool TAIL>
 struct Side<true, TAIL> {
   static_assert(!TAIL, "rows of K are drawn to the last one");
   const char* base;
-  int64_t ld2, rows;
-  uint32_t k_off, col_off;
-  int lane_off, sw;
-  __device__ __forceinline__ void start(const Operand& o, int wave, int lane) {
-    base = reinterpret_cast<const char*>(o.p);
-    ld2 = o.ld * 2;
-    rows = o.rows;
-    const int k = wave * 2 + (lane >> 5), granule = ((lane & 31) >> 2) ^ (k & 3);
-    k_off = (uint32_t)k * (uint32_t)ld2;
-    col_off = (uint32_t)min((int64_t)(granule * 32 + (lane & 3) * 8), o.cols - 8) * 2u;
+  uint32_t ld2, k_off, col_off;
+  int rows, lane_off, col, sw;
+  __device__ __forceinline__ void init(int64_t ld, const uint16_t*, int wave, int lane) {
+    ld2 = (uint32_t)ld * 2u;
+    const int k = wave * 2 + (lane >> 5);
+    k_off = (uint32_t)k * ld2;
+    col = (((lane & 31) >> 2) ^ (k & 3)) * 32 + (lane & 3) * 8;
     sw = (lane & 15) >> 2;
     lane_off = (8 * (lane >> 5) + sw) * BT + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
   }
+  __device__ __forceinline__ void start(const Operand& o) {
+    base = reinterpret_cast<const char*>(o.p);
+    rows = o.rows;
+    col_off = (uint32_t)min(col, o.cols - 8) * 2u;
+  }
   __device__ __forceinline__ const char* source(int j, int k0) const {
-    const uint32_t last = (uint32_t)min(rows - 1 - k0, (int64_t)(BK - 1)) * (uint32_t)ld2;
-    return base + (size_t)k0 * (size_t)ld2 + (min(k_off + (uint32_t)(8 * j) * (uint32_t)ld2, last) + col_off);
+    const uint32_t last = (uint32_t)min(rows - 1 - k0, BK - 1) * ld2;
+    return base + (size_t)k0 * (size_t)ld2 + (min(k_off + (uint32_t)(8 * j) * ld2, last) + col_off);
   }
   __device__ __forceinline__ bf16x8 frag(const uint16_t* tile, int block, int kk, int) const {
     LDS_AS uint16_t* ring = (LDS_AS uint16_t*)tile;
@@ -132,154 +139,16 @@ struct Side<true, TAIL> {
   }
 };
 
-// One tile: acc = sum over K stages of first (256) x second (256), and then
-// epi(fr, fv, j, z): values z[0..3] of the second's index (wr + 2 fr) * 32 +
-// lane % 32 and the first's index wv * 128 + fv * 32 + 8 j + 4 (lane / 32) + 0..3.
-// nb: 32-blocks of the second operand that are wanted.
-template <bool A_BY_K, bool A_TAIL, bool B_BY_K, class Epi>
-__device__ __forceinline__ void tile_product(uint16_t* lds, const Operand& oa, const Operand& ob, int stages, int nb,
-                                             Epi epi) {
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wr = wave >> 1, wv = wave & 1;
-  Side<A_BY_K, A_TAIL> sa;
-  Side<B_BY_K, false> sb;
-  sa.start(oa, wave, lane);
-  sb.start(ob, wave, lane);
+// One tile of a workgroup's work: the operands at its first K, the K it has,
+// the stage it starts with (later ones follow, then those before it) and the
+// 32-blocks of the second operand that are wanted.
+struct Item {
+  Operand a, b;
+  int stages, start, nb;
+};
 
-  // Operand tiles alternate through the ring: the second's of stage q goes to
-  // slot 2q % 5, the first's to (2q + 1) % 5.  Stages behind the last read the
-  // first ones again and are never used.
-  const int K = stages * BK;
-  int a_k0 = 0, a_slot = 1, b_k0 = 0, b_slot = 0;
-  auto next_slot = [](int s) { return s + 2 >= SLOTS ? s + 2 - SLOTS : s + 2; };
-  auto dma = [&](const char* src, int slot, int j) {
-    __builtin_amdgcn_global_load_lds((const void*)src, (LDS_AS void*)(lds + slot * OPT + (wave + 4 * j) * 512), 16, 0, 0);
-  };
-  auto issue_a = [&](int j) { dma(sa.source(j, a_k0), a_slot, j); };
-  auto issue_b = [&](int j) { dma(sb.source(j, b_k0), b_slot, j); };
-  auto advance_a = [&]() {
-    a_slot = next_slot(a_slot);
-    a_k0 = a_k0 + BK == K ? 0 : a_k0 + BK;
-  };
-  auto advance_b = [&]() {
-    b_slot = next_slot(b_slot);
-    b_k0 = b_k0 + BK == K ? 0 : b_k0 + BK;
-  };
-
-  auto run = [&](auto nfr_tag) {
-    constexpr int NFR = decltype(nfr_tag)::value;
-    auto frag = [&](int as, int bs, int kk, int i, bf16x8* fa, bf16x8* fb) {
-      const int f = i >> 1;
-      if ((i & 1) == 0) {
-        if (NFR > 0) fa[f] = sa.frag(lds + as * OPT, wv * 4 + f, kk, lane);
-      } else {
-        if (f < NFR) fb[f] = sb.frag(lds + bs * OPT, wr + 2 * f, kk, lane);
-      }
-    };
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-#pragma unroll
-      for (int j = 0; j < DMAS; ++j) issue_b(j);
-      advance_b();
-#pragma unroll
-      for (int j = 0; j < DMAS; ++j) issue_a(j);
-      advance_a();
-    }
-    stage_sync<2 * DMAS>();
-    bf16x8 fxa[4], fxb[4], fya[4], fyb[4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) frag(1, 0, 0, i, fxa, fxb);
-    f32x16 acc[4][4];
-    const f32x16 zero16 = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    int cas = 1, cbs = 0;
-    auto kstep = [&](const bf16x8* a, const bf16x8* b, auto first_tag, auto between) {
-      constexpr bool FIRST = decltype(first_tag)::value;
-      constexpr int kOrder[16][2] = {{0, 0}, {1, 0}, {0, 1}, {1, 1}, {2, 0}, {2, 1}, {0, 2}, {1, 2},
-                                     {2, 2}, {3, 0}, {3, 1}, {3, 2}, {0, 3}, {1, 3}, {2, 3}, {3, 3}};
-#pragma unroll
-      for (int m = 0; m < 8; ++m) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int fv = kOrder[2 * m + t][0], fr = kOrder[2 * m + t][1];
-          if (fr < NFR)
-            acc[fv][fr] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[fv], b[fr], FIRST ? zero16 : acc[fv][fr], 0, 0, 0);
-        }
-        between(m);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    };
-    auto stage = [&](auto first_tag) {
-      const int nas = next_slot(cas), nbs = next_slot(cbs);
-      kstep(fxa, fxb, first_tag, [&](int m) {
-        if ((m & 1) == 0) issue_b(m >> 1);
-        frag(cas, cbs, 1, m, fya, fyb);
-      });
-      kstep(fya, fyb, std::false_type{}, [&](int m) {
-        if ((m & 1) == 0) issue_b(4 + (m >> 1));
-        frag(cas, cbs, 2, m, fxa, fxb);
-      });
-      advance_b();
-      kstep(fxa, fxb, std::false_type{}, [&](int m) { frag(cas, cbs, 3, m, fya, fyb); });
-      stage_sync<DMAS>();  // the next stage has landed (the second's tile behind it may be in flight); this one is read
-      kstep(fya, fyb, std::false_type{}, [&](int m) {
-        issue_a(m);
-        frag(nas, nbs, 0, m, fxa, fxb);
-      });
-      advance_a();
-      cas = nas;
-      cbs = nbs;
-    };
-    stage(std::true_type{});
-    for (int q = 1; q < stages; ++q) stage(std::false_type{});
-    if constexpr (NFR > 0) {
-      // The accumulators are read one by one, by v_accvgpr_read: left to itself
-      // the register allocator copies all of them at once and spills.  It does
-      // not count these as readers of the matrix results, so the wait states
-      // are written out, behind every matrix instruction by taking all live
-      // accumulators as operands.
-      if constexpr (NFR == 4)
-        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::"a"(acc[0][0]), "a"(acc[0][1]), "a"(acc[0][2]), "a"(acc[0][3]),
-                     "a"(acc[1][0]), "a"(acc[1][1]), "a"(acc[1][2]), "a"(acc[1][3]), "a"(acc[2][0]), "a"(acc[2][1]),
-                     "a"(acc[2][2]), "a"(acc[2][3]), "a"(acc[3][0]), "a"(acc[3][1]), "a"(acc[3][2]), "a"(acc[3][3]));
-      else if constexpr (NFR == 3)
-        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::"a"(acc[0][0]), "a"(acc[0][1]), "a"(acc[0][2]), "a"(acc[1][0]),
-                     "a"(acc[1][1]), "a"(acc[1][2]), "a"(acc[2][0]), "a"(acc[2][1]), "a"(acc[2][2]), "a"(acc[3][0]),
-                     "a"(acc[3][1]), "a"(acc[3][2]));
-      else if constexpr (NFR == 2)
-        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::"a"(acc[0][0]), "a"(acc[0][1]), "a"(acc[1][0]), "a"(acc[1][1]),
-                     "a"(acc[2][0]), "a"(acc[2][1]), "a"(acc[3][0]), "a"(acc[3][1]));
-      else
-        asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::"a"(acc[0][0]), "a"(acc[1][0]), "a"(acc[2][0]), "a"(acc[3][0]));
-#pragma unroll
-      for (int fr = 0; fr < NFR; ++fr)
-#pragma unroll
-        for (int fv = 0; fv < 4; ++fv)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float z[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(z[i]) : "a"(acc[fv][fr][4 * j + i]));
-            epi(fr, fv, j, z);
-          }
-    }
-  };
-  switch (min(4, max(0, (nb - wr + 1) / 2))) {
-    case 4: run(std::integral_constant<int, 4>{}); break;
-    case 3: run(std::integral_constant<int, 3>{}); break;
-    case 2: run(std::integral_constant<int, 2>{}); break;
-    case 1: run(std::integral_constant<int, 1>{}); break;
-    default: run(std::integral_constant<int, 0>{}); break;
-  }
-  // the next tile's prologue counts its DMAs from zero and writes the ring
-  stage_sync<0>();
-}
-
-__device__ __forceinline__ int blocks_of(int rows) { return min(8, max(0, (rows + 31) / 32)); }
-
-// Where a lane's run of four stands in a tile: row of the second operand, and
-// first of the four of the first.
+// Where a lane's values stand in a tile: z[i] of (fr, fv, j) is row(fr) of the
+// second operand, and col(fv, j) + i of the first.
 struct Lane {
   int row0, col0, wr, wv;
   __device__ __forceinline__ Lane() {
@@ -293,44 +162,319 @@ struct Lane {
   __device__ __forceinline__ int col(int fv, int j) const { return col0 + 32 * fv + 8 * j; }
 };
 
+// A workgroup's tiles, one after another.  Their stages are one stream: the
+// DMAs run two stages ahead, across the end of a tile into the next one (with
+// tiles of one stage the one behind that), so that its first stages land while
+// this one's results are stored.
+//
+// work.first(cursor) and work.next(cursor) walk the tiles (false behind the
+// last, the cursor then stays), work.describe(cursor) gives an Item,
+// work.begin(cursor) is called before a tile's first stage, and
+// work.end(cursor, spare, fr, read) behind the last one for each of the lane's
+// rows: read(fv, j, z) gives four accumulators, spare is 8 KiB of LDS of the wave's.
+template <bool A_BY_K, bool A_TAIL, bool B_BY_K, class Work>
+__device__ __forceinline__ void run_tiles(uint16_t* lds, Work& work) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = wave >> 1, wv = wave & 1;
+  typename Work::Cursor cur, ahead;
+  if (!work.first(cur)) return;
+  // this tile, the next and the one behind it; at the end the last one again,
+  // whose stages are then read and not used
+  Item it = work.describe(cur), it1, it2;
+  ahead = cur;
+  bool more = work.next(ahead), more2;
+  it1 = work.describe(ahead);
+  typename Work::Cursor nxt = ahead;
+  more2 = work.next(ahead);
+  it2 = work.describe(ahead);
+
+  Side<A_BY_K, A_TAIL> sa;
+  Side<B_BY_K, false> sb;
+  sa.init(work.lda(), work.zeros(), wave, lane);
+  sb.init(work.ldb(), nullptr, wave, lane);
+  // Operand tiles alternate through the ring: the second's of stage q goes to
+  // slot 2q % 5, the first's to (2q + 1) % 5.
+  int a_k0 = it.start * BK, a_K = it.stages * BK, a_left = it.stages, a_rel = 0, a_slot = 1;
+  int b_k0 = a_k0, b_K = a_K, b_left = a_left, b_rel = 0, b_slot = 0;
+  sa.start(it.a);
+  sb.start(it.b);
+  auto next_slot = [](int s) { return s + 2 >= SLOTS ? s + 2 - SLOTS : s + 2; };
+  auto dma = [&](const char* src, int slot, int j) {
+    __builtin_amdgcn_global_load_lds((const void*)src, (LDS_AS void*)(lds + slot * OPT + (wave + 4 * j) * 512), 16, 0, 0);
+  };
+  // before a stage's first DMA of a side: the next tile's, where this one's are all queued
+  auto turn_a = [&]() {
+    if (a_left > 0) return;
+    const Item& n = a_rel == 0 ? it1 : it2;
+    ++a_rel;
+    sa.start(n.a);
+    a_k0 = n.start * BK;
+    a_K = n.stages * BK;
+    a_left = n.stages;
+  };
+  auto turn_b = [&]() {
+    if (b_left > 0) return;
+    const Item& n = b_rel == 0 ? it1 : it2;
+    ++b_rel;
+    sb.start(n.b);
+    b_k0 = n.start * BK;
+    b_K = n.stages * BK;
+    b_left = n.stages;
+  };
+  auto issue_a = [&](int j) { dma(sa.source(j, a_k0), a_slot, j); };
+  auto issue_b = [&](int j) { dma(sb.source(j, b_k0), b_slot, j); };
+  auto advance_a = [&]() {
+    a_slot = next_slot(a_slot);
+    a_k0 = a_k0 + BK == a_K ? 0 : a_k0 + BK;
+    --a_left;
+  };
+  auto advance_b = [&]() {
+    b_slot = next_slot(b_slot);
+    b_k0 = b_k0 + BK == b_K ? 0 : b_k0 + BK;
+    --b_left;
+  };
+
+  bf16x8 fxa[4], fxb[4], fya[4], fyb[4];
+  auto frag = [&](int as, int bs, int kk, int i, bf16x8* fa, bf16x8* fb) {
+    const int f = i >> 1;
+    if ((i & 1) == 0)
+      fa[f] = sa.frag(lds + as * OPT, wv * 4 + f, kk, lane);
+    else
+      fb[f] = sb.frag(lds + bs * OPT, wr + 2 * f, kk, lane);
+  };
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    turn_b();
+#pragma unroll
+    for (int j = 0; j < DMAS; ++j) issue_b(j);
+    advance_b();
+    turn_a();
+#pragma unroll
+    for (int j = 0; j < DMAS; ++j) issue_a(j);
+    advance_a();
+  }
+  stage_sync<2 * DMAS>();
+  int cas = 1, cbs = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) frag(1, 0, 0, i, fxa, fxb);
+
+  for (;;) {
+    work.begin(cur);
+    auto run = [&](auto nfr_tag) {
+      constexpr int NFR = decltype(nfr_tag)::value;
+      f32x16 acc[4][4];
+      const f32x16 zero16 = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      auto kstep = [&](const bf16x8* a, const bf16x8* b, auto first_tag, auto between) {
+        constexpr bool FIRST = decltype(first_tag)::value;
+        constexpr int kOrder[16][2] = {{0, 0}, {1, 0}, {0, 1}, {1, 1}, {2, 0}, {2, 1}, {0, 2}, {1, 2},
+                                       {2, 2}, {3, 0}, {3, 1}, {3, 2}, {0, 3}, {1, 3}, {2, 3}, {3, 3}};
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int fv = kOrder[2 * m + t][0], fr = kOrder[2 * m + t][1];
+            if (fr < NFR)
+              acc[fv][fr] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[fv], b[fr], FIRST ? zero16 : acc[fv][fr], 0, 0, 0);
+          }
+          between(m);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      auto stage = [&](auto first_tag) {
+        const int nas = next_slot(cas), nbs = next_slot(cbs);
+        turn_b();
+        kstep(fxa, fxb, first_tag, [&](int m) {
+          if ((m & 1) == 0) issue_b(m >> 1);
+          frag(cas, cbs, 1, m, fya, fyb);
+        });
+        kstep(fya, fyb, std::false_type{}, [&](int m) {
+          if ((m & 1) == 0) issue_b(4 + (m >> 1));
+          frag(cas, cbs, 2, m, fxa, fxb);
+        });
+        advance_b();
+        kstep(fxa, fxb, std::false_type{}, [&](int m) { frag(cas, cbs, 3, m, fya, fyb); });
+        stage_sync<DMAS>();  // the next stage has landed (the second's tile behind it may be in flight); this one is read
+        turn_a();
+        kstep(fya, fyb, std::false_type{}, [&](int m) {
+          issue_a(m);
+          frag(nas, nbs, 0, m, fxa, fxb);
+        });
+        advance_a();
+        cas = nas;
+        cbs = nbs;
+      };
+      const int stages = it.stages;
+      stage(std::true_type{});
+      for (int q = 1; q < stages; ++q) stage(std::false_type{});
+      if constexpr (NFR > 0) {
+        // The accumulators are read one by one, by v_accvgpr_read: left to itself
+        // the register allocator copies all of them at once and spills.  It does
+        // not count these as readers of the matrix results, so the wait states
+        // are written out, behind every matrix instruction by taking all live
+        // accumulators as operands.
+        if constexpr (NFR == 4)
+          asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::"a"(acc[0][0]), "a"(acc[0][1]), "a"(acc[0][2]), "a"(acc[0][3]),
+                       "a"(acc[1][0]), "a"(acc[1][1]), "a"(acc[1][2]), "a"(acc[1][3]), "a"(acc[2][0]), "a"(acc[2][1]),
+                       "a"(acc[2][2]), "a"(acc[2][3]), "a"(acc[3][0]), "a"(acc[3][1]), "a"(acc[3][2]), "a"(acc[3][3]));
+        else if constexpr (NFR == 3)
+          asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::"a"(acc[0][0]), "a"(acc[0][1]), "a"(acc[0][2]), "a"(acc[1][0]),
+                       "a"(acc[1][1]), "a"(acc[1][2]), "a"(acc[2][0]), "a"(acc[2][1]), "a"(acc[2][2]), "a"(acc[3][0]),
+                       "a"(acc[3][1]), "a"(acc[3][2]));
+        else if constexpr (NFR == 2)
+          asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::"a"(acc[0][0]), "a"(acc[0][1]), "a"(acc[1][0]), "a"(acc[1][1]),
+                       "a"(acc[2][0]), "a"(acc[2][1]), "a"(acc[3][0]), "a"(acc[3][1]));
+        else
+          asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::"a"(acc[0][0]), "a"(acc[1][0]), "a"(acc[2][0]), "a"(acc[3][0]));
+        // this stage's slot of the first operand is free until the next stage's DMAs
+        uint16_t* spare = lds + (cas + SLOTS - 2) % SLOTS * OPT + wave * (OPT / 4);
+#pragma unroll
+        for (int fr = 0; fr < NFR; ++fr)
+          work.end(cur, spare, fr, [&](int fv, int j, float* z) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(z[i]) : "a"(acc[fv][fr][4 * j + i]));
+          });
+      }
+    };
+    switch (min(4, max(0, (it.nb - wr + 1) / 2))) {
+      case 4: run(std::integral_constant<int, 4>{}); break;
+      case 3: run(std::integral_constant<int, 3>{}); break;
+      case 2: run(std::integral_constant<int, 2>{}); break;
+      case 1: run(std::integral_constant<int, 1>{}); break;
+      default: run(std::integral_constant<int, 0>{}); break;
+    }
+    stage_sync<63>();  // no wave's DMAs reach the spare slot before every wave has left it
+    if (!more) break;
+    cur = nxt;
+    it = it1;
+    --a_rel;
+    --b_rel;
+    nxt = ahead;
+    it1 = it2;
+    more = more2;
+    more2 = work.next(ahead);
+    it2 = work.describe(ahead);
+  }
+  stage_sync<0>();  // the DMAs behind the last stage
+}
+
+__device__ __forceinline__ int blocks_of(int rows) { return min(8, max(0, (rows + 31) / 32)); }
+
+// A lane's results of one row, as bf16, through the wave's 8 KiB of spare LDS
+// [32 rows][128 columns], so that they leave in 256-byte runs: store(row,
+// column, 16 bytes).  Row r holds its 16-byte pieces at piece ^ (r & 15): the 16
+// pieces of a read meet all banks, the rows of a write half of them twice.
+template <class Make, class Store>
+__device__ __forceinline__ void store_rows(uint16_t* spare, const Lane& at, int fr, Make make, Store store) {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));  // the addresses are made here, not kept through the tile's stages
+  const int r = lane & 31, h = lane >> 5;
+  LDS_AS uint8_t* p = (LDS_AS uint8_t*)spare;
+  // the last call's reads are done before this one's writes
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int fv = 0; fv < 4; ++fv)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float z[4];
+      make(fv, j, z);
+      const u32x2 u = {float_bf16(z[0]) | float_bf16(z[1]) << 16, float_bf16(z[2]) | float_bf16(z[3]) << 16};
+      *(LDS_AS u32x2*)(p + r * 256 + ((fv * 4 + j) ^ (r & 15)) * 16 + h * 8) = u;
+      __builtin_amdgcn_sched_barrier(0);  // one run at a time: all of them at once do not fit the registers
+    }
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int rr = i * 4 + (lane >> 4), piece = lane & 15;
+    u32x4 u = *(LDS_AS const u32x4*)(p + rr * 256 + ((piece ^ (rr & 15)) * 16));
+    asm volatile("" : "+v"(u));  // read by all lanes together, not inside the store's bounds
+    store(at.wr * 32 + 64 * fr + rr, at.wv * 128 + piece * 8, make_uint4(u.x, u.y, u.z, u.w));
+  }
+}
+
+template <bool TAIL>
+struct DzWork {
+  const GradArgs& a;
+  int Mp, np, n_rt, n_vt;
+  Lane at;
+  float lse[4], coef[4];
+  int tgt[4];
+  struct Cursor {
+    int e, r0, c0;
+  };
+  __device__ __forceinline__ int64_t lda() const { return a.d; }
+  __device__ __forceinline__ int64_t ldb() const { return a.dp; }
+  __device__ __forceinline__ const uint16_t* zeros() const { return a.zeros; }
+  __device__ __forceinline__ bool place(Cursor& c) const {
+    if (c.e >= n_rt * n_vt) return false;
+    int rt, vt;
+    item_coords(c.e, n_rt, n_vt, rt, vt);
+    c.r0 = rt * BT;
+    c.c0 = vt * BT;
+    return true;
+  }
+  __device__ __forceinline__ bool first(Cursor& c) const {
+    c.e = xcd_remap(blockIdx.x, gridDim.x);
+    return place(c);
+  }
+  __device__ __forceinline__ bool next(Cursor& c) const {
+    Cursor n = c;
+    n.e += gridDim.x;
+    if (!place(n)) return false;
+    c = n;
+    return true;
+  }
+  __device__ __forceinline__ Item describe(const Cursor& c) const {
+    return {{a.W + (int64_t)(a.v0 + c.c0) * a.d, a.n - c.c0, a.d},
+            {a.rows + (int64_t)c.r0 * a.dp, Mp - c.r0, a.dp},
+            a.dp / BK,
+            0,
+            blocks_of(Mp - c.r0)};
+  }
+  __device__ __forceinline__ void begin(const Cursor& c) {
+#pragma unroll
+    for (int fr = 0; fr < 4; ++fr) {
+      const int r = min(c.r0 + at.row(fr), Mp - 1);
+      lse[fr] = a.lse[r];
+      coef[fr] = a.coef[r];
+      tgt[fr] = a.tgt[r];
+    }
+  }
+  template <class Z>
+  __device__ __forceinline__ void end(const Cursor& c, uint16_t* spare, int fr, Z read) const {
+    // the target's place, and the end of the piece, counted from the lane's first column
+    int hit = tgt[fr] - a.v0 - c.c0 - at.col0, end = a.n - c.c0 - at.col0;
+    asm volatile("" : "+v"(hit), "+v"(end));  // made here, not kept through the tile's stages
+    const bool whole = c.c0 + BT <= a.n;
+    store_rows(
+        spare, at, fr,
+        [&](int fv, int j, float* z) {
+          read(fv, j, z);
+          const int col = 32 * fv + 8 * j;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = __builtin_amdgcn_exp2f((z[i] - lse[fr]) * kLog2eF);
+            z[i] = coef[fr] * (p - (hit == col + i ? 1.f : 0.f));
+          }
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = col + i < end ? z[i] : 0.f;
+          }
+        },
+        [&](int row, int col, const uint4& u) {
+          if (c.r0 + row < Mp && c.c0 + col < np)
+            *reinterpret_cast<uint4*>(a.dz + (int64_t)(c.r0 + row) * a.ldz + c.c0 + col) = u;
+        });
+  }
+};
+
 template <bool TAIL>
 __global__ __launch_bounds__(NT, 1) void k_loss_dz(GradArgs a) {
   __shared__ __attribute__((aligned(1024))) uint16_t lds[SLOTS * OPT];
-  const int M = min(a.ctr[0], a.L), Mp = (M + BK - 1) / BK * BK, np = (a.n + BK - 1) / BK * BK;
-  const int n_rt = (M + BT - 1) / BT, n_vt = (a.n + BT - 1) / BT;
-  const Lane at;
-  for (int e = xcd_remap(blockIdx.x, gridDim.x); e < n_rt * n_vt; e += gridDim.x) {
-    int rt, vt;
-    item_coords(e, n_rt, n_vt, rt, vt);
-    const int r0 = rt * BT, c0 = vt * BT;
-    const Operand w = {a.W + (int64_t)(a.v0 + c0) * a.d, a.d, a.n - c0, a.d, a.zeros};
-    const Operand h = {a.rows + (int64_t)r0 * a.dp, a.dp, Mp - r0, a.dp, nullptr};
-    float lse[4], coef[4];
-    int hit[4];  // the target's place in the tile
-#pragma unroll
-    for (int fr = 0; fr < 4; ++fr) {
-      const int r = min(r0 + at.row(fr), Mp - 1);
-      lse[fr] = a.lse[r];
-      coef[fr] = a.coef[r];
-      hit[fr] = a.tgt[r] - a.v0 - c0;
-    }
-    const bool whole = c0 + BT <= a.n;
-    tile_product<false, TAIL, false>(lds, w, h, a.dp / BK, blocks_of(Mp - r0), [&](int fr, int fv, int j, float* z) {
-      const int r = r0 + at.row(fr), c = at.col(fv, j);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = __builtin_amdgcn_exp2f((z[i] - lse[fr]) * kLog2eF);
-        z[i] = coef[fr] * (p - (c + i == hit[fr] ? 1.f : 0.f));
-      }
-      if (!whole) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = c0 + c + i < a.n ? z[i] : 0.f;
-      }
-      if (r < Mp && c0 + c < np)
-        *reinterpret_cast<uint2*>(a.dz + (int64_t)r * a.ldz + c0 + c) =
-            make_uint2(float_bf16(z[0]) | float_bf16(z[1]) << 16, float_bf16(z[2]) | float_bf16(z[3]) << 16);
-    });
-  }
+  const int M = min(a.ctr[0], a.L);
+  DzWork<TAIL> work = {a, (M + BK - 1) / BK * BK, (a.n + BK - 1) / BK * BK, (M + BT - 1) / BT, (a.n + BT - 1) / BT, Lane()};
+  run_tiles<false, TAIL, false>(lds, work);
 }
 
 // d_hidden has rows / 256 x d / 256 tiles, often fewer than compute units or a
@@ -338,46 +482,121 @@ __global__ __launch_bounds__(NT, 1) void k_loss_dz(GradArgs a) {
 // workgroup has the same work.  A workgroup's part of a tile is a share of its
 // own, kept in fp32 in the accumulators' order over all pieces, and the shares
 // are added at the end, in order.
-__global__ __launch_bounds__(NT, 1) void k_loss_d_hidden(GradArgs a) {
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[SLOTS * OPT];
-  const int M = min(a.ctr[0], a.L), Mp = (M + BK - 1) / BK * BK;
-  const int n_rt = (M + BT - 1) / BT, n_ct = (a.d + BT - 1) / BT;
-  const int64_t tiles = (int64_t)n_rt * n_ct, stages = (a.n + BK - 1) / BK, line = tiles * stages;
-  const int64_t cuts = loss_cuts(tiles, a.ldz);
-  for (int64_t g = xcd_remap(blockIdx.x, gridDim.x); g < cuts; g += gridDim.x) {
-    const int64_t lo = line * g / cuts, hi = line * (g + 1) / cuts;
-    const int64_t t0 = tiles * g / cuts, t1 = (tiles * (g + 1) + cuts - 1) / cuts;
-    for (int64_t t = t0; t < t1; ++t) {
-      const int64_t s0 = max(lo, t * stages) - t * stages, s1 = min(hi, (t + 1) * stages) - t * stages;
-      float4* share = reinterpret_cast<float4*>(a.acc) + (g + t) * (BT * BT / 4) + threadIdx.x;
-      if (s1 <= s0) {  // a piece too short to give this workgroup a stage of the tile
-        if (a.first)
-          for (int i = 0; i < BT * BT / 4 / NT; ++i) share[i * NT] = make_float4(0.f, 0.f, 0.f, 0.f);
-        continue;
-      }
+//
+// A workgroup takes its tiles from the last to the first.  With less than a
+// tile each (cuts just above tiles) it has the first stages of one tile and the
+// last ones of the tile before, and in that order it works, like all the
+// others, near the stage that as much time has passed: one region of W and dz
+// is in the caches, not one for each workgroup.  Whole tiles start where the
+// time stands, too, and wrap around.
+struct DHiddenWork {
+  const GradArgs& a;
+  int M, Mp, n_rt, n_ct, stages;
+  int64_t g, lo, hi, low, high;  // the workgroup's cut, its stages of the line, and the tiles that it may have some of
+  Lane at;
+  struct Cursor {
+    int64_t t;
+    int s0, s1, r0, c0, passed;
+  };
+  __device__ __forceinline__ DHiddenWork(const GradArgs& args, int m, int64_t cut, int64_t tiles, int64_t cuts) : a(args), M(m), g(cut) {
+    Mp = (M + BK - 1) / BK * BK;
+    n_rt = (M + BT - 1) / BT;
+    n_ct = (a.d + BT - 1) / BT;
+    stages = (a.n + BK - 1) / BK;
+    lo = tiles * stages * g / cuts;
+    hi = tiles * stages * (g + 1) / cuts;
+    low = tiles * g / cuts;
+    high = (tiles * (g + 1) + cuts - 1) / cuts;
+  }
+  // the cut's stages of tile t; none where a piece is too short to have one
+  __device__ __forceinline__ void part(int64_t t, int& s0, int& s1) const {
+    s0 = (int)max(lo - t * stages, (int64_t)0);
+    s1 = (int)min(hi - t * stages, (int64_t)stages);
+  }
+  __device__ __forceinline__ int64_t lda() const { return a.d; }
+  __device__ __forceinline__ int64_t ldb() const { return a.ldz; }
+  __device__ __forceinline__ const uint16_t* zeros() const { return nullptr; }
+  // from tile t on, downwards, to a part that has stages
+  __device__ __forceinline__ bool place(Cursor& c) const {
+    for (; c.t >= low; --c.t) {
+      part(c.t, c.s0, c.s1);
+      if (c.s1 <= c.s0) continue;
       int rt, ct;
-      item_coords((int)t, n_rt, n_ct, rt, ct);
-      const int r0 = rt * BT, c0 = ct * BT, k0 = (int)s0 * BK;
-      const Operand w = {a.W + (int64_t)(a.v0 + k0) * a.d + c0, a.d, a.n - k0, a.d - c0, nullptr};
-      const Operand z = {a.dz + (int64_t)r0 * a.ldz + k0, a.ldz, Mp - r0, 0, nullptr};
-      tile_product<true, false, false>(lds, w, z, (int)(s1 - s0), blocks_of(M - r0), [&](int fr, int fv, int j, float* v) {
-        float4* o = share + ((fr * 4 + fv) * 4 + j) * NT;
-        float4 x = a.first ? make_float4(0.f, 0.f, 0.f, 0.f) : *o;
-        x.x += v[0];
-        x.y += v[1];
-        x.z += v[2];
-        x.w += v[3];
-        *o = x;
-      });
+      item_coords((int)c.t, n_rt, n_ct, rt, ct);
+      c.r0 = rt * BT;
+      c.c0 = ct * BT;
+      return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ bool first(Cursor& c) const {
+    c.passed = 0;
+    c.t = high - 1;
+    return place(c);
+  }
+  __device__ __forceinline__ bool next(Cursor& c) const {
+    Cursor n = c;
+    n.passed += n.s1 - n.s0;
+    if (n.passed >= stages) n.passed -= stages;
+    --n.t;
+    if (!place(n)) return false;
+    c = n;
+    return true;
+  }
+  __device__ __forceinline__ Item describe(const Cursor& c) const {
+    const int k0 = c.s0 * BK;
+    return {{a.W + (int64_t)(a.v0 + k0) * a.d + c.c0, a.n - k0, a.d - c.c0},
+            {a.dz + (int64_t)c.r0 * a.ldz + k0, Mp - c.r0, 0},
+            c.s1 - c.s0,
+            c.s1 - c.s0 == stages ? c.passed : 0,
+            blocks_of(M - c.r0)};
+  }
+  __device__ __forceinline__ void begin(const Cursor&) const {}
+  template <class Z>
+  __device__ __forceinline__ void end(const Cursor& c, uint16_t*, int fr, Z read) const {
+    float4* share = reinterpret_cast<float4*>(a.acc) + (g + c.t) * (BT * BT / 4) + threadIdx.x;
+#pragma unroll
+    for (int fv = 0; fv < 4; ++fv) {
+      float4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = a.first ? make_float4(0.f, 0.f, 0.f, 0.f) : share[((fr * 4 + fv) * 4 + j) * NT];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v[4];
+        read(fv, j, v);
+        x[j].x += v[0];
+        x[j].y += v[1];
+        x[j].z += v[2];
+        x[j].w += v[3];
+        share[((fr * 4 + fv) * 4 + j) * NT] = x[j];
+      }
     }
   }
+};
+
+__global__ __launch_bounds__(NT, 1) void k_loss_d_hidden(GradArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[SLOTS * OPT];
+  const int M = min(a.ctr[0], a.L), n_rt = (M + BT - 1) / BT, n_ct = (a.d + BT - 1) / BT;
+  const int64_t tiles = (int64_t)n_rt * n_ct, cuts = min(loss_cuts(tiles, a.ldz), (int64_t)gridDim.x);
+  const int g = xcd_remap(blockIdx.x, gridDim.x);
+  if (g >= cuts) return;
+  DHiddenWork work(a, M, g, tiles, cuts);
+  if (a.first)
+    for (int64_t t = work.low; t < work.high; ++t) {
+      int s0, s1;
+      work.part(t, s0, s1);
+      float4* share = reinterpret_cast<float4*>(a.acc) + (g + t) * (BT * BT / 4) + threadIdx.x;
+      if (s1 <= s0)  // a part that this piece does not reach, and a later one may
+        for (int i = 0; i < BT * BT / 4 / NT; ++i) share[i * NT] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  run_tiles<true, false, false>(lds, work);
 }
 
 // d_hidden of a tile: its shares added, in the order of the cuts.
-__global__ __launch_bounds__(NT) void k_loss_join(GradArgs a) {
+__global__ __launch_bounds__(NT) void k_loss_join(GradArgs a, int grid) {
   const int M = min(a.ctr[0], a.L);
   const int n_rt = (M + BT - 1) / BT, n_ct = (a.d + BT - 1) / BT;
-  const int64_t tiles = (int64_t)n_rt * n_ct, cuts = loss_cuts(tiles, a.ldz);
+  const int64_t tiles = (int64_t)n_rt * n_ct, cuts = min(loss_cuts(tiles, a.ldz), (int64_t)grid);
   const Lane at;
   constexpr int kParts = 16;  // of a tile: one (fr, fv)
   for (int64_t e = blockIdx.x; e < tiles * kParts; e += gridDim.x) {
@@ -408,9 +627,72 @@ __global__ __launch_bounds__(NT) void k_loss_join(GradArgs a) {
   }
 }
 
+struct DWWork {
+  const GradArgs& a;
+  int Mp, n_vt, n_ct;
+  Lane at;
+  struct Cursor {
+    int e, r0, c0;
+  };
+  __device__ __forceinline__ int64_t lda() const { return a.dp; }
+  __device__ __forceinline__ int64_t ldb() const { return a.ldz; }
+  __device__ __forceinline__ const uint16_t* zeros() const { return nullptr; }
+  __device__ __forceinline__ bool place(Cursor& c) const {
+    if (c.e >= n_vt * n_ct) return false;
+    int vt, ct;
+    item_coords(c.e, n_vt, n_ct, vt, ct);
+    c.r0 = vt * BT;
+    c.c0 = ct * BT;
+    return true;
+  }
+  __device__ __forceinline__ bool first(Cursor& c) const {
+    c.e = xcd_remap(blockIdx.x, gridDim.x);
+    return place(c);
+  }
+  __device__ __forceinline__ bool next(Cursor& c) const {
+    Cursor n = c;
+    n.e += gridDim.x;
+    if (!place(n)) return false;
+    c = n;
+    return true;
+  }
+  __device__ __forceinline__ Item describe(const Cursor& c) const {
+    return {{a.rows + c.c0, Mp, a.dp - c.c0}, {a.dz + c.r0, Mp, (int)a.ldz - c.r0}, Mp / BK, 0, blocks_of(a.n - c.r0)};
+  }
+  __device__ __forceinline__ void begin(const Cursor&) const {}
+  template <class Z>
+  __device__ __forceinline__ void end(const Cursor& c, uint16_t* spare, int fr, Z read) const {
+    if (!a.accumulate) {
+      store_rows(spare, at, fr, read, [&](int row, int col, const uint4& u) {
+        if (c.r0 + row < a.n && c.c0 + col < a.d)
+          *reinterpret_cast<uint4*>(a.d_W + (int64_t)(a.v0 + c.r0 + row) * a.d + c.c0 + col) = u;
+      });
+      return;
+    }
+    // added in fp32 and rounded once, so not through the bf16 rows above
+    const int r = c.r0 + at.row(fr);
+#pragma unroll
+    for (int fv = 0; fv < 4; ++fv)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v[4];
+        read(fv, j, v);
+        const int col = c.c0 + at.col(fv, j);
+        if (r >= a.n || col >= a.d) continue;
+        uint2* o = reinterpret_cast<uint2*>(a.d_W + (int64_t)(a.v0 + r) * a.d + col);
+        const uint2 u = *o;
+        v[0] += bf16_float(u.x & 0xFFFF);
+        v[1] += bf16_float(u.x >> 16);
+        v[2] += bf16_float(u.y & 0xFFFF);
+        v[3] += bf16_float(u.y >> 16);
+        *o = make_uint2(float_bf16(v[0]) | float_bf16(v[1]) << 16, float_bf16(v[2]) | float_bf16(v[3]) << 16);
+      }
+  }
+};
+
 __global__ __launch_bounds__(NT, 1) void k_loss_d_W(GradArgs a) {
   __shared__ __attribute__((aligned(1024))) uint16_t lds[SLOTS * OPT];
-  const int M = min(a.ctr[0], a.L), Mp = (M + BK - 1) / BK * BK;
+  const int M = min(a.ctr[0], a.L);
   if (M == 0) {
     if (a.accumulate) return;
     const int64_t n = (int64_t)a.n * a.d / 8;
@@ -418,28 +700,8 @@ __global__ __launch_bounds__(NT, 1) void k_loss_d_W(GradArgs a) {
     for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < n; i += (int64_t)gridDim.x * NT) o[i] = make_uint4(0, 0, 0, 0);
     return;
   }
-  const int n_vt = (a.n + BT - 1) / BT, n_ct = (a.d + BT - 1) / BT;
-  const Lane at;
-  for (int64_t e = xcd_remap(blockIdx.x, gridDim.x); e < (int64_t)n_vt * n_ct; e += gridDim.x) {
-    int vt, ct;
-    item_coords((int)e, n_vt, n_ct, vt, ct);
-    const int r0 = vt * BT, c0 = ct * BT;
-    const Operand h = {a.rows + c0, a.dp, Mp, a.dp - c0, nullptr};
-    const Operand z = {a.dz + r0, a.ldz, Mp, a.ldz - r0, nullptr};
-    tile_product<true, false, true>(lds, h, z, Mp / BK, blocks_of(a.n - r0), [&](int fr, int fv, int j, float* v) {
-      const int r = r0 + at.row(fr), c = c0 + at.col(fv, j);
-      if (r >= a.n || c >= a.d) return;
-      uint2* o = reinterpret_cast<uint2*>(a.d_W + (int64_t)(a.v0 + r) * a.d + c);
-      if (a.accumulate) {
-        const uint2 u = *o;
-        v[0] += bf16_float(u.x & 0xFFFF);
-        v[1] += bf16_float(u.x >> 16);
-        v[2] += bf16_float(u.y & 0xFFFF);
-        v[3] += bf16_float(u.y >> 16);
-      }
-      *o = make_uint2(float_bf16(v[0]) | float_bf16(v[1]) << 16, float_bf16(v[2]) | float_bf16(v[3]) << 16);
-    });
-  }
+  DWWork work = {a, (M + BK - 1) / BK * BK, (a.n + BT - 1) / BT, (a.d + BT - 1) / BT, Lane()};
+  run_tiles<true, false, true>(lds, work);
 }
 
 }  // namespace
@@ -460,7 +722,7 @@ hipError_t launch_loss_d_W(const GradArgs& a, int grid, hipStream_t stream) {
   return hipGetLastError();
 }
 hipError_t launch_loss_join(const GradArgs& a, int grid, hipStream_t stream) {
-  hipLaunchKernelGGL(k_loss_join, dim3(grid), dim3(NT), 0, stream, a);
+  hipLaunchKernelGGL(k_loss_join, dim3(16 * grid), dim3(NT), 0, stream, a, grid);
   return hipGetLastError();
 }
 

@@ -33,6 +33,7 @@ struct GradArgs {
   int first, accumulate;
 };
 
+// grid: workgroups of the products, the same for all of a call
 hipError_t launch_loss_dz(const GradArgs& a, int grid, hipStream_t stream);        // dz
 hipError_t launch_loss_d_hidden(const GradArgs& a, int grid, hipStream_t stream);  // acc += dz . W
 hipError_t launch_loss_d_W(const GradArgs& a, int grid, hipStream_t stream);       // d_W = dz^T . rows
