@@ -95,41 +95,63 @@ __global__ __launch_bounds__(1024) void k_loss_total(const float* __restrict__ t
 
 // What backward keeps of each counted row, in order: its hidden state and
 // scalars, filled up with rows and columns of zeros; and zeros for the rows of
-// d_hidden that do not count.
+// d_hidden that do not count.  A wave takes a row.
 struct PrepareArgs {
-  const uint16_t* H;
+  const uint16_t *W, *H;
   const uint8_t* counted;
   const int32_t* targets;
   const float *weights, *grad, *lse;
   const int32_t *idx, *ctr;
   int L, d, dp;
   uint16_t *rows, *zeros;
-  float *row_lse, *coef;
+  float* bias;
+  uint32_t* flip;
   int32_t* tgt;
+  float* at_tgt;
   uint16_t* d_hidden;
 };
 
 __global__ __launch_bounds__(256) void k_loss_prepare(PrepareArgs a) {
-  const int M = min(a.ctr[0], a.L), Mp = (M + kLossStep - 1) / kLossStep * kLossStep;
+  const int M = min(a.ctr[0], a.L), Mp = (M + kLossStep - 1) / kLossStep * kLossStep, lane = threadIdx.x & 63;
   const uint4 none = make_uint4(0, 0, 0, 0);
   if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<uint4*>(a.zeros) = none;
-  for (int i = blockIdx.x; i < max(a.L, Mp); i += gridDim.x) {
-    if (i < Mp) {
-      const int pos = i < M ? a.idx[i] : 0;
-      if (threadIdx.x == 0) {
-        a.row_lse[i] = i < M ? a.lse[pos] : 0.f;
-        a.coef[i] = i < M ? (a.weights ? a.weights[pos] : 1.f) * (a.grad ? *a.grad : 1.f) : 0.f;
-        a.tgt[i] = i < M ? a.targets[pos] : -1;
-      }
-      for (int c = 8 * threadIdx.x; c < a.dp; c += 8 * 256) {
+  for (int i = blockIdx.x * 4 + (threadIdx.x >> 6); i < max(a.L, Mp); i += gridDim.x * 4) {
+    if (i < M) {
+      const int pos = a.idx[i], t = a.targets[pos];
+      const uint16_t *h = a.H + (int64_t)pos * a.d, *w = a.W + (int64_t)t * a.d;
+      float z = 0.f;
+      for (int c = 8 * lane; c < a.dp; c += 8 * 64) {
         uint4 u = make_uint4(0, 0, 0, 0);
-        if (i < M && c < a.d) u = *reinterpret_cast<const uint4*>(a.H + (int64_t)pos * a.d + c);
+        if (c < a.d) {
+          u = *reinterpret_cast<const uint4*>(h + c);
+          float x[8], y[8];
+          unpack8(u, x);
+          unpack8(*reinterpret_cast<const uint4*>(w + c), y);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z = fmaf(x[j], y[j], z);
+        }
         *reinterpret_cast<uint4*>(a.rows + (int64_t)i * a.dp + c) = u;
+      }
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) z += __shfl_xor(z, off);
+      if (lane == 0) {
+        const float lse = a.lse[pos], c = (a.weights ? a.weights[pos] : 1.f) * (a.grad ? *a.grad : 1.f);
+        a.bias[i] = __builtin_amdgcn_logf(fabsf(c)) - lse * kLog2eF;
+        a.flip[i] = c < 0.f ? 0x80008000u : 0u;
+        a.tgt[i] = t;
+        a.at_tgt[i] = c * expm1f(z - lse);
+      }
+    } else if (i < Mp) {
+      for (int c = 8 * lane; c < a.dp; c += 8 * 64) *reinterpret_cast<uint4*>(a.rows + (int64_t)i * a.dp + c) = none;
+      if (lane == 0) {
+        a.bias[i] = -INFINITY;
+        a.flip[i] = 0u;
+        a.tgt[i] = -1;
+        a.at_tgt[i] = 0.f;
       }
     }
     if (a.d_hidden && i < a.L && !a.counted[i])
-      for (int c = 8 * threadIdx.x; c < a.d; c += 8 * 256)
-        *reinterpret_cast<uint4*>(a.d_hidden + (int64_t)i * a.d + c) = none;
+      for (int c = 8 * lane; c < a.d; c += 8 * 64) *reinterpret_cast<uint4*>(a.d_hidden + (int64_t)i * a.d + c) = none;
   }
 }
 
@@ -147,8 +169,10 @@ struct Rows {
   int32_t *idx, *ctr;
   float* terms;
   Partials part;
-  float *row_lse, *coef;
+  float* bias;
+  uint32_t* flip;
   int32_t* tgt;
+  float* at_tgt;
   uint16_t *zeros, *rows, *dz;
   float* acc;
 };
@@ -172,9 +196,10 @@ size_t carve(int64_t d, int64_t L, int64_t piece, uint8_t* base, Rows* r) {
     x.part.s = reinterpret_cast<float*>(take((size_t)part_cap(L) * 4));
   } else {
     const size_t rows = (size_t)loss_padded(L);
-    x.row_lse = reinterpret_cast<float*>(take(rows * 4));
-    x.coef = reinterpret_cast<float*>(take(rows * 4));
+    x.bias = reinterpret_cast<float*>(take(rows * 4));
+    x.flip = reinterpret_cast<uint32_t*>(take(rows * 4));
     x.tgt = reinterpret_cast<int32_t*>(take(rows * 4));
+    x.at_tgt = reinterpret_cast<float*>(take(rows * 4));
     x.zeros = reinterpret_cast<uint16_t*>(take(16));
     x.rows = reinterpret_cast<uint16_t*>(take(rows * (size_t)loss_padded(d) * 2));
     x.dz = reinterpret_cast<uint16_t*>(take(rows * (size_t)piece * 2));
@@ -322,11 +347,11 @@ dllm_status dllm_loss_backward(const dllm_loss* p, const float* lse, const float
   plan.tile_rows = dllm::kLargeBM;
   if (dllm::launch_mask_compact(r.counted, 0, L, 0, plan, r.idx, r.ctr, st) != hipSuccess) return DLLM_ERR_HIP;
   const int dp = (int)dllm::loss_padded(d), grid = cus < dllm::kLossGrid ? cus : dllm::kLossGrid;
-  const dllm::PrepareArgs pa = {p->hidden, r.counted, p->targets, p->weights, grad,      lse,    r.idx, r.ctr,   (int)L,
-                                (int)d,    dp,        r.rows,     r.zeros,    r.row_lse, r.coef, r.tgt, d_hidden};
-  hipLaunchKernelGGL(dllm::k_loss_prepare, dim3(dllm::grid_for(dllm::loss_padded(L), 65536)), dim3(256), 0, st, pa);
-  dllm::GradArgs a = {p->W_lm, r.zeros,  r.rows, r.idx, r.ctr,  r.row_lse, r.coef, r.tgt, r.dz, r.acc,
-                      d_hidden, d_W,     piece,  (int)V, (int)d, dp,       (int)L, 0,     0,    0,     accumulate};
+  const dllm::PrepareArgs pa = {p->W_lm, p->hidden, r.counted, p->targets, p->weights, grad,  lse,      r.idx,   r.ctr, (int)L,
+                                (int)d,  dp,        r.rows,    r.zeros,    r.bias,     r.flip, r.tgt, r.at_tgt, d_hidden};
+  hipLaunchKernelGGL(dllm::k_loss_prepare, dim3(dllm::grid_for(dllm::loss_padded(L) / 4, 65536)), dim3(256), 0, st, pa);
+  dllm::GradArgs a = {p->W_lm, r.zeros,  r.rows, r.idx, r.ctr,  r.bias, r.flip, r.tgt, r.at_tgt, r.dz, r.acc,
+                      d_hidden, d_W,     piece,  (int)V, (int)d, dp,    (int)L, 0,     0,        0,    accumulate};
   for (int64_t v = 0; v < V; v += piece) {
     a.v0 = (int)v;
     a.n = (int)(V - v < piece ? V - v : piece);

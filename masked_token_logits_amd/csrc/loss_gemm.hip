@@ -365,25 +365,25 @@ __device__ __forceinline__ int blocks_of(int rows) { return min(8, max(0, (rows 
 // [32 rows][128 columns], so that they leave in 256-byte runs: store(row,
 // column, 16 bytes).  Row r holds its 16-byte pieces at piece ^ (r & 15): the 16
 // pieces of a read meet all banks, the rows of a write half of them twice.
-template <class Make, class Store>
-__device__ __forceinline__ void store_rows(uint16_t* spare, const Lane& at, int fr, Make make, Store store) {
+// patch(p, r, h) may change a row of the lane's in LDS before.
+template <class Make, class Patch, class Store>
+__device__ __forceinline__ void store_rows(uint16_t* spare, const Lane& at, int fr, Make make, Patch patch, Store store) {
   int lane = threadIdx.x & 63;
   asm volatile("" : "+v"(lane));  // the addresses are made here, not kept through the tile's stages
   const int r = lane & 31, h = lane >> 5;
   LDS_AS uint8_t* p = (LDS_AS uint8_t*)spare;
-  // the last call's reads are done before this one's writes
-  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");  // a wave's LDS accesses are done in order: the last call's reads, these writes
 #pragma unroll
   for (int fv = 0; fv < 4; ++fv)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float z[4];
-      make(fv, j, z);
-      const u32x2 u = {float_bf16(z[0]) | float_bf16(z[1]) << 16, float_bf16(z[2]) | float_bf16(z[3]) << 16};
+      const u32x2 u = make(fv, j);
       *(LDS_AS u32x2*)(p + r * 256 + ((fv * 4 + j) ^ (r & 15)) * 16 + h * 8) = u;
       __builtin_amdgcn_sched_barrier(0);  // one run at a time: all of them at once do not fit the registers
     }
-  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+  patch(p, r, h);
+  asm volatile("" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int rr = i * 4 + (lane >> 4), piece = lane & 15;
@@ -398,7 +398,8 @@ struct DzWork {
   const GradArgs& a;
   int Mp, np, n_rt, n_vt;
   Lane at;
-  float lse[4], coef[4];
+  float bias[4], at_tgt[4];
+  uint32_t flip[4];
   int tgt[4];
   struct Cursor {
     int e, r0, c0;
@@ -436,31 +437,35 @@ struct DzWork {
 #pragma unroll
     for (int fr = 0; fr < 4; ++fr) {
       const int r = min(c.r0 + at.row(fr), Mp - 1);
-      lse[fr] = a.lse[r];
-      coef[fr] = a.coef[r];
+      bias[fr] = a.bias[r];
+      flip[fr] = a.flip[r];
       tgt[fr] = a.tgt[r];
+      at_tgt[fr] = a.at_tgt[r];
     }
   }
   template <class Z>
   __device__ __forceinline__ void end(const Cursor& c, uint16_t* spare, int fr, Z read) const {
-    // the target's place, and the end of the piece, counted from the lane's first column
-    int hit = tgt[fr] - a.v0 - c.c0 - at.col0, end = a.n - c.c0 - at.col0;
+    // the end of the piece counted from the lane's first column, and the target's place in the wave's
+    int end = a.n - c.c0 - at.col0, hit = tgt[fr] - a.v0 - c.c0 - at.wv * 128;
     asm volatile("" : "+v"(hit), "+v"(end));  // made here, not kept through the tile's stages
     const bool whole = c.c0 + BT <= a.n;
     store_rows(
         spare, at, fr,
-        [&](int fv, int j, float* z) {
+        [&](int fv, int j) {
+          float z[4];
           read(fv, j, z);
-          const int col = 32 * fv + 8 * j;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float p = __builtin_amdgcn_exp2f((z[i] - lse[fr]) * kLog2eF);
-            z[i] = coef[fr] * (p - (hit == col + i ? 1.f : 0.f));
-          }
+          for (int i = 0; i < 4; ++i) z[i] = __builtin_amdgcn_exp2f(fmaf(z[i], kLog2eF, bias[fr]));
           if (!whole) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[i] = col + i < end ? z[i] : 0.f;
+            for (int i = 0; i < 4; ++i) z[i] = 32 * fv + 8 * j + i < end ? z[i] : 0.f;
           }
+          return u32x2{(float_bf16(z[0]) | float_bf16(z[1]) << 16) ^ flip[fr],
+                       (float_bf16(z[2]) | float_bf16(z[3]) << 16) ^ flip[fr]};
+        },
+        [&](LDS_AS uint8_t* p, int r, int h) {
+          if (h == 0 && hit >= 0 && hit < 128)
+            *(LDS_AS uint16_t*)(p + r * 256 + ((hit >> 3) ^ (r & 15)) * 16 + (hit & 7) * 2) = (uint16_t)float_bf16(at_tgt[fr]);
         },
         [&](int row, int col, const uint4& u) {
           if (c.r0 + row < Mp && c.c0 + col < np)
@@ -663,10 +668,18 @@ struct DWWork {
   template <class Z>
   __device__ __forceinline__ void end(const Cursor& c, uint16_t* spare, int fr, Z read) const {
     if (!a.accumulate) {
-      store_rows(spare, at, fr, read, [&](int row, int col, const uint4& u) {
-        if (c.r0 + row < a.n && c.c0 + col < a.d)
-          *reinterpret_cast<uint4*>(a.d_W + (int64_t)(a.v0 + c.r0 + row) * a.d + c.c0 + col) = u;
-      });
+      store_rows(
+          spare, at, fr,
+          [&](int fv, int j) {
+            float z[4];
+            read(fv, j, z);
+            return u32x2{float_bf16(z[0]) | float_bf16(z[1]) << 16, float_bf16(z[2]) | float_bf16(z[3]) << 16};
+          },
+          [](LDS_AS uint8_t*, int, int) {},
+          [&](int row, int col, const uint4& u) {
+            if (c.r0 + row < a.n && c.c0 + col < a.d)
+              *reinterpret_cast<uint4*>(a.d_W + (int64_t)(a.v0 + c.r0 + row) * a.d + c.c0 + col) = u;
+          });
       return;
     }
     // added in fp32 and rounded once, so not through the bf16 rows above

@@ -22,8 +22,10 @@ struct GradArgs {
   const uint16_t* zeros;    // 16 bytes of them
   const uint16_t* rows;     // [Mp, dp] the counted rows of hidden, zeros behind d and M
   const int32_t *idx, *ctr;
-  const float *lse, *coef;  // [Mp] log-sum-exp, and grad * weight; zeros behind M
+  const float* bias;        // [Mp] log2 |c| - log2(e) lse, c = grad * weight: |c| p = 2^(log2(e) z + bias); -inf behind M
+  const uint32_t* flip;     // [Mp] the sign bits of two bf16 where c < 0
   const int32_t* tgt;       // [Mp] the target, -1 behind M
+  const float* at_tgt;      // [Mp] dz there
   uint16_t* dz;             // [Mp, ldz]: the piece's gradient of the logits
   float* acc;               // the rows' gradient over the pieces so far, in shares of a tile each
   uint16_t *d_hidden, *d_W;
