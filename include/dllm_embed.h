@@ -35,7 +35,7 @@ extern "C" {
 
 /*
  * out [T, d] = scale * table[tokens].
- *   table   [V, d] bf16, 1 <= V < 2^31 - 1, d a multiple of 8, d < 2^24
+ *   table   [V, d] bf16, 1 <= V < 2^31 - 1024, d a multiple of 8, d < 2^20
  *   tokens  [T] int32, any values; 0 <= T < 2^31 - 1024.  T = 0 queues nothing
  *   scale   finite; 1 copies rows as they are
  *   out     [T, d] bf16, no overlap with table or tokens

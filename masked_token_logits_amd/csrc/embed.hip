@@ -3,7 +3,7 @@
 // each token's places.
 //
 // The gradient goes by the tokens in sorted order (stable, so a token's places
-// ascend): runs of equal tokens are cut into chunks of kChunk places, one wave
+// ascend): runs of equal tokens are cut into chunks of 32 (or 8) places, one wave
 // to a chunk and 512 columns, which sums rows in fp32 in that order.  A run
 // inside one chunk is written at once; the shares of one that spans chunks go
 // to the workspace and a second kernel adds them, again in order.  So a token
@@ -18,7 +18,9 @@
 namespace dllm {
 namespace {
 
-constexpr int kChunk = 32;       // places of a chunk
+// Places of a chunk.  Short batches have chunks of 8, so that they fill more of
+// the chip: @SHORT@
+constexpr int kChunkMost = 32, kChunkShort = 8, kShortMost = 8192;
 constexpr int kCols = 512;       // columns of a wave: 64 lanes of 8
 constexpr int kNoToken = 0x7FFFFFFF;  // sorts behind every token; its places have no row
 
@@ -46,31 +48,136 @@ __global__ __launch_bounds__(256) void k_embed(const uint16_t* __restrict__ tabl
   }
 }
 
-// A token's place in the sorted order is the number of tokens before it: the
-// smaller ones, and the equal ones further up.  A wave counts for 64 tokens.
-__global__ __launch_bounds__(64) void k_embed_rank(const int32_t* __restrict__ tokens, int T, int V,
-                                                   int32_t* __restrict__ sorted, int32_t* __restrict__ place) {
-  const int i = blockIdx.x * 64 + threadIdx.x;
+// Up to kRankMost tokens are sorted in one launch: a token's place in the
+// order is the number of tokens before it, the smaller ones and the equal ones
+// further up.  A workgroup places 64 tokens, its sixteen waves compare them
+// with a sixteenth of the batch each, two instructions for 64 comparisons.
+constexpr int kRankMost = 16384, kRankWaves = 16;
+
+__global__ __launch_bounds__(64 * kRankWaves) void k_embed_rank(const int32_t* __restrict__ tokens, int T, int V,
+                                                                int32_t* __restrict__ sorted,
+                                                                int32_t* __restrict__ place) {
+  __shared__ int part[kRankWaves][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int first = blockIdx.x * 64, i = first + lane;
   const int mine = i < T ? known(tokens[i], V) : kNoToken;
+  const int lo = (int)((int64_t)T * wave / kRankWaves), hi = (int)((int64_t)T * (wave + 1) / kRankWaves);
   int rank = 0;
-  for (int base = 0; base < T; base += 64) {
-    const int j0 = base + threadIdx.x;
-    const int other = j0 < T ? known(tokens[j0], V) : kNoToken;
-    const int n = min(64, T - base);
-    for (int j = 0; j < n; ++j) {
-      const int o = __builtin_amdgcn_readlane(other, j);
-      rank += (o < mine || (o == mine && base + j < i)) ? 1 : 0;
-    }
+  // those before the workgroup's own count where they are equal, those behind do not
+  const int a = min(max(first, lo), hi), b = min(max(first + 64, lo), hi);
+#pragma unroll 16
+  for (int j = lo; j < a; ++j) rank += known(tokens[j], V) <= mine ? 1 : 0;
+  for (int j = a; j < b; ++j) {
+    const int o = known(tokens[j], V);
+    rank += o < mine || (o == mine && j < i) ? 1 : 0;
   }
-  if (i < T) {
+#pragma unroll 16
+  for (int j = b; j < hi; ++j) rank += known(tokens[j], V) < mine ? 1 : 0;
+  part[wave][lane] = rank;
+  __syncthreads();
+  if (wave == 0 && i < T) {
+#pragma unroll
+    for (int w = 1; w < kRankWaves; ++w) rank += part[w][lane];
     sorted[rank] = mine;
     place[rank] = i;
   }
 }
 
+// More are sorted by digits, the lowest first, each pass stable: how often each
+// digit occurs in each tile of kTile tokens, where those of a tile begin, and
+// the tokens to their places.
+constexpr int kTile = 1024, kBinsMost = 1024;
+
+struct PassArgs {
+  const int32_t *tok, *at;  // at: the places so far; null = tokens in their own order
+  int32_t *tok_out, *at_out;
+  int32_t* counts;          // [bins][tiles]
+  int T, V, tiles, shift, bins;
+};
+
+// A token's digit; tokens without a row sort as V.
+__device__ __forceinline__ int digit(const PassArgs& p, int tok) {
+  return (min(tok, p.V) >> p.shift) & (p.bins - 1);
+}
+
+__global__ __launch_bounds__(256) void k_embed_count(PassArgs p) {
+  __shared__ int hist[kBinsMost];
+  for (int b = threadIdx.x; b < p.bins; b += 256) hist[b] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kTile / 256; ++k) {
+    const int i = blockIdx.x * kTile + k * 256 + threadIdx.x;
+    if (i < p.T) atomicAdd(&hist[digit(p, known(p.tok[i], p.V))], 1);
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < p.bins; b += 256) p.counts[(int64_t)b * p.tiles + blockIdx.x] = hist[b];
+}
+
+// Where each digit's tokens of each tile begin: exclusive sums, in place, 16 to
+// a thread.
+__global__ __launch_bounds__(1024) void k_embed_begin(int32_t* __restrict__ counts, int64_t n) {
+  __shared__ int part[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int carry = 0;
+  for (int64_t base = 0; base < n; base += 16 * 1024) {
+    const int64_t i = base + threadIdx.x * 16;
+    int v[16], mine = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = i + k < n ? counts[i + k] : 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) mine += v[k];
+    int sum = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(sum, off);
+      if (lane >= off) sum += o;
+    }
+    if (lane == 63) part[wave] = sum;
+    __syncthreads();
+    int before = carry, all = carry;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      before += w < wave ? part[w] : 0;
+      all += part[w];
+    }
+    int run = before + sum - mine;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (i + k < n) counts[i + k] = run;
+      run += v[k];
+    }
+    carry = all;
+    __syncthreads();
+  }
+}
+
+// Sixteen waves of 64 tokens: a token's place is its digit's beginning in the
+// tile, the digit's tokens of the waves before, and those of the lanes before,
+// which the digit's bits' ballots tell.
+__global__ __launch_bounds__(kTile) void k_embed_place(PassArgs p) {
+  __shared__ uint16_t count[kTile / 64][kBinsMost];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = blockIdx.x * kTile + threadIdx.x;
+  for (int b = lane; b < p.bins; b += 64) count[wave][b] = 0;
+  const int tok = i < p.T ? known(p.tok[i], p.V) : kNoToken, d = digit(p, tok);
+  unsigned long long same = __ballot(i < p.T);
+  for (int b = 1; b < p.bins; b <<= 1) {
+    const unsigned long long set = __ballot((d & b) != 0);
+    same &= d & b ? set : ~set;
+  }
+  const unsigned long long below = lane ? same & (~0ull >> (64 - lane)) : 0ull;
+  if (i < p.T && below == 0) count[wave][d] = (uint16_t)__popcll(same);
+  __syncthreads();
+  if (i < p.T) {
+    int to = p.counts[(int64_t)d * p.tiles + blockIdx.x] + __popcll(below);
+    for (int w = 0; w < wave; ++w) to += count[w][d];
+    p.tok_out[to] = tok;
+    p.at_out[to] = p.at ? p.at[i] : i;
+  }
+}
+
 struct SumArgs {
   const int32_t *sorted, *place;
-  int T, d;
+  int T, d, chunk;
   const uint16_t* d_out;
   float scale;
   int accumulate;
@@ -88,43 +195,6 @@ __device__ __forceinline__ void finish(const SumArgs& a, int tok, int c, float* 
   *reinterpret_cast<uint4*>(o) = pack8(f);
 }
 
-__global__ __launch_bounds__(64) void k_embed_sum(SumArgs a) {
-  const int lane = threadIdx.x, begin = blockIdx.x * kChunk, n = min(kChunk, a.T - begin);
-  const int c = blockIdx.y * kCols + lane * 8;
-  const int at = begin + (lane < n ? lane : n - 1);
-  const int tok = a.sorted[at], pl = a.place[at];
-  const int before = begin > 0 ? a.sorted[begin - 1] : -1;
-  const int behind = begin + n < a.T ? a.sorted[begin + n] : -1;
-  const bool in = c < a.d;
-  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  int first = 0;  // where the run began
-  for (int k = 0; k < n; ++k) {
-    const int t = __builtin_amdgcn_readlane(tok, k), p = __builtin_amdgcn_readlane(pl, k);
-    if (t == kNoToken) return;  // only those follow
-    if (in) {
-      float g[8];
-      unpack8(*reinterpret_cast<const uint4*>(a.d_out + (int64_t)p * a.d + c), g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] += g[j];
-    }
-    const int next = k + 1 < n ? __builtin_amdgcn_readlane(tok, k + 1) : behind;
-    if (k + 1 < n && next == t) continue;
-    const bool from = first == 0 && before == t, on = k + 1 == n && next == t;
-    if (in) {
-      if (!from && !on) {
-        finish(a, t, c, f);
-      } else {
-        float* o = a.part + ((int64_t)blockIdx.x * 2 + (from ? 0 : 1)) * a.d + c;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = f[j];
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = 0.f;
-    first = k + 1;
-  }
-}
-
 // The first place at or behind lo whose token is above tok.
 __device__ __forceinline__ int upper(const int32_t* __restrict__ sorted, int lo, int T, int tok) {
   int hi = T;
@@ -138,59 +208,212 @@ __device__ __forceinline__ int upper(const int32_t* __restrict__ sorted, int lo,
   return lo;
 }
 
-// Runs that span chunks, by the chunk in which they begin.  Sixteen waves take
-// a sixteenth of the chunks each; a lane has 8 columns.
-constexpr int kJoinWaves = 16, kJoinLanes = 64;
-
-__global__ __launch_bounds__(kJoinWaves * kJoinLanes) void k_embed_join(SumArgs a) {
-  __shared__ float lds[kJoinWaves][kJoinLanes][8];
-  const int begin = blockIdx.x * kChunk, end = begin + kChunk;
-  if (end >= a.T) return;  // nothing behind this chunk
-  const int tok = a.sorted[end - 1];
-  if (tok == kNoToken || a.sorted[end] != tok) return;
-  if (a.sorted[begin] == tok && begin > 0 && a.sorted[begin - 1] == tok) return;  // it began further up
-  const int last = (upper(a.sorted, end, a.T, tok) - 1) / kChunk;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// A chunk's runs, 512 columns.
+__device__ __forceinline__ void sum_chunk(const SumArgs& a, int chunk) {
+  constexpr int kAtOnce = 8;  // rows whose loads are on their way together
+  const int lane = threadIdx.x, begin = chunk * a.chunk, n = min(a.chunk, a.T - begin);
   const int c = blockIdx.y * kCols + lane * 8;
-  const int n = last - blockIdx.x + 1;
-  const int lo = (int)((int64_t)n * wave / kJoinWaves), hi = (int)((int64_t)n * (wave + 1) / kJoinWaves);
+  const int at = begin + (lane < n ? lane : n - 1);
+  const int tok = a.sorted[at], pl = a.place[at];
+  const int before = begin > 0 ? a.sorted[begin - 1] : -1;
+  const int behind = begin + n < a.T ? a.sorted[begin + n] : -1;
+  const bool in = c < a.d;
   float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (c < a.d)
-    for (int k = lo; k < hi; ++k) {
-      const float* p = a.part + ((int64_t)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * a.d + c;
+  bool from = before == __builtin_amdgcn_readlane(tok, 0);  // whether the run began in a chunk before
+  for (int k0 = 0; k0 < n; k0 += kAtOnce) {
+    if (__builtin_amdgcn_readlane(tok, k0) == kNoToken) return;  // only those follow
+    uint4 u[kAtOnce];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] += p[j];
+    for (int k = 0; k < kAtOnce; ++k) {
+      u[k] = make_uint4(0, 0, 0, 0);
+      const int p = __builtin_amdgcn_readlane(pl, min(k0 + k, n - 1));
+      if (in && k0 + k < n) u[k] = *reinterpret_cast<const uint4*>(a.d_out + (int64_t)p * a.d + c);
     }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) lds[wave][lane][j] = f[j];
-  __syncthreads();
-  if (wave == 0 && c < a.d) {
-    for (int w = 1; w < kJoinWaves; ++w)
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (k0 + k >= n) break;
+      const int t = __builtin_amdgcn_readlane(tok, k0 + k);
+      if (t == kNoToken) return;
+      float g[8];
+      unpack8(u[k], g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] += lds[w][lane][j];
-    finish(a, tok, c, f);
+      for (int j = 0; j < 8; ++j) f[j] += g[j];
+      const bool last = k0 + k + 1 == n;
+      const int next = last ? behind : __builtin_amdgcn_readlane(tok, min(k0 + k + 1, n - 1));
+      if (!last && next == t) continue;
+      const bool on = last && next == t;
+      if (in) {
+        if (!from && !on) {
+          finish(a, t, c, f);
+        } else {
+          float4* o = reinterpret_cast<float4*>(a.part + ((int64_t)chunk * 2 + (from ? 0 : 1)) * a.d + c);
+          o[0] = make_float4(f[0], f[1], f[2], f[3]);
+          o[1] = make_float4(f[4], f[5], f[6], f[7]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = 0.f;
+      from = false;
+    }
   }
 }
 
-// Zeros for the rows of tokens that do not occur.
-__global__ __launch_bounds__(256) void k_embed_clear(const int32_t* __restrict__ sorted, int T, int V, int d,
-                                                     uint16_t* __restrict__ d_table) {
-  for (int v = blockIdx.x; v < V; v += gridDim.x) {
-    const int at = T > 0 ? upper(sorted, 0, T, v - 1) : 0;
-    if (at < T && sorted[at] == v) continue;
-    for (int c = threadIdx.x * 8; c < d; c += 256 * 8)
-      *reinterpret_cast<uint4*>(d_table + (int64_t)v * d + c) = make_uint4(0, 0, 0, 0);
+// Zeros for the rows of 64 tokens that do not occur, 512 columns.
+__device__ __forceinline__ void clear_rows(const SumArgs& a, int V, int first) {
+  const int v = first + threadIdx.x, c = blockIdx.y * kCols + threadIdx.x * 8;
+  const int at = v < V ? upper(a.sorted, 0, a.T, v - 1) : 0;
+  unsigned long long none = __ballot(v < V && !(at < a.T && a.sorted[at] == v));
+  while (none) {
+    const int r = first + __ffsll((long long)none) - 1;
+    none &= none - 1;
+    if (c < a.d) *reinterpret_cast<uint4*>(a.d_table + (int64_t)r * a.d + c) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Workgroups of one wave: those of the chunks, and behind them those that clear.
+__global__ __launch_bounds__(64) void k_embed_sum(SumArgs a, int V, int chunks) {
+  if ((int)blockIdx.x < chunks)
+    sum_chunk(a, blockIdx.x);
+  else
+    clear_rows(a, V, (blockIdx.x - chunks) * 64);
+}
+
+// Runs that span chunks, by the chunk in which they begin.  A workgroup looks
+// through every gridDim.x-th chunk, a thread to each, and joins 128 columns of
+// the runs it finds: those of few shares by a wave each, those of many by all
+// its waves, a sixteenth of the shares to each.
+constexpr int kJoinWaves = 16, kJoinCols = 128, kJoinFew = 16;
+
+// Shares lo .. hi - 1 of a run that begins in chunk `first`, two columns.
+__device__ __forceinline__ float2 shares(const SumArgs& a, int first, int lo, int hi, int c) {
+  float2 f = make_float2(0.f, 0.f);
+#pragma unroll 8
+  for (int s = lo; s < hi; ++s) {
+    const float2 x = *reinterpret_cast<const float2*>(a.part + ((int64_t)(first + s) * 2 + (s == 0 ? 1 : 0)) * a.d + c);
+    f = make_float2(f.x + x.x, f.y + x.y);
+  }
+  return f;
+}
+__device__ __forceinline__ void finish2(const SumArgs& a, int tok, int c, const float2& f) {
+  uint32_t* o = reinterpret_cast<uint32_t*>(a.d_table + (int64_t)tok * a.d + c);
+  const uint32_t old = a.accumulate ? *o : 0u;
+  const float x = a.accumulate ? fmaf(f.x, a.scale, bf16_float(old & 0xFFFFu)) : f.x * a.scale;
+  const float y = a.accumulate ? fmaf(f.y, a.scale, bf16_float(old >> 16)) : f.y * a.scale;
+  *o = float_bf16(x) | float_bf16(y) << 16;
+}
+
+__global__ __launch_bounds__(64 * kJoinWaves) void k_embed_join(SumArgs a, int chunks) {
+  __shared__ float2 lds[kJoinWaves][64];
+  __shared__ int few[3 * 64 * kJoinWaves], many[3 * 64 * kJoinWaves];  // first chunk, shares, token
+  __shared__ int n_few, n_many;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.y * kJoinCols + lane * 2;
+  const bool in = c < a.d;
+  for (int64_t base = blockIdx.x; base < chunks; base += (int64_t)gridDim.x * blockDim.x) {
+    if (threadIdx.x == 0) n_few = n_many = 0;
+    __syncthreads();
+    const int64_t chunk = base + (int64_t)threadIdx.x * gridDim.x;
+    if (chunk < chunks && (chunk + 1) * a.chunk < a.T) {
+      const int begin = (int)chunk * a.chunk, end = begin + a.chunk;
+      const int tok = a.sorted[end - 1];
+      const bool goes_on = tok != kNoToken && a.sorted[end] == tok;
+      const bool came = a.sorted[begin] == tok && begin > 0 && a.sorted[begin - 1] == tok;
+      if (goes_on && !came) {
+        const int n = (upper(a.sorted, end, a.T, tok) - 1) / a.chunk - (int)chunk + 1;
+        int* to = n <= kJoinFew ? few + 3 * atomicAdd(&n_few, 1) : many + 3 * atomicAdd(&n_many, 1);
+        to[0] = (int)chunk;  // the lists' order changes no result
+        to[1] = n;
+        to[2] = tok;
+      }
+    }
+    __syncthreads();
+    for (int k = wave; k < n_few; k += kJoinWaves)
+      if (in) finish2(a, few[3 * k + 2], c, shares(a, few[3 * k], 0, few[3 * k + 1], c));
+    for (int k = 0; k < n_many; ++k) {
+      const int n = many[3 * k + 1];
+      float2 f = make_float2(0.f, 0.f);
+      if (in)
+        f = shares(a, many[3 * k], (int)((int64_t)n * wave / kJoinWaves), (int)((int64_t)n * (wave + 1) / kJoinWaves), c);
+      lds[wave][lane] = f;
+      __syncthreads();
+      if (wave == 0 && in) {
+#pragma unroll
+        for (int w = 1; w < kJoinWaves; ++w) f = make_float2(f.x + lds[w][lane].x, f.y + lds[w][lane].y);
+        finish2(a, many[3 * k + 2], c, f);
+      }
+      __syncthreads();
+    }
+    __syncthreads();  // the lists are read
   }
 }
 
 bool sizes_ok(int64_t V, int64_t d, int64_t T) {
-  return V >= 1 && V < ((int64_t)1 << 31) - 1 && d >= 1 && T >= 0 && T < ((int64_t)1 << 31) - 1024;
+  return V >= 1 && V < ((int64_t)1 << 31) - 1024 && d >= 1 && T >= 0 && T < ((int64_t)1 << 31) - 1024;
 }
-bool supported(int64_t d) { return d % 8 == 0 && d < ((int64_t)1 << 24); }
+bool supported(int64_t d) { return d % 8 == 0 && d < ((int64_t)1 << 20); }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-int64_t chunks_of(int64_t T) { return (T + kChunk - 1) / kChunk; }
+int chunk_of(int64_t T) { return T <= kShortMost ? kChunkShort : kChunkMost; }
+int64_t chunks_of(int64_t T) { return (T + chunk_of(T) - 1) / chunk_of(T); }
+int64_t tiles_of(int64_t T) { return (T + kTile - 1) / kTile; }
+
+// Digits of a token of 0 .. V: as few passes of at most 10 bits as there can be.
+struct Digits {
+  int passes, bits;
+};
+Digits digits_of(int64_t V) {
+  int all = 1;
+  while (V >> all) ++all;
+  const int passes = (all + 9) / 10;
+  return {passes, (all + passes - 1) / passes};
+}
+
+// Workspace of the gradient; returns its size.
+struct Sorting {
+  int32_t *sorted, *place, *sorted2, *place2, *counts;
+  float* part;
+};
+size_t carve(int64_t V, int64_t d, int64_t T, uint8_t* base, Sorting* s) {
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = up256(off + bytes);
+    return base ? base + o : nullptr;
+  };
+  const size_t list = (size_t)T * 4, more = T > kRankMost ? list : 0;
+  Sorting x;
+  x.sorted = reinterpret_cast<int32_t*>(take(list));
+  x.place = reinterpret_cast<int32_t*>(take(list));
+  x.sorted2 = reinterpret_cast<int32_t*>(take(more));
+  x.place2 = reinterpret_cast<int32_t*>(take(more));
+  x.counts = reinterpret_cast<int32_t*>(take(more ? ((size_t)4 << digits_of(V).bits) * (size_t)tiles_of(T) : 0));
+  x.part = reinterpret_cast<float*>(take((size_t)chunks_of(T) * 2 * (size_t)d * 4));
+  if (s) *s = x;
+  return off + 256;
+}
+
+void sort_tokens(const int32_t* tokens, int T, int V, const Sorting& s, hipStream_t st) {
+  if (T <= kRankMost) {
+    hipLaunchKernelGGL(k_embed_rank, dim3((unsigned)((T + 63) / 64)), dim3(64 * kRankWaves), 0, st, tokens, T, V, s.sorted,
+                       s.place);
+    return;
+  }
+  const Digits g = digits_of(V);
+  const int tiles = (int)tiles_of(T);
+  PassArgs p = {tokens, nullptr, nullptr, nullptr, s.counts, T, V, tiles, 0, 1 << g.bits};
+  for (int k = 0; k < g.passes; ++k) {
+    const bool to_first = (g.passes - 1 - k) % 2 == 0;  // the last pass ends in sorted, place
+    p.tok_out = to_first ? s.sorted : s.sorted2;
+    p.at_out = to_first ? s.place : s.place2;
+    hipLaunchKernelGGL(k_embed_count, dim3((unsigned)tiles), dim3(256), 0, st, p);
+    hipLaunchKernelGGL(k_embed_begin, dim3(1), dim3(1024), 0, st, s.counts, (int64_t)tiles << g.bits);
+    hipLaunchKernelGGL(k_embed_place, dim3((unsigned)tiles), dim3(kTile), 0, st, p);
+    p.tok = p.tok_out;
+    p.at = p.at_out;
+    p.shift += g.bits;
+  }
+}
 
 }  // namespace
 }  // namespace dllm
@@ -215,7 +438,7 @@ dllm_status dllm_embed(const uint16_t* table, int64_t V, int64_t d, const int32_
 
 size_t dllm_embed_backward_workspace_bytes(int64_t V, int64_t d, int64_t T) {
   if (!dllm::sizes_ok(V, d, T) || !dllm::supported(d)) return 0;
-  return 256 + 2 * dllm::up256((size_t)T * 4) + dllm::up256((size_t)dllm::chunks_of(T) * 2 * (size_t)d * 4);
+  return dllm::carve(V, d, T, nullptr, nullptr);
 }
 
 dllm_status dllm_embed_backward(const int32_t* tokens, int64_t T, const uint16_t* d_out, int64_t V, int64_t d,
@@ -231,21 +454,17 @@ dllm_status dllm_embed_backward(const int32_t* tokens, int64_t T, const uint16_t
       dllm::overlaps(d_table, n, workspace, need))
     return DLLM_ERR_INVALID_ARG;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  uint8_t* w = reinterpret_cast<uint8_t*>(workspace);
-  int32_t* sorted = reinterpret_cast<int32_t*>(w);
-  int32_t* place = reinterpret_cast<int32_t*>(w + dllm::up256((size_t)T * 4));
-  float* part = reinterpret_cast<float*>(w + 2 * dllm::up256((size_t)T * 4));
-  if (T > 0)
-    hipLaunchKernelGGL(dllm::k_embed_rank, dim3((unsigned)((T + 63) / 64)), dim3(64), 0, st, tokens, (int)T, (int)V,
-                       sorted, place);
-  if (!accumulate)
-    hipLaunchKernelGGL(dllm::k_embed_clear, dim3((unsigned)(V < (1 << 18) ? V : 1 << 18)), dim3(256), 0, st, sorted,
-                       (int)T, (int)V, (int)d, d_table);
-  if (T > 0) {
-    const dllm::SumArgs a = {sorted, place, (int)T, (int)d, d_out, scale, accumulate, d_table, part};
-    const dim3 grid((unsigned)dllm::chunks_of(T), (unsigned)((d + dllm::kCols - 1) / dllm::kCols));
-    hipLaunchKernelGGL(dllm::k_embed_sum, grid, dim3(64), 0, st, a);
-    hipLaunchKernelGGL(dllm::k_embed_join, grid, dim3(dllm::kJoinWaves * dllm::kJoinLanes), 0, st, a);
+  dllm::Sorting w;
+  dllm::carve(V, d, T, reinterpret_cast<uint8_t*>(workspace), &w);
+  if (T > 0) dllm::sort_tokens(tokens, (int)T, (int)V, w, st);
+  const int64_t chunks = dllm::chunks_of(T), clears = accumulate ? 0 : (V + 63) / 64;
+  const dllm::SumArgs a = {w.sorted, w.place, (int)T, (int)d, dllm::chunk_of(T), d_out, scale, accumulate, d_table, w.part};
+  const unsigned cols = (unsigned)((d + dllm::kCols - 1) / dllm::kCols);
+  if (chunks + clears > 0)
+    hipLaunchKernelGGL(dllm::k_embed_sum, dim3((unsigned)(chunks + clears), cols), dim3(64), 0, st, a, (int)V, (int)chunks);
+  if (chunks > 1) {
+    const dim3 grid((unsigned)(chunks < 64 ? chunks : 64), (unsigned)((d + dllm::kJoinCols - 1) / dllm::kJoinCols));
+    hipLaunchKernelGGL(dllm::k_embed_join, grid, dim3(64 * dllm::kJoinWaves), 0, st, a, (int)chunks);
   }
   return hipGetLastError() == hipSuccess ? DLLM_OK : DLLM_ERR_HIP;
 }

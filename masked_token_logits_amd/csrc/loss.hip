@@ -107,7 +107,7 @@ struct PrepareArgs {
   float* bias;
   uint32_t* flip;
   int32_t* tgt;
-  float* at_tgt;
+  float *at_tgt, *left;
   uint16_t* d_hidden;
 };
 
@@ -139,7 +139,9 @@ __global__ __launch_bounds__(256) void k_loss_prepare(PrepareArgs a) {
         a.bias[i] = __builtin_amdgcn_logf(fabsf(c)) - lse * kLog2eF;
         a.flip[i] = c < 0.f ? 0x80008000u : 0u;
         a.tgt[i] = t;
-        a.at_tgt[i] = c * expm1f(z - lse);
+        const float at = c * expm1f(z - lse);
+        a.at_tgt[i] = at;
+        a.left[i] = at - bf16_float(float_bf16(at));
       }
     } else if (i < Mp) {
       for (int c = 8 * lane; c < a.dp; c += 8 * 64) *reinterpret_cast<uint4*>(a.rows + (int64_t)i * a.dp + c) = none;
@@ -148,6 +150,7 @@ __global__ __launch_bounds__(256) void k_loss_prepare(PrepareArgs a) {
         a.flip[i] = 0u;
         a.tgt[i] = -1;
         a.at_tgt[i] = 0.f;
+        a.left[i] = 0.f;
       }
     }
     if (a.d_hidden && i < a.L && !a.counted[i])
@@ -172,9 +175,10 @@ struct Rows {
   float* bias;
   uint32_t* flip;
   int32_t* tgt;
-  float* at_tgt;
+  float *at_tgt, *left;
   uint16_t *zeros, *rows, *dz;
   float* acc;
+  uint16_t* fix;
 };
 
 // Workspace of both directions; returns its size.
@@ -200,9 +204,11 @@ size_t carve(int64_t d, int64_t L, int64_t piece, uint8_t* base, Rows* r) {
     x.flip = reinterpret_cast<uint32_t*>(take(rows * 4));
     x.tgt = reinterpret_cast<int32_t*>(take(rows * 4));
     x.at_tgt = reinterpret_cast<float*>(take(rows * 4));
+    x.left = reinterpret_cast<float*>(take(rows * 4));
     x.zeros = reinterpret_cast<uint16_t*>(take(16));
     x.rows = reinterpret_cast<uint16_t*>(take(rows * (size_t)loss_padded(d) * 2));
     x.dz = reinterpret_cast<uint16_t*>(take(rows * (size_t)piece * 2));
+    x.fix = reinterpret_cast<uint16_t*>(take((size_t)(L < kLossFew ? L : kLossFew) * (size_t)d * 2));
     x.acc = reinterpret_cast<float*>(take((size_t)loss_shares(L, d, piece) * kLossTile * kLossTile * 4));
   }
   if (r) *r = x;
@@ -347,19 +353,41 @@ dllm_status dllm_loss_backward(const dllm_loss* p, const float* lse, const float
   plan.tile_rows = dllm::kLargeBM;
   if (dllm::launch_mask_compact(r.counted, 0, L, 0, plan, r.idx, r.ctr, st) != hipSuccess) return DLLM_ERR_HIP;
   const int dp = (int)dllm::loss_padded(d), grid = cus < dllm::kLossGrid ? cus : dllm::kLossGrid;
-  const dllm::PrepareArgs pa = {p->W_lm, p->hidden, r.counted, p->targets, p->weights, grad,  lse,      r.idx,   r.ctr, (int)L,
-                                (int)d,  dp,        r.rows,    r.zeros,    r.bias,     r.flip, r.tgt, r.at_tgt, d_hidden};
+  const dllm::PrepareArgs pa = {p->W_lm, p->hidden, r.counted, p->targets, p->weights, grad,  lse,      r.idx,  r.ctr,   (int)L,
+                                (int)d,  dp,        r.rows,    r.zeros,    r.bias,     r.flip, r.tgt, r.at_tgt, r.left, d_hidden};
   hipLaunchKernelGGL(dllm::k_loss_prepare, dim3(dllm::grid_for(dllm::loss_padded(L) / 4, 65536)), dim3(256), 0, st, pa);
-  dllm::GradArgs a = {p->W_lm, r.zeros,  r.rows, r.idx, r.ctr,  r.bias, r.flip, r.tgt, r.at_tgt, r.dz, r.acc,
-                      d_hidden, d_W,     piece,  (int)V, (int)d, dp,    (int)L, 0,     0,        0,    accumulate};
+  dllm::GradArgs a = {};
+  a.W = p->W_lm;
+  a.zeros = r.zeros;
+  a.rows = r.rows;
+  a.idx = r.idx;
+  a.ctr = r.ctr;
+  a.bias = r.bias;
+  a.flip = r.flip;
+  a.tgt = r.tgt;
+  a.at_tgt = r.at_tgt;
+  a.left = r.left;
+  a.dz = r.dz;
+  a.acc = r.acc;
+  a.fix = r.fix;
+  a.d_hidden = d_hidden;
+  a.d_W = d_W;
+  a.ldz = piece;
+  a.V = (int)V;
+  a.d = (int)d;
+  a.dp = dp;
+  a.L = (int)L;
+  a.accumulate = accumulate;
   for (int64_t v = 0; v < V; v += piece) {
     a.v0 = (int)v;
     a.n = (int)(V - v < piece ? V - v : piece);
     a.first = v == 0;
     if (dllm::launch_loss_dz(a, grid, st) != hipSuccess) return DLLM_ERR_HIP;
     if (d_hidden && dllm::launch_loss_d_hidden(a, grid, st) != hipSuccess) return DLLM_ERR_HIP;
+    if (d_W && dllm::launch_loss_targets(a, st) != hipSuccess) return DLLM_ERR_HIP;
     if (d_W && dllm::launch_loss_d_W(a, grid, st) != hipSuccess) return DLLM_ERR_HIP;
   }
+  if (d_W && dllm::launch_loss_put(a, st) != hipSuccess) return DLLM_ERR_HIP;
   if (d_hidden && dllm::launch_loss_join(a, grid, st) != hipSuccess) return DLLM_ERR_HIP;
   return hipGetLastError() == hipSuccess ? DLLM_OK : DLLM_ERR_HIP;
 }

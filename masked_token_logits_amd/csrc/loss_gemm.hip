@@ -603,32 +603,25 @@ __global__ __launch_bounds__(NT) void k_loss_join(GradArgs a, int grid) {
   const int n_rt = (M + BT - 1) / BT, n_ct = (a.d + BT - 1) / BT;
   const int64_t tiles = (int64_t)n_rt * n_ct, cuts = min(loss_cuts(tiles, a.ldz), (int64_t)grid);
   const Lane at;
-  constexpr int kParts = 16;  // of a tile: one (fr, fv)
+  constexpr int kParts = 64;  // of a tile: one (fr, fv, j)
   for (int64_t e = blockIdx.x; e < tiles * kParts; e += gridDim.x) {
     const int64_t t = e / kParts;
-    const int part = (int)(e - t * kParts), fr = part >> 2, fv = part & 3;
+    const int part = (int)(e - t * kParts), fr = part >> 4, fv = (part >> 2) & 3, j = part & 3;
     int rt, ct;
     item_coords((int)t, n_rt, n_ct, rt, ct);
-    const int r = rt * BT + at.row(fr);
+    const int r = rt * BT + at.row(fr), c = ct * BT + at.col(fv, j);
     const int64_t g0 = t * cuts / tiles, g1 = ((t + 1) * cuts + tiles - 1) / tiles;
-    if (r >= M) continue;
-    const int64_t o = (int64_t)a.idx[r] * a.d;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4* p = reinterpret_cast<const float4*>(a.acc) + (g0 + t) * (BT * BT / 4) + (part * 4 + j) * NT + threadIdx.x;
-      float4 s = *p;
-      for (int64_t g = g0 + 1; g < g1; ++g) {
-        p += BT * BT / 4;
-        s.x += p->x;
-        s.y += p->y;
-        s.z += p->z;
-        s.w += p->w;
-      }
-      const int c = ct * BT + at.col(fv, j);
-      if (c < a.d)
-        *reinterpret_cast<uint2*>(a.d_hidden + o + c) =
-            make_uint2(float_bf16(s.x) | float_bf16(s.y) << 16, float_bf16(s.z) | float_bf16(s.w) << 16);
-    }
+    if (r >= M || c >= a.d) continue;
+    // what dz's rounding left of the target's entry, times its row of W
+    const float left = a.left[r];
+    const uint2 w = *reinterpret_cast<const uint2*>(a.W + (int64_t)a.tgt[r] * a.d + c);
+    float4 s = make_float4(left * bf16_float(w.x & 0xFFFF), left * bf16_float(w.x >> 16), left * bf16_float(w.y & 0xFFFF),
+                           left * bf16_float(w.y >> 16));
+    const float4* p = reinterpret_cast<const float4*>(a.acc) + (g0 + t) * (BT * BT / 4) + part * NT + threadIdx.x;
+#pragma unroll 4
+    for (int64_t g = g0; g < g1; ++g, p += BT * BT / 4) s = make_float4(s.x + p->x, s.y + p->y, s.z + p->z, s.w + p->w);
+    *reinterpret_cast<uint2*>(a.d_hidden + (int64_t)a.idx[r] * a.d + c) =
+        make_uint2(float_bf16(s.x) | float_bf16(s.y) << 16, float_bf16(s.z) | float_bf16(s.w) << 16);
   }
 }
 
@@ -717,6 +710,52 @@ __global__ __launch_bounds__(NT, 1) void k_loss_d_W(GradArgs a) {
   run_tiles<true, false, true>(lds, work);
 }
 
+// Few rows: the rows of d_W that are targets, with what dz's rounding left of
+// their entries.  They are summed anew, in fp32 and the order of the rows, into
+// `fix` before the piece's product is stored (accumulated, the product's old
+// values are gone behind it) and take their places at the end.  A workgroup of
+// one wave has 512 columns of one target, which the first row with it answers for.
+__device__ __forceinline__ bool first_with(const GradArgs& a, int M, int i, int v) {
+  bool before = false;
+  for (int k = threadIdx.x & 63; k < M; k += 64) before |= k < i && a.tgt[k] == v;
+  return __ballot(before) == 0;
+}
+
+__global__ __launch_bounds__(64) void k_loss_targets(GradArgs a) {
+  const int M = min(a.ctr[0], a.L), i = blockIdx.x, c = blockIdx.y * 512 + threadIdx.x * 8;
+  if (M > kLossFew || i >= M) return;
+  const int v = a.tgt[i] - a.v0;
+  if (v < 0 || v >= a.n || !first_with(a, M, i, a.tgt[i])) return;
+  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int m0 = 0; m0 < M; m0 += 64) {
+    const int m = m0 + threadIdx.x;
+    float z = 0.f;
+    if (m < M) z = bf16_float(a.dz[(int64_t)m * a.ldz + v]) + (a.tgt[m] - a.v0 == v ? a.left[m] : 0.f);
+#pragma unroll 8
+    for (int k = 0; k < min(64, M - m0); ++k) {
+      const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(z), k));
+      float h[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (c < a.d) unpack8(*reinterpret_cast<const uint4*>(a.rows + (int64_t)(m0 + k) * a.dp + c), h);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = fmaf(w, h[j], f[j]);
+    }
+  }
+  if (c >= a.d) return;
+  if (a.accumulate) {
+    float old[8];
+    unpack8(*reinterpret_cast<const uint4*>(a.d_W + (int64_t)(a.v0 + v) * a.d + c), old);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] += old[j];
+  }
+  *reinterpret_cast<uint4*>(a.fix + (int64_t)i * a.d + c) = pack8(f);
+}
+
+__global__ __launch_bounds__(64) void k_loss_put(GradArgs a) {
+  const int M = min(a.ctr[0], a.L), i = blockIdx.x, c = blockIdx.y * 512 + threadIdx.x * 8;
+  if (M > kLossFew || i >= M || !first_with(a, M, i, a.tgt[i]) || c >= a.d) return;
+  *reinterpret_cast<uint4*>(a.d_W + (int64_t)a.tgt[i] * a.d + c) = *reinterpret_cast<const uint4*>(a.fix + (int64_t)i * a.d + c);
+}
+
 }  // namespace
 
 hipError_t launch_loss_dz(const GradArgs& a, int grid, hipStream_t stream) {
@@ -732,6 +771,14 @@ hipError_t launch_loss_d_hidden(const GradArgs& a, int grid, hipStream_t stream)
 }
 hipError_t launch_loss_d_W(const GradArgs& a, int grid, hipStream_t stream) {
   hipLaunchKernelGGL(k_loss_d_W, dim3(grid), dim3(NT), 0, stream, a);
+  return hipGetLastError();
+}
+hipError_t launch_loss_targets(const GradArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL(k_loss_targets, dim3(a.L < kLossFew ? a.L : kLossFew, (a.d + 511) / 512), dim3(64), 0, stream, a);
+  return hipGetLastError();
+}
+hipError_t launch_loss_put(const GradArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL(k_loss_put, dim3(a.L < kLossFew ? a.L : kLossFew, (a.d + 511) / 512), dim3(64), 0, stream, a);
   return hipGetLastError();
 }
 hipError_t launch_loss_join(const GradArgs& a, int grid, hipStream_t stream) {

@@ -14,6 +14,13 @@ constexpr int kLossGrid = 256;  // most workgroups of a product
 
 inline int64_t loss_padded(int64_t n) { return (n + kLossStep - 1) / kLossStep * kLossStep; }
 
+// dz is rounded to bf16, and what that leaves of a row's largest entry, the
+// target's, is given back to the fp32 sums: to d_hidden always (one more row of W
+// each), to d_W with up to so many rows.  With more, d_W's errors average out to
+// 1.41 times the output's own rounding; with few, single rows decide them (102
+// rows: up to 1.6 times).
+constexpr int kLossFew = 256;
+
 // The backward pass of one vocabulary piece.  Rows are the counted positions
 // in ascending order, M = ctr[0] of them, filled up to Mp with rows that have
 // no gradient.
@@ -26,8 +33,10 @@ struct GradArgs {
   const uint32_t* flip;     // [Mp] the sign bits of two bf16 where c < 0
   const int32_t* tgt;       // [Mp] the target, -1 behind M
   const float* at_tgt;      // [Mp] dz there
+  const float* left;        // [Mp] what its rounding to bf16 leaves of it
   uint16_t* dz;             // [Mp, ldz]: the piece's gradient of the logits
   float* acc;               // the rows' gradient over the pieces so far, in shares of a tile each
+  uint16_t* fix;            // [kLossFew, d] few rows: d_W's rows of the targets
   uint16_t *d_hidden, *d_W;
   int64_t ldz;              // entries of a whole piece
   int V, d, dp, L;
@@ -39,6 +48,8 @@ struct GradArgs {
 hipError_t launch_loss_dz(const GradArgs& a, int grid, hipStream_t stream);        // dz
 hipError_t launch_loss_d_hidden(const GradArgs& a, int grid, hipStream_t stream);  // acc += dz . W
 hipError_t launch_loss_d_W(const GradArgs& a, int grid, hipStream_t stream);       // d_W = dz^T . rows
+hipError_t launch_loss_targets(const GradArgs& a, hipStream_t stream);             // few rows: fix, before d_W
+hipError_t launch_loss_put(const GradArgs& a, hipStream_t stream);                 // and behind it
 hipError_t launch_loss_join(const GradArgs& a, int grid, hipStream_t stream);      // d_hidden = sum of acc's shares
 
 // How d_hidden's product is cut: its tiles' stages as one line, dealt to so

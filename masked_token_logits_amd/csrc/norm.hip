@@ -149,6 +149,18 @@ struct NormGrads {
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, NormGrads g) {
   __shared__ float lds[2 * (THREADS / 64)][3];
+  // The weights and the gate of a thread's pieces, its own: loaded from memory
+  // they would wait, in order, behind the next row's loads.
+  __shared__ uint4 kept[3][kPieces][THREADS];
+  auto keep = [&](int which, const uint16_t* p) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int c = 8 * (threadIdx.x + i * THREADS);
+      if (c < a.d) kept[which][i][threadIdx.x] = load8(p + c);
+    }
+  };
+  if (a.pre) keep(0, a.pre);
+  if (a.post) keep(1, a.post);
   const float per = 1.0f / (float)a.d;
   int64_t t0, t1;
   if (g.chunks > 0) {
@@ -161,13 +173,13 @@ __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, 
   }
   float s_pre[kPieces][8] = {}, s_post[kPieces][8] = {}, s_gate[kPieces][8] = {};
   int64_t run_end = g.chunks > 0 ? t1 : t0 + a.group_rows;
-  for (int64_t t = t0; t < t1; ++t) {
-    const uint16_t* gate = a.gate ? a.gate + (t / a.group_rows) * a.d : nullptr;
-    uint4 xu[kPieces], yu[kPieces], nu[kPieces], du[kPieces];
+  uint4 xu[kPieces], yu[kPieces], nu[kPieces], du[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) xu[i] = yu[i] = nu[i] = du[i] = make_uint4(0, 0, 0, 0);
+  auto load = [&](int64_t t) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int c = 8 * (threadIdx.x + i * THREADS);
-      xu[i] = yu[i] = nu[i] = du[i] = make_uint4(0, 0, 0, 0);
       if (c < a.d) {
         const int64_t o = t * a.d + c;
         if (g.d_n) xu[i] = load8(a.x + o);
@@ -175,6 +187,17 @@ __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, 
         if (g.d_n) nu[i] = load8(g.d_n + o);
         if (g.d_x_out) du[i] = load8(g.d_x_out + o);
       }
+    }
+  };
+  if (t0 < t1) load(t0);
+  int64_t run = t0 / a.group_rows;
+  if (a.gate) keep(2, a.gate + run * a.d);
+  const bool gate = a.gate != nullptr;
+  for (int64_t t = t0; t < t1; ++t) {
+    if (gate && g.chunks == 0 && t == run_end) {
+      ++run;
+      run_end += a.group_rows;
+      keep(2, a.gate + run * a.d);
     }
     float x[kPieces][8], y[kPieces][8], dn[kPieces][8], dx[kPieces][8];
 #pragma unroll
@@ -184,6 +207,7 @@ __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, 
       unpack8(nu[i], dn[i]);
       unpack8(du[i], dx[i]);
     }
+    if (t + 1 < t1) load(t + 1);  // on their way while this row is worked on
     // sums of x'^2, of D x' and of y^2
     float s[3] = {0.f, 0.f, 0.f};
     float w[kPieces][8];
@@ -191,7 +215,7 @@ __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, 
     for (int i = 0; i < kPieces; ++i) {
       const int c = 8 * (threadIdx.x + i * THREADS);
       if (c < a.d && a.pre) {
-        unpack8(load8(a.pre + c), w[i]);
+        unpack8(kept[0][i][threadIdx.x], w[i]);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) w[i][j] = 0.f;
@@ -227,8 +251,8 @@ __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, 
         const int c = 8 * (threadIdx.x + i * THREADS);
         if (c < a.d) {
           float p[8], gt[8];
-          if (a.post) unpack8(load8(a.post + c), p);
-          if (gate) unpack8(load8(gate + c), gt);
+          if (a.post) unpack8(kept[1][i][threadIdx.x], p);
+          if (gate) unpack8(kept[2][i][threadIdx.x], gt);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float yq = y[i][j] * q;
@@ -260,13 +284,13 @@ __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, 
           store8(g.d_y + t * a.d + c, pack8(dx[i]));
         }
       }
-      if (t + 1 == run_end && g.chunks == 0) {
+      if (g.chunks == 0 && t + 1 == run_end) {
         if (g.d_gate) {
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
             const int c = 8 * (threadIdx.x + i * THREADS);
             if (c < a.d) {
-              float* o = g.d_gate + (t / a.group_rows) * a.d + c;
+              float* o = g.d_gate + run * a.d + c;
 #pragma unroll
               for (int j = 0; j < 8; ++j) o[j] = s_gate[i][j];
             }
@@ -274,7 +298,6 @@ __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, 
             for (int j = 0; j < 8; ++j) s_gate[i][j] = 0.f;
           }
         }
-        run_end += a.group_rows;
       }
     }
     if (THREADS > 64 && !(a.y && a.post)) __syncthreads();  // one slot only: the next row's sums wait
@@ -294,29 +317,36 @@ __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, 
   }
 }
 
-// out[run, c] = sum of part[run * count .. + count - 1, c]: four waves take a
-// quarter of the workgroups' shares each, in order.
+// out[run, c] = sum of part[run * count .. + count - 1, c]: sixteen waves take
+// a sixteenth of the workgroups' shares each, in order.
+constexpr int kSumWaves = 16;
+
 struct Sums {
   const float* part[3];
   float* out[3];
   int count[3];
 };
 
-__global__ __launch_bounds__(256) void k_norm_sums(Sums s, int d) {
-  __shared__ float lds[4][64];
+__global__ __launch_bounds__(64 * kSumWaves) void k_norm_sums(Sums s, int d) {
+  __shared__ float lds[kSumWaves][64];
   const int which = blockIdx.z, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * 64 + lane;
   const int n = s.count[which], run = blockIdx.y;
   if (!s.part[which] || (which < 2 && run > 0)) return;
-  const int lo = (int)((int64_t)n * wave / 4), hi = (int)((int64_t)n * (wave + 1) / 4);
+  const int lo = (int)((int64_t)n * wave / kSumWaves), hi = (int)((int64_t)n * (wave + 1) / kSumWaves);
   float v = 0.f;
   if (c < d) {
     const float* p = s.part[which] + (int64_t)run * n * d + c;
+#pragma unroll 8
     for (int k = lo; k < hi; ++k) v += p[(int64_t)k * d];
   }
   lds[wave][lane] = v;
   __syncthreads();
-  if (wave == 0 && c < d) s.out[which][(int64_t)run * d + c] = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
+  if (wave == 0 && c < d) {
+#pragma unroll
+    for (int w = 1; w < kSumWaves; ++w) v += lds[w][lane];
+    s.out[which][(int64_t)run * d + c] = v;
+  }
 }
 
 // How the tokens of a backward call are dealt to workgroups.
@@ -326,7 +356,7 @@ struct Deal {
   int chunks;      // workgroups to a gate's run, 0 = a workgroup has whole runs
 };
 
-constexpr int64_t kDealTo = 1024;
+constexpr int64_t kDealTo = 512;  // two workgroups to a compute unit, as many as fit beside each other
 
 Deal deal_tokens(int64_t T, int64_t runs) {  // T >= 1
   const int64_t n = runs > 0 ? runs : 1, rows = T / n;
@@ -468,7 +498,7 @@ dllm_status dllm_residual_norm_backward(const dllm_norm* p, const uint16_t* x, c
                              {d_pre, d_post, d_gate},
                              {(int)deal.groups, (int)deal.groups, deal.chunks}};
     const dim3 grid((unsigned)((p->d + 63) / 64), (unsigned)(g.part_gate ? groups : 1), g.part_gate ? 3 : 2);
-    hipLaunchKernelGGL(dllm::k_norm_sums, grid, dim3(256), 0, s, sums, (int)p->d);
+    hipLaunchKernelGGL(dllm::k_norm_sums, grid, dim3(64 * dllm::kSumWaves), 0, s, sums, (int)p->d);
   }
   return hipGetLastError() == hipSuccess ? DLLM_OK : DLLM_ERR_HIP;
 }

@@ -68,6 +68,10 @@ CASES = [  # T, V, d, scale, share of the last token
     (4096, 5000, 72, 1.0, 0.5),
     (20001, 40, 16, 1.0, 0.8),     # long runs
     (9000, 130000, 24, 1.0, 0.1),  # many rows without a token
+    (16384, 700, 8, 1.0, 0.2),     # the most that are ranked in one launch
+    (16385, 700, 8, 1.0, 0.2),     # sorted by one digit
+    (18000, 1500, 16, 2.0, 0.0),   # by two
+    (17001, 1 << 21, 8, 1.0, 0.5), # by three, most rows without a token
 ]
 
 

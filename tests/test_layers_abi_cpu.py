@@ -99,11 +99,11 @@ def _embed_backward(**kw):
 
 
 def test_embed_refused():
-    sizes = (dict(V=0), dict(V=(1 << 31) - 1), dict(d=0), dict(T=-1), dict(T=(1 << 31) - 1024), dict(scale=float("nan")),
+    sizes = (dict(V=0), dict(V=(1 << 31) - 1024), dict(d=0), dict(T=-1), dict(T=(1 << 31) - 1024), dict(scale=float("nan")),
              dict(scale=float("-inf")))
     for kw in sizes + (dict(table=None), dict(tokens=None), dict(out=None), dict(out=_at(0) + 16), dict(out=_at(1) - 16)):
         assert _embed(**kw) == E.DLLM_ERR_INVALID_ARG, kw
-    for kw in (dict(d=60), dict(d=1 << 24), dict(table=_at(0) + 8), dict(out=_at(2) + 2), dict(tokens=_at(1) + 2)):
+    for kw in (dict(d=60), dict(d=1 << 20), dict(table=_at(0) + 8), dict(out=_at(2) + 2), dict(tokens=_at(1) + 2)):
         assert _embed(**kw) == E.DLLM_ERR_UNSUPPORTED, kw
     assert _embed(T=0, tokens=None, out=None) == E.DLLM_OK
     for kw in sizes + (dict(tokens=None), dict(d_out=None), dict(d_table=None), dict(accumulate=2), dict(accumulate=-1),
