@@ -56,10 +56,12 @@ constexpr int kRankMost = 16384, kRankWaves = 16;
 
 __global__ __launch_bounds__(64 * kRankWaves) void k_embed_rank(const int32_t* __restrict__ tokens, int T, int V,
                                                                 int32_t* __restrict__ sorted,
-                                                                int32_t* __restrict__ place) {
+                                                                int32_t* __restrict__ place,
+                                                                int32_t* __restrict__ runs) {
   __shared__ int part[kRankWaves][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int first = blockIdx.x * 64, i = first + lane;
+  if (blockIdx.x == 0 && threadIdx.x < 2) runs[threadIdx.x] = 0;
   const int mine = i < T ? known(tokens[i], V) : kNoToken;
   const int lo = (int)((int64_t)T * wave / kRankWaves), hi = (int)((int64_t)T * (wave + 1) / kRankWaves);
   int rank = 0;
@@ -92,6 +94,7 @@ struct PassArgs {
   const int32_t *tok, *at;  // at: the places so far; null = tokens in their own order
   int32_t *tok_out, *at_out;
   int32_t* counts;          // [bins][tiles]
+  int32_t* runs;            // [2]: cleared for the sums
   int T, V, tiles, shift, bins;
 };
 
@@ -102,6 +105,7 @@ __device__ __forceinline__ int digit(const PassArgs& p, int tok) {
 
 __global__ __launch_bounds__(256) void k_embed_count(PassArgs p) {
   __shared__ int hist[kBinsMost];
+  if (blockIdx.x == 0 && threadIdx.x < 2) p.runs[threadIdx.x] = 0;
   for (int b = threadIdx.x; b < p.bins; b += 256) hist[b] = 0;
   __syncthreads();
 #pragma unroll
@@ -113,26 +117,29 @@ __global__ __launch_bounds__(256) void k_embed_count(PassArgs p) {
   for (int b = threadIdx.x; b < p.bins; b += 256) p.counts[(int64_t)b * p.tiles + blockIdx.x] = hist[b];
 }
 
-// Where each digit's tokens of each tile begin: exclusive sums, in place, 16 to
-// a thread.
+// Where each digit's tokens of each tile begin: exclusive sums, in place.  A
+// wave takes 1024 in a row, 64 at a time.
 __global__ __launch_bounds__(1024) void k_embed_begin(int32_t* __restrict__ counts, int64_t n) {
   __shared__ int part[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int carry = 0;
   for (int64_t base = 0; base < n; base += 16 * 1024) {
-    const int64_t i = base + threadIdx.x * 16;
-    int v[16], mine = 0;
+    const int64_t i = base + wave * 1024 + lane;
+    int v[16], run = 0;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = i + k < n ? counts[i + k] : 0;
+    for (int k = 0; k < 16; ++k) v[k] = i + 64 * k < n ? counts[i + 64 * k] : 0;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) mine += v[k];
-    int sum = mine;
+    for (int k = 0; k < 16; ++k) {
+      int sum = v[k];
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(sum, off);
-      if (lane >= off) sum += o;
+      for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(sum, off);
+        if (lane >= off) sum += o;
+      }
+      v[k] = run + sum - v[k];
+      run += __shfl(sum, 63);
     }
-    if (lane == 63) part[wave] = sum;
+    if (lane == 0) part[wave] = run;
     __syncthreads();
     int before = carry, all = carry;
 #pragma unroll
@@ -140,12 +147,9 @@ __global__ __launch_bounds__(1024) void k_embed_begin(int32_t* __restrict__ coun
       before += w < wave ? part[w] : 0;
       all += part[w];
     }
-    int run = before + sum - mine;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      if (i + k < n) counts[i + k] = run;
-      run += v[k];
-    }
+    for (int k = 0; k < 16; ++k)
+      if (i + 64 * k < n) counts[i + 64 * k] = before + v[k];
     carry = all;
     __syncthreads();
   }
@@ -175,6 +179,16 @@ __global__ __launch_bounds__(kTile) void k_embed_place(PassArgs p) {
   }
 }
 
+// Runs that span chunks: where a run begins, its shares and its token.
+struct Run {
+  int first, shares, tok;
+};
+struct Runs {
+  int32_t* count;   // [2]: runs of few shares, runs of many
+  Run *few, *many;  // [chunks] each; their order changes no result
+};
+constexpr int kFewShares = 16;
+
 struct SumArgs {
   const int32_t *sorted, *place;
   int T, d, chunk;
@@ -182,6 +196,7 @@ struct SumArgs {
   float scale;
   int accumulate;
   uint16_t* d_table;
+  Runs runs;
   float* part;  // [chunks][2][d]: a run that comes from the chunk before, and one that begins here and goes on
 };
 
@@ -242,6 +257,11 @@ __device__ __forceinline__ void sum_chunk(const SumArgs& a, int chunk) {
       const int next = last ? behind : __builtin_amdgcn_readlane(tok, min(k0 + k + 1, n - 1));
       if (!last && next == t) continue;
       const bool on = last && next == t;
+      if (on && !from && blockIdx.y == 0 && lane == 0) {
+        const int shares = (upper(a.sorted, begin + n, a.T, t) - 1) / a.chunk - chunk + 1;
+        const bool few = shares <= kFewShares;
+        (few ? a.runs.few : a.runs.many)[atomicAdd(a.runs.count + (few ? 0 : 1), 1)] = {chunk, shares, t};
+      }
       if (in) {
         if (!from && !on) {
           finish(a, t, c, f);
@@ -278,11 +298,10 @@ __global__ __launch_bounds__(64) void k_embed_sum(SumArgs a, int V, int chunks) 
     clear_rows(a, V, (blockIdx.x - chunks) * 64);
 }
 
-// Runs that span chunks, by the chunk in which they begin.  A workgroup looks
-// through every gridDim.x-th chunk, a thread to each, and joins 128 columns of
-// the runs it finds: those of few shares by a wave each, those of many by all
-// its waves, a sixteenth of the shares to each.
-constexpr int kJoinWaves = 16, kJoinCols = 128, kJoinFew = 16;
+// The runs that span chunks.  Those of many shares take a workgroup for each 128
+// columns, its sixteen waves a sixteenth of the shares each; those of few a
+// wave for each 128 columns.
+constexpr int kJoinWaves = 16, kJoinCols = 128;
 
 // Shares lo .. hi - 1 of a run that begins in chunk `first`, two columns.
 __device__ __forceinline__ float2 shares(const SumArgs& a, int first, int lo, int hi, int c) {
@@ -302,48 +321,29 @@ __device__ __forceinline__ void finish2(const SumArgs& a, int tok, int c, const 
   *o = float_bf16(x) | float_bf16(y) << 16;
 }
 
-__global__ __launch_bounds__(64 * kJoinWaves) void k_embed_join(SumArgs a, int chunks) {
+__global__ __launch_bounds__(64 * kJoinWaves) void k_embed_join(SumArgs a) {
   __shared__ float2 lds[kJoinWaves][64];
-  __shared__ int few[3 * 64 * kJoinWaves], many[3 * 64 * kJoinWaves];  // first chunk, shares, token
-  __shared__ int n_few, n_many;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.y * kJoinCols + lane * 2;
-  const bool in = c < a.d;
-  for (int64_t base = blockIdx.x; base < chunks; base += (int64_t)gridDim.x * blockDim.x) {
-    if (threadIdx.x == 0) n_few = n_many = 0;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, blocks = (a.d + kJoinCols - 1) / kJoinCols;
+  const int64_t many = (int64_t)a.runs.count[1] * blocks, few = (int64_t)a.runs.count[0] * blocks;
+  for (int64_t k = blockIdx.x; k < many; k += gridDim.x) {
+    const Run r = a.runs.many[k / blocks];
+    const int c = (int)(k % blocks) * kJoinCols + lane * 2;
+    float2 f = make_float2(0.f, 0.f);
+    if (c < a.d)
+      f = shares(a, r.first, (int)((int64_t)r.shares * wave / kJoinWaves), (int)((int64_t)r.shares * (wave + 1) / kJoinWaves), c);
+    lds[wave][lane] = f;
     __syncthreads();
-    const int64_t chunk = base + (int64_t)threadIdx.x * gridDim.x;
-    if (chunk < chunks && (chunk + 1) * a.chunk < a.T) {
-      const int begin = (int)chunk * a.chunk, end = begin + a.chunk;
-      const int tok = a.sorted[end - 1];
-      const bool goes_on = tok != kNoToken && a.sorted[end] == tok;
-      const bool came = a.sorted[begin] == tok && begin > 0 && a.sorted[begin - 1] == tok;
-      if (goes_on && !came) {
-        const int n = (upper(a.sorted, end, a.T, tok) - 1) / a.chunk - (int)chunk + 1;
-        int* to = n <= kJoinFew ? few + 3 * atomicAdd(&n_few, 1) : many + 3 * atomicAdd(&n_many, 1);
-        to[0] = (int)chunk;  // the lists' order changes no result
-        to[1] = n;
-        to[2] = tok;
-      }
-    }
-    __syncthreads();
-    for (int k = wave; k < n_few; k += kJoinWaves)
-      if (in) finish2(a, few[3 * k + 2], c, shares(a, few[3 * k], 0, few[3 * k + 1], c));
-    for (int k = 0; k < n_many; ++k) {
-      const int n = many[3 * k + 1];
-      float2 f = make_float2(0.f, 0.f);
-      if (in)
-        f = shares(a, many[3 * k], (int)((int64_t)n * wave / kJoinWaves), (int)((int64_t)n * (wave + 1) / kJoinWaves), c);
-      lds[wave][lane] = f;
-      __syncthreads();
-      if (wave == 0 && in) {
+    if (wave == 0 && c < a.d) {
 #pragma unroll
-        for (int w = 1; w < kJoinWaves; ++w) f = make_float2(f.x + lds[w][lane].x, f.y + lds[w][lane].y);
-        finish2(a, many[3 * k + 2], c, f);
-      }
-      __syncthreads();
+      for (int w = 1; w < kJoinWaves; ++w) f = make_float2(f.x + lds[w][lane].x, f.y + lds[w][lane].y);
+      finish2(a, r.tok, c, f);
     }
-    __syncthreads();  // the lists are read
+    __syncthreads();
+  }
+  for (int64_t k = (int64_t)blockIdx.x * kJoinWaves + wave; k < few; k += (int64_t)gridDim.x * kJoinWaves) {
+    const Run r = a.runs.few[k / blocks];
+    const int c = (int)(k % blocks) * kJoinCols + lane * 2;
+    if (c < a.d) finish2(a, r.tok, c, shares(a, r.first, 0, r.shares, c));
   }
 }
 
@@ -372,6 +372,7 @@ Digits digits_of(int64_t V) {
 // Workspace of the gradient; returns its size.
 struct Sorting {
   int32_t *sorted, *place, *sorted2, *place2, *counts;
+  Runs runs;
   float* part;
 };
 size_t carve(int64_t V, int64_t d, int64_t T, uint8_t* base, Sorting* s) {
@@ -388,6 +389,9 @@ size_t carve(int64_t V, int64_t d, int64_t T, uint8_t* base, Sorting* s) {
   x.sorted2 = reinterpret_cast<int32_t*>(take(more));
   x.place2 = reinterpret_cast<int32_t*>(take(more));
   x.counts = reinterpret_cast<int32_t*>(take(more ? ((size_t)4 << digits_of(V).bits) * (size_t)tiles_of(T) : 0));
+  x.runs.count = reinterpret_cast<int32_t*>(take(2 * 4));
+  x.runs.few = reinterpret_cast<Run*>(take((size_t)chunks_of(T) * sizeof(Run)));
+  x.runs.many = reinterpret_cast<Run*>(take((size_t)chunks_of(T) * sizeof(Run)));
   x.part = reinterpret_cast<float*>(take((size_t)chunks_of(T) * 2 * (size_t)d * 4));
   if (s) *s = x;
   return off + 256;
@@ -396,12 +400,12 @@ size_t carve(int64_t V, int64_t d, int64_t T, uint8_t* base, Sorting* s) {
 void sort_tokens(const int32_t* tokens, int T, int V, const Sorting& s, hipStream_t st) {
   if (T <= kRankMost) {
     hipLaunchKernelGGL(k_embed_rank, dim3((unsigned)((T + 63) / 64)), dim3(64 * kRankWaves), 0, st, tokens, T, V, s.sorted,
-                       s.place);
+                       s.place, s.runs.count);
     return;
   }
   const Digits g = digits_of(V);
   const int tiles = (int)tiles_of(T);
-  PassArgs p = {tokens, nullptr, nullptr, nullptr, s.counts, T, V, tiles, 0, 1 << g.bits};
+  PassArgs p = {tokens, nullptr, nullptr, nullptr, s.counts, s.runs.count, T, V, tiles, 0, 1 << g.bits};
   for (int k = 0; k < g.passes; ++k) {
     const bool to_first = (g.passes - 1 - k) % 2 == 0;  // the last pass ends in sorted, place
     p.tok_out = to_first ? s.sorted : s.sorted2;
@@ -458,14 +462,12 @@ dllm_status dllm_embed_backward(const int32_t* tokens, int64_t T, const uint16_t
   dllm::carve(V, d, T, reinterpret_cast<uint8_t*>(workspace), &w);
   if (T > 0) dllm::sort_tokens(tokens, (int)T, (int)V, w, st);
   const int64_t chunks = dllm::chunks_of(T), clears = accumulate ? 0 : (V + 63) / 64;
-  const dllm::SumArgs a = {w.sorted, w.place, (int)T, (int)d, dllm::chunk_of(T), d_out, scale, accumulate, d_table, w.part};
+  const dllm::SumArgs a = {w.sorted, w.place, (int)T, (int)d, dllm::chunk_of(T), d_out, scale, accumulate, d_table, w.runs, w.part};
   const unsigned cols = (unsigned)((d + dllm::kCols - 1) / dllm::kCols);
   if (chunks + clears > 0)
     hipLaunchKernelGGL(dllm::k_embed_sum, dim3((unsigned)(chunks + clears), cols), dim3(64), 0, st, a, (int)V, (int)chunks);
-  if (chunks > 1) {
-    const dim3 grid((unsigned)(chunks < 64 ? chunks : 64), (unsigned)((d + dllm::kJoinCols - 1) / dllm::kJoinCols));
-    hipLaunchKernelGGL(dllm::k_embed_join, grid, dim3(64 * dllm::kJoinWaves), 0, st, a, (int)chunks);
-  }
+  if (chunks > 1)
+    hipLaunchKernelGGL(dllm::k_embed_join, dim3((unsigned)(chunks < 512 ? chunks : 512)), dim3(64 * dllm::kJoinWaves), 0, st, a);
   return hipGetLastError() == hipSuccess ? DLLM_OK : DLLM_ERR_HIP;
 }
 

@@ -430,7 +430,7 @@ struct DzWork {
     return {{a.W + (int64_t)(a.v0 + c.c0) * a.d, a.n - c.c0, a.d},
             {a.rows + (int64_t)c.r0 * a.dp, Mp - c.r0, a.dp},
             a.dp / BK,
-            0,
+            n_rt == 1 ? c.e * 7 % (a.dp / BK) : 0,
             blocks_of(Mp - c.r0)};
   }
   __device__ __forceinline__ void begin(const Cursor& c) {
@@ -713,34 +713,48 @@ __global__ __launch_bounds__(NT, 1) void k_loss_d_W(GradArgs a) {
 // Few rows: the rows of d_W that are targets, with what dz's rounding left of
 // their entries.  They are summed anew, in fp32 and the order of the rows, into
 // `fix` before the piece's product is stored (accumulated, the product's old
-// values are gone behind it) and take their places at the end.  A workgroup of
-// one wave has 512 columns of one target, which the first row with it answers for.
+// values are gone behind it) and take their places at the end.  A workgroup has
+// 512 columns of one target, which the first row with it answers for; its waves
+// take a quarter of the rows each.
 __device__ __forceinline__ bool first_with(const GradArgs& a, int M, int i, int v) {
   bool before = false;
   for (int k = threadIdx.x & 63; k < M; k += 64) before |= k < i && a.tgt[k] == v;
   return __ballot(before) == 0;
 }
 
-__global__ __launch_bounds__(64) void k_loss_targets(GradArgs a) {
-  const int M = min(a.ctr[0], a.L), i = blockIdx.x, c = blockIdx.y * 512 + threadIdx.x * 8;
+__global__ __launch_bounds__(256) void k_loss_targets(GradArgs a) {
+  __shared__ float z[kLossFew], part[4][512];
+  const int M = min(a.ctr[0], a.L), i = blockIdx.x;
   if (M > kLossFew || i >= M) return;
   const int v = a.tgt[i] - a.v0;
   if (v < 0 || v >= a.n || !first_with(a, M, i, a.tgt[i])) return;
+  for (int m = threadIdx.x; m < M; m += 256)
+    z[m] = bf16_float(a.dz[(int64_t)m * a.ldz + v]) + (a.tgt[m] - a.v0 == v ? a.left[m] : 0.f);
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.y * 512 + lane * 8;
+  const int lo = M * wave / 4, hi = M * (wave + 1) / 4;
   float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int m0 = 0; m0 < M; m0 += 64) {
-    const int m = m0 + threadIdx.x;
-    float z = 0.f;
-    if (m < M) z = bf16_float(a.dz[(int64_t)m * a.ldz + v]) + (a.tgt[m] - a.v0 == v ? a.left[m] : 0.f);
-#pragma unroll 8
-    for (int k = 0; k < min(64, M - m0); ++k) {
-      const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(z), k));
-      float h[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (c < a.d) unpack8(*reinterpret_cast<const uint4*>(a.rows + (int64_t)(m0 + k) * a.dp + c), h);
+  if (c < a.d)
+    for (int m0 = lo; m0 < hi; m0 += 8) {
+      uint4 u[8];  // loads of eight rows together; those behind the last one are the last one's
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = fmaf(w, h[j], f[j]);
+      for (int k = 0; k < 8; ++k) u[k] = *reinterpret_cast<const uint4*>(a.rows + (int64_t)min(m0 + k, hi - 1) * a.dp + c);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (m0 + k >= hi) break;
+        float h[8];
+        unpack8(u[k], h);
+        const float w = z[m0 + k];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = fmaf(w, h[j], f[j]);
+      }
     }
-  }
-  if (c >= a.d) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) part[wave][lane * 8 + j] = f[j];
+  __syncthreads();
+  if (wave > 0 || c >= a.d) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = (part[0][lane * 8 + j] + part[1][lane * 8 + j]) + (part[2][lane * 8 + j] + part[3][lane * 8 + j]);
   if (a.accumulate) {
     float old[8];
     unpack8(*reinterpret_cast<const uint4*>(a.d_W + (int64_t)(a.v0 + v) * a.d + c), old);
@@ -774,7 +788,7 @@ hipError_t launch_loss_d_W(const GradArgs& a, int grid, hipStream_t stream) {
   return hipGetLastError();
 }
 hipError_t launch_loss_targets(const GradArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(k_loss_targets, dim3(a.L < kLossFew ? a.L : kLossFew, (a.d + 511) / 512), dim3(64), 0, stream, a);
+  hipLaunchKernelGGL(k_loss_targets, dim3(a.L < kLossFew ? a.L : kLossFew, (a.d + 511) / 512), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 hipError_t launch_loss_put(const GradArgs& a, hipStream_t stream) {
