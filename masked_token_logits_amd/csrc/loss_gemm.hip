@@ -699,15 +699,94 @@ struct DWWork {
 __global__ __launch_bounds__(NT, 1) void k_loss_d_W(GradArgs a) {
   __shared__ __attribute__((aligned(1024))) uint16_t lds[SLOTS * OPT];
   const int M = min(a.ctr[0], a.L);
-  if (M == 0) {
-    if (a.accumulate) return;
-    const int64_t n = (int64_t)a.n * a.d / 8;
-    uint4* o = reinterpret_cast<uint4*>(a.d_W + (int64_t)a.v0 * a.d);
-    for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < n; i += (int64_t)gridDim.x * NT) o[i] = make_uint4(0, 0, 0, 0);
-    return;
-  }
+  if (M <= kLossFew) return;  // k_loss_d_W_few's
   DWWork work = {a, (M + BK - 1) / BK * BK, (a.n + BT - 1) / BT, (a.d + BT - 1) / BT, Lane()};
   run_tiles<true, false, true>(lds, work);
+}
+
+// d_W of few rows: K is a few stages and the time is d_W's own bytes, so what
+// counts is that stores never stop.  128 entries x 256 columns to a workgroup, one
+// stage of both operands in 48 KiB of LDS, three workgroups to a compute unit:
+// while one stores, the others load and multiply.
+constexpr int FV = 128;  // entries of a tile
+
+__global__ __launch_bounds__(NT, 3) void k_loss_d_W_few(GradArgs a, int n_vt, int n_ct) {
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[BK * (BT + FV)];
+  const int M = min(a.ctr[0], a.L), Mp = (M + BK - 1) / BK * BK;
+  if (M > kLossFew || (M == 0 && a.accumulate)) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wr = wave >> 1, wv = wave & 1;
+  const int vt = blockIdx.x / n_ct, ct = blockIdx.x - vt * n_ct, r0 = vt * FV, c0 = ct * BT;
+  uint16_t *la = lds, *lb = lds + BK * BT;
+  Side<true, false> sa;
+  sa.init(a.dp, nullptr, wave, lane);
+  sa.start({a.rows + c0, Mp, a.dp - c0});
+  // the entries' side is half as wide: rows of K of 256 bytes, four to a DMA,
+  // swizzled like the wide ones
+  const int bk = wave * 4 + (lane >> 4), bcol = (((lane & 15) >> 2) ^ (bk & 3)) * 32 + (lane & 3) * 8;
+  const char* bsrc = reinterpret_cast<const char*>(a.dz + (int64_t)bk * a.ldz + min(r0 + bcol, (int)a.ldz - 8));
+  const int bsw = (lane & 15) >> 2, boff = (8 * (lane >> 5) + bsw) * FV + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  f32x16 acc[4][2] = {};
+  for (int k0 = 0; k0 < Mp; k0 += BK) {
+#pragma unroll
+    for (int j = 0; j < DMAS; ++j)
+      __builtin_amdgcn_global_load_lds((const void*)sa.source(j, k0), (LDS_AS void*)(la + (wave + 4 * j) * 512), 16, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      __builtin_amdgcn_global_load_lds((const void*)(bsrc + (size_t)(k0 + 16 * j) * (size_t)a.ldz * 2),
+                                       (LDS_AS void*)(lb + (wave + 4 * j) * 512), 16, 0, 0);
+    stage_sync<0>();
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      bf16x8 fa[4], fb[2];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) fa[f] = sa.frag(la, wv * 4 + f, kk, lane);
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        LDS_AS uint16_t* ring = (LDS_AS uint16_t*)lb;
+        LDS_AS const uint16_t* p = ring + boff + (((wr * 2 + f) ^ bsw) * 32) + kk * 16 * FV;
+        const bf16x4 lo = read_tr(p, ring), hi = read_tr(p + 4 * FV, ring);
+        fb[f] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      }
+#pragma unroll
+      for (int fv = 0; fv < 4; ++fv)
+#pragma unroll
+        for (int fr = 0; fr < 2; ++fr) acc[fv][fr] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[fv], fb[fr], acc[fv][fr], 0, 0, 0);
+    }
+    stage_sync<0>();  // everyone has read the stage
+  }
+  Lane at;
+#pragma unroll
+  for (int fr = 0; fr < 2; ++fr) {
+    const int first = r0 + wr * 64 + fr * 32;  // of the wave's 32 entries
+    if (!a.accumulate) {
+      store_rows(
+          lds + wave * (OPT / 4), at, 0,
+          [&](int fv, int j) {
+            return u32x2{float_bf16(acc[fv][fr][4 * j]) | float_bf16(acc[fv][fr][4 * j + 1]) << 16,
+                         float_bf16(acc[fv][fr][4 * j + 2]) | float_bf16(acc[fv][fr][4 * j + 3]) << 16};
+          },
+          [](LDS_AS uint8_t*, int, int) {},
+          [&](int row, int col, const uint4& u) {
+            const int r = first + row - wr * 32;
+            if (r < a.n && c0 + col < a.d) *reinterpret_cast<uint4*>(a.d_W + (int64_t)(a.v0 + r) * a.d + c0 + col) = u;
+          });
+      continue;
+    }
+    const int r = first + (lane & 31);
+#pragma unroll
+    for (int fv = 0; fv < 4; ++fv)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = c0 + at.col(fv, j);
+        if (r >= a.n || col >= a.d) continue;
+        uint2* o = reinterpret_cast<uint2*>(a.d_W + (int64_t)(a.v0 + r) * a.d + col);
+        const uint2 u = *o;
+        const f32x16& z = acc[fv][fr];
+        *o = make_uint2(float_bf16(z[4 * j] + bf16_float(u.x & 0xFFFF)) | float_bf16(z[4 * j + 1] + bf16_float(u.x >> 16)) << 16,
+                        float_bf16(z[4 * j + 2] + bf16_float(u.y & 0xFFFF)) | float_bf16(z[4 * j + 3] + bf16_float(u.y >> 16)) << 16);
+      }
+  }
 }
 
 // Few rows: the rows of d_W that are targets, with what dz's rounding left of
@@ -784,7 +863,10 @@ hipError_t launch_loss_d_hidden(const GradArgs& a, int grid, hipStream_t stream)
   return hipGetLastError();
 }
 hipError_t launch_loss_d_W(const GradArgs& a, int grid, hipStream_t stream) {
-  hipLaunchKernelGGL(k_loss_d_W, dim3(grid), dim3(NT), 0, stream, a);
+  // how many rows there are is known on the device: one of the two returns at once
+  if (a.L > kLossFew) hipLaunchKernelGGL(k_loss_d_W, dim3(grid), dim3(NT), 0, stream, a);
+  const int n_vt = (a.n + FV - 1) / FV, n_ct = (a.d + BT - 1) / BT;
+  hipLaunchKernelGGL(k_loss_d_W_few, dim3((unsigned)n_vt * (unsigned)n_ct), dim3(NT), 0, stream, a, n_vt, n_ct);
   return hipGetLastError();
 }
 hipError_t launch_loss_targets(const GradArgs& a, hipStream_t stream) {
