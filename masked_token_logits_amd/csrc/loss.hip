@@ -1,44 +1,124 @@
 // Host side and row kernels of the masked cross entropy (include/dllm_loss.h).
 //
 // Forward is the readout's projection: the counted rows are compacted, the
-// LM-head GEMM folds each row's logits into a running maximum and sum per
-// vocabulary slice, and a wave for each row joins the slices and takes the
-// target's logit.  Backward walks the vocabulary in pieces (loss_gemm.hip).
+// LM-head GEMM (for few rows of a small head the loss's own) folds each row's logits into
+// a running maximum and sum per vocabulary slice, and a wave for each row joins
+// the slices and takes the target's logit.  Backward walks the vocabulary in pieces (loss_gemm.hip).
 #include "dllm_loss.h"
 
 #include <math.h>
+
+#include <atomic>
 
 #include "bf16.h"
 #include "loss_internal.h"
 #include "online_state.h"
 #include "readout_internal.h"
+#include "work_plan.h"
 
 namespace dllm {
 namespace {
 
-// Which positions count; zeros for the others' outputs.
-__global__ __launch_bounds__(256) void k_loss_counted(const uint8_t* __restrict__ mask,
-                                                      const int32_t* __restrict__ targets, int L, int V,
-                                                      uint8_t* __restrict__ counted, float* __restrict__ losses,
-                                                      float* __restrict__ lse) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < L; i += (int64_t)gridDim.x * 256) {
-    const int t = targets[i];
-    const bool yes = mask[i] != 0 && t >= 0 && t < V;
-    counted[i] = yes ? 1 : 0;
-    if (!yes && losses) {
-      losses[i] = 0.f;
-      lse[i] = 0.f;
+__device__ __forceinline__ bool counts(uint8_t mask, int target, int V) { return mask != 0 && target >= 0 && target < V; }
+
+// The positions that count, ascending, and zeros for the others' outputs.  One
+// workgroup walks them in chunks, 16 positions to a thread; a thread's place in
+// the list comes from the ballots of its count's bits and the waves before it.
+// It also says how the forward product is split: few rows have slices of their
+// own (k_loss_lse_few) and none of the persistent GEMM's row tiles.
+constexpr int kCompactThreads = 1024;
+
+struct CompactArgs {
+  const uint8_t* mask;
+  const int32_t* targets;
+  int L, V;
+  PlanParams plan;
+  int few, few_slices;  // up to so many rows have slices of their own
+  float *losses, *lse;  // null: not wanted
+  int32_t *idx, *ctr;
+  uint16_t* zeros;      // 16 bytes of zeros for the products
+};
+
+__global__ __launch_bounds__(kCompactThreads) void k_loss_compact(CompactArgs a) {
+  __shared__ unsigned long long best;
+  __shared__ int wave_total[kCompactThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const unsigned long long below = lane ? ~0ull >> (64 - lane) : 0ull;
+  const bool vector = (((uintptr_t)a.mask | (uintptr_t)a.targets) & 15u) == 0;
+  int M = 0;
+  for (int64_t base = 0; base < a.L; base += 16 * kCompactThreads) {
+    const int64_t p0 = base + tid * 16;
+    unsigned bits = 0;
+    if (vector && p0 + 16 <= a.L) {
+      const uint4 m = *reinterpret_cast<const uint4*>(a.mask + p0);
+      const uint32_t w[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int4 t = *reinterpret_cast<const int4*>(a.targets + p0 + 4 * q);
+        bits |= counts(w[q] & 0xFF, t.x, a.V) ? 1u << (4 * q) : 0u;
+        bits |= counts(w[q] >> 8 & 0xFF, t.y, a.V) ? 2u << (4 * q) : 0u;
+        bits |= counts(w[q] >> 16 & 0xFF, t.z, a.V) ? 4u << (4 * q) : 0u;
+        bits |= counts(w[q] >> 24, t.w, a.V) ? 8u << (4 * q) : 0u;
+      }
+    } else {
+      for (int j = 0; j < 16 && p0 + j < a.L; ++j) bits |= counts(a.mask[p0 + j], a.targets[p0 + j], a.V) ? 1u << j : 0u;
     }
+    if (a.losses)
+      for (int j = 0; j < 16 && p0 + j < a.L; ++j)
+        if (!(bits >> j & 1)) a.losses[p0 + j] = a.lse[p0 + j] = 0.f;
+    const int c = __popc(bits);
+    int before = 0;
+#pragma unroll
+    for (int b = 0; b < 5; ++b) before += __popcll(__ballot((c >> b) & 1) & below) << b;
+    if (lane == 63) wave_total[wave] = before + c;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kCompactThreads / 64; ++w) {
+      before += w < wave ? wave_total[w] : 0;
+      total += wave_total[w];
+    }
+    for (int o = M + before; bits; bits &= bits - 1) a.idx[o++] = (int)p0 + __ffs(bits) - 1;
+    M += total;
+    __syncthreads();
+  }
+  int S = a.few_slices, n_rt = 0;
+  if (M > a.few) choose_plan(M, a.plan, &best, S, n_rt);
+  if (tid == 0) {
+    a.ctr[0] = M;
+    a.ctr[3] = S;
+    a.ctr[4] = n_rt;
+    a.ctr[5] = 0;  // workgroups of k_loss_rows that have ended
+    *reinterpret_cast<uint4*>(a.zeros) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// The weighted sum of the rows' terms, in fp64 and a fixed order, by a workgroup.
+template <int THREADS>
+__device__ __forceinline__ void total_of(const float* terms, int M, float* loss) {
+  __shared__ double part[THREADS / 64];
+  double s = 0.0;
+  for (int i = threadIdx.x; i < M; i += THREADS) s += (double)__hip_atomic_load(terms + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double t = 0.0;
+    for (int w = 0; w < THREADS / 64; ++w) t += part[w];
+    *loss = (float)t;
   }
 }
 
 // One wave for each row: the slices' partials joined, and the target's logit.
+// With `loss` the last workgroup to end adds the terms, too.
 __global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* __restrict__ W, const uint16_t* __restrict__ H,
                                                    int d, int L, const int32_t* __restrict__ targets,
                                                    const float* __restrict__ weights,
                                                    const int32_t* __restrict__ idx, const int32_t* __restrict__ ctr,
-                                                   Partials p, float* __restrict__ terms, float* __restrict__ losses,
-                                                   float* __restrict__ lse) {
+                                                   Partials p, float* terms, float* __restrict__ losses,
+                                                   float* __restrict__ lse, int32_t* __restrict__ ended,
+                                                   float* __restrict__ loss) {
   const int M = min(ctr[0], L), slices = ctr[3];
   const int lane = threadIdx.x & 63;
   for (int row = blockIdx.x * 4 + (threadIdx.x >> 6); row < M; row += gridDim.x * 4) {
@@ -57,7 +137,6 @@ __global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* __restrict__ 
     for (int j = lane; j < slices; j += 64) {
       RowState y = row_state_empty();
       y.m = p.m[base + j];
-      y.a = p.a[base + j];
       y.s = p.s[base + j];
       row_merge<false>(r, y);
     }
@@ -72,25 +151,21 @@ __global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* __restrict__ 
       lse[pos] = l;
       terms[row] = (l - z) * (weights ? weights[pos] : 1.f);
     }
-  }
-}
-
-// The weighted sum, in fp64 and a fixed order.
-__global__ __launch_bounds__(1024) void k_loss_total(const float* __restrict__ terms, const int32_t* __restrict__ ctr,
-                                                     int L, float* __restrict__ loss) {
-  __shared__ double part[16];
-  const int M = min(ctr[0], L);
-  double s = 0.0;
-  for (int i = threadIdx.x; i < M; i += 1024) s += (double)terms[i];
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+  }  if (!loss) return;
+  __shared__ int last;
   __syncthreads();
   if (threadIdx.x == 0) {
-    double t = 0.0;
-    for (int w = 0; w < 16; ++w) t += part[w];
-    *loss = (float)t;
+    __threadfence();  // the workgroup's terms, before its arrival
+    last = atomicAdd(ended, 1) == (int)gridDim.x - 1;
+    __threadfence();
   }
+  __syncthreads();
+  if (last) total_of<256>(terms, M, loss);
+}
+
+__global__ __launch_bounds__(1024) void k_loss_total(const float* __restrict__ terms, const int32_t* __restrict__ ctr,
+                                                     int L, float* __restrict__ loss) {
+  total_of<1024>(terms, min(ctr[0], L), loss);
 }
 
 // What backward keeps of each counted row, in order: its hidden state and
@@ -98,12 +173,12 @@ __global__ __launch_bounds__(1024) void k_loss_total(const float* __restrict__ t
 // d_hidden that do not count.  A wave takes a row.
 struct PrepareArgs {
   const uint16_t *W, *H;
-  const uint8_t* counted;
+  const uint8_t* mask;
   const int32_t* targets;
   const float *weights, *grad, *lse;
   const int32_t *idx, *ctr;
-  int L, d, dp;
-  uint16_t *rows, *zeros;
+  int V, L, d, dp;
+  uint16_t* rows;
   float* bias;
   uint32_t* flip;
   int32_t* tgt;
@@ -114,7 +189,6 @@ struct PrepareArgs {
 __global__ __launch_bounds__(256) void k_loss_prepare(PrepareArgs a) {
   const int M = min(a.ctr[0], a.L), Mp = (M + kLossStep - 1) / kLossStep * kLossStep, lane = threadIdx.x & 63;
   const uint4 none = make_uint4(0, 0, 0, 0);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<uint4*>(a.zeros) = none;
   for (int i = blockIdx.x * 4 + (threadIdx.x >> 6); i < max(a.L, Mp); i += gridDim.x * 4) {
     if (i < M) {
       const int pos = a.idx[i], t = a.targets[pos];
@@ -153,7 +227,7 @@ __global__ __launch_bounds__(256) void k_loss_prepare(PrepareArgs a) {
         a.left[i] = 0.f;
       }
     }
-    if (a.d_hidden && i < a.L && !a.counted[i])
+    if (a.d_hidden && i < a.L && !counts(a.mask[i], a.targets[i], a.V))
       for (int c = 8 * lane; c < a.d; c += 8 * 64) *reinterpret_cast<uint4*>(a.d_hidden + (int64_t)i * a.d + c) = none;
   }
 }
@@ -165,10 +239,23 @@ bool sizes_ok(int64_t V, int64_t d, int64_t L) {
 }
 bool supported(int64_t d) { return d % 8 == 0 && d < ((int64_t)1 << 20); }
 
-int64_t part_cap(int64_t L) { return (L + kLargeBM - 1) / kLargeBM * kLargeBM * kMaxLargeSlices; }
+// Up to so many rows, forward is the small tiles' (k_loss_lse_few): few rows of
+// a small head, and any of so little work that an empty launch of the persistent
+// GEMM would count (512 positions, 4096 entries of 256: 19 -> 16 us).
+int few_rows(int64_t V, int64_t d, int64_t L) {
+  if (V > kLossSmallHead) return 0;
+  return L * V * d <= (int64_t)1 << 31 ? (int)L : kLossFew;
+}
+
+// Partials of the forward product: the persistent GEMM's plan, or a slice for
+// each tile of few rows.
+int64_t part_cap(int64_t V, int64_t d, int64_t L) {
+  const int64_t many = (L + kLargeBM - 1) / kLargeBM * kLargeBM * kMaxLargeSlices;
+  const int64_t few = (L < few_rows(V, d, L) ? L : few_rows(V, d, L)) * loss_few_slices(V);
+  return many > few ? many : few;
+}
 
 struct Rows {
-  uint8_t* counted;
   int32_t *idx, *ctr;
   float* terms;
   Partials part;
@@ -182,7 +269,7 @@ struct Rows {
 };
 
 // Workspace of both directions; returns its size.
-size_t carve(int64_t d, int64_t L, int64_t piece, uint8_t* base, Rows* r) {
+size_t carve(int64_t V, int64_t d, int64_t L, int64_t piece, uint8_t* base, Rows* r) {
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -190,14 +277,14 @@ size_t carve(int64_t d, int64_t L, int64_t piece, uint8_t* base, Rows* r) {
     return base ? base + o : nullptr;
   };
   Rows x = {};
-  x.counted = take((size_t)L);
+  x.zeros = reinterpret_cast<uint16_t*>(take(16));
   x.idx = reinterpret_cast<int32_t*>(take((size_t)L * 4));
   x.ctr = reinterpret_cast<int32_t*>(take(16 * 4));
   if (piece == 0) {
     x.terms = reinterpret_cast<float*>(take((size_t)L * 4));
-    x.part.m = reinterpret_cast<float*>(take((size_t)part_cap(L) * 4));
-    x.part.a = reinterpret_cast<int32_t*>(take((size_t)part_cap(L) * 4));
-    x.part.s = reinterpret_cast<float*>(take((size_t)part_cap(L) * 4));
+    x.part.m = reinterpret_cast<float*>(take((size_t)part_cap(V, d, L) * 4));
+    x.part.a = reinterpret_cast<int32_t*>(take((size_t)part_cap(V, d, L) * 4));
+    x.part.s = reinterpret_cast<float*>(take((size_t)part_cap(V, d, L) * 4));
   } else {
     const size_t rows = (size_t)loss_padded(L);
     x.bias = reinterpret_cast<float*>(take(rows * 4));
@@ -205,7 +292,6 @@ size_t carve(int64_t d, int64_t L, int64_t piece, uint8_t* base, Rows* r) {
     x.tgt = reinterpret_cast<int32_t*>(take(rows * 4));
     x.at_tgt = reinterpret_cast<float*>(take(rows * 4));
     x.left = reinterpret_cast<float*>(take(rows * 4));
-    x.zeros = reinterpret_cast<uint16_t*>(take(16));
     x.rows = reinterpret_cast<uint16_t*>(take(rows * (size_t)loss_padded(d) * 2));
     x.dz = reinterpret_cast<uint16_t*>(take(rows * (size_t)piece * 2));
     x.fix = reinterpret_cast<uint16_t*>(take((size_t)(L < kLossFew ? L : kLossFew) * (size_t)d * 2));
@@ -246,10 +332,15 @@ bool over_inputs(const dllm_loss* p, const void* out, size_t n) {
          overlaps(out, n, p->mask, L) || overlaps(out, n, p->targets, L * 4) || overlaps(out, n, p->weights, L * 4);
 }
 
+// The current device's compute units, 0 where there is none; asked for once a device.
 int device_cus() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
   int dev = 0, cus = 0;
   if (hipGetDevice(&dev) != hipSuccess) return 0;
+  if (dev >= 0 && dev < kDevices && (cus = known[dev].load(std::memory_order_relaxed)) > 0) return cus;
   if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
+  if (dev >= 0 && dev < kDevices) known[dev].store(cus, std::memory_order_relaxed);
   return cus;
 }
 
@@ -262,7 +353,7 @@ extern "C" {
 
 size_t dllm_loss_forward_workspace_bytes(int64_t V, int64_t d, int64_t L) {
   if (!dllm::sizes_ok(V, d, L) || !dllm::supported(d)) return 0;
-  return dllm::carve(d, L, 0, nullptr, nullptr);
+  return dllm::carve(V, d, L, 0, nullptr, nullptr);
 }
 
 dllm_status dllm_loss_forward(const dllm_loss* p, float* loss, float* losses, float* lse, void* workspace,
@@ -272,7 +363,7 @@ dllm_status dllm_loss_forward(const dllm_loss* p, float* loss, float* losses, fl
   if (!loss || !losses || !lse) return DLLM_ERR_INVALID_ARG;
   if (!dllm::aligned(loss, 4) || !dllm::aligned(losses, 4) || !dllm::aligned(lse, 4)) return DLLM_ERR_UNSUPPORTED;
   const int64_t L = p->L;
-  const size_t n = (size_t)L * 4, need = dllm::carve(p->d, L, 0, nullptr, nullptr);
+  const size_t n = (size_t)L * 4, need = dllm::carve(p->V, p->d, L, 0, nullptr, nullptr);
   if (!workspace || workspace_bytes < need || !dllm::aligned(workspace, 256)) return DLLM_ERR_WORKSPACE;
   if (dllm::over_inputs(p, loss, 4) || dllm::over_inputs(p, losses, n) || dllm::over_inputs(p, lse, n) ||
       dllm::over_inputs(p, workspace, need) || dllm::overlaps(losses, n, lse, n) || dllm::overlaps(loss, 4, losses, n) ||
@@ -283,9 +374,7 @@ dllm_status dllm_loss_forward(const dllm_loss* p, float* loss, float* losses, fl
   if (cus <= 0) return DLLM_ERR_HIP;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   dllm::Rows r;
-  dllm::carve(p->d, L, 0, reinterpret_cast<uint8_t*>(workspace), &r);
-  hipLaunchKernelGGL(dllm::k_loss_counted, dim3(dllm::grid_for((L + 255) / 256, 4096)), dim3(256), 0, st, p->mask,
-                     p->targets, (int)L, (int)p->V, r.counted, losses, lse);
+  dllm::carve(p->V, p->d, L, 0, reinterpret_cast<uint8_t*>(workspace), &r);
   // as the readout chooses it: the persistent GEMM where its 32-bit offsets reach, else the streaming one
   const int64_t n_vt = (p->V + dllm::kLargeBN - 1) / dllm::kLargeBN, n_rt = (L + dllm::kLargeBM - 1) / dllm::kLargeBM;
   const bool persistent = p->d % dllm::kPersistBK == 0 && (int64_t)dllm::kPersistBN * p->d * 2 < ((int64_t)1 << 32) &&
@@ -295,27 +384,39 @@ dllm_status dllm_loss_forward(const dllm_loss* p, float* loss, float* losses, fl
   plan.n_vt = (int)n_vt;
   plan.grid = cus;
   plan.max_slices = 1024;
-  plan.part_cap = dllm::part_cap(L);
+  plan.part_cap = dllm::part_cap(p->V, p->d, L);
   if (!persistent) {
     int64_t s = (4 * (int64_t)cus + n_rt - 1) / n_rt;
     if (s > dllm::kMaxLargeSlices) s = dllm::kMaxLargeSlices;
     plan.fixed_slices = (int)(s < n_vt ? s : n_vt);
   }
-  if (dllm::launch_mask_compact(r.counted, 0, L, 0, plan, r.idx, r.ctr, st) != hipSuccess) return DLLM_ERR_HIP;
-  const hipError_t e =
-      persistent ? dllm::launch_gemm_persistent(p->W_lm, p->hidden, (int)p->d, (int)p->V, r.idx, r.ctr, cus, r.part, st)
-                 : dllm::launch_gemm_large(p->W_lm, p->hidden, (int)p->d, (int)p->V, r.idx, r.ctr, (int)n_rt,
-                                           plan.fixed_slices, r.part, st);
-  if (e != hipSuccess) return DLLM_ERR_HIP;
+  const int few = dllm::few_rows(p->V, p->d, L);
+  const dllm::CompactArgs ca = {p->mask, p->targets, (int)L, (int)p->V, plan, few, (int)dllm::loss_few_slices(p->V),
+                                losses,  lse,        r.idx,  r.ctr,     r.zeros};
+  hipLaunchKernelGGL(dllm::k_loss_compact, dim3(1), dim3(dllm::kCompactThreads), 0, st, ca);
+  // How many rows there are is known on the device: the persistent GEMM or the product of few rows
+  // returns at once.  The streaming GEMM does few rows too, so that product comes behind it.
+  const dllm::LseArgs la = {p->W_lm, p->hidden, r.zeros, r.idx, r.ctr, r.part.m, r.part.s, (int)p->V, (int)p->d, (int)L, few};
+  if (L > few) {
+    const hipError_t e =
+        persistent ? dllm::launch_gemm_persistent(p->W_lm, p->hidden, (int)p->d, (int)p->V, r.idx, r.ctr, cus, r.part, st)
+                   : dllm::launch_gemm_large(p->W_lm, p->hidden, (int)p->d, (int)p->V, r.idx, r.ctr, (int)n_rt,
+                                             plan.fixed_slices, r.part, st);
+    if (e != hipSuccess) return DLLM_ERR_HIP;
+  }
+  if (few > 0 && dllm::launch_loss_lse_few(la, st) != hipSuccess) return DLLM_ERR_HIP;
+  // the last workgroup to end adds up to 4096 terms itself; more are a kernel's of more threads
+  const bool ends = L <= 4096;
   hipLaunchKernelGGL(dllm::k_loss_rows, dim3(dllm::grid_for((L + 3) / 4, 65536)), dim3(256), 0, st, p->W_lm, p->hidden,
-                     (int)p->d, (int)L, p->targets, p->weights, r.idx, r.ctr, r.part, r.terms, losses, lse);
-  hipLaunchKernelGGL(dllm::k_loss_total, dim3(1), dim3(1024), 0, st, r.terms, r.ctr, (int)L, loss);
+                     (int)p->d, (int)L, p->targets, p->weights, r.idx, r.ctr, r.part, r.terms, losses, lse, r.ctr + 5,
+                     ends ? loss : nullptr);
+  if (!ends) hipLaunchKernelGGL(dllm::k_loss_total, dim3(1), dim3(1024), 0, st, r.terms, r.ctr, (int)L, loss);
   return hipGetLastError() == hipSuccess ? DLLM_OK : DLLM_ERR_HIP;
 }
 
 size_t dllm_loss_backward_workspace_bytes(int64_t V, int64_t d, int64_t L, int64_t piece) {
   if (!dllm::sizes_ok(V, d, L) || !dllm::supported(d) || piece < 0 || piece % 256 != 0) return 0;
-  return dllm::carve(d, L, dllm::piece_of(V, L, piece), nullptr, nullptr);
+  return dllm::carve(V, d, L, dllm::piece_of(V, L, piece), nullptr, nullptr);
 }
 
 dllm_status dllm_loss_backward(const dllm_loss* p, const float* lse, const float* grad, uint16_t* d_hidden,
@@ -329,7 +430,7 @@ dllm_status dllm_loss_backward(const dllm_loss* p, const float* lse, const float
     return DLLM_ERR_UNSUPPORTED;
   const int64_t L = p->L, d = p->d, V = p->V;
   piece = dllm::piece_of(V, L, piece);
-  const size_t need = dllm::carve(d, L, piece, nullptr, nullptr);
+  const size_t need = dllm::carve(V, d, L, piece, nullptr, nullptr);
   if (!workspace || workspace_bytes < need || !dllm::aligned(workspace, 256)) return DLLM_ERR_WORKSPACE;
   const size_t nh = (size_t)L * (size_t)d * 2, nw = (size_t)V * (size_t)d * 2;
   const void* out[] = {d_hidden, d_W, workspace};
@@ -345,16 +446,15 @@ dllm_status dllm_loss_backward(const dllm_loss* p, const float* lse, const float
   if (cus <= 0) return DLLM_ERR_HIP;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   dllm::Rows r;
-  dllm::carve(d, L, piece, reinterpret_cast<uint8_t*>(workspace), &r);
-  hipLaunchKernelGGL(dllm::k_loss_counted, dim3(dllm::grid_for((L + 255) / 256, 4096)), dim3(256), 0, st, p->mask,
-                     p->targets, (int)L, (int)V, r.counted, nullptr, nullptr);
+  dllm::carve(V, d, L, piece, reinterpret_cast<uint8_t*>(workspace), &r);
   dllm::PlanParams plan = {};
   plan.fixed_slices = 1;
   plan.tile_rows = dllm::kLargeBM;
-  if (dllm::launch_mask_compact(r.counted, 0, L, 0, plan, r.idx, r.ctr, st) != hipSuccess) return DLLM_ERR_HIP;
+  const dllm::CompactArgs ca = {p->mask, p->targets, (int)L, (int)V, plan, 0, 1, nullptr, nullptr, r.idx, r.ctr, r.zeros};
+  hipLaunchKernelGGL(dllm::k_loss_compact, dim3(1), dim3(dllm::kCompactThreads), 0, st, ca);
   const int dp = (int)dllm::loss_padded(d), grid = cus < dllm::kLossGrid ? cus : dllm::kLossGrid;
-  const dllm::PrepareArgs pa = {p->W_lm, p->hidden, r.counted, p->targets, p->weights, grad,  lse,      r.idx,  r.ctr,   (int)L,
-                                (int)d,  dp,        r.rows,    r.zeros,    r.bias,     r.flip, r.tgt, r.at_tgt, r.left, d_hidden};
+  const dllm::PrepareArgs pa = {p->W_lm, p->hidden, p->mask, p->targets, p->weights, grad,   lse,   r.idx,    r.ctr,  (int)V,
+                                (int)L,  (int)d,    dp,      r.rows,     r.bias,     r.flip, r.tgt, r.at_tgt, r.left, d_hidden};
   hipLaunchKernelGGL(dllm::k_loss_prepare, dim3(dllm::grid_for(dllm::loss_padded(L) / 4, 65536)), dim3(256), 0, st, pa);
   dllm::GradArgs a = {};
   a.W = p->W_lm;

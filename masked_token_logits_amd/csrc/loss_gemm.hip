@@ -430,7 +430,10 @@ struct DzWork {
     return {{a.W + (int64_t)(a.v0 + c.c0) * a.d, a.n - c.c0, a.d},
             {a.rows + (int64_t)c.r0 * a.dp, Mp - c.r0, a.dp},
             a.dp / BK,
-            n_rt == 1 ? c.e * 7 % (a.dp / BK) : 0,
+            // One row tile: the time is W's bytes.  Its rows are a power of two apart, and tiles that all
+            // stand at the same place of them ask a few channels for everything (102 rows, 126464 entries
+            // of 4096: 260 us; 206 where each stands at another).  More row tiles share W's tiles in step.
+            n_rt == 1 ? (int)((int64_t)c.e * 7 % (a.dp / BK)) : 0,
             blocks_of(Mp - c.r0)};
   }
   __device__ __forceinline__ void begin(const Cursor& c) {
@@ -789,6 +792,101 @@ __global__ __launch_bounds__(NT, 3) void k_loss_d_W_few(GradArgs a, int n_vt, in
   }
 }
 
+// Forward for few rows of a small head, which gives the persistent GEMM few
+// tiles: 128 rows x 128 entries to a workgroup, 64 x 64 to a wave, two 32 KiB
+// stages in LDS and two workgroups to a compute unit (256 rows, 4096 entries of
+// 256: 7.0 us; the persistent GEMM 15.9).  A large head is the persistent GEMM's:
+// there these tiles, two to a unit, keep too few bytes on their way (102 rows,
+// 126464 entries of 4096: 394 us; the persistent GEMM 240).
+constexpr int FR = 128;  // rows of a tile
+
+template <bool TAIL>
+__global__ __launch_bounds__(NT, 2) void k_loss_lse_few(LseArgs a, int n_rt, int slices) {
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[2 * BK * (FR + kLossFewEntries)];
+  __shared__ float wave_m[2][FR], wave_s[2][FR];
+  const int M = min(a.ctr[0], a.L);
+  const int vt = blockIdx.x / n_rt, rt = blockIdx.x - vt * n_rt, r0 = rt * FR, c0 = vt * kLossFewEntries;
+  if (M > a.few || r0 >= M) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wr = wave >> 1, wv = wave & 1;
+  // DMA j of a wave has rows (wave + 4 j) * 8 + lane / 8 of a side; row r holds its 16-byte pieces at piece ^ ((r >> 1) & 7)
+  const int row = wave * 8 + (lane >> 3), col = ((lane & 7) ^ ((row >> 1) & 7)) * 8;
+  const uint16_t *pw[4], *ph[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    pw[j] = a.W + (int64_t)min(c0 + row + 32 * j, a.V - 1) * a.d + col;
+    ph[j] = a.H + (int64_t)a.idx[min(r0 + row + 32 * j, M - 1)] * a.d + col;
+  }
+  const int stages = (a.d + BK - 1) / BK;
+  int k0 = vt * 7 % stages * BK;  // W's rows may be powers of two apart: not all tiles at the same place of them
+  auto issue = [&](int slot) {
+    const bool in = !TAIL || k0 + col < a.d;
+    uint16_t* to = lds + slot * BK * (FR + kLossFewEntries) + wave * 512;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      __builtin_amdgcn_global_load_lds((const void*)(in ? pw[j] + k0 : a.zeros), (LDS_AS void*)(to + 4 * j * 512), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((const void*)(in ? ph[j] + k0 : a.zeros),
+                                       (LDS_AS void*)(to + BK * kLossFewEntries + 4 * j * 512), 16, 0, 0);
+    }
+    k0 = k0 + BK >= stages * BK ? 0 : k0 + BK;
+  };
+  issue(0);
+  issue(1);  // with one stage, the same again: never used
+  f32x16 acc[2][2] = {};
+  const int swz = ((lane & 31) >> 1) & 7;
+  for (int q = 0; q < stages; ++q) {
+    stage_sync<8>();  // stage q has landed; the next one's DMAs may be in flight
+    const uint16_t* w = lds + (q & 1) * BK * (FR + kLossFewEntries) + (wv * 64 + (lane & 31)) * BK;
+    const uint16_t* h = lds + (q & 1) * BK * (FR + kLossFewEntries) + BK * kLossFewEntries + (wr * 64 + (lane & 31)) * BK;
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const int piece = ((kk * 2 + (lane >> 5)) ^ swz) * 8;
+      bf16x8 fw[2], fh[2];
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        fw[f] = *reinterpret_cast<const bf16x8*>(w + f * 32 * BK + piece);
+        fh[f] = *reinterpret_cast<const bf16x8*>(h + f * 32 * BK + piece);
+      }
+#pragma unroll
+      for (int fv = 0; fv < 2; ++fv)
+#pragma unroll
+        for (int fr = 0; fr < 2; ++fr) acc[fv][fr] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fw[fv], fh[fr], acc[fv][fr], 0, 0, 0);
+    }
+    stage_sync<8>();  // every wave has read the slot
+    issue(q & 1);
+  }
+  auto off = [](int x) { return 8 * (x >> 2) + (x & 3); };
+#pragma unroll
+  for (int fr = 0; fr < 2; ++fr) {
+    RowState r = row_state_empty();
+#pragma unroll
+    for (int fv = 0; fv < 2; ++fv) {
+      const int v = c0 + wv * 64 + fv * 32 + 4 * (lane >> 5);
+      float z[16];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) z[x] = v + off(x) < a.V ? acc[fv][fr][x] : -INFINITY;
+      row_fold<false, 16>(r, z, 0, off);
+    }
+    const RowState y = shfl_xor_state(r, 32);
+    row_merge<false>(r, y);
+    if (lane < 32) {
+      wave_m[wv][wr * 64 + fr * 32 + lane] = r.m;
+      wave_s[wv][wr * 64 + fr * 32 + lane] = r.s;
+    }
+  }
+  __syncthreads();
+  if (tid < FR && r0 + tid < M) {
+    RowState x = row_state_empty(), y = row_state_empty();
+    x.m = wave_m[0][tid];
+    x.s = wave_s[0][tid];
+    y.m = wave_m[1][tid];
+    y.s = wave_s[1][tid];
+    row_merge<false>(x, y);
+    a.m[(int64_t)(r0 + tid) * slices + vt] = x.m;
+    a.s[(int64_t)(r0 + tid) * slices + vt] = x.s;
+  }
+}
+
 // Few rows: the rows of d_W that are targets, with what dz's rounding left of
 // their entries.  They are summed anew, in fp32 and the order of the rows, into
 // `fix` before the piece's product is stored (accumulated, the product's old
@@ -851,6 +949,15 @@ __global__ __launch_bounds__(64) void k_loss_put(GradArgs a) {
 
 }  // namespace
 
+hipError_t launch_loss_lse_few(const LseArgs& a, hipStream_t stream) {
+  const int n_rt = ((a.L < a.few ? a.L : a.few) + FR - 1) / FR, slices = (int)loss_few_slices(a.V);
+  const dim3 grid((unsigned)slices * (unsigned)n_rt);
+  if (a.d % BK == 0)
+    hipLaunchKernelGGL(k_loss_lse_few<false>, grid, dim3(NT), 0, stream, a, n_rt, slices);
+  else
+    hipLaunchKernelGGL(k_loss_lse_few<true>, grid, dim3(NT), 0, stream, a, n_rt, slices);
+  return hipGetLastError();
+}
 hipError_t launch_loss_dz(const GradArgs& a, int grid, hipStream_t stream) {
   if (a.d % BK == 0)
     hipLaunchKernelGGL(k_loss_dz<false>, dim3(grid), dim3(NT), 0, stream, a);

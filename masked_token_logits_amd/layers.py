@@ -245,6 +245,7 @@ class MaskedLoss(_Workspace):
         if piece is not None and (int(piece) < 256 or int(piece) % 256):
             raise ValueError(f"piece {piece} is not a positive multiple of 256")
         self.W_lm, self.piece, self.stream = W_lm, int(piece or 0), _stream(stream, self.device)
+        self._bytes = {}     # workspace sizes of the lengths seen: (forward, backward)
 
     def _struct(self, hidden, mask, targets, weights):
         L = _rows(hidden, "hidden", self.d, self.device)
@@ -256,6 +257,13 @@ class MaskedLoss(_Workspace):
             _need(weights, "weights", _F32, (L,), self.device)
         return _abi.dllm_loss(self.W_lm.data_ptr(), hidden.data_ptr(), mask.data_ptr(), targets.data_ptr(),
                               _at(weights), self.V, self.d, L)
+
+    def _workspaces(self, L: int):
+        got = self._bytes.get(L)
+        if got is None:
+            got = self._bytes[L] = (_abi.dllm_loss_forward_workspace_bytes(self.V, self.d, L),
+                                    _abi.dllm_loss_backward_workspace_bytes(self.V, self.d, L, self.piece))
+        return got
 
     def __call__(self, hidden, mask, targets, weights=None, out=None):
         """Queue the loss of hidden [L, d] at the masked positions (mask [L] u8
@@ -276,11 +284,12 @@ class MaskedLoss(_Workspace):
         def make(stream):
             nonlocal box
             if box is None:
-                box = [torch.empty(n, dtype=torch.float32, device=self.device) for n in (1, L, L)]
-            lib = _abi.load()
-            nbytes = lib.dllm_loss_forward_workspace_bytes(self.V, self.d, L)
+                new = self.W_lm.new_empty
+                box = [new((n,), dtype=torch.float32) for n in (1, L, L)]
+            nbytes = self._workspaces(L)[0]
             ws = self._workspace(nbytes, "dllm_loss_forward_workspace_bytes")
-            return lib.dllm_loss_forward(C.byref(p), *(t.data_ptr() for t in box), ws.data_ptr(), nbytes, stream)
+            return _abi.load().dllm_loss_forward(C.byref(p), box[0].data_ptr(), box[1].data_ptr(), box[2].data_ptr(),
+                                                 ws.data_ptr(), nbytes, stream)
 
         self._call("dllm_loss_forward", (hidden, mask, targets, weights, self.W_lm) + tuple(out or ()), make)
         return tuple(box)
@@ -315,11 +324,10 @@ class MaskedLoss(_Workspace):
                 box[0] = torch.empty_like(hidden)
             if box[1] is None and "W" in need:
                 box[1] = torch.empty_like(self.W_lm)
-            lib = _abi.load()
-            nbytes = lib.dllm_loss_backward_workspace_bytes(self.V, self.d, L, self.piece)
+            nbytes = self._workspaces(L)[1]
             ws = self._workspace(nbytes, "dllm_loss_backward_workspace_bytes")
-            return lib.dllm_loss_backward(C.byref(p), lse.data_ptr(), _at(grad), _at(box[0]), _at(box[1]),
-                                          1 if accumulate else 0, self.piece, ws.data_ptr(), nbytes, stream)
+            return _abi.load().dllm_loss_backward(C.byref(p), lse.data_ptr(), _at(grad), _at(box[0]), _at(box[1]),
+                                                  1 if accumulate else 0, self.piece, ws.data_ptr(), nbytes, stream)
 
         self._call("dllm_loss_backward", (hidden, mask, targets, lse, weights, grad, d_hidden, d_W, self.W_lm), make)
         return box[0], box[1]

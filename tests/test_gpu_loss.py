@@ -93,6 +93,11 @@ CASES = [  # L, d, V, ratio, piece
     (700, 200, 777, 0.7, 256),
     (1100, 64, 300, 0.02, None),    # few rows of many positions
     (130, 1024, 640, 1.0, None),
+    (40, 72, 70001, 0.9, 8192),     # few rows of a large head
+    (600, 128, 65537, 0.3, 16384),  # two tiles of them
+    (260, 64, 66000, 1.0, None),    # just over few
+    (257, 136, 900, 1.0, 256),      # few and over with a d that is no multiple of 32
+    (300, 40, 500, 0.7, None),
 ]
 
 
