@@ -118,29 +118,39 @@ __global__ __launch_bounds__(256) void k_embed_count(PassArgs p) {
   for (int b = threadIdx.x; b < p.bins; b += 256) p.counts[(int64_t)b * p.tiles + blockIdx.x] = hist[b];
 }
 
-// Where each digit's tokens of each tile begin: exclusive sums, in place.  A
-// wave takes 1024 in a row, 64 at a time.
+// Where each digit's tokens of each tile begin: exclusive sums, in place, 16 to
+// a thread.  One workgroup: 32768 counts are two rounds.
 __global__ __launch_bounds__(1024) void k_embed_begin(int32_t* __restrict__ counts, int64_t n) {
   __shared__ int part[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int carry = 0;
   for (int64_t base = 0; base < n; base += 16 * 1024) {
-    const int64_t i = base + wave * 1024 + lane;
-    int v[16], run = 0;
+    const int64_t i = base + threadIdx.x * 16;
+    int v[16], mine = 0;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = i + 64 * k < n ? counts[i + 64 * k] : 0;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      int sum = v[k];
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int o = __shfl_up(sum, off);
-        if (lane >= off) sum += o;
+    for (int k = 0; k < 16; k += 4) {
+      int4 u = make_int4(0, 0, 0, 0);
+      if (i + k + 3 < n) {
+        u = *reinterpret_cast<const int4*>(counts + i + k);
+      } else {
+        if (i + k < n) u.x = counts[i + k];
+        if (i + k + 1 < n) u.y = counts[i + k + 1];
+        if (i + k + 2 < n) u.z = counts[i + k + 2];
       }
-      v[k] = run + sum - v[k];
-      run += __shfl(sum, 63);
+      v[k] = u.x;
+      v[k + 1] = u.y;
+      v[k + 2] = u.z;
+      v[k + 3] = u.w;
     }
-    if (lane == 0) part[wave] = run;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) mine += v[k];
+    int sum = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(sum, off);
+      if (lane >= off) sum += o;
+    }
+    if (lane == 63) part[wave] = sum;
     __syncthreads();
     int before = carry, all = carry;
 #pragma unroll
@@ -148,9 +158,23 @@ __global__ __launch_bounds__(1024) void k_embed_begin(int32_t* __restrict__ coun
       before += w < wave ? part[w] : 0;
       all += part[w];
     }
+    int run = before + sum - mine;
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (i + 64 * k < n) counts[i + 64 * k] = before + v[k];
+    for (int k = 0; k < 16; ++k) {
+      const int c = v[k];
+      v[k] = run;
+      run += c;
+    }
+#pragma unroll
+    for (int k = 0; k < 16; k += 4) {
+      if (i + k + 3 < n) {
+        *reinterpret_cast<int4*>(counts + i + k) = make_int4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+      } else {
+        if (i + k < n) counts[i + k] = v[k];
+        if (i + k + 1 < n) counts[i + k + 1] = v[k + 1];
+        if (i + k + 2 < n) counts[i + k + 2] = v[k + 2];
+      }
+    }
     carry = all;
     __syncthreads();
   }
