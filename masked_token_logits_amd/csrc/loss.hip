@@ -98,7 +98,14 @@ template <int THREADS>
 __device__ __forceinline__ void total_of(const float* terms, int M, float* loss) {
   __shared__ double part[THREADS / 64];
   double s = 0.0;
-  for (int i = threadIdx.x; i < M; i += THREADS) s += (double)__hip_atomic_load(terms + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int i0 = threadIdx.x; i0 < M; i0 += 8 * THREADS) {
+    float t[8];  // loaded together; past the chip's own cache, since other chips' workgroups wrote them
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      t[k] = __hip_atomic_load(terms + min(i0 + k * THREADS, M - 1), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += i0 + k * THREADS < M ? (double)t[k] : 0.0;
+  }
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
@@ -116,9 +123,9 @@ __global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* __restrict__ 
                                                    int d, int L, const int32_t* __restrict__ targets,
                                                    const float* __restrict__ weights,
                                                    const int32_t* __restrict__ idx, const int32_t* __restrict__ ctr,
-                                                   Partials p, float* terms, float* __restrict__ losses,
-                                                   float* __restrict__ lse, int32_t* __restrict__ ended,
-                                                   float* __restrict__ loss) {
+                                                   Partials p, bool records, float* terms,
+                                                   float* __restrict__ losses, float* __restrict__ lse,
+                                                   int32_t* __restrict__ ended, float* __restrict__ loss) {
   const int M = min(ctr[0], L), slices = ctr[3];
   const int lane = threadIdx.x & 63;
   for (int row = blockIdx.x * 4 + (threadIdx.x >> 6); row < M; row += gridDim.x * 4) {
@@ -136,8 +143,14 @@ __global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* __restrict__ 
     const size_t base = (size_t)row * (size_t)slices;
     for (int j = lane; j < slices; j += 64) {
       RowState y = row_state_empty();
-      y.m = p.m[base + j];
-      y.s = p.s[base + j];
+      if (records) {  // the few-row GEMM's (m, index, s, 0)
+        const float4 rec = reinterpret_cast<const float4*>(p.m)[base + j];
+        y.m = rec.x;
+        y.s = rec.z;
+      } else {
+        y.m = p.m[base + j];
+        y.s = p.s[base + j];
+      }
       row_merge<false>(r, y);
     }
 #pragma unroll
@@ -239,6 +252,13 @@ bool sizes_ok(int64_t V, int64_t d, int64_t L) {
 }
 bool supported(int64_t d) { return d % 8 == 0 && d < ((int64_t)1 << 20); }
 
+// The readout's few-row GEMM takes up to 32 rows: its slices, and four floats
+// for each row's partial.
+int64_t stream_slices(int64_t V) {
+  const int64_t n = (V + kSmallBN - 1) / kSmallBN;
+  return n < kMaxSmallSlices ? n : kMaxSmallSlices;
+}
+
 // Up to so many rows, forward is the small tiles' (k_loss_lse_few): few rows of
 // a small head, and any of so little work that an empty launch of the persistent
 // GEMM would count (512 positions, 4096 entries of 256: 19 -> 16 us).
@@ -250,7 +270,11 @@ int few_rows(int64_t V, int64_t d, int64_t L) {
 // Partials of the forward product: the persistent GEMM's plan, or a slice for
 // each tile of few rows.
 int64_t part_cap(int64_t V, int64_t d, int64_t L) {
-  const int64_t many = (L + kLargeBM - 1) / kLargeBM * kLargeBM * kMaxLargeSlices;
+  int64_t many = (L + kLargeBM - 1) / kLargeBM * kLargeBM * kMaxLargeSlices;
+  // room for a plan that gives every compute unit an item, with one row tile, too
+  // (102 rows, 126464 entries of 4096: 240 us; with 64 slices, for 256 rows, 540)
+  if (many < kLargeBM * 1024) many = kLargeBM * 1024;
+  if (L <= kSmallBM && many < 4 * kSmallBM * stream_slices(V)) many = 4 * kSmallBM * stream_slices(V);
   const int64_t few = (L < few_rows(V, d, L) ? L : few_rows(V, d, L)) * loss_few_slices(V);
   return many > few ? many : few;
 }
@@ -375,7 +399,8 @@ dllm_status dllm_loss_forward(const dllm_loss* p, float* loss, float* losses, fl
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   dllm::Rows r;
   dllm::carve(p->V, p->d, L, 0, reinterpret_cast<uint8_t*>(workspace), &r);
-  // as the readout chooses it: the persistent GEMM where its 32-bit offsets reach, else the streaming one
+  // as the readout chooses it: up to 32 rows the few-row GEMM, more the persistent one where its
+  // 32-bit offsets reach, else the streaming one; or the small tiles
   const int64_t n_vt = (p->V + dllm::kLargeBN - 1) / dllm::kLargeBN, n_rt = (L + dllm::kLargeBM - 1) / dllm::kLargeBM;
   const bool persistent = p->d % dllm::kPersistBK == 0 && (int64_t)dllm::kPersistBN * p->d * 2 < ((int64_t)1 << 32) &&
                           (p->d % dllm::kPersistWideBK == 0 || L * p->d * 2 < ((int64_t)1 << 32));
@@ -391,13 +416,19 @@ dllm_status dllm_loss_forward(const dllm_loss* p, float* loss, float* losses, fl
     plan.fixed_slices = (int)(s < n_vt ? s : n_vt);
   }
   const int few = dllm::few_rows(p->V, p->d, L);
+  const bool stream_w = few == 0 && L <= dllm::kSmallBM;
+  if (stream_w) plan.fixed_slices = (int)dllm::stream_slices(p->V);
   const dllm::CompactArgs ca = {p->mask, p->targets, (int)L, (int)p->V, plan, few, (int)dllm::loss_few_slices(p->V),
                                 losses,  lse,        r.idx,  r.ctr,     r.zeros};
   hipLaunchKernelGGL(dllm::k_loss_compact, dim3(1), dim3(dllm::kCompactThreads), 0, st, ca);
   // How many rows there are is known on the device: the persistent GEMM or the product of few rows
   // returns at once.  The streaming GEMM does few rows too, so that product comes behind it.
   const dllm::LseArgs la = {p->W_lm, p->hidden, r.zeros, r.idx, r.ctr, r.part.m, r.part.s, (int)p->V, (int)p->d, (int)L, few};
-  if (L > few) {
+  if (stream_w) {
+    if (dllm::launch_gemm_small(p->W_lm, p->hidden, (int)p->d, (int)p->V, r.idx, r.ctr, plan.fixed_slices, r.part, nullptr, st) !=
+        hipSuccess)
+      return DLLM_ERR_HIP;
+  } else if (L > few) {
     const hipError_t e =
         persistent ? dllm::launch_gemm_persistent(p->W_lm, p->hidden, (int)p->d, (int)p->V, r.idx, r.ctr, cus, r.part, st)
                    : dllm::launch_gemm_large(p->W_lm, p->hidden, (int)p->d, (int)p->V, r.idx, r.ctr, (int)n_rt,
@@ -408,7 +439,7 @@ dllm_status dllm_loss_forward(const dllm_loss* p, float* loss, float* losses, fl
   // the last workgroup to end adds up to 4096 terms itself; more are a kernel's of more threads
   const bool ends = L <= 4096;
   hipLaunchKernelGGL(dllm::k_loss_rows, dim3(dllm::grid_for((L + 3) / 4, 65536)), dim3(256), 0, st, p->W_lm, p->hidden,
-                     (int)p->d, (int)L, p->targets, p->weights, r.idx, r.ctr, r.part, r.terms, losses, lse, r.ctr + 5,
+                     (int)p->d, (int)L, p->targets, p->weights, r.idx, r.ctr, r.part, stream_w, r.terms, losses, lse, r.ctr + 5,
                      ends ? loss : nullptr);
   if (!ends) hipLaunchKernelGGL(dllm::k_loss_total, dim3(1), dim3(1024), 0, st, r.terms, r.ctr, (int)L, loss);
   return hipGetLastError() == hipSuccess ? DLLM_OK : DLLM_ERR_HIP;

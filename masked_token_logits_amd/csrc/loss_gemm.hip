@@ -172,7 +172,8 @@ struct Lane {
 // work.begin(cursor) is called before a tile's first stage, and
 // work.end(cursor, spare, fr, read) behind the last one for each of the lane's
 // rows: read(fv, j, z) gives four accumulators, spare is 8 KiB of LDS of the wave's.
-template <bool A_BY_K, bool A_TAIL, bool B_BY_K, class Work>
+// STREAM_A: the first operand's tiles are read by this workgroup only.
+template <bool A_BY_K, bool A_TAIL, bool B_BY_K, bool STREAM_A, class Work>
 __device__ __forceinline__ void run_tiles(uint16_t* lds, Work& work) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -200,9 +201,7 @@ __device__ __forceinline__ void run_tiles(uint16_t* lds, Work& work) {
   sa.start(it.a);
   sb.start(it.b);
   auto next_slot = [](int s) { return s + 2 >= SLOTS ? s + 2 - SLOTS : s + 2; };
-  auto dma = [&](const char* src, int slot, int j) {
-    __builtin_amdgcn_global_load_lds((const void*)src, (LDS_AS void*)(lds + slot * OPT + (wave + 4 * j) * 512), 16, 0, 0);
-  };
+  constexpr int kPolicy = STREAM_A ? 2 : 0;  // 2: non-temporal
   // before a stage's first DMA of a side: the next tile's, where this one's are all queued
   auto turn_a = [&]() {
     if (a_left > 0) return;
@@ -222,8 +221,14 @@ __device__ __forceinline__ void run_tiles(uint16_t* lds, Work& work) {
     b_K = n.stages * BK;
     b_left = n.stages;
   };
-  auto issue_a = [&](int j) { dma(sa.source(j, a_k0), a_slot, j); };
-  auto issue_b = [&](int j) { dma(sb.source(j, b_k0), b_slot, j); };
+  auto issue_a = [&](int j) {
+    __builtin_amdgcn_global_load_lds((const void*)sa.source(j, a_k0), (LDS_AS void*)(lds + a_slot * OPT + (wave + 4 * j) * 512), 16,
+                                     0, kPolicy);
+  };
+  auto issue_b = [&](int j) {
+    __builtin_amdgcn_global_load_lds((const void*)sb.source(j, b_k0), (LDS_AS void*)(lds + b_slot * OPT + (wave + 4 * j) * 512), 16,
+                                     0, 0);
+  };
   auto advance_a = [&]() {
     a_slot = next_slot(a_slot);
     a_k0 = a_k0 + BK == a_K ? 0 : a_k0 + BK;
@@ -482,7 +487,11 @@ __global__ __launch_bounds__(NT, 1) void k_loss_dz(GradArgs a) {
   __shared__ __attribute__((aligned(1024))) uint16_t lds[SLOTS * OPT];
   const int M = min(a.ctr[0], a.L);
   DzWork<TAIL> work = {a, (M + BK - 1) / BK * BK, (a.n + BK - 1) / BK * BK, (M + BT - 1) / BT, (a.n + BT - 1) / BT, Lane()};
-  run_tiles<false, TAIL, false>(lds, work);
+  // With one row tile W is streamed (102 rows, 126464 entries of 4096: 217 -> 198 us); more share its tiles.
+  if (work.n_rt <= 1)
+    run_tiles<false, TAIL, false, true>(lds, work);
+  else
+    run_tiles<false, TAIL, false, false>(lds, work);
 }
 
 // d_hidden has rows / 256 x d / 256 tiles, often fewer than compute units or a
@@ -597,7 +606,7 @@ __global__ __launch_bounds__(NT, 1) void k_loss_d_hidden(GradArgs a) {
       if (s1 <= s0)  // a part that this piece does not reach, and a later one may
         for (int i = 0; i < BT * BT / 4 / NT; ++i) share[i * NT] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-  run_tiles<true, false, false>(lds, work);
+  run_tiles<true, false, false, false>(lds, work);
 }
 
 // d_hidden of a tile: its shares added, in the order of the cuts.
@@ -704,7 +713,7 @@ __global__ __launch_bounds__(NT, 1) void k_loss_d_W(GradArgs a) {
   const int M = min(a.ctr[0], a.L);
   if (M <= kLossFew) return;  // k_loss_d_W_few's
   DWWork work = {a, (M + BK - 1) / BK * BK, (a.n + BT - 1) / BT, (a.d + BT - 1) / BT, Lane()};
-  run_tiles<true, false, true>(lds, work);
+  run_tiles<true, false, true, false>(lds, work);
 }
 
 // d_W of few rows: K is a few stages and the time is d_W's own bytes, so what
@@ -772,7 +781,10 @@ __global__ __launch_bounds__(NT, 3) void k_loss_d_W_few(GradArgs a, int n_vt, in
           [](LDS_AS uint8_t*, int, int) {},
           [&](int row, int col, const uint4& u) {
             const int r = first + row - wr * 32;
-            if (r < a.n && c0 + col < a.d) *reinterpret_cast<uint4*>(a.d_W + (int64_t)(a.v0 + r) * a.d + c0 + col) = u;
+            // written once and not read here: kept out of the caches that W's next pass wants (274 -> 248 us)
+            if (r < a.n && c0 + col < a.d)
+              __builtin_nontemporal_store(u32x4{u.x, u.y, u.z, u.w},
+                                          reinterpret_cast<u32x4*>(a.d_W + (int64_t)(a.v0 + r) * a.d + c0 + col));
           });
       continue;
     }

@@ -93,6 +93,8 @@ CASES = [  # L, d, V, ratio, piece
     (700, 200, 777, 0.7, 256),
     (1100, 64, 300, 0.02, None),    # few rows of many positions
     (130, 1024, 640, 1.0, None),
+    (32, 72, 70001, 0.9, 8192),     # the readout's few rows
+    (7, 128, 140000, 1.0, None),
     (40, 72, 70001, 0.9, 8192),     # few rows of a large head
     (600, 128, 65537, 0.3, 16384),  # two tiles of them
     (260, 64, 66000, 1.0, None),    # just over few
