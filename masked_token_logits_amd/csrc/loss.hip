@@ -1,7 +1,7 @@
 // Host side and row kernels of the masked cross entropy (include/dllm_loss.h).
 //
 // Forward is the readout's projection: the counted rows are compacted, the
-// LM-head GEMM (for few rows of a small head the loss's own) folds each row's logits into
+// LM-head GEMM (for small products the loss's own) folds each row's logits into
 // a running maximum and sum per vocabulary slice, and a wave for each row joins
 // the slices and takes the target's logit.  Backward walks the vocabulary in pieces (loss_gemm.hip).
 #include "dllm_loss.h"
@@ -24,8 +24,7 @@ __device__ __forceinline__ bool counts(uint8_t mask, int target, int V) { return
 // The positions that count, ascending, and zeros for the others' outputs.  One
 // workgroup walks them in chunks, 16 positions to a thread; a thread's place in
 // the list comes from the ballots of its count's bits and the waves before it.
-// It also says how the forward product is split: few rows have slices of their
-// own (k_loss_lse_few) and none of the persistent GEMM's row tiles.
+// It also makes the persistent GEMM's plan, now that the number of rows is known.
 constexpr int kCompactThreads = 1024;
 
 struct CompactArgs {
@@ -33,7 +32,6 @@ struct CompactArgs {
   const int32_t* targets;
   int L, V;
   PlanParams plan;
-  int few, few_slices;  // up to so many rows have slices of their own
   float *losses, *lse;  // null: not wanted
   int32_t *idx, *ctr;
   uint16_t* zeros;      // 16 bytes of zeros for the products
@@ -82,8 +80,8 @@ __global__ __launch_bounds__(kCompactThreads) void k_loss_compact(CompactArgs a)
     M += total;
     __syncthreads();
   }
-  int S = a.few_slices, n_rt = 0;
-  if (M > a.few) choose_plan(M, a.plan, &best, S, n_rt);
+  int S, n_rt;
+  choose_plan(M, a.plan, &best, S, n_rt);
   if (tid == 0) {
     a.ctr[0] = M;
     a.ctr[3] = S;
@@ -259,23 +257,15 @@ int64_t stream_slices(int64_t V) {
   return n < kMaxSmallSlices ? n : kMaxSmallSlices;
 }
 
-// Up to so many rows, forward is the small tiles' (k_loss_lse_few): few rows of
-// a small head, and any of so little work that an empty launch of the persistent
-// GEMM would count (512 positions, 4096 entries of 256: 19 -> 16 us).
-int few_rows(int64_t V, int64_t d, int64_t L) {
-  if (V > kLossSmallHead) return 0;
-  return L * V * d <= (int64_t)1 << 31 ? (int)L : kLossFew;
-}
-
 // Partials of the forward product: the persistent GEMM's plan, or a slice for
 // each tile of few rows.
-int64_t part_cap(int64_t V, int64_t d, int64_t L) {
+int64_t part_cap(int64_t V, int64_t L) {
   int64_t many = (L + kLargeBM - 1) / kLargeBM * kLargeBM * kMaxLargeSlices;
   // room for a plan that gives every compute unit an item, with one row tile, too
   // (102 rows, 126464 entries of 4096: 240 us; with 64 slices, for 256 rows, 540)
   if (many < kLargeBM * 1024) many = kLargeBM * 1024;
   if (L <= kSmallBM && many < 4 * kSmallBM * stream_slices(V)) many = 4 * kSmallBM * stream_slices(V);
-  const int64_t few = (L < few_rows(V, d, L) ? L : few_rows(V, d, L)) * loss_few_slices(V);
+  const int64_t few = loss_small(V, L) ? L * loss_few_slices(V) : 0;
   return many > few ? many : few;
 }
 
@@ -306,9 +296,9 @@ size_t carve(int64_t V, int64_t d, int64_t L, int64_t piece, uint8_t* base, Rows
   x.ctr = reinterpret_cast<int32_t*>(take(16 * 4));
   if (piece == 0) {
     x.terms = reinterpret_cast<float*>(take((size_t)L * 4));
-    x.part.m = reinterpret_cast<float*>(take((size_t)part_cap(V, d, L) * 4));
-    x.part.a = reinterpret_cast<int32_t*>(take((size_t)part_cap(V, d, L) * 4));
-    x.part.s = reinterpret_cast<float*>(take((size_t)part_cap(V, d, L) * 4));
+    x.part.m = reinterpret_cast<float*>(take((size_t)part_cap(V, L) * 4));
+    x.part.a = reinterpret_cast<int32_t*>(take((size_t)part_cap(V, L) * 4));
+    x.part.s = reinterpret_cast<float*>(take((size_t)part_cap(V, L) * 4));
   } else {
     const size_t rows = (size_t)loss_padded(L);
     x.bias = reinterpret_cast<float*>(take(rows * 4));
@@ -400,7 +390,7 @@ dllm_status dllm_loss_forward(const dllm_loss* p, float* loss, float* losses, fl
   dllm::Rows r;
   dllm::carve(p->V, p->d, L, 0, reinterpret_cast<uint8_t*>(workspace), &r);
   // as the readout chooses it: up to 32 rows the few-row GEMM, more the persistent one where its
-  // 32-bit offsets reach, else the streaming one; or the small tiles
+  // 32-bit offsets reach, else the streaming one; but small products have tiles of their own
   const int64_t n_vt = (p->V + dllm::kLargeBN - 1) / dllm::kLargeBN, n_rt = (L + dllm::kLargeBM - 1) / dllm::kLargeBM;
   const bool persistent = p->d % dllm::kPersistBK == 0 && (int64_t)dllm::kPersistBN * p->d * 2 < ((int64_t)1 << 32) &&
                           (p->d % dllm::kPersistWideBK == 0 || L * p->d * 2 < ((int64_t)1 << 32));
@@ -409,35 +399,28 @@ dllm_status dllm_loss_forward(const dllm_loss* p, float* loss, float* losses, fl
   plan.n_vt = (int)n_vt;
   plan.grid = cus;
   plan.max_slices = 1024;
-  plan.part_cap = dllm::part_cap(p->V, p->d, L);
+  plan.part_cap = dllm::part_cap(p->V, L);
   if (!persistent) {
     int64_t s = (4 * (int64_t)cus + n_rt - 1) / n_rt;
     if (s > dllm::kMaxLargeSlices) s = dllm::kMaxLargeSlices;
     plan.fixed_slices = (int)(s < n_vt ? s : n_vt);
   }
-  const int few = dllm::few_rows(p->V, p->d, L);
-  const bool stream_w = few == 0 && L <= dllm::kSmallBM;
+  const bool small = dllm::loss_small(p->V, L), stream_w = !small && L <= dllm::kSmallBM;
+  if (small) plan.fixed_slices = (int)dllm::loss_few_slices(p->V);
   if (stream_w) plan.fixed_slices = (int)dllm::stream_slices(p->V);
-  const dllm::CompactArgs ca = {p->mask, p->targets, (int)L, (int)p->V, plan, few, (int)dllm::loss_few_slices(p->V),
-                                losses,  lse,        r.idx,  r.ctr,     r.zeros};
+  const dllm::CompactArgs ca = {p->mask, p->targets, (int)L, (int)p->V, plan, losses, lse, r.idx, r.ctr, r.zeros};
   hipLaunchKernelGGL(dllm::k_loss_compact, dim3(1), dim3(dllm::kCompactThreads), 0, st, ca);
-  // How many rows there are is known on the device: the persistent GEMM or the product of few rows
-  // returns at once.  The streaming GEMM does few rows too, so that product comes behind it.
-  const dllm::LseArgs la = {p->W_lm, p->hidden, r.zeros, r.idx, r.ctr, r.part.m, r.part.s, (int)p->V, (int)p->d, (int)L, few};
-  if (stream_w) {
-    if (dllm::launch_gemm_small(p->W_lm, p->hidden, (int)p->d, (int)p->V, r.idx, r.ctr, plan.fixed_slices, r.part, nullptr, st) !=
-        hipSuccess)
-      return DLLM_ERR_HIP;
-  } else if (L > few) {
-    const hipError_t e =
-        persistent ? dllm::launch_gemm_persistent(p->W_lm, p->hidden, (int)p->d, (int)p->V, r.idx, r.ctr, cus, r.part, st)
-                   : dllm::launch_gemm_large(p->W_lm, p->hidden, (int)p->d, (int)p->V, r.idx, r.ctr, (int)n_rt,
-                                             plan.fixed_slices, r.part, st);
-    if (e != hipSuccess) return DLLM_ERR_HIP;
-  }
-  if (few > 0 && dllm::launch_loss_lse_few(la, st) != hipSuccess) return DLLM_ERR_HIP;
-  // the last workgroup to end adds up to 4096 terms itself; more are a kernel's of more threads
-  const bool ends = L <= 4096;
+  const dllm::LseArgs la = {p->W_lm, p->hidden, r.zeros, r.idx, r.ctr, r.part.m, r.part.s, (int)p->V, (int)p->d, (int)L};
+  const int V = (int)p->V, d = (int)p->d;
+  const hipError_t e = small      ? dllm::launch_loss_lse_small(la, st)
+                       : stream_w ? dllm::launch_gemm_small(p->W_lm, p->hidden, d, V, r.idx, r.ctr, plan.fixed_slices, r.part, nullptr, st)
+                       : persistent
+                           ? dllm::launch_gemm_persistent(p->W_lm, p->hidden, d, V, r.idx, r.ctr, cus, r.part, st)
+                           : dllm::launch_gemm_large(p->W_lm, p->hidden, d, V, r.idx, r.ctr, (int)n_rt, plan.fixed_slices, r.part, st);
+  if (e != hipSuccess) return DLLM_ERR_HIP;
+  // The last workgroup to end adds up to 512 terms itself.  More are another kernel's: each workgroup's arrival
+  // waits for its chip's cache to be written back (4096 rows: 49 us; 9 in two kernels).
+  const bool ends = L <= 512;
   hipLaunchKernelGGL(dllm::k_loss_rows, dim3(dllm::grid_for((L + 3) / 4, 65536)), dim3(256), 0, st, p->W_lm, p->hidden,
                      (int)p->d, (int)L, p->targets, p->weights, r.idx, r.ctr, r.part, stream_w, r.terms, losses, lse, r.ctr + 5,
                      ends ? loss : nullptr);
@@ -481,7 +464,7 @@ dllm_status dllm_loss_backward(const dllm_loss* p, const float* lse, const float
   dllm::PlanParams plan = {};
   plan.fixed_slices = 1;
   plan.tile_rows = dllm::kLargeBM;
-  const dllm::CompactArgs ca = {p->mask, p->targets, (int)L, (int)V, plan, 0, 1, nullptr, nullptr, r.idx, r.ctr, r.zeros};
+  const dllm::CompactArgs ca = {p->mask, p->targets, (int)L, (int)V, plan, nullptr, nullptr, r.idx, r.ctr, r.zeros};
   hipLaunchKernelGGL(dllm::k_loss_compact, dim3(1), dim3(dllm::kCompactThreads), 0, st, ca);
   const int dp = (int)dllm::loss_padded(d), grid = cus < dllm::kLossGrid ? cus : dllm::kLossGrid;
   const dllm::PrepareArgs pa = {p->W_lm, p->hidden, p->mask, p->targets, p->weights, grad,   lse,   r.idx,    r.ctr,  (int)V,

@@ -804,52 +804,41 @@ __global__ __launch_bounds__(NT, 3) void k_loss_d_W_few(GradArgs a, int n_vt, in
   }
 }
 
-// Forward for few rows of a small head, which gives the persistent GEMM few
-// tiles: 128 rows x 128 entries to a workgroup, 64 x 64 to a wave, two 32 KiB
-// stages in LDS and two workgroups to a compute unit (256 rows, 4096 entries of
-// 256: 7.0 us; the persistent GEMM 15.9).  A large head is the persistent GEMM's:
-// there these tiles, two to a unit, keep too few bytes on their way (102 rows,
-// 126464 entries of 4096: 394 us; the persistent GEMM 240).
-constexpr int FR = 128;  // rows of a tile
+// Small products, whose 256 x 256 tiles would leave most of the chip idle: 128
+// rows x 128 entries to a workgroup, 64 x 64 to a wave, and a ring of four 32 KiB
+// stages with one barrier each, three stages ahead: with few tiles nothing else
+// hides the memory's latency (3700 rows, 1000 entries of 1024: 16 us, where the persistent GEMM takes 38; 16 rows, 500 entries of 2048: 21).
+constexpr int FR = 128, FV2 = kLossFewEntries, FRING = 4;
+constexpr int FSTAGE = BK * (FR + FV2);  // elements of a stage
 
+// pw, ph: where this lane's DMAs read W and the rows (row (wave + 4 j) * 8 + lane / 8 of each side, 16-byte
+// piece ^ ((row >> 1) & 7) of it); K's stages from k0 on, then those before; zeros behind d.
 template <bool TAIL>
-__global__ __launch_bounds__(NT, 2) void k_loss_lse_few(LseArgs a, int n_rt, int slices) {
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[2 * BK * (FR + kLossFewEntries)];
-  __shared__ float wave_m[2][FR], wave_s[2][FR];
-  const int M = min(a.ctr[0], a.L);
-  const int vt = blockIdx.x / n_rt, rt = blockIdx.x - vt * n_rt, r0 = rt * FR, c0 = vt * kLossFewEntries;
-  if (M > a.few || r0 >= M) return;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wr = wave >> 1, wv = wave & 1;
-  // DMA j of a wave has rows (wave + 4 j) * 8 + lane / 8 of a side; row r holds its 16-byte pieces at piece ^ ((r >> 1) & 7)
+__device__ __forceinline__ void small_product(uint16_t* lds, const uint16_t* const (&pw)[4], const uint16_t* const (&ph)[4],
+                                              int stages, int k0, int d, const uint16_t* zeros, f32x16 (&acc)[2][2]) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave >> 1, wv = wave & 1;
   const int row = wave * 8 + (lane >> 3), col = ((lane & 7) ^ ((row >> 1) & 7)) * 8;
-  const uint16_t *pw[4], *ph[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    pw[j] = a.W + (int64_t)min(c0 + row + 32 * j, a.V - 1) * a.d + col;
-    ph[j] = a.H + (int64_t)a.idx[min(r0 + row + 32 * j, M - 1)] * a.d + col;
-  }
-  const int stages = (a.d + BK - 1) / BK;
-  int k0 = vt * 7 % stages * BK;  // W's rows may be powers of two apart: not all tiles at the same place of them
   auto issue = [&](int slot) {
-    const bool in = !TAIL || k0 + col < a.d;
-    uint16_t* to = lds + slot * BK * (FR + kLossFewEntries) + wave * 512;
+    const bool in = !TAIL || k0 + col < d;
+    uint16_t* to = lds + slot * FSTAGE + wave * 512;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      __builtin_amdgcn_global_load_lds((const void*)(in ? pw[j] + k0 : a.zeros), (LDS_AS void*)(to + 4 * j * 512), 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((const void*)(in ? ph[j] + k0 : a.zeros),
-                                       (LDS_AS void*)(to + BK * kLossFewEntries + 4 * j * 512), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((const void*)(in ? pw[j] + k0 : zeros), (LDS_AS void*)(to + 4 * j * 512), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((const void*)(in ? ph[j] + k0 : zeros), (LDS_AS void*)(to + BK * FV2 + 4 * j * 512), 16, 0, 0);
     }
     k0 = k0 + BK >= stages * BK ? 0 : k0 + BK;
   };
+  // stages behind the last are the first ones again, and never used
   issue(0);
-  issue(1);  // with one stage, the same again: never used
-  f32x16 acc[2][2] = {};
+  issue(1);
+  issue(2);
   const int swz = ((lane & 31) >> 1) & 7;
   for (int q = 0; q < stages; ++q) {
-    stage_sync<8>();  // stage q has landed; the next one's DMAs may be in flight
-    const uint16_t* w = lds + (q & 1) * BK * (FR + kLossFewEntries) + (wv * 64 + (lane & 31)) * BK;
-    const uint16_t* h = lds + (q & 1) * BK * (FR + kLossFewEntries) + BK * kLossFewEntries + (wr * 64 + (lane & 31)) * BK;
+    stage_sync<16>();  // stage q has landed, the two behind it may be in flight; and every wave has read stage q - 1
+    issue((q + 3) & (FRING - 1));
+    const uint16_t* w = lds + (q & (FRING - 1)) * FSTAGE + (wv * 64 + (lane & 31)) * BK;
+    const uint16_t* h = lds + (q & (FRING - 1)) * FSTAGE + BK * FV2 + (wr * 64 + (lane & 31)) * BK;
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       const int piece = ((kk * 2 + (lane >> 5)) ^ swz) * 8;
@@ -864,9 +853,28 @@ __global__ __launch_bounds__(NT, 2) void k_loss_lse_few(LseArgs a, int n_rt, int
 #pragma unroll
         for (int fr = 0; fr < 2; ++fr) acc[fv][fr] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fw[fv], fh[fr], acc[fv][fr], 0, 0, 0);
     }
-    stage_sync<8>();  // every wave has read the slot
-    issue(q & 1);
   }
+  stage_sync<0>();  // the DMAs behind the last stage
+}
+
+template <bool TAIL>
+__global__ __launch_bounds__(NT, 1) void k_loss_lse_small(LseArgs a, int n_rt, int slices) {
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[FRING * FSTAGE];
+  const int M = min(a.ctr[0], a.L);
+  const int vt = blockIdx.x / n_rt, rt = blockIdx.x - vt * n_rt, r0 = rt * FR, c0 = vt * FV2;
+  if (r0 >= M) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wr = wave >> 1, wv = wave & 1;
+  const int row = wave * 8 + (lane >> 3), col = ((lane & 7) ^ ((row >> 1) & 7)) * 8, stages = (a.d + BK - 1) / BK;
+  const uint16_t *pw[4], *ph[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    pw[j] = a.W + (int64_t)min(c0 + row + 32 * j, a.V - 1) * a.d + col;
+    ph[j] = a.H + (int64_t)a.idx[min(r0 + row + 32 * j, M - 1)] * a.d + col;
+  }
+  f32x16 acc[2][2] = {};
+  small_product<TAIL>(lds, pw, ph, stages, vt * 7 % stages * BK, a.d, a.zeros, acc);
+  float* wave_m = reinterpret_cast<float*>(lds);  // [2][FR] of the two waves with the same rows
+  float* wave_s = wave_m + 2 * FR;
   auto off = [](int x) { return 8 * (x >> 2) + (x & 3); };
 #pragma unroll
   for (int fr = 0; fr < 2; ++fr) {
@@ -879,23 +887,63 @@ __global__ __launch_bounds__(NT, 2) void k_loss_lse_few(LseArgs a, int n_rt, int
       for (int x = 0; x < 16; ++x) z[x] = v + off(x) < a.V ? acc[fv][fr][x] : -INFINITY;
       row_fold<false, 16>(r, z, 0, off);
     }
-    const RowState y = shfl_xor_state(r, 32);
-    row_merge<false>(r, y);
+    row_merge<false>(r, shfl_xor_state(r, 32));
     if (lane < 32) {
-      wave_m[wv][wr * 64 + fr * 32 + lane] = r.m;
-      wave_s[wv][wr * 64 + fr * 32 + lane] = r.s;
+      wave_m[wv * FR + wr * 64 + fr * 32 + lane] = r.m;
+      wave_s[wv * FR + wr * 64 + fr * 32 + lane] = r.s;
     }
   }
   __syncthreads();
   if (tid < FR && r0 + tid < M) {
     RowState x = row_state_empty(), y = row_state_empty();
-    x.m = wave_m[0][tid];
-    x.s = wave_s[0][tid];
-    y.m = wave_m[1][tid];
-    y.s = wave_s[1][tid];
+    x.m = wave_m[tid];
+    x.s = wave_s[tid];
+    y.m = wave_m[FR + tid];
+    y.s = wave_s[FR + tid];
     row_merge<false>(x, y);
     a.m[(int64_t)(r0 + tid) * slices + vt] = x.m;
     a.s[(int64_t)(r0 + tid) * slices + vt] = x.s;
+  }
+}
+
+template <bool TAIL>
+__global__ __launch_bounds__(NT, 1) void k_loss_dz_small(GradArgs a, int n_rt) {
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[FRING * FSTAGE];
+  const int M = min(a.ctr[0], a.L), Mp = (M + BK - 1) / BK * BK, np = (a.n + BK - 1) / BK * BK;
+  const int vt = blockIdx.x / n_rt, rt = blockIdx.x - vt * n_rt, r0 = rt * FR, c0 = vt * FV2;
+  if (r0 >= Mp) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wr = wave >> 1, wv = wave & 1;
+  const int row = wave * 8 + (lane >> 3), col = ((lane & 7) ^ ((row >> 1) & 7)) * 8, stages = a.dp / BK;
+  const uint16_t *pw[4], *ph[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    pw[j] = a.W + (int64_t)(a.v0 + min(c0 + row + 32 * j, a.n - 1)) * a.d + col;
+    ph[j] = a.rows + (int64_t)min(r0 + row + 32 * j, Mp - 1) * a.dp + col;
+  }
+  f32x16 acc[2][2] = {};
+  small_product<TAIL>(lds, pw, ph, stages, vt * 7 % stages * BK, a.d, a.zeros, acc);
+#pragma unroll
+  for (int fr = 0; fr < 2; ++fr) {
+    const int r = r0 + wr * 64 + fr * 32 + (lane & 31);
+    if (r >= Mp) continue;
+    const float bias = a.bias[r];
+    const uint32_t flip = a.flip[r], target = float_bf16(a.at_tgt[r]);
+    const int hit = a.tgt[r] - a.v0;
+#pragma unroll
+    for (int fv = 0; fv < 2; ++fv)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + wv * 64 + fv * 32 + 8 * j + 4 * (lane >> 5);
+        if (c >= np) continue;
+        uint32_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          b[i] = (float_bf16(__builtin_amdgcn_exp2f(fmaf(acc[fv][fr][4 * j + i], kLog2eF, bias))) ^ flip) & 0xFFFFu;
+          b[i] = c + i == hit ? target : b[i];
+          b[i] = c + i < a.n ? b[i] : 0u;
+        }
+        *reinterpret_cast<uint2*>(a.dz + (int64_t)r * a.ldz + c) = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+      }
   }
 }
 
@@ -961,20 +1009,28 @@ __global__ __launch_bounds__(64) void k_loss_put(GradArgs a) {
 
 }  // namespace
 
-hipError_t launch_loss_lse_few(const LseArgs& a, hipStream_t stream) {
-  const int n_rt = ((a.L < a.few ? a.L : a.few) + FR - 1) / FR, slices = (int)loss_few_slices(a.V);
+hipError_t launch_loss_lse_small(const LseArgs& a, hipStream_t stream) {
+  const int n_rt = (a.L + FR - 1) / FR, slices = (int)loss_few_slices(a.V);
   const dim3 grid((unsigned)slices * (unsigned)n_rt);
   if (a.d % BK == 0)
-    hipLaunchKernelGGL(k_loss_lse_few<false>, grid, dim3(NT), 0, stream, a, n_rt, slices);
+    hipLaunchKernelGGL(k_loss_lse_small<false>, grid, dim3(NT), 0, stream, a, n_rt, slices);
   else
-    hipLaunchKernelGGL(k_loss_lse_few<true>, grid, dim3(NT), 0, stream, a, n_rt, slices);
+    hipLaunchKernelGGL(k_loss_lse_small<true>, grid, dim3(NT), 0, stream, a, n_rt, slices);
   return hipGetLastError();
 }
 hipError_t launch_loss_dz(const GradArgs& a, int grid, hipStream_t stream) {
-  if (a.d % BK == 0)
+  if (loss_small(a.n, a.L)) {
+    const int n_rt = (a.L + FR - 1) / FR;
+    const dim3 small((unsigned)((a.n + FV2 - 1) / FV2) * (unsigned)n_rt);
+    if (a.d % BK == 0)
+      hipLaunchKernelGGL(k_loss_dz_small<false>, small, dim3(NT), 0, stream, a, n_rt);
+    else
+      hipLaunchKernelGGL(k_loss_dz_small<true>, small, dim3(NT), 0, stream, a, n_rt);
+  } else if (a.d % BK == 0) {
     hipLaunchKernelGGL(k_loss_dz<false>, dim3(grid), dim3(NT), 0, stream, a);
-  else
+  } else {
     hipLaunchKernelGGL(k_loss_dz<true>, dim3(grid), dim3(NT), 0, stream, a);
+  }
   return hipGetLastError();
 }
 hipError_t launch_loss_d_hidden(const GradArgs& a, int grid, hipStream_t stream) {

@@ -18,8 +18,7 @@ inline int64_t loss_padded(int64_t n) { return (n + kLossStep - 1) / kLossStep *
 // target's, is given back to the fp32 sums: to d_hidden always (one more row of W
 // each), to d_W with up to so many rows.  With more, d_W's errors average out to
 // 1.41 times the output's own rounding; with few, single rows decide them (102
-// rows: up to 1.6 times).  Up to as many, forward and d_W have kernels whose time
-// is the head's bytes.
+// rows: up to 1.6 times).  Up to as many, d_W has a kernel whose time is its own bytes.
 constexpr int kLossFew = 256;
 
 // The backward pass of one vocabulary piece.  Rows are the counted positions
@@ -45,19 +44,22 @@ struct GradArgs {
   int first, accumulate;
 };
 
-// Forward for few rows of a head of at most 512 tiles: the running maximum and
-// sum of each row and tile.
+// A product of L rows (at most) and n entries is small if its 256 x 256 tiles are
+// too few for half the chip; it then has tiles of 128 x 128.
+inline bool loss_small(int64_t n, int64_t L) {
+  return (n + kLossTile - 1) / kLossTile * ((L + kLossTile - 1) / kLossTile) <= kLossGrid / 2;
+}
+
+// The small forward product: the running maximum and sum of each row and tile.
 constexpr int kLossFewEntries = 128;  // of a tile
-constexpr int64_t kLossSmallHead = 512 * kLossFewEntries;
 inline int64_t loss_few_slices(int64_t V) { return (V + kLossFewEntries - 1) / kLossFewEntries; }
 struct LseArgs {
   const uint16_t *W, *H, *zeros;
   const int32_t *idx, *ctr;
   float *m, *s;  // [rows][slices]
   int V, d, L;
-  int few;       // with more rows than this it returns
 };
-hipError_t launch_loss_lse_few(const LseArgs& a, hipStream_t stream);
+hipError_t launch_loss_lse_small(const LseArgs& a, hipStream_t stream);
 
 // grid: workgroups of the products, the same for all of a call
 hipError_t launch_loss_dz(const GradArgs& a, int grid, hipStream_t stream);        // dz
