@@ -157,12 +157,15 @@ __global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* __restrict__ 
       row_merge<false>(r, shfl_xor_state(r, off));
     }
     if (lane == 0) {
-      const float l = row_finish<false>(r).lse;
+      // Logits this large lie 32 or more apart, or are the same: the sum's logarithm, at most 22, is less than half
+      // of that.  The running sum's reference, m log2(e) rounded, is then off by so much that the sum may be infinite.
+      const float l = fabsf(r.m) >= 0x1p29f ? r.m : row_finish<false>(r).lse;
       losses[pos] = l - z;
       lse[pos] = l;
       terms[row] = (l - z) * (weights ? weights[pos] : 1.f);
     }
-  }  if (!loss) return;
+  }
+  if (!loss) return;
   __shared__ int last;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -190,8 +193,7 @@ struct PrepareArgs {
   const int32_t *idx, *ctr;
   int V, L, d, dp;
   uint16_t* rows;
-  float* bias;
-  uint32_t* flip;
+  float *lse_of, *coef;
   int32_t* tgt;
   float *at_tgt, *left;
   uint16_t* d_hidden;
@@ -221,8 +223,8 @@ __global__ __launch_bounds__(256) void k_loss_prepare(PrepareArgs a) {
       for (int off = 32; off >= 1; off >>= 1) z += __shfl_xor(z, off);
       if (lane == 0) {
         const float lse = a.lse[pos], c = (a.weights ? a.weights[pos] : 1.f) * (a.grad ? *a.grad : 1.f);
-        a.bias[i] = __builtin_amdgcn_logf(fabsf(c)) - lse * kLog2eF;
-        a.flip[i] = c < 0.f ? 0x80008000u : 0u;
+        a.lse_of[i] = lse * kLossPScale;
+        a.coef[i] = fabsf(lse) < INFINITY ? c : NAN;
         a.tgt[i] = t;
         const float at = c * expm1f(z - lse);
         a.at_tgt[i] = at;
@@ -231,8 +233,8 @@ __global__ __launch_bounds__(256) void k_loss_prepare(PrepareArgs a) {
     } else if (i < Mp) {
       for (int c = 8 * lane; c < a.dp; c += 8 * 64) *reinterpret_cast<uint4*>(a.rows + (int64_t)i * a.dp + c) = none;
       if (lane == 0) {
-        a.bias[i] = -INFINITY;
-        a.flip[i] = 0u;
+        a.lse_of[i] = 0.f;
+        a.coef[i] = 0.f;
         a.tgt[i] = -1;
         a.at_tgt[i] = 0.f;
         a.left[i] = 0.f;
@@ -273,8 +275,7 @@ struct Rows {
   int32_t *idx, *ctr;
   float* terms;
   Partials part;
-  float* bias;
-  uint32_t* flip;
+  float *lse_of, *coef;
   int32_t* tgt;
   float *at_tgt, *left;
   uint16_t *zeros, *rows, *dz;
@@ -301,8 +302,8 @@ size_t carve(int64_t V, int64_t d, int64_t L, int64_t piece, uint8_t* base, Rows
     x.part.s = reinterpret_cast<float*>(take((size_t)part_cap(V, L) * 4));
   } else {
     const size_t rows = (size_t)loss_padded(L);
-    x.bias = reinterpret_cast<float*>(take(rows * 4));
-    x.flip = reinterpret_cast<uint32_t*>(take(rows * 4));
+    x.lse_of = reinterpret_cast<float*>(take(rows * 4));
+    x.coef = reinterpret_cast<float*>(take(rows * 4));
     x.tgt = reinterpret_cast<int32_t*>(take(rows * 4));
     x.at_tgt = reinterpret_cast<float*>(take(rows * 4));
     x.left = reinterpret_cast<float*>(take(rows * 4));
@@ -468,7 +469,7 @@ dllm_status dllm_loss_backward(const dllm_loss* p, const float* lse, const float
   hipLaunchKernelGGL(dllm::k_loss_compact, dim3(1), dim3(dllm::kCompactThreads), 0, st, ca);
   const int dp = (int)dllm::loss_padded(d), grid = cus < dllm::kLossGrid ? cus : dllm::kLossGrid;
   const dllm::PrepareArgs pa = {p->W_lm, p->hidden, p->mask, p->targets, p->weights, grad,   lse,   r.idx,    r.ctr,  (int)V,
-                                (int)L,  (int)d,    dp,      r.rows,     r.bias,     r.flip, r.tgt, r.at_tgt, r.left, d_hidden};
+                                (int)L,  (int)d,    dp,      r.rows,     r.lse_of,   r.coef, r.tgt, r.at_tgt, r.left, d_hidden};
   hipLaunchKernelGGL(dllm::k_loss_prepare, dim3(dllm::grid_for(dllm::loss_padded(L) / 4, 65536)), dim3(256), 0, st, pa);
   dllm::GradArgs a = {};
   a.W = p->W_lm;
@@ -476,8 +477,8 @@ dllm_status dllm_loss_backward(const dllm_loss* p, const float* lse, const float
   a.rows = r.rows;
   a.idx = r.idx;
   a.ctr = r.ctr;
-  a.bias = r.bias;
-  a.flip = r.flip;
+  a.lse = r.lse_of;
+  a.coef = r.coef;
   a.tgt = r.tgt;
   a.at_tgt = r.at_tgt;
   a.left = r.left;

@@ -403,8 +403,7 @@ struct DzWork {
   const GradArgs& a;
   int Mp, np, n_rt, n_vt;
   Lane at;
-  float bias[4], at_tgt[4];
-  uint32_t flip[4];
+  float lse[4], coef[4], at_tgt[4];
   int tgt[4];
   struct Cursor {
     int e, r0, c0;
@@ -445,8 +444,8 @@ struct DzWork {
 #pragma unroll
     for (int fr = 0; fr < 4; ++fr) {
       const int r = min(c.r0 + at.row(fr), Mp - 1);
-      bias[fr] = a.bias[r];
-      flip[fr] = a.flip[r];
+      lse[fr] = a.lse[r];
+      coef[fr] = a.coef[r];
       tgt[fr] = a.tgt[r];
       at_tgt[fr] = a.at_tgt[r];
     }
@@ -463,13 +462,12 @@ struct DzWork {
           float z[4];
           read(fv, j, z);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) z[i] = __builtin_amdgcn_exp2f(fmaf(z[i], kLog2eF, bias[fr]));
+          for (int i = 0; i < 4; ++i) z[i] = loss_p(z[i], lse[fr]) * coef[fr];
           if (!whole) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) z[i] = 32 * fv + 8 * j + i < end ? z[i] : 0.f;
           }
-          return u32x2{(float_bf16(z[0]) | float_bf16(z[1]) << 16) ^ flip[fr],
-                       (float_bf16(z[2]) | float_bf16(z[3]) << 16) ^ flip[fr]};
+          return u32x2{float_bf16(z[0]) | float_bf16(z[1]) << 16, float_bf16(z[2]) | float_bf16(z[3]) << 16};
         },
         [&](LDS_AS uint8_t* p, int r, int h) {
           if (h == 0 && hit >= 0 && hit < 128)
@@ -926,8 +924,8 @@ __global__ __launch_bounds__(NT, 1) void k_loss_dz_small(GradArgs a, int n_rt) {
   for (int fr = 0; fr < 2; ++fr) {
     const int r = r0 + wr * 64 + fr * 32 + (lane & 31);
     if (r >= Mp) continue;
-    const float bias = a.bias[r];
-    const uint32_t flip = a.flip[r], target = float_bf16(a.at_tgt[r]);
+    const float lse = a.lse[r], coef = a.coef[r];
+    const uint32_t target = float_bf16(a.at_tgt[r]);
     const int hit = a.tgt[r] - a.v0;
 #pragma unroll
     for (int fv = 0; fv < 2; ++fv)
@@ -938,7 +936,7 @@ __global__ __launch_bounds__(NT, 1) void k_loss_dz_small(GradArgs a, int n_rt) {
         uint32_t b[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          b[i] = (float_bf16(__builtin_amdgcn_exp2f(fmaf(acc[fv][fr][4 * j + i], kLog2eF, bias))) ^ flip) & 0xFFFFu;
+          b[i] = float_bf16(loss_p(acc[fv][fr][4 * j + i], lse) * coef);
           b[i] = c + i == hit ? target : b[i];
           b[i] = c + i < a.n ? b[i] : 0u;
         }

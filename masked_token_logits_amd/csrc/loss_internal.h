@@ -21,6 +21,15 @@ inline int64_t loss_padded(int64_t n) { return (n + kLossStep - 1) / kLossStep *
 // rows: up to 1.6 times).  Up to as many, d_W has a kernel whose time is its own bytes.
 constexpr int kLossFew = 256;
 
+// dz's probability, exp(z - lse): the difference is taken before anything rounds
+// it, as (lse - z) / 256 between 0 and 1 (the clamp is the multiply-add's own),
+// so logits of any size give no more than 1, and what lies 256 below gives 0.
+constexpr float kLossPScale = 1.0f / 256.0f;
+__device__ __forceinline__ float loss_p(float z, float scaled_lse) {
+  const float x = __builtin_amdgcn_fmed3f(fmaf(z, -kLossPScale, scaled_lse), 0.0f, 1.0f);
+  return __builtin_amdgcn_exp2f(x * (-1.44269504088896340736f / kLossPScale));
+}
+
 // The backward pass of one vocabulary piece.  Rows are the counted positions
 // in ascending order, M = ctr[0] of them, filled up to Mp with rows that have
 // no gradient.
@@ -29,8 +38,8 @@ struct GradArgs {
   const uint16_t* zeros;    // 16 bytes of them
   const uint16_t* rows;     // [Mp, dp] the counted rows of hidden, zeros behind d and M
   const int32_t *idx, *ctr;
-  const float* bias;        // [Mp] log2 |c| - log2(e) lse, c = grad * weight: |c| p = 2^(log2(e) z + bias); -inf behind M
-  const uint32_t* flip;     // [Mp] the sign bits of two bf16 where c < 0
+  const float* lse;         // [Mp] lse * kLossPScale; 0 behind M
+  const float* coef;        // [Mp] grad * weight; NaN where lse is not finite, 0 behind M
   const int32_t* tgt;       // [Mp] the target, -1 behind M
   const float* at_tgt;      // [Mp] dz there
   const float* left;        // [Mp] what its rounding to bf16 leaves of it

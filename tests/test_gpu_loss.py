@@ -202,6 +202,42 @@ def test_sure_and_hopeless_rows():
     _check_backward(dh, dW, a, o)
 
 
+@pytest.mark.parametrize("top", [10, 20, 40])
+def test_large_logits(top):
+    """Logits of up to 2^top that fp32 holds exactly, one hidden value and one weight each, and apart by
+    at least 2^-7 of that: no probability passes 1."""
+    import torch
+
+    import masked_token_logits_amd as mtl
+    L, d, V = 300, 64, 128
+    i, v, k = np.arange(L)[:, None], np.arange(V)[:, None], np.arange(d)[None, :]
+    Hf = np.where(i % d == k, 2.0 ** (top - i % 4) * np.where(i % 8 < 4, 1.0, -1.0), 0.0)
+    H, Hf = bf16_of(Hf)
+    W, Wf = bf16_of((1.0 + (v * 37 + k * 11) % V) / V)
+    t = ((np.arange(L) * 13) % V).astype(np.int32)
+    best = (Hf @ Wf.T).argmax(axis=1)
+    t[::3] = best[::3]
+    a = dict(H=H, Hf=Hf, W=W, Wf=Wf, mask=np.ones(L, np.uint8), t=t, w=(np.ones(L) / L).astype(np.float32))
+    x, head = _dev(a), mtl.MaskedLoss(dev_bf16(a["W"]))
+    got = head(x["hidden"], x["mask"], x["targets"], weights=x["weights"])
+    dh, dW = head.backward(x["hidden"], x["mask"], x["targets"], got[2], weights=x["weights"])
+    torch.cuda.synchronize()
+    o = ol.loss(a["Wf"], a["Hf"], a["mask"], a["t"], a["w"])
+    # the logits are exact; lse and the difference round to half a step of the largest, and lse is within 2^-17 besides
+    e = 2.0 ** -17 + 2.0 ** -24 * np.abs(o["lse"])
+    close(got[2], o["lse"], e, "lse")
+    close(got[1], o["losses"], e + 2.0 ** -24 * np.abs(o["losses"]), "losses")
+    # a probability below 1 that counts is of logits up to 2^10 alone, where e is below 2^-13
+    off = np.where(o["p"] < 1 - 2.0 ** -20, np.minimum(e, 2.0 ** -13)[:, None] * 2, 2.0 ** -16) * o["p"] / L
+    # fp32 and bf16 have no normal numbers below 2^-126: a probability, dz, a product, a sum or an output there may
+    # be zero instead, each off by less than that (this was left out at first: gradients of e-38 came out as 0)
+    step = HALF * np.abs(o["dz"]) + 2 * 2.0 ** -126
+    tol_h = (V + 2) * 2.0 ** -126 + (step + off) @ np.abs(a["Wf"]) + HALF * np.abs(o["d_hidden"]) + V * 2.0 ** -24 * (np.abs(o["dz"]) @ np.abs(a["Wf"]))
+    close(dh, o["d_hidden"], tol_h, "d_hidden")
+    tol_w = (L + 2) * 2.0 ** -126 + (step + off).T @ np.abs(Hf) + HALF * np.abs(o["d_W"]) + L * 2.0 ** -24 * (np.abs(o["dz"]).T @ np.abs(Hf))
+    close(dW, o["d_W"], tol_w, "d_W")
+
+
 def test_values_that_do_not_count_are_not_read_into_results():
     """NaN hidden states, weights and lse at positions that do not count change nothing."""
     import torch
