@@ -47,9 +47,10 @@ dllm_status dllm_embed(const uint16_t *table, int64_t V, int64_t d, const int32_
 size_t dllm_embed_backward_workspace_bytes(int64_t V, int64_t d, int64_t T);
 
 /*
- * The gradient of the table.
+ * The gradient of the table, of T < 2^30 tokens.
  *   d_out       [T, d] bf16
- *   d_table     [V, d] bf16, no overlap with tokens or d_out
+ *   d_table     [V, d] bf16, no overlap with tokens or d_out (nor has the
+ *               workspace)
  *   accumulate  0: every row is written (zero where no token is).
  *               1: added to what d_table holds, once and rounded once; rows
  *               of no token are not touched (a table tied to the LM head takes

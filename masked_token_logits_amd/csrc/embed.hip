@@ -377,6 +377,11 @@ bool sizes_ok(int64_t V, int64_t d, int64_t T) {
 }
 bool supported(int64_t d) { return d % 8 == 0 && d < ((int64_t)1 << 20); }
 
+// Of the gradient: its sums' grid, a wave for each 32 places and one for each 64
+// rows to clear, holds for fewer tokens than this.
+constexpr int64_t kPlacesMost = (int64_t)1 << 30;
+bool gradient_sizes_ok(int64_t V, int64_t d, int64_t T) { return sizes_ok(V, d, T) && T < kPlacesMost; }
+
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 int chunk_of(int64_t T) { return T <= kShortMost ? kChunkShort : kChunkMost; }
@@ -466,21 +471,22 @@ dllm_status dllm_embed(const uint16_t* table, int64_t V, int64_t d, const int32_
 }
 
 size_t dllm_embed_backward_workspace_bytes(int64_t V, int64_t d, int64_t T) {
-  if (!dllm::sizes_ok(V, d, T) || !dllm::supported(d)) return 0;
+  if (!dllm::gradient_sizes_ok(V, d, T) || !dllm::supported(d)) return 0;
   return dllm::carve(V, d, T, nullptr, nullptr);
 }
 
 dllm_status dllm_embed_backward(const int32_t* tokens, int64_t T, const uint16_t* d_out, int64_t V, int64_t d,
                                 float scale, int32_t accumulate, uint16_t* d_table, void* workspace,
                                 size_t workspace_bytes, void* stream) {
-  if (!dllm::sizes_ok(V, d, T) || !isfinite(scale) || (accumulate != 0 && accumulate != 1)) return DLLM_ERR_INVALID_ARG;
+  if (!dllm::gradient_sizes_ok(V, d, T) || !isfinite(scale) || (accumulate != 0 && accumulate != 1)) return DLLM_ERR_INVALID_ARG;
   if (!dllm::supported(d)) return DLLM_ERR_UNSUPPORTED;
   if (!d_table || (T > 0 && (!tokens || !d_out))) return DLLM_ERR_INVALID_ARG;
   if (!dllm::aligned(d_table, 16) || !dllm::aligned(d_out, 16) || !dllm::aligned(tokens, 4)) return DLLM_ERR_UNSUPPORTED;
   const size_t need = dllm_embed_backward_workspace_bytes(V, d, T), n = (size_t)V * (size_t)d * 2;
   if (!workspace || workspace_bytes < need || !dllm::aligned(workspace, 256)) return DLLM_ERR_WORKSPACE;
   if (dllm::overlaps(d_table, n, d_out, (size_t)T * (size_t)d * 2) || dllm::overlaps(d_table, n, tokens, (size_t)T * 4) ||
-      dllm::overlaps(d_table, n, workspace, need))
+      dllm::overlaps(d_table, n, workspace, need) || dllm::overlaps(workspace, need, tokens, (size_t)T * 4) ||
+      dllm::overlaps(workspace, need, d_out, (size_t)T * (size_t)d * 2))
     return DLLM_ERR_INVALID_ARG;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   dllm::Sorting w;

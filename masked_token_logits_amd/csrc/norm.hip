@@ -475,9 +475,10 @@ dllm_status dllm_residual_norm_backward(const dllm_norm* p, const uint16_t* x, c
   const size_t need = dllm_residual_norm_backward_workspace_bytes(p, T, groups);
   if (!workspace || workspace_bytes < need || !dllm::aligned(workspace, 256)) return DLLM_ERR_WORKSPACE;
   const dllm::Span in[] = {{x, rows},   {y, rows},     {gate, (size_t)groups * one}, {p->pre, one},
-                           {p->post, one}, {d_n, rows}, {d_x_out, rows},              {workspace, need}};
-  const dllm::Span out[] = {{d_x, rows}, {d_y, rows}, {d_pre, 2 * one}, {d_post, 2 * one}, {d_gate, 2 * (size_t)groups * one}};
-  for (int i = 0; i < 5; ++i) {
+                           {p->post, one}, {d_n, rows}, {d_x_out, rows}};
+  const dllm::Span out[] = {{d_x, rows},       {d_y, rows}, {d_pre, 2 * one}, {d_post, 2 * one}, {d_gate, 2 * (size_t)groups * one},
+                            {workspace, need}};
+  for (int i = 0; i < 6; ++i) {
     const void* same = i == 0 ? (const void*)d_x_out : i == 1 ? (const void*)y : nullptr;
     if (dllm::clashes(out[i], in, same, i == 0 ? d_n : nullptr)) return DLLM_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)

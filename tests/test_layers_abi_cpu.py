@@ -85,6 +85,25 @@ def test_residual_norm_backward_refused():
         assert _backward(d_x=_at(7), d_pre=None, d_post=None, d_gate=None) == E.DLLM_ERR_HIP
 
 
+def test_workspace_is_apart_from_the_inputs():
+    """A workspace that holds an input would be written while the input is still read."""
+    for i in (0, 1, 2, 3, 4, 7, 8):
+        assert _backward(workspace=_at(i)) == E.DLLM_ERR_INVALID_ARG, i
+    for i in (1, 2):
+        assert _embed_backward(workspace=_at(i)) == E.DLLM_ERR_INVALID_ARG, i
+    for i in range(5):
+        assert _loss(workspace=_at(i)) == E.DLLM_ERR_INVALID_ARG, i
+    for i in (0, 1, 2, 3, 4, 7, 9):
+        assert _loss_backward(workspace=_at(i)) == E.DLLM_ERR_INVALID_ARG, i
+
+
+def test_most_places_of_a_table_gradient():
+    most = (1 << 30) - 1
+    assert mtl.dllm_embed_backward_workspace_bytes(100, 8, most) > 0
+    assert mtl.dllm_embed_backward_workspace_bytes(100, 8, most + 1) == 0
+    assert _embed_backward(T=most + 1, d=8) == E.DLLM_ERR_INVALID_ARG
+
+
 def _embed(**kw):
     a = dict(table=_at(0), V=100, d=64, tokens=_at(1), T=10, scale=1.0, out=_at(2))
     a.update(kw)
