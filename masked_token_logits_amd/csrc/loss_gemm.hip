@@ -20,6 +20,12 @@
 //     Such operands are staged as they lie, [64 of K][256], and read by
 //     ds_read_b64_tr_b16, which hands each lane four consecutive K of its
 //     column: no transposed copy of W, dz or the hidden states exists.
+//   * With many rows the matrix instructions are the time.  3900 rows (16 row
+//     tiles), 152064 entries of 3584, 4.2 Tflop a product: dz 3.9 ms (1.08
+//     Pflop/s), d_hidden 3.3 (1.27), d_W 3.7 (1.16); a library's plain products
+//     of 8192^3 reach 1.39, 1.22 and 1.07 with operands laid out like that.  dz
+//     has the exponentials and 1.2 GB of stores at each tile's end on top.
+//   * With few rows W's bytes are (see k_loss_dz, k_loss_d_W_few).
 #include <math.h>
 
 #include <type_traits>
@@ -503,7 +509,8 @@ __global__ __launch_bounds__(NT, 1) void k_loss_dz(GradArgs a) {
 // last ones of the tile before, and in that order it works, like all the
 // others, near the stage that as much time has passed: one region of W and dz
 // is in the caches, not one for each workgroup.  Whole tiles start where the
-// time stands, too, and wrap around.
+// time stands, too, and wrap around.  (102 rows, 126464 entries of 4096: 227 us
+// for W's 1.04 GB, 4.6 TB/s.)
 struct DHiddenWork {
   const GradArgs& a;
   int M, Mp, n_rt, n_ct, stages;
@@ -607,7 +614,8 @@ __global__ __launch_bounds__(NT, 1) void k_loss_d_hidden(GradArgs a) {
   run_tiles<true, false, false, false>(lds, work);
 }
 
-// d_hidden of a tile: its shares added, in the order of the cuts.
+// d_hidden of a tile: its shares added, in the order of the cuts (3900 rows of
+// 3584, 480 shares of 256 KiB: 75 us; 102 rows: 10).
 __global__ __launch_bounds__(NT) void k_loss_join(GradArgs a, int grid) {
   const int M = min(a.ctr[0], a.L);
   const int n_rt = (M + BT - 1) / BT, n_ct = (a.d + BT - 1) / BT;
@@ -717,7 +725,9 @@ __global__ __launch_bounds__(NT, 1) void k_loss_d_W(GradArgs a) {
 // d_W of few rows: K is a few stages and the time is d_W's own bytes, so what
 // counts is that stores never stop.  128 entries x 256 columns to a workgroup, one
 // stage of both operands in 48 KiB of LDS, three workgroups to a compute unit:
-// while one stores, the others load and multiply.
+// while one stores, the others load and multiply (126464 entries of 4096: 205 us
+// for 60 rows, 265 for 102, 397 for 250, where the 256 x 256 tiles take 345 for 102
+// and 450 for 250; d_W's bytes alone, 150).
 constexpr int FV = 128;  // entries of a tile
 
 __global__ __launch_bounds__(NT, 3) void k_loss_d_W_few(GradArgs a, int n_vt, int n_ct) {
@@ -779,7 +789,7 @@ __global__ __launch_bounds__(NT, 3) void k_loss_d_W_few(GradArgs a, int n_vt, in
           [](LDS_AS uint8_t*, int, int) {},
           [&](int row, int col, const uint4& u) {
             const int r = first + row - wr * 32;
-            // written once and not read here: kept out of the caches that W's next pass wants (274 -> 248 us)
+            // written once and not read here: kept out of the caches that W's next pass wants (102 rows: 248 us, cached 274)
             if (r < a.n && c0 + col < a.d)
               __builtin_nontemporal_store(u32x4{u.x, u.y, u.z, u.w},
                                           reinterpret_cast<u32x4*>(a.d_W + (int64_t)(a.v0 + r) * a.d + c0 + col));
@@ -950,7 +960,8 @@ __global__ __launch_bounds__(NT, 1) void k_loss_dz_small(GradArgs a, int n_rt) {
 // `fix` before the piece's product is stored (accumulated, the product's old
 // values are gone behind it) and take their places at the end.  A workgroup has
 // 512 columns of one target, which the first row with it answers for; its waves
-// take a quarter of the rows each.
+// take a quarter of the rows each.  Every target reads all rows, from the caches
+// (102 rows of 4096: 17 us; 250: 43).
 __device__ __forceinline__ bool first_with(const GradArgs& a, int M, int i, int v) {
   bool before = false;
   for (int k = threadIdx.x & 63; k < M; k += 64) before |= k < i && a.tgt[k] == v;
