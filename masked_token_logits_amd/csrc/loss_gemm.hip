@@ -509,8 +509,7 @@ __global__ __launch_bounds__(NT, 1) void k_loss_dz(GradArgs a) {
 // last ones of the tile before, and in that order it works, like all the
 // others, near the stage that as much time has passed: one region of W and dz
 // is in the caches, not one for each workgroup.  Whole tiles start where the
-// time stands, too, and wrap around.  (102 rows, 126464 entries of 4096: 227 us
-// for W's 1.04 GB, 4.6 TB/s.)
+// time stands, too, and wrap around.
 struct DHiddenWork {
   const GradArgs& a;
   int M, Mp, n_rt, n_ct, stages;
@@ -596,12 +595,31 @@ struct DHiddenWork {
   }
 };
 
+// With one row tile: the j-th of the cuts in the order of the stages, within a
+// tile, at which they begin, a multiple of cuts / gcd(tiles, cuts) each.
+// Neighbours in an XCD then have the same stages of different columns and share
+// dz's tiles; W is then streamed (102 rows, 126464 entries of 4096: 234 us in the
+// cuts' own order, 211 in this one, 207 with W past the caches).
+__device__ __forceinline__ int cut_by_stage(int j, int tiles, int cuts) {
+  int r0 = cuts, r1 = tiles, x0 = 0, x1 = 1;  // x1 * tiles = r1 modulo cuts
+  while (r1 != 0) {
+    const int k = r0 / r1, r = r0 - k * r1, x = x0 - k * x1;
+    r0 = r1;
+    r1 = r;
+    x0 = x1;
+    x1 = x;
+  }
+  const int n = cuts / r0, inverse = (x0 % n + n) % n;
+  return (int)((int64_t)(j / r0) * inverse % n) + j % r0 * n;
+}
+
 __global__ __launch_bounds__(NT, 1) void k_loss_d_hidden(GradArgs a) {
   __shared__ __attribute__((aligned(1024))) uint16_t lds[SLOTS * OPT];
   const int M = min(a.ctr[0], a.L), n_rt = (M + BT - 1) / BT, n_ct = (a.d + BT - 1) / BT;
   const int64_t tiles = (int64_t)n_rt * n_ct, cuts = min(loss_cuts(tiles, a.ldz), (int64_t)gridDim.x);
-  const int g = xcd_remap(blockIdx.x, gridDim.x);
+  int g = xcd_remap(blockIdx.x, gridDim.x);
   if (g >= cuts) return;
+  if (n_rt == 1) g = cut_by_stage(g, (int)tiles, (int)cuts);
   DHiddenWork work(a, M, g, tiles, cuts);
   if (a.first)
     for (int64_t t = work.low; t < work.high; ++t) {
@@ -611,7 +629,10 @@ __global__ __launch_bounds__(NT, 1) void k_loss_d_hidden(GradArgs a) {
       if (s1 <= s0)  // a part that this piece does not reach, and a later one may
         for (int i = 0; i < BT * BT / 4 / NT; ++i) share[i * NT] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-  run_tiles<true, false, false, false>(lds, work);
+  if (n_rt == 1)
+    run_tiles<true, false, false, true>(lds, work);
+  else
+    run_tiles<true, false, false, false>(lds, work);
 }
 
 // d_hidden of a tile: its shares added, in the order of the cuts (3900 rows of
@@ -726,7 +747,7 @@ __global__ __launch_bounds__(NT, 1) void k_loss_d_W(GradArgs a) {
 // counts is that stores never stop.  128 entries x 256 columns to a workgroup, one
 // stage of both operands in 48 KiB of LDS, three workgroups to a compute unit:
 // while one stores, the others load and multiply (126464 entries of 4096: 205 us
-// for 60 rows, 265 for 102, 397 for 250, where the 256 x 256 tiles take 345 for 102
+// for 60 rows, 253 for 102, 370 for 250, where the 256 x 256 tiles take 345 for 102
 // and 450 for 250; d_W's bytes alone, 150).
 constexpr int FV = 128;  // entries of a tile
 
