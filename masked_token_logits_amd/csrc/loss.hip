@@ -503,10 +503,11 @@ dllm_status dllm_loss_backward(const dllm_loss* p, const float* lse, const float
     a.first = v == 0;
     if (dllm::launch_loss_dz(a, grid, st) != hipSuccess) return DLLM_ERR_HIP;
     if (d_hidden && dllm::launch_loss_d_hidden(a, grid, st) != hipSuccess) return DLLM_ERR_HIP;
-    if (d_W && dllm::launch_loss_targets(a, st) != hipSuccess) return DLLM_ERR_HIP;
+    if (d_W && accumulate && dllm::launch_loss_targets(a, st) != hipSuccess) return DLLM_ERR_HIP;
     if (d_W && dllm::launch_loss_d_W(a, grid, st) != hipSuccess) return DLLM_ERR_HIP;
+    if (d_W && !accumulate && dllm::launch_loss_targets(a, st) != hipSuccess) return DLLM_ERR_HIP;
   }
-  if (d_W && dllm::launch_loss_put(a, st) != hipSuccess) return DLLM_ERR_HIP;
+  if (d_W && accumulate && dllm::launch_loss_put(a, st) != hipSuccess) return DLLM_ERR_HIP;
   if (d_hidden && dllm::launch_loss_join(a, grid, st) != hipSuccess) return DLLM_ERR_HIP;
   return hipGetLastError() == hipSuccess ? DLLM_OK : DLLM_ERR_HIP;
 }

@@ -977,9 +977,10 @@ __global__ __launch_bounds__(NT, 1) void k_loss_dz_small(GradArgs a, int n_rt) {
 }
 
 // Few rows: the rows of d_W that are targets, with what dz's rounding left of
-// their entries.  They are summed anew, in fp32 and the order of the rows, into
-// `fix` before the piece's product is stored (accumulated, the product's old
-// values are gone behind it) and take their places at the end.  A workgroup has
+// their entries.  They are summed anew, in fp32 and the order of the rows, and take
+// their places behind the piece's product; where it is accumulated, whose old
+// values are gone then, they go to `fix` before it and to their places at the end
+// (k_loss_put).  A workgroup has
 // 512 columns of one target, which the first row with it answers for; its waves
 // take a quarter of the rows each.  Every target reads all rows, from the caches
 // (102 rows of 4096: 17 us; 250: 43).
@@ -1028,7 +1029,8 @@ __global__ __launch_bounds__(256) void k_loss_targets(GradArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] += old[j];
   }
-  *reinterpret_cast<uint4*>(a.fix + (int64_t)i * a.d + c) = pack8(f);
+  uint16_t* row = a.accumulate ? a.fix + (int64_t)i * a.d : a.d_W + (int64_t)(a.v0 + v) * a.d;
+  *reinterpret_cast<uint4*>(row + c) = pack8(f);
 }
 
 __global__ __launch_bounds__(64) void k_loss_put(GradArgs a) {

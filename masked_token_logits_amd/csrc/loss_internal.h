@@ -45,7 +45,7 @@ struct GradArgs {
   const float* left;        // [Mp] what its rounding to bf16 leaves of it
   uint16_t* dz;             // [Mp, ldz]: the piece's gradient of the logits
   float* acc;               // the rows' gradient over the pieces so far, in shares of a tile each
-  uint16_t* fix;            // [kLossFew, d] few rows: d_W's rows of the targets
+  uint16_t* fix;            // [kLossFew, d] few rows, accumulated: d_W's rows of the targets
   uint16_t *d_hidden, *d_W;
   int64_t ldz;              // entries of a whole piece
   int V, d, dp, L;
@@ -77,8 +77,8 @@ hipError_t launch_loss_lse_small(const LseArgs& a, hipStream_t stream);
 hipError_t launch_loss_dz(const GradArgs& a, int grid, hipStream_t stream);        // dz
 hipError_t launch_loss_d_hidden(const GradArgs& a, int grid, hipStream_t stream);  // acc += dz . W
 hipError_t launch_loss_d_W(const GradArgs& a, int grid, hipStream_t stream);       // d_W = dz^T . rows
-hipError_t launch_loss_targets(const GradArgs& a, hipStream_t stream);             // few rows: fix, before d_W
-hipError_t launch_loss_put(const GradArgs& a, hipStream_t stream);                 // and behind it
+hipError_t launch_loss_targets(const GradArgs& a, hipStream_t stream);             // few rows: behind d_W, or before it where that accumulates
+hipError_t launch_loss_put(const GradArgs& a, hipStream_t stream);                 // and that behind all pieces
 hipError_t launch_loss_join(const GradArgs& a, int grid, hipStream_t stream);      // d_hidden = sum of acc's shares
 
 // How d_hidden's product is cut: its tiles' stages as one line, dealt to so

@@ -101,6 +101,7 @@ CASES = [  # L, d, V, ratio, piece
     (257, 136, 900, 1.0, 256),      # few and over with a d that is no multiple of 32
     (300, 40, 500, 0.7, None),
     (60, 1544, 5000, 1.0, None),    # one row tile, seven column tiles whose cuts do not line up
+    (20, 66056, 300, 1.0, None),    # more column tiles than compute units
     (200, 784, 34000, 0.5, 16384),  # one row tile against a large head, four column tiles in three pieces
 ]
 
