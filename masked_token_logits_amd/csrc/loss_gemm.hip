@@ -976,6 +976,91 @@ __global__ __launch_bounds__(NT, 1) void k_loss_dz_small(GradArgs a, int n_rt) {
   }
 }
 
+// d_W of few tiles: both sides by rows of K, 128 x 128 to a workgroup, the same
+// ring (460 rows, 4096 entries of 256: 9.8 us, by 256 x 256 tiles 21.5; the step of
+// 3700 rows, 1000 entries of 1024: 140 and 177; of 1000, 8000 of 1024, 128 large
+// tiles: 170 either way).
+__global__ __launch_bounds__(NT, 1) void k_loss_d_W_small(GradArgs a, int n_ct) {
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[FRING * FSTAGE];
+  const int M = min(a.ctr[0], a.L), stages = (M + BK - 1) / BK;
+  if (M == 0 && a.accumulate) return;
+  const int vt = blockIdx.x / n_ct, ct = blockIdx.x - vt * n_ct, r0 = vt * FV2, c0 = ct * FR;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave >> 1, wv = wave & 1;
+  // rows of K of 256 bytes, four to a DMA: row k holds its four granules of 32 at granule ^ (k & 3)
+  const int bk = wave * 4 + (lane >> 4), bcol = (((lane & 15) >> 2) ^ (bk & 3)) * 32 + (lane & 3) * 8;
+  const int bsw = (lane & 15) >> 2, boff = (8 * (lane >> 5) + bsw) * FR + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  const uint16_t* pa = a.rows + (int64_t)bk * a.dp + min(c0 + bcol, a.dp - 8);
+  const uint16_t* pb = a.dz + (int64_t)bk * a.ldz + min(r0 + bcol, (int)a.ldz - 8);
+  f32x16 acc[2][2] = {};
+  if (stages > 0) {
+    int k0 = 0;
+    auto issue = [&](int slot) {
+      uint16_t* to = lds + slot * FSTAGE + wave * 512;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        __builtin_amdgcn_global_load_lds((const void*)(pa + (int64_t)(k0 + 16 * j) * a.dp), (LDS_AS void*)(to + 4 * j * 512), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((const void*)(pb + (int64_t)(k0 + 16 * j) * a.ldz),
+                                         (LDS_AS void*)(to + BK * FR + 4 * j * 512), 16, 0, 0);
+      }
+      k0 = k0 + BK >= stages * BK ? 0 : k0 + BK;
+    };
+    auto frag = [&](const uint16_t* tile, int block, int kk) {
+      LDS_AS uint16_t* ring = (LDS_AS uint16_t*)tile;
+      LDS_AS const uint16_t* p = ring + boff + ((block ^ bsw) * 32) + kk * 16 * FR;
+      const bf16x4 lo = read_tr(p, ring), hi = read_tr(p + 4 * FR, ring);
+      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    // as in small_product
+    issue(0);
+    issue(1);
+    issue(2);
+    for (int q = 0; q < stages; ++q) {
+      stage_sync<16>();
+      issue((q + 3) & (FRING - 1));
+      const uint16_t* t = lds + (q & (FRING - 1)) * FSTAGE;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        bf16x8 fa[2], fb[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          fa[f] = frag(t, wv * 2 + f, kk);
+          fb[f] = frag(t + BK * FR, wr * 2 + f, kk);
+        }
+#pragma unroll
+        for (int fv = 0; fv < 2; ++fv)
+#pragma unroll
+          for (int fr = 0; fr < 2; ++fr) acc[fv][fr] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[fv], fb[fr], acc[fv][fr], 0, 0, 0);
+      }
+    }
+    stage_sync<0>();  // the DMAs behind the last stage
+  }
+#pragma unroll
+  for (int fr = 0; fr < 2; ++fr) {
+    const int row = r0 + wr * 64 + fr * 32 + (lane & 31);
+    if (row >= a.n) continue;
+#pragma unroll
+    for (int fv = 0; fv < 2; ++fv)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = c0 + wv * 64 + fv * 32 + 8 * j + 4 * (lane >> 5);
+        if (col >= a.d) continue;
+        uint2* o = reinterpret_cast<uint2*>(a.d_W + (int64_t)(a.v0 + row) * a.d + col);
+        float z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = acc[fv][fr][4 * j + i];
+        if (a.accumulate) {
+          const uint2 u = *o;
+          z[0] += bf16_float(u.x & 0xFFFF);
+          z[1] += bf16_float(u.x >> 16);
+          z[2] += bf16_float(u.y & 0xFFFF);
+          z[3] += bf16_float(u.y >> 16);
+        }
+        *o = make_uint2(float_bf16(z[0]) | float_bf16(z[1]) << 16, float_bf16(z[2]) | float_bf16(z[3]) << 16);
+      }
+  }
+}
+
 // Few rows: the rows of d_W that are targets, with what dz's rounding left of
 // their entries.  They are summed anew, in fp32 and the order of the rows, and take
 // their places behind the piece's product; where it is accumulated, whose old
@@ -1070,6 +1155,11 @@ hipError_t launch_loss_d_hidden(const GradArgs& a, int grid, hipStream_t stream)
   return hipGetLastError();
 }
 hipError_t launch_loss_d_W(const GradArgs& a, int grid, hipStream_t stream) {
+  if (loss_small(a.n, a.d)) {
+    const int cols = (a.d + FR - 1) / FR;
+    hipLaunchKernelGGL(k_loss_d_W_small, dim3((unsigned)((a.n + FV2 - 1) / FV2) * (unsigned)cols), dim3(NT), 0, stream, a, cols);
+    return hipGetLastError();
+  }
   // how many rows there are is known on the device: one of the two returns at once
   if (a.L > kLossFew) hipLaunchKernelGGL(k_loss_d_W, dim3(grid), dim3(NT), 0, stream, a);
   const int n_vt = (a.n + FV - 1) / FV, n_ct = (a.d + BT - 1) / BT;

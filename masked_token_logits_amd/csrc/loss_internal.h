@@ -53,7 +53,7 @@ struct GradArgs {
   int first, accumulate;
 };
 
-// A product of L rows (at most) and n entries is small if its 256 x 256 tiles are
+// A product of L rows (at most) and n entries, or of n entries and d columns, is small if its 256 x 256 tiles are
 // too few for half the chip; it then has tiles of 128 x 128 (the whole loss of 128
 // rows, 16384 entries of 4096, 64 large tiles: 51 us, by large ones 69; 8 rows,
 // 32000 of 4096: 53 and 75; 256 rows, 32000 of 2048, 125 tiles: 58 and 53, but

@@ -184,6 +184,20 @@ def test_either_gradient_and_accumulation():
     _check_backward(None, w4, a, ol.loss(a["Wf"], a["Hf"], a["mask"], a["t"], a["w"]), old=of)
 
 
+@pytest.mark.parametrize("L,d,V", [(700, 192, 900), (420, 136, 34000), (40, 264, 33300)])
+def test_accumulation(L, d, V):
+    """Many and few rows, small and large heads: added once, rounded once."""
+    import masked_token_logits_amd as mtl
+    rng = np.random.default_rng(L)
+    a = _inputs(rng, L, d, V, 0.8)
+    x, head = _dev(a), mtl.MaskedLoss(dev_bf16(a["W"]))
+    args = (x["hidden"], x["mask"], x["targets"])
+    lse = head(*args, weights=x["weights"])[2]
+    old, of = bf16(rng, (V, d), 0.01)
+    dh, dW = head.backward(*args, lse, weights=x["weights"], d_W=dev_bf16(old), accumulate=True)
+    _check_backward(dh, dW, a, ol.loss(a["Wf"], a["Hf"], a["mask"], a["t"], a["w"]), old=of)
+
+
 def test_sure_and_hopeless_rows():
     """Logits tens apart: probabilities of 1 and of almost 0 at the target."""
     import torch
