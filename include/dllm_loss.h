@@ -12,6 +12,8 @@
  *   dz_iv  = grad w_i (exp(z_iv - lse_i) - [v = targets[i]])
  *   d_hidden[i] = sum_v dz_iv W_lm[v],   d_W[v] = sum_i dz_iv hidden[i]
  * bf16 inputs, fp32 products' sums and softmax statistics.
+ * A NaN logit makes the position's lse, loss and gradients NaN, and with them
+ * d_W; logits of +inf make lse infinite and the gradients NaN.
  *
  * The vocabulary is taken in pieces.  Forward keeps a running maximum and sum
  * for each row; backward computes a piece's logits again, turns them into dz

@@ -160,9 +160,7 @@ __global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* __restrict__ 
       row_merge<false>(r, shfl_xor_state(r, off));
     }
     if (lane == 0) {
-      // Logits this large lie 32 or more apart, or are the same: the sum's logarithm, at most 22, is less than half
-      // of that.  The running sum's reference, m log2(e) rounded, is then off by so much that the sum may be infinite.
-      const float l = fabsf(r.m) >= 0x1p29f ? r.m : row_finish<false>(r).lse;
+      const float l = row_finish<false>(r).lse;
       losses[pos] = l - z;
       lse[pos] = l;
       terms[row] = (l - z) * (weights ? weights[pos] : 1.f);

@@ -18,11 +18,18 @@
 //   lse     = m + (log2 s - q) ln 2     (natural log-sum-exp)
 //   margin  = conf (1 - e^(m2 - m))     (largest minus second-largest probability)
 //   entropy = ln s - t / s              (-sum p ln p; independent of the reference)
+// A NaN logit makes s NaN, nothing else does, and nothing takes that away; m is the
+// largest of the others, -inf where there are none.  From |m| = 2^29 on, where the
+// rounding of sc(m) passes 16, 2^(g_v) soon overflows and s may be infinite: sc is
+// kept finite and rescaling factors above 0, so that no inf - inf or 0 inf occurs.
+// Two such logits that are not equal lie 32 or more apart, and lse is m itself (the
+// logarithm of a sum of less than 2^31 of them is below half a step).
 // These are the statistics of the confidence- and entropy-driven unmasking
 // policies (Accelerating Masked Diffusion Large Language Models: A Survey of
 // Efficient Inference Techniques, Main Findings).
 #pragma once
 
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -32,11 +39,21 @@ namespace dllm {
 constexpr float kLog2eF = 1.4426950408889634f;
 constexpr float kLn2F = 0.6931471805599453f;
 
-// sc(m) = fl(m * log2(e)), rounded once: never fused into a neighbouring
-// add, so that equal maxima always give bit-equal references.
-__device__ __forceinline__ float log2_ref(float m) {
+// fl(m * log2(e)), rounded once: never fused into a neighbouring add, so that
+// equal maxima always give bit-equal references.
+__device__ __forceinline__ float log2_scaled(float m) {
 #pragma clang fp contract(off)
   return m * kLog2eF;
+}
+
+// sc(m): finite, also where m or the product is not.
+__device__ __forceinline__ float log2_ref(float m) { return __builtin_amdgcn_fmed3f(log2_scaled(m), -FLT_MAX, FLT_MAX); }
+
+// log2 of the factor that takes a sum from the reference of m to a larger one, sc.
+// What is 2^-126 of itself then changes no sum, and an empty side's sum is 0.
+__device__ __forceinline__ float log2_rescale(float m, float sc) {
+#pragma clang fp contract(off)
+  return fmaxf(log2_scaled(m) - sc, -126.f);
 }
 
 struct RowState {
@@ -61,12 +78,11 @@ __device__ __forceinline__ void row_merge(RowState& x, const RowState& y) {
   const bool take_y = (y.m > x.m) || (y.m == x.m && y.a < x.a);
   const float mn = fmaxf(x.m, y.m);
   const float sn = log2_ref(mn);
-  const float dx = log2_ref(x.m) - sn, dy = log2_ref(y.m) - sn;  // <= 0; -inf or NaN for an empty side
-  const float cx = (x.m == -INFINITY) ? 0.f : (dx == 0.f ? 1.f : __builtin_amdgcn_exp2f(dx));
-  const float cy = (y.m == -INFINITY) ? 0.f : (dy == 0.f ? 1.f : __builtin_amdgcn_exp2f(dy));
+  const float dx = log2_rescale(x.m, sn), dy = log2_rescale(y.m, sn);  // <= 0
+  const float cx = __builtin_amdgcn_exp2f(dx), cy = __builtin_amdgcn_exp2f(dy);            // exactly 1 at 0
   if (EXT) {
-    const float tx = (x.m == -INFINITY) ? 0.f : cx * fmaf(dx * kLn2F, x.s, x.t);
-    const float ty = (y.m == -INFINITY) ? 0.f : cy * fmaf(dy * kLn2F, y.s, y.t);
+#pragma clang fp contract(off)  // the two sides alike
+    const float tx = cx * fmaf(dx * kLn2F, x.s, x.t), ty = cy * fmaf(dy * kLn2F, y.s, y.t);
     x.t = tx + ty;
     x.m2 = fmaxf(fminf(x.m, y.m), fmaxf(x.m2, y.m2));
   }
@@ -113,7 +129,10 @@ __device__ __forceinline__ void row_fold(RowState& r, const float* z, int v0, Of
     for (int i = N - 1; i >= 0; --i) bi = z[i] == bm ? off(i) : bi;
   }
   const float mn = fmaxf(r.m, bm);
-  if (mn == -INFINITY) return;
+  // Never taken, as v0 >= 0, which the compiler does not know: the branch keeps the
+  // fold's instructions from those of the blocks behind it, whose accumulators would
+  // otherwise be read at once, and the GEMMs spill.
+  if (__builtin_amdgcn_readfirstlane(v0) < 0) return;
   const float sc = log2_ref(mn);
   float sum = 0.f, tt = 0.f;
 #pragma unroll
@@ -125,11 +144,10 @@ __device__ __forceinline__ void row_fold(RowState& r, const float* z, int v0, Of
     // below -256 e is 0 anyway, so the clamp changes nothing else
     if (EXT) tt = fmaf(e, fmaxf(g, -256.f), tt);
   }
-  const float d = log2_ref(r.m) - sc;  // exactly 0 while the maximum is unchanged
-  const float c = (r.m == -INFINITY) ? 0.f : (d == 0.f ? 1.f : __builtin_amdgcn_exp2f(d));
+  const float d = log2_rescale(r.m, sc);  // exactly 0 while the maximum is unchanged
+  const float c = __builtin_amdgcn_exp2f(d);
   if (EXT) {
-    const float old_t = (r.m == -INFINITY) ? 0.f : c * fmaf(d * kLn2F, r.s, r.t);
-    r.t = fmaf(tt, kLn2F, old_t);
+    r.t = fmaf(tt, kLn2F, c * fmaf(d * kLn2F, r.s, r.t));
     r.m2 = fmaxf(fminf(r.m, bm), fmaxf(r.m2, b2));
   }
   r.s = r.s * c + sum;
@@ -148,7 +166,7 @@ __device__ __forceinline__ RowStats row_finish(const RowState& r) {
   const float q = fmaf(r.m, kLog2eF, -log2_ref(r.m));  // rounding residual of sc(m), |q| <= ulp/2
   const float log2_s = __builtin_amdgcn_logf(r.s);     // v_log_f32: base 2
   o.conf = __builtin_amdgcn_exp2f(q) / r.s;
-  o.lse = fmaf(log2_s - q, kLn2F, r.m);
+  o.lse = fabsf(r.m) < 0x1p29f ? fmaf(log2_s - q, kLn2F, r.m) : (r.s == r.s ? r.m : r.s);
   if (EXT) {
     const float e2 = (r.m2 == -INFINITY) ? 0.f : __builtin_amdgcn_exp2f((r.m2 - r.m) * kLog2eF);
     o.margin = (1.0f - e2) * o.conf;
