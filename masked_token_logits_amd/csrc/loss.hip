@@ -228,7 +228,8 @@ __global__ __launch_bounds__(256) void k_loss_prepare(PrepareArgs a) {
         a.lse_of[i] = lse * kLossPScale;
         a.coef[i] = fabsf(lse) < INFINITY ? c : NAN;
         a.tgt[i] = t;
-        const float at = c * expm1f(z - lse);
+        // z and lse are sums in different orders: a sure target's z may come out above (by 2 at logits of 2^20)
+        const float over = z - lse, at = c * expm1f(over > 0.f ? 0.f : over);
         a.at_tgt[i] = at;
         a.left[i] = at - bf16_float(float_bf16(at));
       }

@@ -1,0 +1,51 @@
+"""Sure targets at large logits.  The target's logit and lse come from sums in different orders, so their difference is
+off by several steps of the logit in either direction, where the true gradient is 0: whatever it is, the probability
+stays between 0 and 1."""
+import numpy as np
+import pytest
+
+from _layer_cases import HALF, dev_bf16, dev_f32, f64
+from test_gpu_loss import _dev, bf16_of
+
+pytestmark = pytest.mark.gpu
+
+CASES = [(64, 1024, 512), (300, 1024, 512), (64, 1544, 33000), (300, 1024, 33000), (20, 4096, 33000)]
+
+
+def _sure(L, d, V, top):
+    """Rows along their target's entry of a positive head: (inputs, z, the most that lse - z may be off, others' gap)."""
+    rng = np.random.default_rng(L + d + V)
+    W, Wf = bf16_of(0.5 + rng.random((V, d), dtype=np.float32))
+    t = rng.permutation(V)[:L]
+    H, Hf = bf16_of(2.0 ** top / (Wf[t] ** 2).sum(axis=1, keepdims=True) * Wf[t])
+    a = dict(H=H, Hf=Hf, W=W, Wf=Wf, mask=np.ones(L, np.uint8), t=t.astype(np.int32), w=np.ones(L, np.float32))
+    z = (Hf * Wf[t]).sum(axis=1)
+    others = Hf @ Wf.T
+    others[np.arange(L), t] = -np.inf
+    assert (z - others.max(axis=1)).min() > 150     # every other probability is below fp32's smallest number
+    # two logits, d 2^-24 sum |h w| each in any order, their difference's rounding, and lse's own 2^-17
+    return a, 2 * d * 2.0 ** -24 * z + 2.0 ** -24 * z + 2.0 ** -17
+
+
+@pytest.mark.parametrize("top", [14, 20, 30])
+@pytest.mark.parametrize("L,d,V", CASES)
+def test_gradients_of_sure_targets(L, d, V, top):
+    """dz at the target lies in [-grad, 0] and is 0 elsewhere, so each gradient is a share of one row, of one sign."""
+    import torch
+
+    import masked_token_logits_amd as mtl
+    print(f"[case] sure L={L} d={d} V={V} top={top}", flush=True)
+    a, off = _sure(L, d, V, top)
+    x, head, grad = _dev(a), mtl.MaskedLoss(dev_bf16(a["W"])), 3.0
+    args = (x["hidden"], x["mask"], x["targets"])
+    lse = head(*args)[2]
+    dh, dW = head.backward(*args, lse, grad=dev_f32([grad]))
+    torch.cuda.synchronize()
+    most = np.minimum(off, 1.0)[:, None] * grad * (1 + 2 * HALF)
+    dh, dW = f64(dh), f64(dW)
+    assert np.isfinite(dh).all() and np.isfinite(dW).all()
+    share = dh / a["Wf"][a["t"]]
+    assert (share <= 0).all() and (share >= -most).all(), (share.min(), share.max())
+    share = dW[a["t"]] / a["Hf"]
+    assert (share <= 0).all() and (share >= -most).all(), (share.min(), share.max())
+    assert not np.delete(dW, a["t"], axis=0).any()
