@@ -161,9 +161,11 @@ __global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* __restrict__ 
     }
     if (lane == 0) {
       const float l = row_finish<false>(r).lse;
-      losses[pos] = l - z;
+      // l and z are sums in different orders: a sure target's z may come out above
+      const float over = l - z, x = over < 0.f ? 0.f : over;
+      losses[pos] = x;
       lse[pos] = l;
-      terms[row] = (l - z) * (weights ? weights[pos] : 1.f);
+      terms[row] = x * (weights ? weights[pos] : 1.f);
     }
   }
   if (!loss) return;

@@ -49,3 +49,20 @@ def test_gradients_of_sure_targets(L, d, V, top):
     share = dW[a["t"]] / a["Hf"]
     assert (share <= 0).all() and (share >= -most).all(), (share.min(), share.max())
     assert not np.delete(dW, a["t"], axis=0).any()
+
+
+@pytest.mark.parametrize("top", [14, 20, 30])
+@pytest.mark.parametrize("L,d,V", CASES)
+def test_losses_of_sure_targets(L, d, V, top):
+    """No cross entropy is below 0."""
+    import torch
+
+    import masked_token_logits_amd as mtl
+    print(f"[case] sure losses L={L} d={d} V={V} top={top}", flush=True)
+    a, off = _sure(L, d, V, top)
+    x = _dev(a)
+    loss, losses, lse = mtl.MaskedLoss(dev_bf16(a["W"]))(x["hidden"], x["mask"], x["targets"])
+    torch.cuda.synchronize()
+    losses, loss = f64(losses), f64(loss)[0]
+    assert (losses >= 0).all() and (losses <= off).all(), (losses.min(), losses.max())
+    assert abs(loss - losses.sum()) <= 2.0 ** -24 * losses.sum()
