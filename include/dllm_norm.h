@@ -78,6 +78,7 @@ size_t dllm_residual_norm_backward_workspace_bytes(const dllm_norm *norm, int64_
  * Gradients of dllm_residual_norm from those of its outputs.
  *   x        [T, d] bf16: the stream behind the update (x_out; x without y)
  *   y, gate, groups   as in the forward call
+ *            (y's values are read only where post or d_gate is there)
  *   d_n      [T, d] bf16 gradient of n; NULL exactly if there is no pre
  *   d_x_out  [T, d] bf16 gradient of x' from elsewhere; NULL = none
  *   d_x      [T, d] bf16: gradient of x (and of x'); may be d_x_out or d_n

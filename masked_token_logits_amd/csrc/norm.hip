@@ -146,13 +146,18 @@ struct NormGrads {
   float *part_pre, *part_post, *part_gate;  // [workgroups, d] else
   int64_t chunk;                  // tokens of a workgroup
   int chunks;                     // workgroups to a gate's run; 0: a workgroup has whole runs
+  bool reads_y;                   // a gradient depends on y: through its norm or in the gate's sum
 };
 
 // A workgroup walks its tokens and keeps their share of the sums over tokens in
 // registers; the next row's loads are on their way while one is worked on.  Six
 // arrays pass once (32768 tokens of 3584 with both norms and a gate: 307 us with
-// the sums, 4.6 TB/s, where a copy of as many bytes takes 5.0).
-template <int THREADS>
+// the sums, 4.6 TB/s, where a copy of as many bytes takes 5.0), and five where no
+// gradient depends on y (32768 of 4096 with the norm before a block alone: 275 us,
+// 4.9 TB/s; with y read 330).  POST, a norm behind the block, is the kernel's own
+// constant: asked for within the loops it costs 1 percent at 3584 columns and
+// 6 to 14 at 1024 and 256.
+template <int THREADS, bool POST>
 __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, NormGrads g) {
   __shared__ float lds[2 * (THREADS / 64)][3];
   // The weights and the gate of a thread's pieces, its own: loaded from memory
@@ -166,7 +171,7 @@ __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, 
     }
   };
   if (a.pre) keep(0, a.pre);
-  if (a.post) keep(1, a.post);
+  if (POST) keep(1, a.post);
   const float per = 1.0f / (float)a.d;
   int64_t t0, t1;
   if (g.chunks > 0) {
@@ -189,7 +194,7 @@ __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, 
       if (c < a.d) {
         const int64_t o = t * a.d + c;
         if (g.d_n) xu[i] = load8(a.x + o);
-        if (a.y) yu[i] = load8(a.y + o);
+        if (g.reads_y) yu[i] = load8(a.y + o);
         if (g.d_n) nu[i] = load8(g.d_n + o);
         if (g.d_x_out) du[i] = load8(g.d_x_out + o);
       }
@@ -250,24 +255,24 @@ __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, 
       if (c < a.d) store8(g.d_x + t * a.d + c, pack8(dx[i]));
     }
     if (a.y) {
-      const float q = a.post ? 1.0f / sqrtf(s[2] * per + a.eps) : 1.0f;
+      const float q = POST ? 1.0f / sqrtf(s[2] * per + a.eps) : 1.0f;
       float e[3] = {0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int c = 8 * (threadIdx.x + i * THREADS);
         if (c < a.d) {
           float p[8], gt[8];
-          if (a.post) unpack8(kept[1][i][threadIdx.x], p);
+          if (POST) unpack8(kept[1][i][threadIdx.x], p);
           if (gate) unpack8(kept[2][i][threadIdx.x], gt);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float yq = y[i][j] * q;
             float z = a.scale * dx[i][j];
             if (gate) {
-              s_gate[i][j] = fmaf(z, a.post ? yq * p[j] : yq, s_gate[i][j]);
+              s_gate[i][j] = fmaf(z, POST ? yq * p[j] : yq, s_gate[i][j]);
               z *= gt[j];
             }
-            if (a.post) {
+            if (POST) {
               s_post[i][j] = fmaf(z, yq, s_post[i][j]);
               z *= p[j];
               e[0] = fmaf(z, y[i][j], e[0]);
@@ -277,7 +282,7 @@ __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, 
         }
       }
       float m = 0.f;
-      if (a.post) {
+      if (POST) {
         group_sum<THREADS, 3>(e, lds, 1);
         m = e[0] * per * q * q;
       }
@@ -285,8 +290,10 @@ __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, 
       for (int i = 0; i < kPieces; ++i) {
         const int c = 8 * (threadIdx.x + i * THREADS);
         if (c < a.d) {
+          if (POST) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dx[i][j] = q * (dx[i][j] - y[i][j] * m);
+            for (int j = 0; j < 8; ++j) dx[i][j] = q * (dx[i][j] - y[i][j] * m);
+          }
           store8(g.d_y + t * a.d + c, pack8(dx[i]));
         }
       }
@@ -306,7 +313,7 @@ __global__ __launch_bounds__(THREADS) void k_residual_norm_backward(NormArgs a, 
         }
       }
     }
-    if (THREADS > 64 && !(a.y && a.post)) __syncthreads();  // one slot only: the next row's sums wait
+    if (THREADS > 64 && !(a.y && POST)) __syncthreads();  // one slot only: the next row's sums wait
   }
 #pragma unroll
   for (int i = 0; i < kPieces; ++i) {
@@ -497,11 +504,14 @@ dllm_status dllm_residual_norm_backward(const dllm_norm* p, const uint16_t* x, c
   const bool whole = deal.chunks == 0;
   const dllm::NormGrads g = {d_n, d_x_out, d_x, d_y, whole ? d_gate : nullptr, d_pre ? part : nullptr,
                              d_post ? part + size : nullptr, !whole && d_gate ? part + 2 * size : nullptr, deal.chunk,
-                             deal.chunks};
+                             deal.chunks, p->post || d_gate};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   dllm::by_threads(p->d, [&](auto threads) {
     constexpr int N = decltype(threads)::value;
-    hipLaunchKernelGGL(dllm::k_residual_norm_backward<N>, dim3((unsigned)deal.groups), dim3(N), 0, s, a, g);
+    if (p->post)
+      hipLaunchKernelGGL((dllm::k_residual_norm_backward<N, true>), dim3((unsigned)deal.groups), dim3(N), 0, s, a, g);
+    else
+      hipLaunchKernelGGL((dllm::k_residual_norm_backward<N, false>), dim3((unsigned)deal.groups), dim3(N), 0, s, a, g);
   });
   if (hipGetLastError() != hipSuccess) return DLLM_ERR_HIP;
   if (g.part_pre || g.part_post || g.part_gate) {

@@ -234,3 +234,25 @@ def test_streams():
     for (f, b), (_, h) in zip(got, sets):
         _check_forward(f, h, eps, 1.0)
         _check_backward(b, h, eps, 1.0)
+
+
+@pytest.mark.parametrize("pre,groups", [(0, 0), (1, 0), (0, 3), (1, 3), (1, 600)])
+@pytest.mark.parametrize("d", [64, 2056])
+def test_y_reaches_no_gradient_of_its_own_without_a_norm(d, pre, groups):
+    """Without a norm behind the block d_y = scale gate d_x: an infinite or NaN y changes nothing but its gate's gradient."""
+    import torch
+    dev, _ = _inputs(np.random.default_rng(d + groups), 600, d, pre, 0, groups)
+    layer = _layer(dev, 1e-5, 0.5)
+    want = layer.backward(dev["x"], dev["d_n"], y=dev["y"], d_x=dev["d_x"], gate=dev["gate"])
+    dev["y"][3, 7], dev["y"][5], dev["y"][8, 0] = float("nan"), float("inf"), float("-inf")
+    got = layer.backward(dev["x"], dev["d_n"], y=dev["y"], d_x=dev["d_x"], gate=dev["gate"])
+    torch.cuda.synchronize()
+    for k in ("d_x", "d_y") + (("d_pre",) if pre else ()):
+        assert torch.equal(got[k], want[k]), k
+    assert torch.isfinite(got["d_y"]).all()
+    if groups:
+        run = 600 // groups
+        bad = np.zeros((groups, d), bool)
+        bad[5 // run], bad[3 // run, 7], bad[8 // run, 0] = True, True, True
+        g = f64(got["d_gate"])
+        assert np.array_equal(~np.isfinite(g), bad) and np.array_equal(g[~bad], f64(want["d_gate"])[~bad])
