@@ -291,7 +291,7 @@ class MaskedLoss(_Workspace):
             return _abi.load().dllm_loss_forward(C.byref(p), box[0].data_ptr(), box[1].data_ptr(), box[2].data_ptr(),
                                                  ws.data_ptr(), nbytes, stream)
 
-        self._call("dllm_loss_forward", (hidden, mask, targets, weights, self.W_lm) + tuple(out or ()), make)
+        self._call("dllm_loss_forward", (hidden, mask, targets, weights, self.W_lm, *(box or ())), make)
         return tuple(box)
 
     def backward(self, hidden, mask, targets, lse, weights=None, grad=None, d_hidden=None, d_W=None,

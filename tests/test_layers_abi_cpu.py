@@ -300,3 +300,13 @@ def test_masked_loss_checks():
         with pytest.raises(mtl.DllmError) as e:
             call()
         assert e.value.status == E.DLLM_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("form", [tuple, list, iter])
+def test_masked_loss_keeps_its_outputs_for_the_stream(form, monkeypatch):
+    """Outputs are among the tensors that a call on another stream keeps alive, in whatever form they come."""
+    head, kept = mtl.MaskedLoss(bf(10, 64)), []
+    monkeypatch.setattr(head, "_call", lambda where, tensors, make: kept.extend(tensors))
+    out = [torch.zeros(1), torch.zeros(7), torch.zeros(7)]
+    got = head(bf(7, 64), torch.zeros(7, dtype=torch.uint8), torch.zeros(7, dtype=torch.int32), out=form(out))
+    assert all(any(t is k for k in kept) for t in out) and all(g is t for g, t in zip(got, out))
