@@ -424,9 +424,11 @@ dllm_status dllm_loss_forward(const dllm_loss* p, float* loss, float* losses, fl
                            ? dllm::launch_gemm_persistent(p->W_lm, p->hidden, d, V, r.idx, r.ctr, cus, r.part, st)
                            : dllm::launch_gemm_large(p->W_lm, p->hidden, d, V, r.idx, r.ctr, (int)n_rt, plan.fixed_slices, r.part, st);
   if (e != hipSuccess) return DLLM_ERR_HIP;
-  // The last workgroup to end adds up to 512 terms itself.  More are another kernel's: each workgroup's arrival
-  // waits for its chip's cache to be written back (4096 rows: 49 us; 9 in two kernels).
-  const bool ends = L <= 512;
+  // The last workgroup to end adds the terms of up to 768 positions itself.  More are another kernel's: each
+  // workgroup's arrival waits for its chip's cache to be written back.  Half of the positions counted, 4096 entries
+  // of 256, us a call with the last workgroup and with a kernel: 64 positions 19 and 22, 512 19 and 23, 768 20.6 and
+  // 22.6, 1024 23.3 and 22.7, 1536 32 and 23.5, 4096 60 and 30.
+  const bool ends = L <= 768;
   hipLaunchKernelGGL(dllm::k_loss_rows, dim3(dllm::grid_for((L + 3) / 4, 65536)), dim3(256), 0, st, p->W_lm, p->hidden,
                      (int)p->d, (int)L, p->targets, p->weights, r.idx, r.ctr, r.part, stream_w, r.terms, losses, lse, r.ctr + 5,
                      ends ? loss : nullptr);
