@@ -48,6 +48,7 @@ extern "C" {
  * One set of positions against one LM head (host struct), shared by both
  * directions.
  *   W_lm     [V, d] bf16; 1 <= V < 2^31 - 1024; d a multiple of 8, d < 2^20
+ *            (the forward pass is fastest where d is a multiple of 32)
  *   hidden   [L, d] bf16; 1 <= L < 2^31 - 1024
  *   mask     [L] u8: nonzero = the position holds the mask token
  *   targets  [L] int32: the tokens to predict; any other value = no target
@@ -69,7 +70,7 @@ size_t dllm_loss_forward_workspace_bytes(int64_t V, int64_t d, int64_t L);
 
 /*
  *   loss    [1] float32
- *   losses  [L] float32: l_i, and 0 where a position does not count
+ *   losses  [L] float32: l_i, never below 0, and 0 where a position does not count
  *   lse     [L] float32: lse_i, and 0 where a position does not count
  *   workspace  256-byte aligned
  * Outputs overlap no input and not each other.

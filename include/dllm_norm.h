@@ -11,7 +11,8 @@
  * y is the block's output, x the residual stream before it and x' behind it,
  * and n the input of the next block.  bf16 in and out; sums and everything
  * between input and output are fp32, and x' and n are rounded once each (n is
- * taken from x' before its rounding).
+ * taken from x' before its rounding).  A row whose sum of squares passes fp32's
+ * range (2^128) has a norm of 0.
  *
  * Memory: every pointer is a DEVICE pointer unless marked "host"; bf16 is
  * passed as uint16_t bit patterns; arrays are row-major, contiguous and

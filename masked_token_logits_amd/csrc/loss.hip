@@ -3,7 +3,8 @@
 // Forward is the readout's projection: the counted rows are compacted, the
 // LM-head GEMM (for small products the loss's own) folds each row's logits into
 // a running maximum and sum per vocabulary slice, and a wave for each row joins
-// the slices and takes the target's logit.  Backward walks the vocabulary in pieces (loss_gemm.hip).
+// the slices and takes the target's logit.  Backward walks the vocabulary in
+// pieces (loss_gemm.hip).
 #include "dllm_loss.h"
 
 #include <math.h>
@@ -395,8 +396,12 @@ dllm_status dllm_loss_forward(const dllm_loss* p, float* loss, float* losses, fl
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   dllm::Rows r;
   dllm::carve(p->V, p->d, L, 0, reinterpret_cast<uint8_t*>(workspace), &r);
-  // as the readout chooses it: up to 32 rows the few-row GEMM, more the persistent one where its
-  // 32-bit offsets reach, else the streaming one; but small products have tiles of their own
+  // As the readout chooses it: up to 32 rows the few-row GEMM, more the persistent one where d is a multiple of 32
+  // and its 32-bit offsets reach, else the streaming one; but small products have tiles of their own.
+  // The streaming one is slower, more so with few rows, whose slices do not go by the count (50000 entries, us: 100
+  // rows of 1000 149, of 1024 39; of 2040 270, of 2048 57; 4000 rows of 1000 586, of 1024 369; of 2040 1108, of 2048
+  // 676).  All go by L, since the count stays on the device: 20 counted rows of 126464 x 4096 take 169 us as 20
+  // positions, 197 among 1024 and 207 among 8192; of 4096 x 256 20, 20 and 26.
   const int64_t n_vt = (p->V + dllm::kLargeBN - 1) / dllm::kLargeBN, n_rt = (L + dllm::kLargeBM - 1) / dllm::kLargeBM;
   const bool persistent = p->d % dllm::kPersistBK == 0 && (int64_t)dllm::kPersistBN * p->d * 2 < ((int64_t)1 << 32) &&
                           (p->d % dllm::kPersistWideBK == 0 || L * p->d * 2 < ((int64_t)1 << 32));

@@ -23,7 +23,8 @@ constexpr int kLossFew = 256;
 
 // dz's probability, exp(z - lse): the difference is taken before anything rounds
 // it, as (lse - z) / 256 between 0 and 1 (the clamp is the multiply-add's own),
-// so logits of any size give no more than 1, and what lies 256 below gives 0.
+// so logits of any size give no more than 1, and what lies 256 below gives 0.  A
+// NaN logit gives a number, too: its row's lse is NaN, and so is its coefficient.
 constexpr float kLossPScale = 1.0f / 256.0f;
 __device__ __forceinline__ float loss_p(float z, float scaled_lse) {
   const float x = __builtin_amdgcn_fmed3f(fmaf(z, -kLossPScale, scaled_lse), 0.0f, 1.0f);

@@ -369,9 +369,13 @@ struct Deal {
   int chunks;      // workgroups to a gate's run, 0 = a workgroup has whole runs
 };
 
-// Two workgroups to a compute unit, as many as fit beside each other; two tokens
-// to a workgroup where there are no more, as writing and adding the shares is
-// then most of the time (509 tokens of 4096: 16.1 us; a token to each 18.8).
+// Two workgroups to a compute unit, the best of 512, 1024 and 2048 workgroups for
+// rows of 256 threads and more (32768 tokens of 3584: 307, 321 and 351 us).  Narrow
+// rows, whose workgroups are one or two waves, would rather have more of them (of
+// 2048: 213, 190 and 227; of 1024 164, 103 and 108; of 256 98, 56 and 41), short
+// batches of them not always (4096 tokens of 512: 27, 25 and 29).  Two tokens to a
+// workgroup where there are no more, as writing and adding the shares is then most
+// of the time (509 tokens of 4096: 16.1 us; a token to each 18.8).
 int64_t deal_to(int64_t T) { return T <= 512 ? (T + 1) / 2 : 512; }
 
 Deal deal_tokens(int64_t T, int64_t runs) {  // T >= 1
