@@ -118,52 +118,145 @@ __device__ __forceinline__ void total_of(const float* terms, int M, float* loss)
   }
 }
 
+// The target's logit, summed as the forward product sums it: by its matrix
+// instruction, in its order of K.  Where the target is almost sure, or logits are
+// large, lse is this logit and little more, and the loss is their difference: from
+// a sum in another order it had the roundings of both (a loss of 0.008 at a logit
+// of 12, d 4096: 1e-3 of itself off, now 2e-5; at logits of 2^20 off by 2).
+// Eight rows to a workgroup, one brought to LDS by each wave in pieces of 1024
+// columns; one wave multiplies them, and the sums beside the diagonal are not
+// used.  `first` is the stage that the wave's row begins with; `meanwhile` is done
+// while the first piece is on its way.  The time is the chain of dependent
+// instructions (d of 4096: 256 of them, 64 cycles each, 8 us) and, with many rows,
+// how many workgroups a compute unit holds (k_loss_rows for 102 rows of 4096 17 us,
+// with a sum in any order 10; 3900 of 3584 20 and 13; 7400 of 4096 38 and 20; by
+// four rows to a workgroup 15, 28 and 44).
+typedef short bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+constexpr int kDotRows = 8, kDotCols = 1024, kDotThreads = 64 * kDotRows;
+
+struct DotLds {
+  uint16_t w[kDotRows][kDotCols + 16], h[kDotRows][kDotCols + 16];  // rows 8 banks apart: 8 rows and 2 halves meet all 64
+  float z[kDotRows];
+};
+
+template <class F>
+__device__ __forceinline__ float target_logit(DotLds& lds, const uint16_t* w, const uint16_t* h, int d, int first, F meanwhile) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int stages = (d + kLossStep - 1) / kLossStep;
+  uint4 x[2], y[2];
+  auto load = [&](int q0) {  // stages q0 .. q0 + 15 in the row's order, zeros behind d and the last one
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int q = q0 + i * 8 + (lane >> 3), k = (first + q < stages ? first + q : first + q - stages) * kLossStep + (lane & 7) * 8;
+      x[i] = y[i] = make_uint4(0, 0, 0, 0);
+      if (q < stages && k < d) {
+        x[i] = *reinterpret_cast<const uint4*>(w + k);
+        y[i] = *reinterpret_cast<const uint4*>(h + k);
+      }
+    }
+  };
+  f32x16 acc = {};
+  load(0);
+  meanwhile();
+  const int multiplier = (int)(blockIdx.x + blockIdx.x / 256) & 3;  // workgroups of a compute unit: each on another SIMD
+  for (int q0 = 0; q0 < stages; q0 += kDotCols / kLossStep) {
+    __syncthreads();  // the piece before has been read
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      *reinterpret_cast<uint4*>(&lds.w[wave][i * 512 + lane * 8]) = x[i];
+      *reinterpret_cast<uint4*>(&lds.h[wave][i * 512 + lane * 8]) = y[i];
+    }
+    __syncthreads();
+    load(q0 + kDotCols / kLossStep);
+    if (wave == multiplier) {
+      const uint16_t *fw = &lds.w[lane & (kDotRows - 1)][8 * (lane >> 5)], *fh = &lds.h[lane & (kDotRows - 1)][8 * (lane >> 5)];
+      const int steps = min(stages - q0, kDotCols / kLossStep) * (kLossStep / 16);
+      bf16x8 a[4], b[4];
+      auto read = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = *reinterpret_cast<const bf16x8*>(fw + 16 * (k + i));
+          b[i] = *reinterpret_cast<const bf16x8*>(fh + 16 * (k + i));
+        }
+      };
+      read(0);
+      for (int k = 0; k < steps; k += 4) {  // the next four steps' operands are read behind these ones'
+        bf16x8 c[4], e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          c[i] = a[i];
+          e[i] = b[i];
+        }
+        read(min(k + 4, steps - 4));
+        asm volatile("" ::: "memory");  // not moved to where they are used
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c[i], e[i], acc, 0, 0, 0);
+      }
+    }
+  }
+  const int r = lane & 31;  // the lane's column; it has rows 0 .. 3, or 4 .. 7 behind lane 32, in its first results
+  if (wave == multiplier && r < kDotRows && (lane >> 5) == (r >> 2)) {
+    float z = acc[0];
+#pragma unroll
+    for (int i = 1; i < 4; ++i) z = (r & 3) == i ? acc[i] : z;
+    lds.z[r] = z;
+  }
+  __syncthreads();
+  return lds.z[wave];
+}
+
+// The stage of K that the forward product's tile with entry t begins with.
+__device__ __forceinline__ int first_stage(bool small, int t, int d) {
+  return small ? loss_few_start(t / kLossFewEntries, (d + kLossStep - 1) / kLossStep) : 0;
+}
+
+// lse - z for a logit z of the row, without lse's rounding: ln(s / 2^q) + m - z.
+// The largest logit's own exponential in s is 2^q as the instruction rounds it, so
+// what is left of their difference are the others'.
+__device__ __forceinline__ float row_loss(const RowState& r, float lse, float z) {
+  if (!(fabsf(r.m) < 0x1p29f)) return lse - z;
+  const float top = __builtin_amdgcn_exp2f(fmaf(r.m, kLog2eF, -log2_ref(r.m)));
+  return log1pf((r.s - top) / top) + (r.m - z);
+}
+
 // One wave for each row: the slices' partials joined, and the target's logit, which
-// is a row of W for each (3900 rows of 3584: 13 us, 4.3 TB/s).
-// With `loss` the last workgroup to end adds the terms, too.
-__global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* __restrict__ W, const uint16_t* __restrict__ H,
+// is a row of W for each.  With `loss` the last workgroup to end adds the terms, too.
+__global__ __launch_bounds__(kDotThreads, 4) void k_loss_rows(const uint16_t* __restrict__ W, const uint16_t* __restrict__ H,
                                                    int d, int L, const int32_t* __restrict__ targets,
                                                    const float* __restrict__ weights,
                                                    const int32_t* __restrict__ idx, const int32_t* __restrict__ ctr,
-                                                   Partials p, bool records, float* terms,
+                                                   Partials p, bool records, bool small, float* terms,
                                                    float* __restrict__ losses, float* __restrict__ lse,
                                                    int32_t* __restrict__ ended, float* __restrict__ loss) {
+  __shared__ DotLds dot;
   const int M = min(ctr[0], L), slices = ctr[3];
   const int lane = threadIdx.x & 63;
-  for (int row = blockIdx.x * 4 + (threadIdx.x >> 6); row < M; row += gridDim.x * 4) {
-    const int pos = idx[row];
-    const uint16_t *h = H + (int64_t)pos * d, *w = W + (int64_t)targets[pos] * d;
-    float z = 0.f;
-    for (int c = 8 * lane; c < d; c += 8 * 64) {
-      float x[8], y[8];
-      unpack8(*reinterpret_cast<const uint4*>(h + c), x);
-      unpack8(*reinterpret_cast<const uint4*>(w + c), y);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z = fmaf(x[j], y[j], z);
-    }
+  for (int row0 = blockIdx.x * kDotRows; row0 < M; row0 += gridDim.x * kDotRows) {
+    const int row = row0 + (threadIdx.x >> 6), pos = idx[min(row, M - 1)], t = targets[pos];
     RowState r = row_state_empty();
-    const size_t base = (size_t)row * (size_t)slices;
-    for (int j = lane; j < slices; j += 64) {
-      RowState y = row_state_empty();
-      if (records) {  // the few-row GEMM's (m, index, s, 0)
-        const float4 rec = reinterpret_cast<const float4*>(p.m)[base + j];
-        y.m = rec.x;
-        y.s = rec.z;
-      } else {
-        y.m = p.m[base + j];
-        y.s = p.s[base + j];
+    const float z = target_logit(dot, W + (int64_t)t * d, H + (int64_t)pos * d, d, first_stage(small, t, d), [&]() {
+      const size_t base = (size_t)min(row, M - 1) * (size_t)slices;
+      for (int j = lane; j < slices; j += 64) {
+        RowState y = row_state_empty();
+        if (records) {  // the few-row GEMM's (m, index, s, 0)
+          const float4 rec = reinterpret_cast<const float4*>(p.m)[base + j];
+          y.m = rec.x;
+          y.s = rec.z;
+        } else {
+          y.m = p.m[base + j];
+          y.s = p.s[base + j];
+        }
+        row_merge<false>(r, y);
       }
-      row_merge<false>(r, y);
-    }
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      z += __shfl_xor(z, off);
-      row_merge<false>(r, shfl_xor_state(r, off));
-    }
-    if (lane == 0) {
+      for (int off = 32; off >= 1; off >>= 1) row_merge<false>(r, shfl_xor_state(r, off));
+    });
+    if (lane == 0 && row < M) {
       const float l = row_finish<false>(r).lse;
-      // l and z are sums in different orders: a sure target's z may come out above
-      const float over = l - z, x = over < 0.f ? 0.f : over;
+      // lse - z, before lse is rounded; the sum of exponentials may be a little below the target's own
+      const float over = row_loss(r, l, z), x = over < 0.f ? 0.f : over;
       losses[pos] = x;
       lse[pos] = l;
       terms[row] = x * (weights ? weights[pos] : 1.f);
@@ -178,7 +271,7 @@ __global__ __launch_bounds__(256) void k_loss_rows(const uint16_t* __restrict__ 
     __threadfence();
   }
   __syncthreads();
-  if (last) total_of<256>(terms, M, loss);
+  if (last) total_of<kDotThreads>(terms, M, loss);
 }
 
 __global__ __launch_bounds__(1024) void k_loss_total(const float* __restrict__ terms, const int32_t* __restrict__ ctr,
@@ -189,7 +282,7 @@ __global__ __launch_bounds__(1024) void k_loss_total(const float* __restrict__ t
 // What backward keeps of each counted row, in order: its hidden state and
 // scalars, filled up with rows and columns of zeros; and zeros for the rows of
 // d_hidden that do not count.  A wave takes a row (8192 positions of 3584, 3900
-// counted: 21 us).
+// counted: 27 us).
 struct PrepareArgs {
   const uint16_t *W, *H;
   const uint8_t* mask;
@@ -197,6 +290,7 @@ struct PrepareArgs {
   const float *weights, *grad, *lse;
   const int32_t *idx, *ctr;
   int V, L, d, dp;
+  bool small;  // the forward product's tiles
   uint16_t* rows;
   float *lse_of, *coef;
   int32_t* tgt;
@@ -204,50 +298,41 @@ struct PrepareArgs {
   uint16_t* d_hidden;
 };
 
-__global__ __launch_bounds__(256) void k_loss_prepare(PrepareArgs a) {
+__global__ __launch_bounds__(kDotThreads, 4) void k_loss_prepare(PrepareArgs a) {
   const int M = min(a.ctr[0], a.L), Mp = (M + kLossStep - 1) / kLossStep * kLossStep, lane = threadIdx.x & 63;
-  const uint4 none = make_uint4(0, 0, 0, 0);
-  for (int i = blockIdx.x * 4 + (threadIdx.x >> 6); i < max(a.L, Mp); i += gridDim.x * 4) {
-    if (i < M) {
-      const int pos = a.idx[i], t = a.targets[pos];
-      const uint16_t *h = a.H + (int64_t)pos * a.d, *w = a.W + (int64_t)t * a.d;
-      float z = 0.f;
-      for (int c = 8 * lane; c < a.dp; c += 8 * 64) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (c < a.d) {
-          u = *reinterpret_cast<const uint4*>(h + c);
-          float x[8], y[8];
-          unpack8(u, x);
-          unpack8(*reinterpret_cast<const uint4*>(w + c), y);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) z = fmaf(x[j], y[j], z);
+  __shared__ DotLds dot;
+  for (int i0 = blockIdx.x * kDotRows; i0 < max(a.L, Mp); i0 += gridDim.x * kDotRows) {
+    const int i = i0 + (threadIdx.x >> 6), pos = M > 0 ? a.idx[min(i, M - 1)] : 0;
+    auto rows = [&]() {
+      if (i < Mp) {
+        for (int c = 8 * lane; c < a.dp; c += 8 * 64) {
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (i < M && c < a.d) u = *reinterpret_cast<const uint4*>(a.H + (int64_t)pos * a.d + c);
+          *reinterpret_cast<uint4*>(a.rows + (int64_t)i * a.dp + c) = u;
         }
-        *reinterpret_cast<uint4*>(a.rows + (int64_t)i * a.dp + c) = u;
       }
-#pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) z += __shfl_xor(z, off);
-      if (lane == 0) {
-        const float lse = a.lse[pos], c = (a.weights ? a.weights[pos] : 1.f) * (a.grad ? *a.grad : 1.f);
-        a.lse_of[i] = lse * kLossPScale;
-        a.coef[i] = fabsf(lse) < INFINITY ? c : NAN;
-        a.tgt[i] = t;
-        // z and lse are sums in different orders: a sure target's z may come out above (by 2 at logits of 2^20)
-        const float over = z - lse, at = c * expm1f(over > 0.f ? 0.f : over);
-        a.at_tgt[i] = at;
-        a.left[i] = at - bf16_float(float_bf16(at));
-      }
-    } else if (i < Mp) {
-      for (int c = 8 * lane; c < a.dp; c += 8 * 64) *reinterpret_cast<uint4*>(a.rows + (int64_t)i * a.dp + c) = none;
-      if (lane == 0) {
-        a.lse_of[i] = 0.f;
-        a.coef[i] = 0.f;
-        a.tgt[i] = -1;
-        a.at_tgt[i] = 0.f;
-        a.left[i] = 0.f;
-      }
+      if (a.d_hidden && i < a.L && !counts(a.mask[i], a.targets[i], a.V))
+        for (int c = 8 * lane; c < a.d; c += 8 * 64)
+          *reinterpret_cast<uint4*>(a.d_hidden + (int64_t)i * a.d + c) = make_uint4(0, 0, 0, 0);
+    };
+    float z = 0.f;
+    int t = 0;
+    if (i0 < M) {
+      t = a.targets[pos];
+      z = target_logit(dot, a.W + (int64_t)t * a.d, a.H + (int64_t)pos * a.d, a.d, first_stage(a.small, t, a.d), rows);
+    } else {
+      rows();
     }
-    if (a.d_hidden && i < a.L && !counts(a.mask[i], a.targets[i], a.V))
-      for (int c = 8 * lane; c < a.d; c += 8 * 64) *reinterpret_cast<uint4*>(a.d_hidden + (int64_t)i * a.d + c) = none;
+    if (lane > 0 || i >= Mp) continue;
+    const bool in = i < M;
+    const float lse = in ? a.lse[pos] : 0.f, c = in ? (a.weights ? a.weights[pos] : 1.f) * (a.grad ? *a.grad : 1.f) : 0.f;
+    // lse may be rounded to below a sure target's z
+    const float over = z - lse, at = in ? c * expm1f(over > 0.f ? 0.f : over) : 0.f;
+    a.lse_of[i] = lse * kLossPScale;
+    a.coef[i] = fabsf(lse) < INFINITY ? c : NAN;
+    a.tgt[i] = in ? t : -1;
+    a.at_tgt[i] = at;
+    a.left[i] = at - bf16_float(float_bf16(at));
   }
 }
 
@@ -429,13 +514,13 @@ dllm_status dllm_loss_forward(const dllm_loss* p, float* loss, float* losses, fl
                            ? dllm::launch_gemm_persistent(p->W_lm, p->hidden, d, V, r.idx, r.ctr, cus, r.part, st)
                            : dllm::launch_gemm_large(p->W_lm, p->hidden, d, V, r.idx, r.ctr, (int)n_rt, plan.fixed_slices, r.part, st);
   if (e != hipSuccess) return DLLM_ERR_HIP;
-  // The last workgroup to end adds the terms of up to 768 positions itself.  More are another kernel's: each
+  // The last workgroup to end adds the terms of up to 1024 positions itself.  More are another kernel's: each
   // workgroup's arrival waits for its chip's cache to be written back.  Half of the positions counted, 4096 entries
-  // of 256, us a call with the last workgroup and with a kernel: 64 positions 19 and 22, 512 19 and 23, 768 20.6 and
-  // 22.6, 1024 23.3 and 22.7, 1536 32 and 23.5, 4096 60 and 30.
-  const bool ends = L <= 768;
-  hipLaunchKernelGGL(dllm::k_loss_rows, dim3(dllm::grid_for((L + 3) / 4, 65536)), dim3(256), 0, st, p->W_lm, p->hidden,
-                     (int)p->d, (int)L, p->targets, p->weights, r.idx, r.ctr, r.part, stream_w, r.terms, losses, lse, r.ctr + 5,
+  // of 256, us a call with the last workgroup and with a kernel: 64 positions 19 and 22, 512 20 and 23, 1024 22.0 and
+  // 22.3, 1280 22.6 and 22.4, 1536 28 and 25, 4096 43 and 32.
+  const bool ends = L <= 1024;
+  hipLaunchKernelGGL(dllm::k_loss_rows, dim3(dllm::grid_for((L + dllm::kDotRows - 1) / dllm::kDotRows, 65536)), dim3(dllm::kDotThreads), 0, st, p->W_lm, p->hidden,
+                     (int)p->d, (int)L, p->targets, p->weights, r.idx, r.ctr, r.part, stream_w, small, r.terms, losses, lse, r.ctr + 5,
                      ends ? loss : nullptr);
   if (!ends) hipLaunchKernelGGL(dllm::k_loss_total, dim3(1), dim3(1024), 0, st, r.terms, r.ctr, (int)L, loss);
   return hipGetLastError() == hipSuccess ? DLLM_OK : DLLM_ERR_HIP;
@@ -481,8 +566,8 @@ dllm_status dllm_loss_backward(const dllm_loss* p, const float* lse, const float
   hipLaunchKernelGGL(dllm::k_loss_compact, dim3(1), dim3(dllm::kCompactThreads), 0, st, ca);
   const int dp = (int)dllm::loss_padded(d), grid = cus < dllm::kLossGrid ? cus : dllm::kLossGrid;
   const dllm::PrepareArgs pa = {p->W_lm, p->hidden, p->mask, p->targets, p->weights, grad,   lse,   r.idx,    r.ctr,  (int)V,
-                                (int)L,  (int)d,    dp,      r.rows,     r.lse_of,   r.coef, r.tgt, r.at_tgt, r.left, d_hidden};
-  hipLaunchKernelGGL(dllm::k_loss_prepare, dim3(dllm::grid_for(dllm::loss_padded(L) / 4, 65536)), dim3(256), 0, st, pa);
+                                (int)L,  (int)d,    dp,      dllm::loss_small(V, L), r.rows,     r.lse_of,   r.coef, r.tgt, r.at_tgt, r.left, d_hidden};
+  hipLaunchKernelGGL(dllm::k_loss_prepare, dim3(dllm::grid_for(dllm::loss_padded(L) / dllm::kDotRows, 65536)), dim3(dllm::kDotThreads), 0, st, pa);
   dllm::GradArgs a = {};
   a.W = p->W_lm;
   a.zeros = r.zeros;

@@ -901,7 +901,7 @@ __global__ __launch_bounds__(NT, 1) void k_loss_lse_small(LseArgs a, int n_rt, i
     ph[j] = a.H + (int64_t)a.idx[min(r0 + row + 32 * j, M - 1)] * a.d + col;
   }
   f32x16 acc[2][2] = {};
-  small_product<TAIL>(lds, pw, ph, stages, vt * 7 % stages * BK, a.d, a.zeros, acc);
+  small_product<TAIL>(lds, pw, ph, stages, loss_few_start(vt, stages) * BK, a.d, a.zeros, acc);
   float* wave_m = reinterpret_cast<float*>(lds);  // [2][FR] of the two waves with the same rows
   float* wave_s = wave_m + 2 * FR;
   auto off = [](int x) { return 8 * (x >> 2) + (x & 3); };
