@@ -148,7 +148,8 @@ __device__ __forceinline__ float target_logit(DotLds& lds, const uint16_t* w, co
   auto load = [&](int q0) {  // stages q0 .. q0 + 15 in the row's order, zeros behind d and the last one
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int q = q0 + i * 8 + (lane >> 3), k = (first + q < stages ? first + q : first + q - stages) * kLossStep + (lane & 7) * 8;
+      const int q = q0 + i * 8 + (lane >> 3), own = first + q < stages ? first + q : first + q - stages;
+      const int k = own * kLossStep + (lane & 7) * 8;
       x[i] = y[i] = make_uint4(0, 0, 0, 0);
       if (q < stages && k < d) {
         x[i] = *reinterpret_cast<const uint4*>(w + k);
@@ -170,7 +171,8 @@ __device__ __forceinline__ float target_logit(DotLds& lds, const uint16_t* w, co
     __syncthreads();
     load(q0 + kDotCols / kLossStep);
     if (wave == multiplier) {
-      const uint16_t *fw = &lds.w[lane & (kDotRows - 1)][8 * (lane >> 5)], *fh = &lds.h[lane & (kDotRows - 1)][8 * (lane >> 5)];
+      const uint16_t* fw = &lds.w[lane & (kDotRows - 1)][8 * (lane >> 5)];
+      const uint16_t* fh = &lds.h[lane & (kDotRows - 1)][8 * (lane >> 5)];
       const int steps = min(stages - q0, kDotCols / kLossStep) * (kLossStep / 16);
       bf16x8 a[4], b[4];
       auto read = [&](int k) {
@@ -223,13 +225,15 @@ __device__ __forceinline__ float row_loss(const RowState& r, float lse, float z)
 
 // One wave for each row: the slices' partials joined, and the target's logit, which
 // is a row of W for each.  With `loss` the last workgroup to end adds the terms, too.
-__global__ __launch_bounds__(kDotThreads, 4) void k_loss_rows(const uint16_t* __restrict__ W, const uint16_t* __restrict__ H,
-                                                   int d, int L, const int32_t* __restrict__ targets,
-                                                   const float* __restrict__ weights,
-                                                   const int32_t* __restrict__ idx, const int32_t* __restrict__ ctr,
-                                                   Partials p, bool records, bool small, float* terms,
-                                                   float* __restrict__ losses, float* __restrict__ lse,
-                                                   int32_t* __restrict__ ended, float* __restrict__ loss) {
+__global__ __launch_bounds__(kDotThreads, 4) void k_loss_rows(const uint16_t* __restrict__ W,
+                                                              const uint16_t* __restrict__ H, int d, int L,
+                                                              const int32_t* __restrict__ targets,
+                                                              const float* __restrict__ weights,
+                                                              const int32_t* __restrict__ idx,
+                                                              const int32_t* __restrict__ ctr, Partials p, bool records,
+                                                              bool small, float* terms, float* __restrict__ losses,
+                                                              float* __restrict__ lse, int32_t* __restrict__ ended,
+                                                              float* __restrict__ loss) {
   __shared__ DotLds dot;
   const int M = min(ctr[0], L), slices = ctr[3];
   const int lane = threadIdx.x & 63;
@@ -519,9 +523,9 @@ dllm_status dllm_loss_forward(const dllm_loss* p, float* loss, float* losses, fl
   // of 256, us a call with the last workgroup and with a kernel: 64 positions 19 and 22, 512 20 and 23, 1024 22.0 and
   // 22.3, 1280 22.6 and 22.4, 1536 28 and 25, 4096 43 and 32.
   const bool ends = L <= 1024;
-  hipLaunchKernelGGL(dllm::k_loss_rows, dim3(dllm::grid_for((L + dllm::kDotRows - 1) / dllm::kDotRows, 65536)), dim3(dllm::kDotThreads), 0, st, p->W_lm, p->hidden,
-                     (int)p->d, (int)L, p->targets, p->weights, r.idx, r.ctr, r.part, stream_w, small, r.terms, losses, lse, r.ctr + 5,
-                     ends ? loss : nullptr);
+  hipLaunchKernelGGL(dllm::k_loss_rows, dim3(dllm::grid_for((L + dllm::kDotRows - 1) / dllm::kDotRows, 65536)),
+                     dim3(dllm::kDotThreads), 0, st, p->W_lm, p->hidden, (int)p->d, (int)L, p->targets, p->weights, r.idx,
+                     r.ctr, r.part, stream_w, small, r.terms, losses, lse, r.ctr + 5, ends ? loss : nullptr);
   if (!ends) hipLaunchKernelGGL(dllm::k_loss_total, dim3(1), dim3(1024), 0, st, r.terms, r.ctr, (int)L, loss);
   return hipGetLastError() == hipSuccess ? DLLM_OK : DLLM_ERR_HIP;
 }
@@ -565,9 +569,12 @@ dllm_status dllm_loss_backward(const dllm_loss* p, const float* lse, const float
   const dllm::CompactArgs ca = {p->mask, p->targets, (int)L, (int)V, plan, nullptr, nullptr, r.idx, r.ctr, r.zeros};
   hipLaunchKernelGGL(dllm::k_loss_compact, dim3(1), dim3(dllm::kCompactThreads), 0, st, ca);
   const int dp = (int)dllm::loss_padded(d), grid = cus < dllm::kLossGrid ? cus : dllm::kLossGrid;
-  const dllm::PrepareArgs pa = {p->W_lm, p->hidden, p->mask, p->targets, p->weights, grad,   lse,   r.idx,    r.ctr,  (int)V,
-                                (int)L,  (int)d,    dp,      dllm::loss_small(V, L), r.rows,     r.lse_of,   r.coef, r.tgt, r.at_tgt, r.left, d_hidden};
-  hipLaunchKernelGGL(dllm::k_loss_prepare, dim3(dllm::grid_for(dllm::loss_padded(L) / dllm::kDotRows, 65536)), dim3(dllm::kDotThreads), 0, st, pa);
+  const dllm::PrepareArgs pa = {p->W_lm, p->hidden, p->mask,  p->targets, p->weights, grad,
+                                lse,     r.idx,     r.ctr,    (int)V,     (int)L,     (int)d,
+                                dp,      dllm::loss_small(V, L), r.rows,  r.lse_of,   r.coef,
+                                r.tgt,   r.at_tgt,  r.left,   d_hidden};
+  hipLaunchKernelGGL(dllm::k_loss_prepare, dim3(dllm::grid_for(dllm::loss_padded(L) / dllm::kDotRows, 65536)),
+                     dim3(dllm::kDotThreads), 0, st, pa);
   dllm::GradArgs a = {};
   a.W = p->W_lm;
   a.zeros = r.zeros;
