@@ -1,5 +1,5 @@
-// bf16 words and the host checks shared by the rotary, norm, embedding and
-// loss kernels.
+// bf16 words, and the host checks and workspaces shared by the rotary, norm,
+// embedding and loss kernels.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -39,6 +39,18 @@ inline bool overlaps(const void* p, size_t n, const void* q, size_t m) {
   const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
   return p && q && n && m && a < b + m && b < a + n;
 }
+
+// A workspace's parts, one behind another, each on 256 bytes; without a base only
+// their size.
+struct Parts {
+  uint8_t* base;
+  size_t size = 0;
+  uint8_t* take(size_t bytes) {
+    uint8_t* const p = base ? base + size : nullptr;
+    size = (size + bytes + 255) / 256 * 256;
+    return p;
+  }
+};
 
 inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 

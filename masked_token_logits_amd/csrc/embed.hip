@@ -389,8 +389,6 @@ bool supported(int64_t d) { return d % 8 == 0 && d < ((int64_t)1 << 20); }
 constexpr int64_t kPlacesMost = (int64_t)1 << 30;
 bool gradient_sizes_ok(int64_t V, int64_t d, int64_t T) { return sizes_ok(V, d, T) && T < kPlacesMost; }
 
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-
 int chunk_of(int64_t T) { return T <= kShortMost ? kChunkShort : kChunkMost; }
 int64_t chunks_of(int64_t T) { return (T + chunk_of(T) - 1) / chunk_of(T); }
 int64_t tiles_of(int64_t T) { return (T + kTile - 1) / kTile; }
@@ -413,12 +411,8 @@ struct Sorting {
   float* part;
 };
 size_t carve(int64_t V, int64_t d, int64_t T, uint8_t* base, Sorting* s) {
-  size_t off = 0;
-  auto take = [&](size_t bytes) {
-    const size_t o = off;
-    off = up256(off + bytes);
-    return base ? base + o : nullptr;
-  };
+  Parts parts = {base};
+  auto take = [&](size_t bytes) { return parts.take(bytes); };
   const size_t list = (size_t)T * 4, more = T > kRankMost ? list : 0;
   Sorting x;
   x.sorted = reinterpret_cast<int32_t*>(take(list));
@@ -431,7 +425,7 @@ size_t carve(int64_t V, int64_t d, int64_t T, uint8_t* base, Sorting* s) {
   x.runs.many = reinterpret_cast<Run*>(take((size_t)chunks_of(T) * sizeof(Run)));
   x.part = reinterpret_cast<float*>(take((size_t)chunks_of(T) * 2 * (size_t)d * 4));
   if (s) *s = x;
-  return off + 256;
+  return parts.size + 256;
 }
 
 void sort_tokens(const int32_t* tokens, int T, int V, const Sorting& s, hipStream_t st) {

@@ -340,8 +340,6 @@ __global__ __launch_bounds__(kDotThreads, 4) void k_loss_prepare(PrepareArgs a) 
   }
 }
 
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-
 bool sizes_ok(int64_t V, int64_t d, int64_t L) {
   return V >= 1 && V < ((int64_t)1 << 31) - 1024 && d >= 1 && L >= 1 && L < ((int64_t)1 << 31) - 1024;
 }
@@ -380,12 +378,8 @@ struct Rows {
 
 // Workspace of both directions; returns its size.
 size_t carve(int64_t V, int64_t d, int64_t L, int64_t piece, uint8_t* base, Rows* r) {
-  size_t off = 0;
-  auto take = [&](size_t bytes) {
-    const size_t o = off;
-    off = up256(off + bytes);
-    return base ? base + o : nullptr;
-  };
+  Parts parts = {base};
+  auto take = [&](size_t bytes) { return parts.take(bytes); };
   Rows x = {};
   x.zeros = reinterpret_cast<uint16_t*>(take(16));
   x.idx = reinterpret_cast<int32_t*>(take((size_t)L * 4));
@@ -408,7 +402,7 @@ size_t carve(int64_t V, int64_t d, int64_t L, int64_t piece, uint8_t* base, Rows
     x.acc = reinterpret_cast<float*>(take((size_t)loss_shares(L, d, piece) * kLossTile * kLossTile * 4));
   }
   if (r) *r = x;
-  return off;
+  return parts.size;
 }
 
 // A tile of dz is addressed by 32-bit byte offsets: 256 rows of a piece.

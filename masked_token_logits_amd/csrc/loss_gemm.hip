@@ -145,6 +145,29 @@ struct Side<true, TAIL> {
   }
 };
 
+// By rows of K, half as wide: rows of K of 256 bytes, four to a DMA, swizzled like
+// the wide ones.  LDS [64][128].
+constexpr int kNarrow = 128;
+struct NarrowSide {
+  int k, col, sw, lane_off;
+  __device__ __forceinline__ NarrowSide(int wave, int lane) {
+    k = wave * 4 + (lane >> 4);
+    col = (((lane & 15) >> 2) ^ (k & 3)) * 32 + (lane & 3) * 8;
+    sw = (lane & 15) >> 2;
+    lane_off = (8 * (lane >> 5) + sw) * kNarrow + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  }
+  // where the lane's first DMA of [K][ld] reads the tile from column c0 on, drawn to the last of `cols`
+  __device__ __forceinline__ const uint16_t* source(const uint16_t* p, int64_t ld, int c0, int cols) const {
+    return p + (int64_t)k * ld + min(c0 + col, cols - 8);
+  }
+  __device__ __forceinline__ bf16x8 frag(const uint16_t* tile, int block, int kk) const {
+    LDS_AS uint16_t* ring = (LDS_AS uint16_t*)tile;
+    LDS_AS const uint16_t* p = ring + lane_off + ((block ^ sw) * 32) + kk * 16 * kNarrow;
+    const bf16x4 lo = read_tr(p, ring), hi = read_tr(p + 4 * kNarrow, ring);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
+
 // One tile of a workgroup's work: the operands at its first K, the K it has,
 // the stage it starts with (later ones follow, then those before it) and the
 // 32-blocks of the second operand that are wanted.
@@ -749,7 +772,7 @@ __global__ __launch_bounds__(NT, 1) void k_loss_d_W(GradArgs a) {
 // while one stores, the others load and multiply (126464 entries of 4096: 205 us
 // for 60 rows, 253 for 102, 370 for 250, where the 256 x 256 tiles take 345 for 102
 // and 450 for 250; d_W's bytes alone, 150).
-constexpr int FV = 128;  // entries of a tile
+constexpr int FV = kNarrow;  // entries of a tile
 
 __global__ __launch_bounds__(NT, 3) void k_loss_d_W_few(GradArgs a, int n_vt, int n_ct) {
   __shared__ __attribute__((aligned(1024))) uint16_t lds[BK * (BT + FV)];
@@ -762,11 +785,8 @@ __global__ __launch_bounds__(NT, 3) void k_loss_d_W_few(GradArgs a, int n_vt, in
   Side<true, false> sa;
   sa.init(a.dp, nullptr, wave, lane);
   sa.start({a.rows + c0, Mp, a.dp - c0});
-  // the entries' side is half as wide: rows of K of 256 bytes, four to a DMA,
-  // swizzled like the wide ones
-  const int bk = wave * 4 + (lane >> 4), bcol = (((lane & 15) >> 2) ^ (bk & 3)) * 32 + (lane & 3) * 8;
-  const char* bsrc = reinterpret_cast<const char*>(a.dz + (int64_t)bk * a.ldz + min(r0 + bcol, (int)a.ldz - 8));
-  const int bsw = (lane & 15) >> 2, boff = (8 * (lane >> 5) + bsw) * FV + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  const NarrowSide sb(wave, lane);
+  const char* bsrc = reinterpret_cast<const char*>(sb.source(a.dz, a.ldz, r0, (int)a.ldz));
   f32x16 acc[4][2] = {};
   for (int k0 = 0; k0 < Mp; k0 += BK) {
 #pragma unroll
@@ -783,12 +803,7 @@ __global__ __launch_bounds__(NT, 3) void k_loss_d_W_few(GradArgs a, int n_vt, in
 #pragma unroll
       for (int f = 0; f < 4; ++f) fa[f] = sa.frag(la, wv * 4 + f, kk, lane);
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        LDS_AS uint16_t* ring = (LDS_AS uint16_t*)lb;
-        LDS_AS const uint16_t* p = ring + boff + (((wr * 2 + f) ^ bsw) * 32) + kk * 16 * FV;
-        const bf16x4 lo = read_tr(p, ring), hi = read_tr(p + 4 * FV, ring);
-        fb[f] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-      }
+      for (int f = 0; f < 2; ++f) fb[f] = sb.frag(lb, wr * 2 + f, kk);
 #pragma unroll
       for (int fv = 0; fv < 4; ++fv)
 #pragma unroll
@@ -987,11 +1002,9 @@ __global__ __launch_bounds__(NT, 1) void k_loss_d_W_small(GradArgs a, int n_ct) 
   const int vt = blockIdx.x / n_ct, ct = blockIdx.x - vt * n_ct, r0 = vt * FV2, c0 = ct * FR;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wr = wave >> 1, wv = wave & 1;
-  // rows of K of 256 bytes, four to a DMA: row k holds its four granules of 32 at granule ^ (k & 3)
-  const int bk = wave * 4 + (lane >> 4), bcol = (((lane & 15) >> 2) ^ (bk & 3)) * 32 + (lane & 3) * 8;
-  const int bsw = (lane & 15) >> 2, boff = (8 * (lane >> 5) + bsw) * FR + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-  const uint16_t* pa = a.rows + (int64_t)bk * a.dp + min(c0 + bcol, a.dp - 8);
-  const uint16_t* pb = a.dz + (int64_t)bk * a.ldz + min(r0 + bcol, (int)a.ldz - 8);
+  static_assert(FR == kNarrow && FV2 == kNarrow, "both sides are narrow ones");
+  const NarrowSide side(wave, lane);
+  const uint16_t *pa = side.source(a.rows, a.dp, c0, a.dp), *pb = side.source(a.dz, a.ldz, r0, (int)a.ldz);
   f32x16 acc[2][2] = {};
   if (stages > 0) {
     int k0 = 0;
@@ -1004,12 +1017,6 @@ __global__ __launch_bounds__(NT, 1) void k_loss_d_W_small(GradArgs a, int n_ct) 
                                          (LDS_AS void*)(to + BK * FR + 4 * j * 512), 16, 0, 0);
       }
       k0 = k0 + BK >= stages * BK ? 0 : k0 + BK;
-    };
-    auto frag = [&](const uint16_t* tile, int block, int kk) {
-      LDS_AS uint16_t* ring = (LDS_AS uint16_t*)tile;
-      LDS_AS const uint16_t* p = ring + boff + ((block ^ bsw) * 32) + kk * 16 * FR;
-      const bf16x4 lo = read_tr(p, ring), hi = read_tr(p + 4 * FR, ring);
-      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     };
     // as in small_product
     issue(0);
@@ -1024,8 +1031,8 @@ __global__ __launch_bounds__(NT, 1) void k_loss_d_W_small(GradArgs a, int n_ct) 
         bf16x8 fa[2], fb[2];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-          fa[f] = frag(t, wv * 2 + f, kk);
-          fb[f] = frag(t + BK * FR, wr * 2 + f, kk);
+          fa[f] = side.frag(t, wv * 2 + f, kk);
+          fb[f] = side.frag(t + BK * FR, wr * 2 + f, kk);
         }
 #pragma unroll
         for (int fv = 0; fv < 2; ++fv)
